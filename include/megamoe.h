@@ -3,7 +3,9 @@
  * with, around it, the router (megamoe_router_topk, and
  * megamoe_forward_from_logits for the whole layer from router logits, a
  * shared expert included) and the dense NVFP4 linear with a measured-amax
- * activation scale (megamoe_linear_nvfp4).
+ * scale (megamoe_linear_nvfp4); and the scored router and the MXFP4 operators
+ * (megamoe_router_scored_topk, megamoe_quantize_mxfp4, megamoe_linear_mxfp4,
+ * megamoe_forward_mxfp4 and their companions, at the end of this file).
  *
  * What it computes (sources are the titles and sections of the pages the
  * method is taken from):
@@ -561,6 +563,180 @@ megamoe_status megamoe_forward_static(const megamoe_weights* w, const uint16_t* 
                                       const int32_t* topk_ids, const float* topk_weights, int T,
                                       int k, int pad, uint16_t* out, uint32_t* status_out,
                                       megamoe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Scored router
+ *
+ * Scores of every expert, s_e = 1 / (1 + exp(-l_e)) or softmax(l)_e, in fp32;
+ * the choice is by c_e = s_e + bias_e (bias may be null), the weights by s_e:
+ *   - the E experts form n_group equal runs; a group's score is the sum of
+ *     its group_top (1 or 2) largest c, and the topk_group groups of highest
+ *     score stay;
+ *   - the k experts of largest c among them, in descending order;
+ *   - w_j = scale * s_j / sum_i s_i (renormalize), or scale * s_j.
+ * Ties, of groups and of experts, go to the lower index.  An expert whose
+ * logit or c is NaN or -inf scores 0 and is never taken; slots left over get
+ * id -1 and weight 0 (the forward skips them).  +inf counts as the largest
+ * float.
+ * ------------------------------------------------------------------------ */
+
+/* Element types. */
+#define MEGAMOE_TYPE_BF16 0
+#define MEGAMOE_TYPE_F32 1
+#define MEGAMOE_TYPE_F16 2
+
+/* Scores. */
+#define MEGAMOE_SCORE_SIGMOID 0
+#define MEGAMOE_SCORE_SOFTMAX 1
+
+/*
+ * megamoe_router_scored_topk
+ *   logits        [T, ld_logits] of logits_type (BF16 or F32)
+ *   bias          [E] float or null
+ *   topk_ids      [T, k] int32 (out)
+ *   topk_weights  [T, k] float (out)
+ * Requires 1 <= E <= 1024, 1 <= k <= 16, k <= E, n_group a divisor of E and at
+ * most 32, 1 <= topk_group <= n_group, group_top 1 or 2, T < 2^31.
+ */
+megamoe_status megamoe_router_scored_topk(const void* logits, int logits_type, int64_t T, int E,
+                                          int64_t ld_logits, const float* bias, int score,
+                                          int n_group, int topk_group, int group_top, int k,
+                                          int renormalize, double scale, int32_t* topk_ids,
+                                          float* topk_weights, megamoe_stream_t stream);
+
+/*
+ * megamoe_router_scored_topk_backward -- the gradient of the weights with
+ * respect to the logits, for the ids that the forward call gave (distinct in a
+ * row; ids < 0 or >= E take no part); the choice itself and the bias have none.
+ *   grad_weights  [T, k] float
+ *   grad_logits   [T, ld_grad] of logits_type (out; columns 0 .. E - 1)
+ */
+megamoe_status megamoe_router_scored_topk_backward(
+    const void* logits, int logits_type, int64_t T, int E, int64_t ld_logits,
+    const int32_t* topk_ids, const float* grad_weights, int score, int k, int renormalize,
+    double scale, void* grad_logits, int64_t ld_grad, megamoe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * MXFP4: E2M1 codes (two per byte, even element in the low nibble) and one
+ * E8M0 scale byte per 32 elements, 2^(byte - 127), 255 = NaN.  No tensor-wide
+ * scale.  Encoding: the scale is 2^(floor(log2(amax)) - 2), at least 2^-127;
+ * elements to the nearest E2M1 value, ties to even, saturating at 6 (the rule
+ * of the OCP Microscaling Formats specification 1.0).  A block that holds Inf
+ * or NaN gets scale 255 and zero codes, and MEGAMOE_DEV_NONFINITE is set.
+ *
+ * Scales are [rows, K / 32] bytes (MEGAMOE_SCALES_ROWMAJOR) or in the atom
+ * layout (MEGAMOE_SCALES_MMA): atoms of 128 rows x 4 blocks as above, with the
+ * blocks of a row padded to a multiple of 8 (zero scales) and the rows to a
+ * multiple of 128: MEGAMOE_MX_ATOM_BYTES(rows, K) bytes.
+ * ------------------------------------------------------------------------ */
+#define MEGAMOE_MX_ATOM_BYTES(rows, K) \
+  (((size_t)(rows) + 127) / 128 * 128 * (((size_t)(K) + 255) / 256 * 8))
+
+/*
+ * megamoe_quantize_mxfp4 -- x [rows, K] of x_type, row stride ld.
+ *   transpose 0: blocks along the columns' direction of a row:
+ *                codes [rows, K / 2], scales of [rows, K]
+ *   transpose 1: x^T, blocks along the rows of x: codes [K, R / 2], scales of
+ *                [K, R], R = rows up to a multiple of 32 (the last block's
+ *                missing elements count as zeros)
+ *   status       device status word or null
+ * Requires K a multiple of 32, ld * element size a multiple of 16, x and codes
+ * 16-byte aligned.
+ */
+megamoe_status megamoe_quantize_mxfp4(const void* x, int x_type, int64_t rows, int K, int64_t ld,
+                                      int transpose, uint8_t* codes, uint8_t* scales,
+                                      int scale_layout, uint32_t* status, megamoe_stream_t stream);
+
+/*
+ * megamoe_dequantize_mxfp4 -- values of row-major codes and scales as bf16
+ * (exact) or fp32.  Requires K a multiple of 32, out 16-byte aligned and
+ * ld * element size a multiple of 16.
+ */
+megamoe_status megamoe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows,
+                                        int K, void* out, int out_type, int64_t ld,
+                                        megamoe_stream_t stream);
+
+/* Row-major MXFP4 scales [rows, K / 32] -> atom layout (weights, once). */
+megamoe_status megamoe_swizzle_scales_mxfp4(const uint8_t* src, int64_t rows, int K, uint8_t* dst,
+                                            megamoe_stream_t stream);
+
+/*
+ * megamoe_linear_mxfp4 -- out [T, N] = MXFP4(x) w^T, fp32 accumulation.
+ *   x         [T, K] of x_type, row stride ld_x
+ *   w_codes   [N, K / 2] row-major, w_scales atom layout
+ *   out       [T, N] bf16 (MEGAMOE_EPI_BF16) or fp32 (MEGAMOE_EPI_F32)
+ *   ws        at least megamoe_linear_mxfp4_workspace_size(T, K, N) bytes,
+ *             256-byte aligned; its first 4 bytes are the status word
+ * Requires K and N multiples of 32, pointers 16-byte aligned and rows on
+ * 16-byte boundaries.
+ */
+size_t megamoe_linear_mxfp4_workspace_size(int64_t T, int K, int N);
+megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K, int64_t ld_x,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, int N,
+                                    int out_dtype, void* out, int64_t ld_out, void* ws,
+                                    size_t ws_bytes, megamoe_stream_t stream);
+
+/*
+ * megamoe_linear_mxfp4_backward -- the gradients of the linear for training,
+ * each a product of operands quantised along the dimension it sums over (the
+ * quantisers' own derivative taken as 1):
+ *   grad_x [T, K] = MXFP4(grad_out) MXFP4(w along N)
+ *   grad_w [N, K] = MXFP4(grad_out along T)^T MXFP4(x along T)
+ *   grad_out  [T, N], x [T, K], w [N, K]: of their types, row strides ld_*
+ *             (w the master weight)
+ *   grad_x, grad_w  bf16 or fp32 (MEGAMOE_EPI_*); either may be null and is
+ *             then not computed
+ *   ws        at least megamoe_linear_mxfp4_backward_workspace_size bytes,
+ *             256-byte aligned; its first 4 bytes are the status word
+ * Requires K and N multiples of 32.  T = 0 gives a zero grad_w.
+ */
+size_t megamoe_linear_mxfp4_backward_workspace_size(int64_t T, int K, int N);
+megamoe_status megamoe_linear_mxfp4_backward(
+    const void* grad_out, int grad_type, int64_t ld_grad, const void* x, int x_type, int64_t ld_x,
+    const void* w, int w_type, int64_t ld_w, int64_t T, int K, int N, void* grad_x,
+    int grad_x_dtype, int64_t ld_grad_x, void* grad_w, int grad_w_dtype, int64_t ld_grad_w,
+    void* ws, size_t ws_bytes, megamoe_stream_t stream);
+
+/*
+ * MXFP4 expert weights: as megamoe_weights, without global scales.
+ *   w13_codes   packed by megamoe_pack_weight_codes with half_rows = I
+ *   w13_scales  atom layout of [E*2I, d] (megamoe_swizzle_scales_mxfp4)
+ *   w2_codes    packed with half_rows = 0
+ *   w2_scales   atom layout of [E*d, I]
+ */
+typedef struct megamoe_mx_weights {
+  int32_t num_experts;
+  int32_t hidden;       /* d */
+  int32_t intermediate; /* I */
+  const uint8_t* w13_codes;
+  const uint8_t* w13_scales;
+  const uint8_t* w2_codes;
+  const uint8_t* w2_scales;
+} megamoe_mx_weights;
+
+/*
+ * megamoe_forward_mxfp4 -- the routed-expert forward with MXFP4 weights and
+ * activations: route -> quantise x into routed rows -> L1 grouped GEMM with
+ * SiLU(gate)*up, quantised to MXFP4 in its epilogue -> L2 grouped GEMM into a
+ * BFP16 y -> top-k weighted combine.  Arguments, shapes and errors as
+ * megamoe_forward; workspace of megamoe_workspace_size_mxfp4 bytes.
+ */
+size_t megamoe_workspace_size_mxfp4(int T, int k, int E, int d, int I, int pad);
+megamoe_status megamoe_forward_mxfp4(const megamoe_mx_weights* w, const uint16_t* x,
+                                     const int32_t* topk_ids, const float* topk_weights, int T,
+                                     int k, int pad, uint16_t* out, void* ws, size_t ws_bytes,
+                                     megamoe_stream_t stream);
+
+/*
+ * megamoe_forward_mxfp4_from_logits -- megamoe_router_scored_topk over the
+ * weights' E experts (its ids and weights in the workspace), then
+ * megamoe_forward_mxfp4.
+ */
+megamoe_status megamoe_forward_mxfp4_from_logits(
+    const megamoe_mx_weights* w, const uint16_t* x, const void* logits, int logits_type,
+    int64_t ld_logits, const float* bias, int score, int n_group, int topk_group, int group_top,
+    int renormalize, double scale, int T, int k, int pad, uint16_t* out, void* ws, size_t ws_bytes,
+    megamoe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -185,6 +185,21 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t a_desc, uint6
       : "memory");
 }
 
+// The same with one E8M0 (power-of-two) scale per 32 elements: an MMA's K = 64
+// takes two scale bytes of a row, the low or high half of its 32-bit scale
+// column (the scale ids of the instruction descriptor).
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                         uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+      "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive on `bar` once every tcgen05 operation this thread issued so far is done.
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile(
@@ -241,6 +256,13 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int M, int N) {
          | (1u << 10)                               // B format: E2M1
          | (static_cast<uint32_t>(N >> 3) << 17)    // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);   // M / 16 (scale format bit 23 = E4M3)
+}
+
+// The same with E8M0 scales (bit 23), taken from the low (half = 0) or high
+// (half = 1) two bytes of the scale columns (ids 0 and 2 of A and B).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int M, int N, int half) {
+  return idesc_nvf4(M, N) | (1u << 23) | (static_cast<uint32_t>(2 * half) << 29) |
+         (static_cast<uint32_t>(2 * half) << 4);
 }
 
 // ---------------------------------------------------------------------------

@@ -55,10 +55,16 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "mxfp4.cuh"
 
 namespace megamoe {
 
-template <int BN, int EPI, int STAGES>
+// MX: MXFP4 operands (one E8M0 scale per 32 elements, no global scales) in the
+// same tiles; a K step of 256 then has two weight-scale atoms instead of four
+// and eight scale bytes per token row (in the same 16-byte row of the box).
+// The SiLU * up epilogue quantises h itself: a block of 32 features is one
+// accumulator row quarter, so no amax over the tensor has to be waited for.
+template <int BN, int EPI, int STAGES, bool MX = false>
 struct GemmCfg {
   static constexpr int G = (EPI == MEGAMOE_EPI_SILU_MUL || EPI == kEpiPartial2) ? 2 : 1;
   static constexpr bool PARTIAL = EPI >= kEpiPartial1;
@@ -67,7 +73,7 @@ struct GemmCfg {
   static constexpr int ACC_STAGES = (2 * G * BN + STAGES * (16 * G + 16) <= 512) ? 2 : 1;
   static constexpr int A_TILE = 128 * 128;  // one weight matrix, 128 rows x 128 bytes
   static constexpr int B_TILE = BN * 128;
-  static constexpr int SFW = 2048;     // 4 atoms of 512 bytes (one per 64-element slice)
+  static constexpr int SFW = MX ? 1024 : 2048;  // 4 atoms of 512 bytes (one per 64-element slice); MX: 2
   static constexpr int SFA_RAW = BN * 16;  // token scales as loaded: BN rows x 16 bytes
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = G * A_TILE;
@@ -92,8 +98,9 @@ struct GemmCfg {
   // stages; a lane's 16 tokens of one feature share a BFP16 exponent group
   // with those of 7 neighbouring lanes)
   static constexpr bool STAGED = BF16_OUT || PARTIAL;
+  static constexpr bool MX_SILU = MX && EPI == MEGAMOE_EPI_SILU_MUL;  // h staged as floats
   static constexpr int STG_ROWS = BF16_OUT ? 8 : 16;
-  static constexpr int STG_BYTES = STAGED ? STG_ROWS * 32 * (BF16_OUT ? 2 : 4) : 0;
+  static constexpr int STG_BYTES = STAGED ? STG_ROWS * 32 * (BF16_OUT && !MX_SILU ? 2 : 4) : 0;
   static constexpr int STG_OFF = (TOFF_OFF + 4 * (MEGAMOE_MAX_EXPERTS + 1) + 15) / 16 * 16;
   static constexpr int SMEM = 1024 + STG_OFF + kEpiWarps * STG_BYTES;
   static constexpr uint32_t IDESC = idesc_nvf4(128, BN);
@@ -102,10 +109,10 @@ struct GemmCfg {
   static_assert((4 * STAGES + 2 * ACC_STAGES + 1) * 8 + 8 <= 512, "barrier area");
 };
 
-template <int BN, int EPI, int STAGES>
+template <int BN, int EPI, int STAGES, bool MX = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     k_grouped_gemm(const __grid_constant__ TokenMaps maps, const GemmArgs p) {
-  using C = GemmCfg<BN, EPI, STAGES>;
+  using C = GemmCfg<BN, EPI, STAGES, MX>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const int E = p.E, N = p.N, K = p.K;
   const int MT = (C::G == 2 ? N / 2 : N) / 128;
   const int KT = K / 256;
-  const int slices = K / 64;
+  const int slices = K / (MX ? 128 : 64);  // scale atoms along K
   // pieces per tile (1 unless split-K); piece q -> tile q / S, K range
   // [ks * KT / S, (ks + 1) * KT / S) with ks = q % S
   const int S = C::PARTIAL ? p.ksplit : 1;
@@ -227,9 +234,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           // scales first, on their own barrier: the scale warps move them into
           // tensor memory while the codes are still landing
           mbar_arrive_expect_tx(&sf_full[stage], C::SF_TX);
-          bulk_load(sb + C::OFF_SFW, sfw0 + kt * 2048, C::SFW, &sf_full[stage], pol_w);
+          bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
           if (C::G == 2)
-            bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + kt * 2048, C::SFW, &sf_full[stage], pol_w);
+            bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
           tma_load_2d(sb + C::OFF_SFA_RAW, &maps.scales, &sf_full[stage], kt * 16, a_row0, pol_a);
           mbar_arrive_expect_tx(&full[stage], C::TX);
           // the stage's weight blocks (gate then up for L1) are contiguous and
@@ -280,8 +287,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int g = 0; g < C::G; ++g) {
               const uint64_t adesc = sdesc_sw128(smem_u32(sb + C::OFF_A + g * C::A_TILE) + 32 * c);
-              mma_nvf4(d_col + g * BN, adesc, bdesc, C::IDESC, sf_col + 16 * g + 4 * c,
-                       sfa_col + 4 * c, (kt != k0 || c != 0) ? 1u : 0u);
+              if (MX)
+                mma_mxf4(d_col + g * BN, adesc, bdesc, idesc_mxf4(128, BN, c & 1),
+                         sf_col + 16 * g + 4 * (c >> 1), sfa_col + 4 * (c >> 1),
+                         (kt != k0 || c != 0) ? 1u : 0u);
+              else
+                mma_nvf4(d_col + g * BN, adesc, bdesc, C::IDESC, sf_col + 16 * g + 4 * c,
+                         sfa_col + 4 * c, (kt != k0 || c != 0) ? 1u : 0u);
             }
           }
           tc_commit(&empty[stage]);
@@ -326,7 +338,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
         for (int g = 0; g < C::G; ++g) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < (MX ? 2 : 4); ++c) {
             const uint4 a = reinterpret_cast<const uint4*>(sb + C::OFF_SFW + g * C::SFW + c * 512)[lane];
             tmem_st_32x32b_x4(sf_col + 16 * g + 4 * c, a.x, a.y, a.z, a.w);
           }
@@ -339,8 +351,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           r[j] = (32 * j + lane < BN) ? raw[32 * j + lane] : make_uint4(0u, 0u, 0u, 0u);
         tmem_st_32x32b_x4(sfa_col + 0, r[0].x, r[1].x, r[2].x, r[3].x);
         tmem_st_32x32b_x4(sfa_col + 4, r[0].y, r[1].y, r[2].y, r[3].y);
-        tmem_st_32x32b_x4(sfa_col + 8, r[0].z, r[1].z, r[2].z, r[3].z);
-        tmem_st_32x32b_x4(sfa_col + 12, r[0].w, r[1].w, r[2].w, r[3].w);
+        if (!MX) {
+          tmem_st_32x32b_x4(sfa_col + 8, r[0].z, r[1].z, r[2].z, r[3].z);
+          tmem_st_32x32b_x4(sfa_col + 12, r[0].w, r[1].w, r[2].w, r[3].w);
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -360,7 +374,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3;
     const int half = warp >= kEpiWarp1 ? 1 : 0;
     uint8_t* stg = smem + C::STG_OFF + (half * 4 + q) * C::STG_BYTES;
-    const float a_gs = __ldg(p.a_gs);
+    const float a_gs = MX ? 1.f : __ldg(p.a_gs);
     int acc = 0;
     uint32_t acc_phase = 0;
     float amax = 0.f;
@@ -378,8 +392,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       x.count = __ldg(p.offsets + e + 1) - __ldg(p.offsets + e);
       x.poff = __ldg(p.padded_offsets + e);
       x.off = __ldg(p.offsets + e);
-      x.gs0 = __ldg(p.w_gs + C::G * e);
-      x.gs1 = C::G == 2 ? __ldg(p.w_gs + 2 * e + 1) : 1.f;
+      x.gs0 = MX ? 1.f : __ldg(p.w_gs + C::G * e);
+      x.gs1 = C::G == 2 && !MX ? __ldg(p.w_gs + 2 * e + 1) : 1.f;
       return x;
     };
     ExpertInfo next = fetch(static_cast<int>(blockIdx.x) / S, 0);
@@ -432,6 +446,46 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint32_t u[16];
           tmem_ld_32x32b_x16(lane_base + BN + n0, u);
           tmem_ld_wait();
+          if (MX) {
+            // h stays fp32 up to its one rounding, to MXFP4: the 32 lanes hold
+            // one block of a token row, whose largest value is one warp
+            // reduction; eight rows at a time go through the staging buffer so
+            // that a lane encodes eight consecutive features
+            float* st = reinterpret_cast<float*>(stg);
+            const int64_t code_row = p.N / 4, scale_row = p.N / 32;
+#pragma unroll
+            for (int h8 = 0; h8 < 16; h8 += 8) {
+              uint32_t mine = 0;  // lanes 0..7: the scale byte of row h8 + lane
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const float gv = __uint_as_float(g[h8 + j]), uv = __uint_as_float(u[h8 + j]);
+                const float hv = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+                const uint32_t byte = mx_scale_byte(
+                    __reduce_max_sync(0xffffffffu, __float_as_uint(hv) & 0x7fffffffu));
+                if (lane == j) mine = byte;
+                st[j * 32 + lane] = hv;
+              }
+              __syncwarp();
+              const int r = lane >> 2, part = lane & 3;
+              const uint32_t byte = __shfl_sync(0xffffffffu, mine, r);
+              if (h8 + r < rows) {
+                float v[8];
+                const float4 a = reinterpret_cast<const float4*>(st + r * 32 + 8 * part)[0];
+                const float4 b = reinterpret_cast<const float4*>(st + r * 32 + 8 * part)[1];
+                v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+                v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+                *reinterpret_cast<uint32_t*>(p.rq_codes + (row0 + n0 + h8 + r) * code_row +
+                                             f0 / 2 + 4 * part) = mx_codes8(v, mx_inverse(byte));
+              }
+              if (lane < 8 && h8 + lane < rows) {
+                p.rq_scales[(row0 + n0 + h8 + lane) * scale_row + mx_routed_offset(f0 >> 5)] =
+                    static_cast<uint8_t>(mine);
+                if (mine == kMxNan) set_status(p.status, MEGAMOE_DEV_NONFINITE);
+              }
+              __syncwarp();
+            }
+            continue;
+          }
           __nv_bfloat16* s = reinterpret_cast<__nv_bfloat16*>(stg);
           __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
 #pragma unroll
@@ -518,7 +572,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         acc_phase ^= 1u;
       }
     }
-    if (EPI == MEGAMOE_EPI_SILU_MUL) {
+    if (EPI == MEGAMOE_EPI_SILU_MUL && !MX) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (lane == 0 && amax > 0.f)
@@ -530,7 +584,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (EPI == MEGAMOE_EPI_SILU_MUL && p.rq_arrivals) {  // never split (S = 1)
+  if (EPI == MEGAMOE_EPI_SILU_MUL && !MX && p.rq_arrivals) {  // never split (S = 1)
     __shared__ int s_rq_ok;
     fused_requant(p, s_toff, MT, total, BN, &s_rq_ok);
   }
@@ -622,7 +676,7 @@ static PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
 
 // 2-D map over a [rows, row_bytes] byte matrix, boxes of box_rows x 128 bytes
 // in the 128-byte swizzle the MMA descriptors expect.
-static bool make_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+bool make_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
                            uint32_t box_rows) {
   auto enc = tensor_map_encoder();
   if (!enc) return false;
@@ -659,10 +713,10 @@ static bool make_scales_map(CUtensorMap* map, const void* base, uint64_t rows, u
   return r == CUDA_SUCCESS;
 }
 
-template <int BN, int EPI, int STAGES>
+template <int BN, int EPI, int STAGES, bool MX = false>
 static cudaError_t launch_cfg(const TokenMaps& maps, const GemmArgs& a, cudaStream_t stream) {
-  using C = GemmCfg<BN, EPI, STAGES>;
-  auto kern = k_grouped_gemm<BN, EPI, STAGES>;
+  using C = GemmCfg<BN, EPI, STAGES, MX>;
+  auto kern = k_grouped_gemm<BN, EPI, STAGES, MX>;
   cudaError_t err =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (err != cudaSuccess) return err;
@@ -734,6 +788,24 @@ cudaError_t launch_grouped_gemm(const GemmLaunch& g, cudaStream_t stream) {
     a.rq_codes = g.rq_codes;
     a.rq_scales = g.rq_scales;
     a.rq_gs = g.rq_gs;
+  }
+  if (g.mx) {  // MXFP4 operands: the routed-expert forward's two products
+    a.rq_codes = g.rq_codes;
+    a.rq_scales = g.rq_scales;
+    if (g.epilogue == MEGAMOE_EPI_SILU_MUL) {
+      switch (bn) {
+        case 32: return launch_cfg<32, MEGAMOE_EPI_SILU_MUL, 5, true>(maps, a, stream);
+        case 64: return launch_cfg<64, MEGAMOE_EPI_SILU_MUL, 4, true>(maps, a, stream);
+        case 256: return launch_grouped_gemm_tm(maps, a, kEpiMxSilu, stream);
+      }
+    } else if (bfp16) {
+      switch (bn) {
+        case 32: return launch_cfg<32, MEGAMOE_EPI_BFP16, 9, true>(maps, a, stream);
+        case 64: return launch_cfg<64, MEGAMOE_EPI_BFP16, 8, true>(maps, a, stream);
+        case 128: return launch_cfg<128, MEGAMOE_EPI_BFP16, 6, true>(maps, a, stream);
+      }
+    }
+    return cudaErrorInvalidValue;
   }
   if (bn == 256) {  // token-major tiles: 128 token rows x 256 weight rows
     if (g.ksplit > 1) return cudaErrorInvalidValue;

@@ -46,6 +46,8 @@ struct GemmArgs {
   // encodes the h rows of its own tiles with gs = 2688 / amax(h) into
   // rq_codes [rows, N/4] and row-major rq_scales [rows, N/32], and CTA 0
   // stores gs in *rq_gs.
+  // MXFP4 kernels (MX) always write h this way, from their epilogue and with
+  // no arrivals: codes [rows, N/4] and scales in the routed layout.
   uint32_t* rq_arrivals;
   uint8_t* rq_codes;
   uint8_t* rq_scales;
@@ -77,6 +79,8 @@ cudaError_t launch_grouped_gemm_tm(const TokenMaps& maps, const GemmArgs& a, int
 // Internal epilogue codes of the split-K kernels (G = 1 and G = 2 operands).
 constexpr int kEpiPartial1 = 16;
 constexpr int kEpiPartial2 = 17;
+// Token-major tiles with MXFP4 operands, SiLU * up quantised to MXFP4.
+constexpr int kEpiMxSilu = 18;
 
 struct TileInfo {
   int e, mt, nt, ntiles;  // expert, feature tile, token tile, token tiles of e

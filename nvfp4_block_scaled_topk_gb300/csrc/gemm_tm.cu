@@ -34,16 +34,19 @@
 #include "common.cuh"
 #include "gemm_common.cuh"
 #include "kernels.h"
+#include "mxfp4.cuh"
 
 namespace megamoe {
 
 template <int EPI, int STAGES>
 struct TmCfg {
-  static constexpr bool SILU = EPI == MEGAMOE_EPI_SILU_MUL;
+  static constexpr bool MX = EPI == kEpiMxSilu;  // MXFP4 operands (as in the weights-on-M kernel)
+  static constexpr bool SILU = EPI == MEGAMOE_EPI_SILU_MUL || MX;
   static constexpr int BM = 128;              // token rows per tile (MMA M)
   static constexpr int A_TILE = BM * 128;     // tokens: 128 rows x 128 bytes (one 256-K step)
   static constexpr int B_TILE = 256 * 128;    // weights: two pre-swizzled 16 KB blocks
-  static constexpr int SFW = 2 * 2048;        // weight scale atoms: 2 row groups x 4 slices
+  static constexpr int SFG = MX ? 1024 : 2048;  // scale atoms of a row group: 4 slices (MX: 2)
+  static constexpr int SFW = 2 * SFG;           // 2 row groups
   static constexpr int SFA_RAW = BM * 16;     // token scales as loaded: 128 rows x 16 bytes
   static constexpr int OFF_A = 0;
   static constexpr int OFF_B = A_TILE;
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   // feature tiles per expert: 128 features (gate + up rows) for L1, else 256
   const int MT = C::SILU ? (N / 2) / 128 : N / 256;
   const int KT = K / 256;
-  const int slices = K / 64;
+  const int slices = K / (C::MX ? 128 : 64);  // scale atoms along K
   // first weight row of feature tile mt of expert e, and its second 128-row
   // group (the up rows for L1, the next 128 features otherwise)
   auto w_rows = [&](int e, int mt, int* r0, int* r1) {
@@ -208,8 +211,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           uint8_t* sb = smem + stage * C::STAGE;
           mbar_arrive_expect_tx(&sf_full[stage], C::SFW + box * 16);
-          bulk_load(sb + C::OFF_SFW, sfw0 + kt * 2048, 2048, &sf_full[stage], pol_w);
-          bulk_load(sb + C::OFF_SFW + 2048, sfw1 + kt * 2048, 2048, &sf_full[stage], pol_w);
+          bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
+          bulk_load(sb + C::OFF_SFW + C::SFG, sfw1 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
           tma_load_2d(sb + C::OFF_SFA_RAW, map_s, &sf_full[stage], kt * 16, a_row0, pol_a);
           mbar_arrive_expect_tx(&full[stage], C::B_TILE + box * 128);
           if (C::SILU) {
@@ -257,8 +260,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           for (int c = 0; c < 4; ++c) {
             const uint64_t adesc = sdesc_sw128(smem_u32(sb + C::OFF_A) + 32 * c);
             const uint64_t bdesc = sdesc_sw128(smem_u32(sb + C::OFF_B) + 32 * c);
-            mma_nvf4(tmem, adesc, bdesc, C::IDESC, sf_col + 4 * c, sf_col + 16 + 8 * c,
-                     (kt != 0 || c != 0) ? 1u : 0u);
+            if (C::MX)
+              mma_mxf4(tmem, adesc, bdesc, idesc_mxf4(128, 256, c & 1), sf_col + 4 * (c >> 1),
+                       sf_col + 16 + 8 * (c >> 1), (kt != 0 || c != 0) ? 1u : 0u);
+            else
+              mma_nvf4(tmem, adesc, bdesc, C::IDESC, sf_col + 4 * c, sf_col + 16 + 8 * c,
+                       (kt != 0 || c != 0) ? 1u : 0u);
           }
           tc_commit(&empty[stage]);
           if (++stage == STAGES) {
@@ -300,14 +307,16 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         for (int j = 0; j < 4; ++j) r[j] = raw[32 * j + lane];
         tmem_st_32x32b_x4(sf_col + 0, r[0].x, r[1].x, r[2].x, r[3].x);
         tmem_st_32x32b_x4(sf_col + 4, r[0].y, r[1].y, r[2].y, r[3].y);
-        tmem_st_32x32b_x4(sf_col + 8, r[0].z, r[1].z, r[2].z, r[3].z);
-        tmem_st_32x32b_x4(sf_col + 12, r[0].w, r[1].w, r[2].w, r[3].w);
+        if (!C::MX) {
+          tmem_st_32x32b_x4(sf_col + 8, r[0].z, r[1].z, r[2].z, r[3].z);
+          tmem_st_32x32b_x4(sf_col + 12, r[0].w, r[1].w, r[2].w, r[3].w);
+        }
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < (C::MX ? 2 : 4); ++c) {
             const uint4 a =
-                reinterpret_cast<const uint4*>(sb + C::OFF_SFW + g * 2048 + c * 512)[lane];
+                reinterpret_cast<const uint4*>(sb + C::OFF_SFW + g * C::SFG + c * 512)[lane];
             tmem_st_32x32b_x4(sf_col + 16 + 8 * c + 4 * g, a.x, a.y, a.z, a.w);
           }
         }
@@ -329,7 +338,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     const int q = warp & 3;
     const int half = warp >= kEpiWarp1 ? 1 : 0;
     const int row_in_tile = q * 32 + lane;
-    const float a_gs = __ldg(p.a_gs);
+    const float a_gs = C::MX ? 1.f : __ldg(p.a_gs);
     uint32_t acc_phase = 0;
     float amax = 0.f;
     struct ExpertInfo {
@@ -343,8 +352,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const int e = x.ti.e;
       x.count = __ldg(p.offsets + e + 1) - __ldg(p.offsets + e);
       x.poff = __ldg(p.padded_offsets + e);
-      x.gs0 = __ldg(p.w_gs + (C::SILU ? 2 * e : e));
-      x.gs1 = C::SILU ? __ldg(p.w_gs + 2 * e + 1) : 1.f;
+      x.gs0 = C::MX ? 1.f : __ldg(p.w_gs + (C::SILU ? 2 * e : e));
+      x.gs1 = C::SILU && !C::MX ? __ldg(p.w_gs + 2 * e + 1) : 1.f;
       return x;
     };
     ExpertInfo next = fetch(blockIdx.x, 0);
@@ -359,7 +368,45 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(acc_full, acc_phase, abort_flag, p.status, p.wait_limit_ns)) break;
       tc_fence_after();
       const uint32_t lane_base = tmem + (static_cast<uint32_t>(q * 32) << 16);
-      if (C::SILU) {
+      if (C::MX) {
+        // a lane holds a token row: its blocks of 32 features are in registers,
+        // h stays fp32 up to its one rounding, to MXFP4
+#pragma unroll 1
+        for (int f0 = 64 * half; f0 < 64 * half + 64; f0 += 32) {
+          float hv[32];
+          uint32_t m = 0;
+#pragma unroll
+          for (int i = 0; i < 32; i += 16) {
+            uint32_t g[16], u[16];
+            tmem_ld_32x32b_x16(lane_base + f0 + i, g);
+            tmem_ld_32x32b_x16(lane_base + 128 + f0 + i, u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float gv = __uint_as_float(g[j]), uv = __uint_as_float(u[j]);
+              hv[i + j] = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+              m = max(m, __float_as_uint(hv[i + j]) & 0x7fffffffu);
+            }
+          }
+          const uint32_t byte = mx_scale_byte(m);
+          const float inv = mx_inverse(byte);
+          uint32_t codes[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = hv[8 * i + j];
+            codes[i] = mx_codes8(v, inv);
+          }
+          if (valid) {
+            const int f = ti.mt * 128 + f0;
+            *reinterpret_cast<uint4*>(p.rq_codes + row * (N / 4) + f / 2) =
+                make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            p.rq_scales[row * (N / 32) + mx_routed_offset(f >> 5)] = static_cast<uint8_t>(byte);
+            if (byte == kMxNan) set_status(p.status, MEGAMOE_DEV_NONFINITE);
+          }
+        }
+      } else if (C::SILU) {
         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out) + row * p.ld_out + ti.mt * 128;
 #pragma unroll 1
         for (int f0 = 64 * half; f0 < 64 * half + 64; f0 += 16) {
@@ -429,7 +476,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (lane == 0) mbar_arrive(acc_empty);
       acc_phase ^= 1u;
     }
-    if (C::SILU) {
+    if (C::SILU && !C::MX) {
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       if (lane == 0 && amax > 0.f)
@@ -441,7 +488,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (C::SILU && p.rq_arrivals) {
+  if (C::SILU && !C::MX && p.rq_arrivals) {
     __shared__ int s_rq_ok;
     fused_requant(p, s_toff, MT, total, C::BM, &s_rq_ok);
   }
@@ -463,6 +510,7 @@ cudaError_t launch_grouped_gemm_tm(const TokenMaps& maps, const GemmArgs& a, int
     case MEGAMOE_EPI_SILU_MUL: return launch_tm_cfg<MEGAMOE_EPI_SILU_MUL, 4>(maps, a, stream);
     case MEGAMOE_EPI_BF16: return launch_tm_cfg<MEGAMOE_EPI_BF16, 4>(maps, a, stream);
     case MEGAMOE_EPI_F32: return launch_tm_cfg<MEGAMOE_EPI_F32, 4>(maps, a, stream);
+    case kEpiMxSilu: return launch_tm_cfg<kEpiMxSilu, 4>(maps, a, stream);
   }
   return cudaErrorInvalidValue;
 }

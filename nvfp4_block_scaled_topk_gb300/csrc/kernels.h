@@ -118,6 +118,11 @@ struct GemmLaunch {
   uint8_t* rq_codes = nullptr;
   uint8_t* rq_scales = nullptr;
   float* rq_gs = nullptr;
+  // MXFP4 operands: w_scales atoms of 128 rows x 4 blocks of 32, act_scales in
+  // the routed layout (16 bytes per K step of 256, eight used), no global
+  // scales; SILU_MUL writes rq_codes and rq_scales (routed layout) instead of
+  // out, BFP16 as for NVFP4; no split
+  bool mx = false;
 };
 // Split-K choice for a GEMM of about `tiles` whole-K tiles of KT K steps: the
 // smallest ksplit (<= 8, >= 2 K steps a piece) that minimises the waves of
@@ -133,6 +138,70 @@ uint64_t wait_limit_ns();
 // Router: ids/weights [T, k (+1 with a shared expert)] from fp32 logits.
 cudaError_t launch_router(const float* logits, int64_t T, int E, int64_t ld, const float* bias,
                           int k, int shared, int32_t* ids, float* weights, cudaStream_t stream);
+
+// 2-D tensor map over a [rows, row_bytes] byte matrix, boxes of box_rows x 128
+// bytes in the 128-byte swizzle.
+bool make_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
+                    uint32_t box_rows);
+
+// Scored router (grouped top-k over sigmoid or softmax scores) and its gradient.
+struct ScoredRouter {
+  const void* logits;  // [T, ld], fp32 or bf16
+  bool bf16;
+  int64_t T, ld;
+  int E;
+  const float* bias;
+  int softmax, n_group, topk_group, group_top, k, renormalize;
+  float scale;
+  int32_t* ids;  // [T, k]; read by the gradient
+  float* weights;
+};
+cudaError_t launch_scored_router(const ScoredRouter& r, cudaStream_t stream);
+// grad [T, k] -> out [T, ld_out] of the logits' type.
+cudaError_t launch_scored_router_backward(const ScoredRouter& r, const float* grad, void* out,
+                                          int64_t ld_out, cudaStream_t stream);
+
+// MXFP4 quantisation of x [rows, K] along rows, or (transpose) along columns
+// into codes [K, R / 2] with R = rows up to a multiple of 32.
+struct MxQuant {
+  const void* x;
+  int type;  // MEGAMOE_TYPE_*
+  int64_t rows, ld;
+  int K;
+  bool transpose;
+  uint8_t* codes;
+  uint8_t* scales;
+  int layout;  // MEGAMOE_SCALES_*
+  uint32_t* status;
+};
+cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s);
+// x [T, d] bf16 into routed rows slot_dst[t k + j] (routed scale layout).
+cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t* slot_dst, int k,
+                             uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s);
+// Row-major codes and scales -> values.
+cudaError_t launch_mx_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
+                             void* out, bool f32, int64_t ld, cudaStream_t s);
+cudaError_t launch_mx_swizzle(const uint8_t* src, int64_t rows, int64_t K, uint8_t* dst,
+                              cudaStream_t s);
+
+// out [R, C] = P [R, K] Q [C, K]^T of MXFP4 operands (row-major codes, atom
+// scales); K a multiple of 32, C of 16.
+struct MxProduct {
+  const uint8_t* r_codes;
+  const uint8_t* r_scales;
+  const uint8_t* c_codes;
+  const uint8_t* c_scales;
+  int64_t R, C, K;
+  void* out;
+  bool out_f32;
+  int64_t ld_out;
+  float* partial;      // mx_product_bytes
+  uint32_t* counters;  // mx_product_counters words, zero
+  uint32_t* status;
+};
+size_t mx_product_bytes(int64_t R, int64_t C, int64_t K);
+int mx_product_counters(int64_t R, int64_t C, int64_t K);
+cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);
 
 // Shape and weight-pointer checks of megamoe_forward.
 megamoe_status check_forward_shape(const megamoe_weights* w, int T, int k, int pad);

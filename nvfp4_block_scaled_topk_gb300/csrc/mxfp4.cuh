@@ -1,0 +1,94 @@
+// MXFP4 codec and layouts (internal to the library): E2M1 elements, one
+// power-of-two scale (E8M0 byte, 2^(byte - 127), 255 = NaN) per 32 elements.
+//
+// The scale of a block is 2^(floor(log2(amax)) - 2), at least 2^-127, so the
+// largest element falls in [4, 8) and elements past 6 saturate (the rule of
+// the OCP Microscaling Formats specification 1.0, section 6.3).  Every step is
+// exact but the one rounding to E2M1: dividing by a power of two only moves
+// the exponent.  A block that holds Inf or NaN gets scale 255 and zero codes,
+// so it decodes to NaN.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "common.cuh"
+
+namespace megamoe {
+
+constexpr uint32_t kMxNan = 255u;
+
+// Scale byte from the bits of a block's largest |x| (as fp32).
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax_bits) {
+  if (amax_bits >= 0x7f800000u) return kMxNan;
+  const uint32_t e = amax_bits >> 23;  // biased exponent; 0 for subnormals
+  return e > 2u ? e - 2u : 0u;
+}
+// 2^(127 - byte), what elements are multiplied by before rounding (0 for NaN
+// blocks, whose codes are zero).
+__device__ __forceinline__ float mx_inverse(uint32_t byte) {
+  return byte == kMxNan ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+// 2^(byte - 127)
+__device__ __forceinline__ float mx_scale_value(uint32_t byte) {
+  return byte == kMxNan ? __uint_as_float(0x7fffffffu)
+                        : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+// Eight elements -> four bytes of codes (element 0 in the lowest nibble).
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
+  uint32_t c = 0;
+  if (inv != 0.f) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      c |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+  }
+  return c;
+}
+
+// Atoms along K of a matrix of row length K (a K step of 256 holds two).
+__host__ __device__ __forceinline__ int64_t mx_atoms(int64_t K) { return (K + 255) / 256 * 2; }
+
+// Byte of (row, block) in the atom layout: atoms of 128 rows x 4 blocks, the
+// blocks of a row padded to whole K steps of 256.
+__host__ __device__ __forceinline__ int64_t mx_atom_offset(int64_t row, int64_t block,
+                                                           int64_t atoms) {
+  return ((row >> 7) * atoms + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
+         (block & 3);
+}
+
+// Byte of block b in a routed row's scales: 16 bytes for each K step of 256,
+// the first eight used (a tensor-map box row is at least 16 bytes).
+__host__ __device__ __forceinline__ int64_t mx_routed_offset(int b) {
+  return static_cast<int64_t>(b >> 3) * 16 + (b & 7);
+}
+
+// Eight consecutive elements as floats.
+__device__ __forceinline__ void mx_load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void mx_load8(const __half* p, float (&v)[8]) {
+  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void mx_load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+}  // namespace megamoe

@@ -28,6 +28,8 @@ SCALES_MMA = 1
 EPI_F32 = 0
 EPI_SILU_MUL = 1
 EPI_BF16 = 2
+TYPES = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}
+SCORES = {"sigmoid": 0, "softmax": 1}
 EPI_BFP16 = 3  # BFP16: uint16 values, then one int8 exponent per 16 rows x 8 columns
 
 #: every function the header declares, with (restype, argtypes)
@@ -35,6 +37,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
+_D = ctypes.c_double
 SIGNATURES = {
     "megamoe_status_string": (ctypes.c_char_p, [_I]),
     "megamoe_max_padded_rows": (_I64, [_I, _I, _I, _I]),
@@ -62,6 +65,22 @@ SIGNATURES = {
     "megamoe_ep_forward_end": (_I, [_P, _P, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "megamoe_round_bf16": (_I, [_P, _I64, _P, _P]),
     "megamoe_forward_scan_stages": (_I, [_P, _I, _I, _I, _P, _P, _SZ, _P, _P]),
+    "megamoe_router_scored_topk": (_I, [_P, _I, _I64, _I, _I64, _P, _I, _I, _I, _I, _I, _I, _D, _P,
+                                        _P, _P]),
+    "megamoe_router_scored_topk_backward": (_I, [_P, _I, _I64, _I, _I64, _P, _P, _I, _I, _I, _D, _P,
+                                                 _I64, _P]),
+    "megamoe_quantize_mxfp4": (_I, [_P, _I, _I64, _I, _I64, _I, _P, _P, _I, _P, _P]),
+    "megamoe_dequantize_mxfp4": (_I, [_P, _P, _I64, _I, _P, _I, _I64, _P]),
+    "megamoe_swizzle_scales_mxfp4": (_I, [_P, _I64, _I, _P, _P]),
+    "megamoe_linear_mxfp4_workspace_size": (_SZ, [_I64, _I, _I]),
+    "megamoe_linear_mxfp4": (_I, [_P, _I, _I64, _I, _I64, _P, _P, _I, _I, _P, _I64, _P, _SZ, _P]),
+    "megamoe_linear_mxfp4_backward_workspace_size": (_SZ, [_I64, _I, _I]),
+    "megamoe_linear_mxfp4_backward": (_I, [_P, _I, _I64, _P, _I, _I64, _P, _I, _I64, _I64, _I, _I,
+                                           _P, _I, _I64, _P, _I, _I64, _P, _SZ, _P]),
+    "megamoe_workspace_size_mxfp4": (_SZ, [_I, _I, _I, _I, _I, _I]),
+    "megamoe_forward_mxfp4": (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _SZ, _P]),
+    "megamoe_forward_mxfp4_from_logits": (_I, [_P, _P, _P, _I, _I64, _P, _I, _I, _I, _I, _I, _D, _I,
+                                               _I, _I, _P, _P, _SZ, _P]),
 }
 STAGE_XQ_SCALE = 0x01
 STAGE_H = 0x02
@@ -609,3 +628,313 @@ def _carve_views(ws, off, T, k, E, d, I, pad):
         "rows": rows,
     }
     return v
+
+
+# --------------------------------------------------------------------------
+# scored router
+# --------------------------------------------------------------------------
+def _dev_logits(t, name):
+    if not (t.is_cuda and t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16)
+            and (t.stride(1) == 1 or t.shape[1] <= 1)):
+        raise TypeError(f"{name} must be a CUDA float32 or bfloat16 matrix with unit column stride")
+    _on_current_device(t, name)
+
+
+def _score(score):
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {sorted(SCORES)}")
+    return SCORES[score]
+
+
+def _row_stride(t):
+    """Elements between rows (a matrix of one row may carry any stride)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def router_scored_topk(logits: torch.Tensor, k: int, score: str = "sigmoid", bias=None,
+                       n_group: int = 1, topk_group: int = 1, group_top: int = 2,
+                       renormalize: bool = True, scale: float = 1.0):
+    """(ids int32 [T, k], weights float32 [T, k]) from fp32 or bf16 logits
+    [T, E]: sigmoid or softmax scores of every expert, chosen by score + bias
+    within the topk_group groups (of n_group) whose group_top best experts sum
+    highest, weighted by scale * score, renormalised over the k taken.  Slots
+    without an expert to take get id -1 and weight 0."""
+    _dev_logits(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _dev(bias, torch.float32, "bias")
+        if bias.numel() != E:
+            raise ValueError("bias must have one value per expert")
+    ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
+    w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+    _check("megamoe_router_scored_topk", load().megamoe_router_scored_topk(
+        _p(logits), TYPES[logits.dtype], T, E, _row_stride(logits), _p(bias), _score(score),
+        n_group, topk_group, group_top, k, renormalize, scale, _p(ids), _p(w), _stream()))
+    return ids, w
+
+
+def router_scored_topk_backward(logits: torch.Tensor, ids: torch.Tensor,
+                                grad_weights: torch.Tensor, score: str = "sigmoid",
+                                renormalize: bool = True, scale: float = 1.0):
+    """Gradient [T, E] (of the logits' type) of router_scored_topk's weights
+    with respect to the logits, for the ids it gave."""
+    _dev_logits(logits, "logits")
+    _dev(ids, torch.int32, "ids")
+    _dev(grad_weights, torch.float32, "grad_weights")
+    T, E = logits.shape
+    if ids.dim() != 2 or ids.shape[0] != T or grad_weights.shape != ids.shape:
+        raise ValueError("ids and grad_weights must be [T, k]")
+    out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    _check("megamoe_router_scored_topk_backward", load().megamoe_router_scored_topk_backward(
+        _p(logits), TYPES[logits.dtype], T, E, _row_stride(logits), _p(ids), _p(grad_weights),
+        _score(score), ids.shape[1], renormalize, scale, _p(out), E, _stream()))
+    return out
+
+
+# --------------------------------------------------------------------------
+# MXFP4: E2M1 codes, one power-of-two scale per 32 elements
+# --------------------------------------------------------------------------
+def _dev_float_rows(t, name):
+    if not (t.is_cuda and t.dtype in TYPES and t.dim() == 2
+            and (t.stride(1) == 1 or t.shape[1] <= 1)):
+        raise TypeError(f"{name} must be a CUDA bfloat16, float16 or float32 matrix with unit "
+                        "column stride")
+    _on_current_device(t, name)
+
+
+def mx_atom_bytes(rows: int, K: int) -> int:
+    """Bytes of the atom layout of MXFP4 scales [rows, K / 32]."""
+    return (rows + 127) // 128 * 128 * ((K + 255) // 256 * 8)
+
+
+def quantize_mxfp4(x: torch.Tensor, transpose: bool = False, scale_layout=SCALES_ROWMAJOR,
+                   status=None):
+    """x [rows, K] -> (codes [rows, K / 2] u8, scales [rows, K / 32] u8), or with
+    transpose those of x^T, quantised along the rows of x: codes [K, R / 2],
+    scales [K, R / 32], R = rows up to a multiple of 32 (zeros past the last).
+    With SCALES_MMA the scales are a buffer in the atom layout."""
+    _dev_float_rows(x, "x")
+    rows, K = x.shape
+    out_rows, out_k = (K, (rows + 31) // 32 * 32) if transpose else (rows, K)
+    codes = torch.empty(out_rows, out_k // 2, dtype=torch.uint8, device=x.device)
+    if scale_layout == SCALES_MMA:
+        scales = torch.empty(mx_atom_bytes(out_rows, out_k), dtype=torch.uint8, device=x.device)
+    else:
+        scales = torch.empty(out_rows, out_k // 32, dtype=torch.uint8, device=x.device)
+    _check("megamoe_quantize_mxfp4", load().megamoe_quantize_mxfp4(
+        _p(x), TYPES[x.dtype], rows, K, _row_stride(x), transpose, _p(codes), _p(scales),
+        scale_layout, _p(status), _stream()))
+    return codes, scales
+
+
+def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16):
+    """The values of row-major codes [rows, K / 2] and scales [rows, K / 32]."""
+    _dev(codes, torch.uint8, "codes")
+    _dev(scales, torch.uint8, "scales")
+    rows, half = codes.shape
+    if scales.shape != (rows, half // 16):
+        raise ValueError("scales must be [rows, K / 32]")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("dtype must be bfloat16 or float32")
+    out = torch.empty(rows, 2 * half, dtype=dtype, device=codes.device)
+    if rows and half:
+        _check("megamoe_dequantize_mxfp4", load().megamoe_dequantize_mxfp4(
+            _p(codes), _p(scales), rows, 2 * half, _p(out), TYPES[dtype], 2 * half, _stream()))
+    return out
+
+
+def swizzle_scales_mxfp4(scales: torch.Tensor) -> torch.Tensor:
+    """Row-major MXFP4 scales [rows, K / 32] -> atom layout (weight preparation)."""
+    _dev(scales, torch.uint8, "scales")
+    rows, blocks = scales.shape
+    dst = torch.empty(mx_atom_bytes(rows, blocks * 32), dtype=torch.uint8, device=scales.device)
+    _check("megamoe_swizzle_scales_mxfp4", load().megamoe_swizzle_scales_mxfp4(
+        _p(scales), rows, blocks * 32, _p(dst), _stream()))
+    return dst
+
+
+@dataclass
+class MxLinearWeights:
+    """A dense MXFP4 weight [N, K] for linear_mxfp4: row-major codes, block
+    scales in the atom layout."""
+
+    N: int
+    K: int
+    codes: torch.Tensor
+    scales: torch.Tensor  # atom layout
+
+    @classmethod
+    def prepare(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MxLinearWeights":
+        """From row-major codes [N, K / 2] and scales [N, K / 32]."""
+        _dev(codes, torch.uint8, "codes")
+        N, half = codes.shape
+        if scales.shape != (N, half // 16):
+            raise ValueError("scales must be [N, K / 32]")
+        return cls(N, half * 2, codes, swizzle_scales_mxfp4(scales))
+
+    @classmethod
+    def quantize(cls, w: torch.Tensor) -> "MxLinearWeights":
+        """From a master weight [N, K] (bfloat16, float16 or float32)."""
+        codes, scales = quantize_mxfp4(w, scale_layout=SCALES_MMA)
+        return cls(w.shape[0], w.shape[1], codes, scales)
+
+
+def _epi(dtype):
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError("output dtype must be bfloat16 or float32")
+    return EPI_F32 if dtype == torch.float32 else EPI_BF16
+
+
+def linear_mxfp4_workspace_size(T: int, K: int, N: int) -> int:
+    return int(load().megamoe_linear_mxfp4_workspace_size(T, K, N))
+
+
+def linear_mxfp4(x: torch.Tensor, w: MxLinearWeights, out_dtype=EPI_BF16, out=None, ws=None):
+    """out [T, N] = MXFP4(x) @ w.T, in bf16 (EPI_BF16) or float32 (EPI_F32).
+    Returns (out, ws); ws holds the status word in its first four bytes and may
+    be passed again for calls of the same shape."""
+    _dev_float_rows(x, "x")
+    T, K = x.shape
+    if K != w.K:
+        raise ValueError("x and w disagree on K")
+    if ws is None:
+        ws = torch.empty(linear_mxfp4_workspace_size(T, K, w.N), dtype=torch.uint8,
+                         device=x.device)
+    dt = torch.float32 if out_dtype == EPI_F32 else torch.bfloat16
+    if out is None:
+        out = torch.empty(T, w.N, dtype=dt, device=x.device)
+    elif out.shape != (T, w.N):
+        raise ValueError("out must be [T, N]")
+    _dev_rows(out, dt, "out")
+    _check("megamoe_linear_mxfp4", load().megamoe_linear_mxfp4(
+        _p(x), TYPES[x.dtype], T, K, _row_stride(x), _p(w.codes), _p(w.scales), w.N, out_dtype,
+        _p(out), _row_stride(out), _p(ws), ws.numel(), _stream()))
+    return out, ws
+
+
+def linear_mxfp4_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tensor,
+                          grad_x_dtype=torch.bfloat16, grad_w_dtype=torch.float32, ws=None,
+                          need_x: bool = True, need_w: bool = True):
+    """(grad_x [T, K], grad_w [N, K], ws) of the linear with master weight w
+    [N, K]: grad_out, x and w are each quantised to MXFP4 along the dimension
+    that their product sums over.  need_x / need_w false: that gradient is None."""
+    _dev_float_rows(grad_out, "grad_out")
+    _dev_float_rows(x, "x")
+    _dev_float_rows(w, "w")
+    T, N = grad_out.shape
+    K = x.shape[1]
+    if x.shape[0] != T or w.shape != (N, K):
+        raise ValueError("grad_out [T, N], x [T, K] and w [N, K] disagree")
+    lib = load()
+    if ws is None:
+        ws = torch.empty(lib.megamoe_linear_mxfp4_backward_workspace_size(T, K, N),
+                         dtype=torch.uint8, device=x.device)
+    gx = torch.empty(T, K, dtype=grad_x_dtype, device=x.device) if need_x else None
+    gw = torch.empty(N, K, dtype=grad_w_dtype, device=x.device) if need_w else None
+    _check("megamoe_linear_mxfp4_backward", lib.megamoe_linear_mxfp4_backward(
+        _p(grad_out), TYPES[grad_out.dtype], _row_stride(grad_out), _p(x), TYPES[x.dtype],
+        _row_stride(x), _p(w), TYPES[w.dtype], _row_stride(w), T, K, N, _p(gx), _epi(grad_x_dtype),
+        K, _p(gw), _epi(grad_w_dtype), K, _p(ws), ws.numel(), _stream()))
+    return gx, gw, ws
+
+
+class CMxWeights(ctypes.Structure):
+    _fields_ = [("num_experts", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("intermediate", ctypes.c_int32), ("w13_codes", _P), ("w13_scales", _P),
+                ("w2_codes", _P), ("w2_scales", _P)]
+
+
+@dataclass
+class MxWeights:
+    """Device MXFP4 expert weights, prepared for the library (codes packed
+    tile-major, scales swizzled into the atom layout)."""
+
+    E: int
+    d: int
+    I: int
+    w13_codes: torch.Tensor
+    w13_scales: torch.Tensor  # atom layout
+    w2_codes: torch.Tensor
+    w2_scales: torch.Tensor  # atom layout
+
+    @classmethod
+    def prepare(cls, w: dict) -> "MxWeights":
+        """From row-major stacked weights on the GPU: w13_codes [E, 2I, d/2]
+        (gate rows, then up rows), w13_scales [E, 2I, d/32], w2_codes
+        [E, d, I/2], w2_scales [E, d, I/32]."""
+        E, I2, half_d = w["w13_codes"].shape
+        d, I = half_d * 2, I2 // 2
+        if (w["w13_scales"].shape != (E, I2, d // 32) or w["w2_codes"].shape != (E, d, I // 2)
+                or w["w2_scales"].shape != (E, d, I // 32)):
+            raise ValueError("expert weight shapes disagree")
+        c13 = pack_weight_codes(w["w13_codes"].reshape(E * I2, d // 2), I).view(E, I2, d // 2)
+        c2 = pack_weight_codes(w["w2_codes"].reshape(E * d, I // 2)).view(E, d, I // 2)
+        return cls(E, d, I, c13, swizzle_scales_mxfp4(w["w13_scales"].reshape(E * I2, d // 32)), c2,
+                   swizzle_scales_mxfp4(w["w2_scales"].reshape(E * d, I // 32)))
+
+    def cstruct(self) -> CMxWeights:
+        return CMxWeights(self.E, self.d, self.I, self.w13_codes.data_ptr(),
+                          self.w13_scales.data_ptr(), self.w2_codes.data_ptr(),
+                          self.w2_scales.data_ptr())
+
+
+class MxForward:
+    """megamoe_forward_mxfp4 with a reusable workspace for one (T, k, pad) shape."""
+
+    def __init__(self, weights: MxWeights, T: int, k: int, pad: int = 32, device=None):
+        self.w = weights
+        self.cw = weights.cstruct()
+        self.T, self.k, self.pad = T, k, pad
+        dev = device or weights.w13_codes.device
+        self.ws_bytes = int(load().megamoe_workspace_size_mxfp4(T, k, weights.E, weights.d,
+                                                                weights.I, pad))
+        self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
+        self.ws_off = (-self.ws.data_ptr()) % 256
+        self.ws_ptr = ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
+        self.out = torch.empty(max(T, 1), weights.d, dtype=torch.bfloat16, device=dev)
+
+    def _check_x(self, x, out):
+        _dev(x, torch.bfloat16, "x")
+        if x.shape != (self.T, self.w.d):
+            raise ValueError("x must be [T, d] of the shape this object was built for")
+        out = self.out if out is None else out
+        _dev(out, torch.bfloat16, "out")
+        if out.dim() != 2 or out.shape[0] < self.T or out.shape[1] != self.w.d:
+            raise ValueError("out must be [T, d]")
+        return out
+
+    def __call__(self, x, topk_ids, topk_weights, out=None):
+        out = self._check_x(x, out)
+        _dev(topk_ids, torch.int32, "topk_ids")
+        _dev(topk_weights, torch.float32, "topk_weights")
+        if topk_ids.shape != (self.T, self.k) or topk_weights.shape != (self.T, self.k):
+            raise ValueError("topk_ids and topk_weights must be [T, k]")
+        _check("megamoe_forward_mxfp4", load().megamoe_forward_mxfp4(
+            ctypes.byref(self.cw), _p(x), _p(topk_ids), _p(topk_weights), self.T, self.k, self.pad,
+            _p(out), self.ws_ptr, self.ws_bytes, _stream()))
+        return out[:self.T]
+
+    def from_logits(self, x, logits, score: str = "sigmoid", bias=None, n_group: int = 1,
+                    topk_group: int = 1, group_top: int = 2, renormalize: bool = True,
+                    scale: float = 1.0, out=None):
+        """The whole layer: router_scored_topk over logits [T, E], then the experts."""
+        out = self._check_x(x, out)
+        _dev_logits(logits, "logits")
+        if logits.shape != (self.T, self.w.E):
+            raise ValueError("logits must be [T, E]")
+        if bias is not None:
+            _dev(bias, torch.float32, "bias")
+            if bias.numel() != self.w.E:
+                raise ValueError("bias must have one value per expert")
+        _check("megamoe_forward_mxfp4_from_logits", load().megamoe_forward_mxfp4_from_logits(
+            ctypes.byref(self.cw), _p(x), _p(logits), TYPES[logits.dtype], _row_stride(logits),
+            _p(bias), _score(score), n_group, topk_group, group_top, renormalize, scale, self.T,
+            self.k, self.pad, _p(out), self.ws_ptr, self.ws_bytes, _stream()))
+        return out[:self.T]
+
+    def read_status(self) -> int:
+        bits = ctypes.c_uint32(0)
+        code = load().megamoe_read_status(self.ws_ptr, ctypes.byref(bits), _stream())
+        if code not in (OK, 5):
+            raise MegaMoEError("megamoe_read_status", code)
+        return int(bits.value)
