@@ -144,6 +144,11 @@ cudaError_t launch_router(const float* logits, int64_t T, int E, int64_t ld, con
 bool make_codes_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t row_bytes,
                     uint32_t box_rows);
 
+// 2-D tensor map of any type: [rows, cols] with a row stride of `stride` bytes.
+bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint64_t cols,
+              uint64_t rows, uint64_t stride, uint32_t box_cols, uint32_t box_rows,
+              CUtensorMapSwizzle swizzle);
+
 // Scored router (grouped top-k over sigmoid or softmax scores) and its gradient.
 struct ScoredRouter {
   const void* logits;  // [T, ld], fp32 or bf16

@@ -392,6 +392,277 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------------------
+// Large products: a pair of CTAs on one tile of 256 x 256.
+//
+// A stage of one CTA (a K step of 256) is 128 rows of each operand: 32 KB for
+// 128 x 256 of output, where a CTA on its own loads 48 KB for the same.  All
+// eight copies of a stage complete on one barrier of rank 0, whose one thread
+// then copies the scales into tensor memory (tcgen05.cp, in order with the MMAs
+// and hidden behind them: measured 128.4 cycles an MMA with and 128.3 without)
+// and issues the MMAs of both CTAs.  Commits free the stage, and hand over the
+// accumulator, in both.  The accumulator leaves tensor memory for registers
+// before anything is stored, so the next tile's MMAs run under the stores,
+// which go through shared memory as 128-byte rows by tensor map.
+// ---------------------------------------------------------------------------
+struct PairMaps {
+  CUtensorMap m, n, sfm, sfn, out;
+};
+
+struct PairCfg {
+  static constexpr int THREADS = 320;  // producer, MMA issuer, 8 epilogue warps
+  static constexpr int STAGES = 5;
+  static constexpr int TILE = 128 * 128;  // a CTA's rows of either operand
+  static constexpr int SF = 1024;
+  static constexpr int OFF_N = TILE;
+  static constexpr int OFF_SFM = 2 * TILE;
+  static constexpr int OFF_SFN = OFF_SFM + SF;  // all 256 rows of the N side
+  static constexpr int STAGE = OFF_SFN + 2 * SF;
+  static constexpr uint32_t TX = 2 * STAGE;  // both CTAs
+  static constexpr int SF_COLS = 8 + 16;
+  static constexpr int SF_COL0 = 256;  // two sets, taken in turn
+  static constexpr int STG = 32 * 128;  // 32 rows x 128 bytes per epilogue warp
+  static constexpr int STG_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = STG_OFF + kEpiWarps * STG;
+  static constexpr int SMEM = 1024 + BAR_OFF + 256;
+  static_assert(SMEM <= 232448, "shared memory budget");
+  static_assert(STAGE % 1024 == 0, "128-byte swizzle atoms");
+};
+
+template <typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
+    k_mx_gemm_pair(const __grid_constant__ PairMaps maps, const MxGemmArgs p) {
+  using C = PairCfg;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // rank 0's
+  uint64_t* empty = full + STAGES;
+  uint64_t* acc_full = empty + STAGES;
+  uint64_t* acc_empty = acc_full + 1;  // rank 0's: the epilogue warps of both
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int MT = (p.M + 255) / 256, NT = (p.N + 255) / 256;
+  const int KT = (p.K + 255) / 256;
+  const int total = MT * NT;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.m);
+    prefetch_tensormap(&maps.n);
+    prefetch_tensormap(&maps.sfm);
+    prefetch_tensormap(&maps.sfn);
+    prefetch_tensormap(&maps.out);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there before either is arrived on
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0, issued = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int q = first; ok && q < total; q += step) {
+        const int nt = q / MT, mt = q - nt * MT;
+        const int m0 = mt * 256 + rank * 128, n0 = nt * 256;
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sb = smem + stage * C::STAGE;
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::TX);
+          const uint32_t bar = cluster_address(&full[stage], 0);
+          tma_load_2d_pair(sb, &maps.m, bar, kt * 128, m0, pol);
+          tma_load_2d_pair(sb + C::OFF_N, &maps.n, bar, kt * 128, n0 + rank * 128, pol);
+          tma_load_2d_pair(sb + C::OFF_SFM, &maps.sfm, bar, kt * 256, m0 >> 7, pol);
+          tma_load_2d_pair(sb + C::OFF_SFN, &maps.sfn, bar, kt * 256, n0 >> 7, pol);
+          ++issued;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok) {  // unwinding: let the copies in flight land first
+        if (rank == 0) {
+          for (int s = 0; s < STAGES && s < issued; ++s) {
+            const int i = issued - 1 - s;
+            mbar_drain(&full[i % STAGES], static_cast<uint32_t>(i / STAGES) & 1u);
+          }
+        } else {
+          // rank 1's complete on rank 0's barriers, which may have moved on:
+          // wait a time that no copy takes
+          const uint64_t t0 = globaltimer();
+          while (globaltimer() - t0 < 5000000) __nanosleep(1000);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint64_t codes = sdesc_sw128(smem_u32(smem));
+      const uint64_t scales = sdesc_atom(smem_u32(smem) + C::OFF_SFM);
+      int stage = 0, sets = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int q = first; ok && q < total; q += step) {
+        if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+        tc_fence_after();
+        for (int kt = 0; kt < KT; ++kt) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t cd = sdesc_at(codes, stage * C::STAGE);
+          const uint64_t sd = sdesc_at(scales, stage * C::STAGE);
+          const uint32_t sf = tmem + C::SF_COL0 + (sets & 1) * C::SF_COLS;
+          ++sets;
+          if (leader) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // 128 of K each
+              tc_copy_atom_pair(sf + 4 * h, sdesc_at(sd, 512 * h));
+              tc_copy_atom_pair(sf + 8 + 8 * h, sdesc_at(sd, C::SF + 512 * h));
+              tc_copy_atom_pair(sf + 12 + 8 * h, sdesc_at(sd, 2 * C::SF + 512 * h));
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              mma_mxf4_pair(tmem, sdesc_at(cd, 32 * c), sdesc_at(cd, C::OFF_N + 32 * c),
+                            idesc_mxf4(256, 256, c & 1), sf + 4 * (c >> 1), sf + 8 + 8 * (c >> 1),
+                            (kt != 0 || c != 0) ? 1u : 0u);
+            tc_commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair(acc_full);
+        __syncwarp();
+        acc_phase ^= 1u;
+      }
+      // every MMA issued so far must finish before tensor memory is released
+      if (leader) tc_commit_pair(drain);
+      mbar_drain(drain, 0);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int quarter = warp & 3;
+    const int half = warp >= 6 ? 1 : 0;
+    uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
+    constexpr bool F32 = sizeof(O) == 4;
+    constexpr int COLS = F32 ? 32 : 64;  // columns of a staged chunk
+    uint32_t acc_phase = 0;
+    for (int q = first; q < total; q += step) {
+      const int nt = q / MT, mt = q - nt * MT;
+      if (!mbar_wait(acc_full, acc_phase, abort_flag, p.status, p.wait_limit_ns)) break;
+      tc_fence_after();
+      const uint32_t base = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+      const int m = mt * 256 + rank * 128 + quarter * 32, c0 = nt * 256 + half * 128;
+      uint32_t v[F32 ? 128 : 64];  // this lane's row: 128 values
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (F32) {
+          tmem_ld_32x32b_x32(base + 32 * c, v + 32 * (F32 ? c : 0));
+        } else {
+          uint32_t u[32];
+          tmem_ld_32x32b_x32(base + 32 * c, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * j]),
+                                                           __uint_as_float(u[2 * j + 1]));
+            v[16 * c + j] = *reinterpret_cast<const uint32_t*>(&h);
+          }
+        }
+      }
+      if (F32) tmem_ld_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(acc_empty, 0);
+      acc_phase ^= 1u;
+      if (m >= p.M) continue;  // warp-uniform
+#pragma unroll
+      for (int c = 0; c < 128 / COLS; ++c) {
+        if (lane == 0) bulk_store_wait_read();  // the chunk before has left
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) * 16)) =
+              make_uint4(v[32 * c + 4 * j], v[32 * c + 4 * j + 1], v[32 * c + 4 * j + 2],
+                         v[32 * c + 4 * j + 3]);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && c0 + c * COLS < p.N) tma_store_2d(&maps.out, stg, c0 + c * COLS, m);
+      }
+    }
+    if (lane == 0) bulk_store_wait();
+    __syncwarp();
+  }
+  __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other still reaches into it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename O>
+cudaError_t launch_pair(const MxGemmArgs& a, const uint8_t* m_codes, const uint8_t* n_codes,
+                        int tiles, cudaStream_t stream) {
+  PairMaps maps;
+  const uint64_t row = static_cast<uint64_t>(a.K) / 2;
+  const uint64_t sf_row = static_cast<uint64_t>(mx_atoms(a.K)) * 512;
+  const uint64_t m = a.M, n = a.N;
+  if (!make_codes_map(&maps.m, m_codes, m, row, 128) ||
+      !make_codes_map(&maps.n, n_codes, n, row, 128) ||
+      !make_map(&maps.sfm, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.m_sf, sf_row / 4, (m + 127) / 128,
+                sf_row, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&maps.sfn, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.n_sf, sf_row / 4, (n + 127) / 128,
+                sf_row, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !make_map(&maps.out,
+                sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                a.out, n, m, static_cast<uint64_t>(a.ld_out) * sizeof(O), 128 / sizeof(O), 32,
+                CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto kern = k_mx_gemm_pair<O>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(2 * std::min(num_sms() / 2, tiles)), dim3(PairCfg::THREADS),
+                    PairCfg::SMEM, stream, maps, a);
+}
+
 template <int BN, int STAGES, typename O>
 cudaError_t launch_cfg(const MxGemmArgs& a, const uint8_t* m_codes, const uint8_t* n_codes,
                        int pieces, cudaStream_t stream) {
@@ -412,7 +683,7 @@ cudaError_t launch_cfg(const MxGemmArgs& a, const uint8_t* m_codes, const uint8_
 // the pieces of K.
 struct MxPlan {
   bool swap;  // rows of the output on the N side
-  int bn, ksplit, tiles;
+  int bn, ksplit, tiles;  // bn 0: pairs of CTAs on tiles of 256 x 256
 };
 
 MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
@@ -422,6 +693,12 @@ MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
   // few output rows go on N: an M tile of 128 would be mostly empty
   p.swap = R <= 64;
   const int64_t M = p.swap ? C : R, N = p.swap ? R : C;
+  const int64_t pairs = (M + 255) / 256 * ((N + 255) / 256);
+  if (!p.swap && pairs * 2 >= sms) {
+    p.tiles = static_cast<int>(pairs);
+    p.ksplit = 1;
+    return p;
+  }
   const int64_t mt = (M + 127) / 128;
   p.bn = p.swap ? (N <= 32 ? 32 : 64) : mt * ((N + 255) / 256) >= sms ? 256 : 128;
   p.tiles = static_cast<int>(mt * ((N + p.bn - 1) / p.bn));
@@ -466,6 +743,7 @@ cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
   auto run = [&](auto out) {
     using O = decltype(out);
     switch (p.bn) {
+      case 0: return launch_pair<O>(a, m_codes, n_codes, p.tiles, stream);
       case 32: return launch_cfg<32, 8, O>(a, m_codes, n_codes, pieces, stream);
       case 64: return launch_cfg<64, 8, O>(a, m_codes, n_codes, pieces, stream);
       case 128: return launch_cfg<128, 6, O>(a, m_codes, n_codes, pieces, stream);

@@ -125,16 +125,18 @@ def _check(fn, code):
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the handle of torch.cuda.current_stream(), without the 3 us that building
+    # the Stream object around it takes (a short kernel's own time)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _on_current_device(t, name):
     # the library launches on the current device and its stream
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current CUDA device is "
                          f"cuda:{torch.cuda.current_device()}")
 
@@ -445,7 +447,7 @@ class Forward:
 
     @property
     def ws_ptr(self):
-        return ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
+        return self.ws.data_ptr() + self.ws_off
 
     def status_tensor(self):
         return self.ws[self.ws_off:self.ws_off + 4].view(torch.int32)
@@ -521,7 +523,7 @@ class ShardForward:
 
     @property
     def ws_ptr(self):
-        return ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
+        return self.ws.data_ptr() + self.ws_off
 
     def amax_h(self) -> torch.Tensor:
         """The shard's amax(h) after begin(): a device float [1] view into the
@@ -890,7 +892,7 @@ class MxForward:
                                                                 weights.I, pad))
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
         self.ws_off = (-self.ws.data_ptr()) % 256
-        self.ws_ptr = ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
+        self.ws_ptr = self.ws.data_ptr() + self.ws_off
         self.out = torch.empty(max(T, 1), weights.d, dtype=torch.bfloat16, device=dev)
 
     def _check_x(self, x, out):
