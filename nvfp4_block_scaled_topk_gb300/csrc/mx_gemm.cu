@@ -609,7 +609,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
       if (F32) tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(acc_empty, 0);
+      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
       acc_phase ^= 1u;
       if (m >= p.M) continue;  // warp-uniform
 #pragma unroll
