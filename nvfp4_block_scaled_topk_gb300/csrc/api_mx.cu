@@ -107,8 +107,12 @@ BackwardWs carve_backward(void* base, int64_t T, int K, int N) {
   return w;
 }
 
+// Rows and columns of the products are int; the quantisers' tiles (of 128 x 64
+// at least) are counted in 31 bits over all three matrices.
 bool linear_sizes_ok(int64_t T, int K, int N) {
-  return K % 32 == 0 && N % 32 == 0 && T < (int64_t{1} << 30);
+  if (K % 32 != 0 || N % 32 != 0 || T >= (int64_t{1} << 30)) return false;
+  const int64_t tall = (T + 127) / 128, k = K / 64 + 4, n = N / 64 + 4;
+  return tall * (k + n) + (N / 128 + 1) * k < (int64_t{1} << 30);
 }
 
 MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool transpose,
@@ -299,7 +303,9 @@ megamoe_status megamoe_quantize_mxfp4(const void* x, int x_type, int64_t rows, i
   if (scale_layout != MEGAMOE_SCALES_ROWMAJOR && scale_layout != MEGAMOE_SCALES_MMA)
     return MEGAMOE_ERR_INVALID_ARG;
   if (K % 32 != 0 || rows >= (int64_t{1} << 31)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
-  if (transpose && K > 65535 * 64) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;  // grid rows
+  // the tiles of a transposed launch are counted in 31 bits
+  if (transpose && (rows + 127) / 128 * ((K + 63) / 64) >= (int64_t{1} << 30))
+    return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   if (rows > 0 && (!x || !codes || !scales)) return MEGAMOE_ERR_INVALID_ARG;
   if (rows > 0 && (!vectors_ok(x, ld, size) || !aligned(codes, 16)))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
@@ -394,27 +400,43 @@ megamoe_status megamoe_linear_mxfp4_backward(
       e = cudaMemset2DAsync(grad_w, ld_grad_w * gw_size, 0, K * gw_size, N, s);
     return cuda_status(e);
   }
-  if (grad_x) {
-    e = launch_mx_quantize(quant_of(grad_out, grad_type, T, N, ld_grad, false, wk.dy, wk.status), s);
-    if (e == cudaSuccess)
-      e = launch_mx_quantize(quant_of(w, w_type, N, K, ld_w, true, wk.w_t, wk.status), s);
-    if (e == cudaSuccess)
-      e = launch_mx_product(MxProduct{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K,
-                                      N, grad_x, grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x,
-                                      wk.partial, wk.counters_x, wk.status},
-                            s);
-  }
-  if (grad_w && e == cudaSuccess) {
-    const int64_t R = (T + 31) / 32 * 32;
-    e = launch_mx_quantize(quant_of(grad_out, grad_type, T, N, ld_grad, true, wk.dy_t, wk.status), s);
-    if (e == cudaSuccess)
-      e = launch_mx_quantize(quant_of(x, x_type, T, K, ld_x, true, wk.x_t, wk.status), s);
-    if (e == cudaSuccess)
-      e = launch_mx_product(MxProduct{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N,
-                                      K, R, grad_w, grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w,
-                                      wk.partial, wk.counters_w, wk.status},
-                            s);
-  }
+  // one launch reads grad_out once for both products, x and w once each
+  MxTiles jobs{};
+  auto add = [&](const void* p, int type, int64_t rows, int cols, int64_t ld, const MxOperand* row,
+                 const MxOperand* col) {
+    MxTile& t = jobs.job[jobs.count++];
+    t.x = p;
+    t.type = type;
+    t.rows = rows;
+    t.K = cols;
+    t.ld = ld;
+    if (row) {
+      t.row_codes = row->codes;
+      t.row_scales = row->scales;
+    }
+    if (col) {
+      t.col_codes = col->codes;
+      t.col_scales = col->scales;
+    }
+    t.col_layout = MEGAMOE_SCALES_MMA;
+    t.status = wk.status;
+  };
+  if (grad_x || grad_w)
+    add(grad_out, grad_type, T, N, ld_grad, grad_x ? &wk.dy : nullptr, grad_w ? &wk.dy_t : nullptr);
+  if (grad_w) add(x, x_type, T, K, ld_x, nullptr, &wk.x_t);
+  if (grad_x) add(w, w_type, N, K, ld_w, nullptr, &wk.w_t);
+  e = launch_mx_tiles(jobs, s);
+  if (grad_x && e == cudaSuccess)
+    e = launch_mx_product(MxProduct{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N,
+                                    grad_x, grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.partial,
+                                    wk.counters_x, wk.status},
+                          s);
+  const int64_t R = (T + 31) / 32 * 32;
+  if (grad_w && e == cudaSuccess)
+    e = launch_mx_product(MxProduct{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K,
+                                    R, grad_w, grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w,
+                                    wk.partial, wk.counters_w, wk.status},
+                          s);
   return cuda_status(e);
 }
 

@@ -180,6 +180,27 @@ struct MxQuant {
   uint32_t* status;
 };
 cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s);
+// Matrices quantised tile by tile in one launch, each along its columns (codes
+// of x^T), along its rows (atom layout of the scales), or both from one read.
+struct MxTile {
+  const void* x;
+  int type;
+  int64_t rows, ld;
+  int K;
+  uint8_t* row_codes;  // null: not along the rows
+  uint8_t* row_scales;
+  uint8_t* col_codes;  // null: not along the columns
+  uint8_t* col_scales;
+  int col_layout;
+  uint32_t* status;
+  int first, col_tiles;  // set by the launch
+};
+struct MxTiles {
+  MxTile job[3];
+  int count;
+  int tiles;  // set by the launch
+};
+cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s);
 // x [T, d] bf16 into routed rows slot_dst[t k + j] (routed scale layout).
 cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t* slot_dst, int k,
                              uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s);

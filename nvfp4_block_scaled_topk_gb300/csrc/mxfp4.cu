@@ -14,17 +14,19 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
+// t / n, by 32-bit division whenever t fits.
+__device__ __forceinline__ int64_t task_div(int64_t t, int n) {
+  return (t >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(t) / static_cast<uint32_t>(n))
+                        : t / n;
 }
 
-// Largest of the four lanes that share a 32-element block.
-__device__ __forceinline__ uint32_t block_max(uint32_t m) {
-  m = max(m, __shfl_xor_sync(kAll, m, 1));
-  return max(m, __shfl_xor_sync(kAll, m, 2));
+// Scale byte of the 32-element block that four neighbouring lanes share.
+template <typename X>
+__device__ __forceinline__ uint32_t block_byte(const Eight<X>& x) {
+  uint32_t m = x.widest();
+  m = Eight<X>::wider(m, __shfl_xor_sync(kAll, m, 1));
+  m = Eight<X>::wider(m, __shfl_xor_sync(kAll, m, 2));
+  return mx_scale_byte(Eight<X>::bits(m));
 }
 
 __device__ __forceinline__ int64_t scale_offset(int layout, int64_t row, int64_t b, int64_t K) {
@@ -32,10 +34,14 @@ __device__ __forceinline__ int64_t scale_offset(int layout, int64_t row, int64_t
 }
 
 // Along rows.  Four lanes take a 32-element block, eight elements each, so a
-// warp reads 256 consecutive elements with 16-byte loads and writes 128
-// consecutive bytes of codes; the block's largest value is two shuffles.  One
-// warp task is 256 elements of a row (a whole K step: its scale bytes past
-// the row's end are written as zeros in the atom layout).
+// warp reads 256 consecutive elements (a K step) with 16-byte loads and writes
+// 128 consecutive bytes of codes; the block's largest value is two shuffles.
+// A warp task is four neighbouring steps of a row: their loads are in flight
+// together, they share the address arithmetic, and each lane stores one of the
+// 32 scale bytes (past the row's end zeros, in the atom layout).  Work per
+// element is what bounds this kernel before memory does.
+constexpr int kRowSteps = 4;
+
 template <typename X>
 __global__ void __launch_bounds__(256)
     k_mx_rows(const X* __restrict__ x, int64_t rows, int K, int64_t ld, uint8_t* __restrict__ codes,
@@ -43,131 +49,244 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int steps = (K + 255) / 256;
-  const int64_t tasks = rows * steps;
+  const int groups = (K + 256 * kRowSteps - 1) / (256 * kRowSteps);
+  const int end = layout == MEGAMOE_SCALES_MMA ? static_cast<int>(mx_atoms(K)) * 4 : K / 32;
+  const int64_t tasks = rows * groups;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  bool bad = false;
   for (int64_t w = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
        w < tasks; w += warps) {
-    const int64_t r = w / steps;
-    const int col = static_cast<int>(w - r * steps) * 256 + 8 * lane;
-    const bool in = col < K;
-    float v[8] = {};
-    if (in) mx_load8(x + r * ld + col, v);
-    const uint32_t byte = mx_scale_byte(block_max(amax_bits8(v)));
-    if (in) {
-      *reinterpret_cast<uint32_t*>(codes + r * (K / 2) + col / 2) = mx_codes8(v, mx_inverse(byte));
-      if (byte == kMxNan) set_status(status, MEGAMOE_DEV_NONFINITE);
+    const int64_t r = task_div(w, groups);
+    const int col = static_cast<int>(w - r * groups) * (256 * kRowSteps) + 8 * lane;
+    const X* from = x + r * ld + col;
+    Eight<X> e[kRowSteps];
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      if (col + 256 * i < K) e[i].load(from + 256 * i);
+      else e[i].clear();
     }
-    if ((lane & 3) == 0 && (in || layout == MEGAMOE_SCALES_MMA))
-      scales[scale_offset(layout, r, col >> 5, K)] = static_cast<uint8_t>(in ? byte : 0u);
+    uint8_t* to = codes + (r * K + col) / 2;
+    uint32_t mine = 0;  // the scale byte that this lane stores: of step lane % 4
+#pragma unroll
+    for (int i = 0; i < kRowSteps; ++i) {
+      const uint32_t byte = block_byte(e[i]);
+      if ((lane & 3) == i) mine = byte;
+      float v[8];
+      e[i].values(v);
+      if (col + 256 * i < K)
+        *reinterpret_cast<uint32_t*>(to + 128 * i) = mx_codes8(v, mx_inverse(byte));
+    }
+    // (a step past the end is all zeros: byte 0)
+    const int b = (col >> 5) + 8 * (lane & 3);
+    if (b < end) scales[scale_offset(layout, r, b, K)] = static_cast<uint8_t>(mine);
+    bad |= mine == kMxNan;
   }
+  if (bad) set_status(status, MEGAMOE_DEV_NONFINITE);
 }
 
 // Along columns: codes [K, R / 2] and scales of x^T, R = rows up to a multiple
-// of 32 (elements past the last row count as zeros).  A block takes 256 rows
-// x 64 columns through shared memory: rows come in with 16-byte loads, a
-// thread then takes one pair of neighbouring columns down 32 rows (a 2-byte
-// type: one 32-bit word per row, the warp's words consecutive), and the codes
-// go out through shared memory as 128-byte runs along the columns' rows.
-constexpr int kColRows = 256, kColCols = 64;
+// of 32 (elements past the last row count as zeros); on request the rows' own
+// codes and scales from the same read of x.  A block walks over tiles of 256
+// rows (fp32: 128) x 64 columns, the next one on its way into shared memory
+// (16-byte asynchronous copies) while it encodes the present one.  Down the
+// columns a thread takes 32 rows of two neighbouring columns into registers (a
+// 2-byte type: one 32-bit word per row, the warp's words consecutive; fp32: one
+// column), and their codes go out through shared memory as 128-byte runs.
+constexpr int kTileCols = 64;
+constexpr int kTileBytes = 32768;  // of x in a tile, for every type
+template <typename X>
+constexpr int kTileRows = kTileBytes / kTileCols / static_cast<int>(sizeof(X));
+constexpr int kTileCodes = kTileCols * 128;  // bytes of column codes of a tile
+
+// One row's word of a thread's columns: NC of them.
+template <typename X>
+struct Word {
+  static constexpr int NC = 2;
+  uint32_t u;
+  __device__ __forceinline__ void load(const X* p) { u = *reinterpret_cast<const uint32_t*>(p); }
+  // bit patterns of non-negative values order as the values do
+  __device__ __forceinline__ void widen(Word v) { u = __vmaxu2(u, v.u & 0x7fff7fffu); }
+  __device__ __forceinline__ float value(int c) const;
+};
+template <>
+__device__ __forceinline__ float Word<__nv_bfloat16>::value(int c) const {
+  return __uint_as_float(c ? u & 0xffff0000u : u << 16);
+}
+template <>
+__device__ __forceinline__ float Word<__half>::value(int c) const {
+  return __half2float(__ushort_as_half(static_cast<uint16_t>(c ? u >> 16 : u)));
+}
+template <>
+struct Word<float> {
+  static constexpr int NC = 1;
+  uint32_t u;
+  __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const uint32_t*>(p); }
+  __device__ __forceinline__ void widen(Word v) { u = max(u, v.u & 0x7fffffffu); }
+  __device__ __forceinline__ float value(int) const { return __uint_as_float(u); }
+};
+
+// Starts the copies of a tile (zeros outside the matrix).
+template <typename X>
+__device__ __forceinline__ void load_tile(const MxTile& job, int row_tile, int col_tile,
+                                          uint8_t* buf) {
+  constexpr int per = 16 / sizeof(X), vecs = kTileCols / per;
+  const X* x = static_cast<const X*>(job.x);
+  const int64_t r0 = static_cast<int64_t>(row_tile) * kTileRows<X>;
+  const int c0 = col_tile * kTileCols;
+#pragma unroll
+  for (int i = 0; i < kTileBytes / 16 / 256; ++i) {
+    const int t = threadIdx.x + 256 * i;
+    const int r = t / vecs, c = t % vecs * per;
+    const bool in = r0 + r < job.rows && c0 + c < job.K;
+    const X* from = in ? x + (r0 + r) * job.ld + c0 + c : x;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(buf + 16 * t)),
+                 "l"(from), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
 
 template <typename X>
-struct ColPair;
-template <>
-struct ColPair<__nv_bfloat16> {
-  static __device__ __forceinline__ float2 get(const __nv_bfloat16* p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+__device__ __forceinline__ void encode_tile(const MxTile& job, int row_tile, int col_tile,
+                                            const uint8_t* buf, uint8_t* s_codes) {
+  using W = Word<X>;
+  const X* tile = reinterpret_cast<const X*>(buf);  // [kTileRows][kTileCols]
+  constexpr int R = kTileRows<X>, blocks = R / 32;
+  constexpr int per = 16 / sizeof(X), vecs = kTileCols / per;
+  const int K = job.K;
+  const int64_t rows = job.rows, padded = (rows + 31) / 32 * 32;
+  const int64_t r0 = static_cast<int64_t>(row_tile) * R;
+  const int c0 = col_tile * kTileCols;
+  bool bad = false;
+  if (job.row_codes) {
+    const int64_t atoms = mx_atoms(K);
+#pragma unroll 2
+    for (int i = 0; i < kTileBytes / 16 / 256; ++i) {
+      const int t = threadIdx.x + 256 * i;
+      const int r = t / vecs, col = c0 + t % vecs * per;
+      const X* e = tile + t * per;
+      float v[per];
+      uint32_t m = 0;
+      const uint4 q = *reinterpret_cast<const uint4*>(e);
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        W word;
+        word.u = w[j];
+#pragma unroll
+        for (int c = 0; c < W::NC; ++c) {
+          v[W::NC * j + c] = word.value(c);
+          m = max(m, __float_as_uint(v[W::NC * j + c]) & 0x7fffffffu);
+        }
+      }
+      // the lanes of a row's block of 32 are neighbours
+#pragma unroll
+      for (int o = 1; o < 32 / per; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
+      const uint32_t byte = mx_scale_byte(m);
+      float e8[8] = {};
+#pragma unroll
+      for (int j = 0; j < per; ++j) e8[j] = v[j];
+      const uint32_t code = mx_codes8(e8, mx_inverse(byte));
+      if (r0 + r < rows) {
+        if (col < K) {
+          uint8_t* to = job.row_codes + ((r0 + r) * K + col) / 2;
+          if (per == 8) *reinterpret_cast<uint32_t*>(to) = code;
+          else *reinterpret_cast<uint16_t*>(to) = static_cast<uint16_t>(code);
+          bad |= byte == kMxNan;
+        }
+        // past the row's end, up to whole K steps: zeros (a zero block's byte)
+        if ((col & 31) == 0 && col < atoms * 128)
+          job.row_scales[mx_atom_offset(r0 + r, col >> 5, atoms)] = static_cast<uint8_t>(byte);
+      }
+    }
   }
-};
-template <>
-struct ColPair<__half> {
-  static __device__ __forceinline__ float2 get(const __half* p) {
-    return __half22float2(*reinterpret_cast<const __half2*>(p));
+  if (job.col_codes && c0 < K) {  // block-uniform
+    // chunk q (16 bytes) of column c at q ^ (c / NC % 8): the chunks written
+    // together (one block of 32 columns) and read together (the blocks of a
+    // column) fall in different banks
+    constexpr int lanes = kTileCols / W::NC;  // threads across the columns
+    const int across = threadIdx.x % lanes, blk = threadIdx.x / lanes;
+    const X* from = tile + blk * 32 * kTileCols + W::NC * across;
+    W v[32], m;
+    m.u = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      v[i].load(from + i * kTileCols);
+      m.widen(v[i]);
+    }
+    const int64_t block = r0 / 32 + blk;
+#pragma unroll
+    for (int c = 0; c < W::NC; ++c) {
+      const uint32_t byte = mx_scale_byte(__float_as_uint(m.value(c)));
+      const float inv = mx_inverse(byte);
+      uint32_t q[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        float e8[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e8[i] = v[8 * g + i].value(c);
+        q[g] = mx_codes8(e8, inv);
+      }
+      const int col = W::NC * across + c;
+      *reinterpret_cast<uint4*>(s_codes + col * (16 * blocks) +
+                                ((blk ^ (across % blocks)) * 16)) = make_uint4(q[0], q[1], q[2], q[3]);
+      if (c0 + col < K && (block * 32 < rows || (job.col_layout == MEGAMOE_SCALES_MMA &&
+                                                 block < mx_atoms(padded) * 4))) {
+        job.col_scales[scale_offset(job.col_layout, c0 + col, block, padded)] =
+            static_cast<uint8_t>(byte);
+        bad |= byte == kMxNan;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kTileCols * blocks / 256; ++i) {
+      const int t = threadIdx.x + 256 * i;
+      const int col = t / blocks, part = t % blocks;
+      if (c0 + col < K && r0 + part * 32 < rows)
+        *reinterpret_cast<uint4*>(job.col_codes + (c0 + col) * (padded / 2) + r0 / 2 + part * 16) =
+            *reinterpret_cast<const uint4*>(s_codes + col * (16 * blocks) +
+                                            ((part ^ (col / W::NC % blocks)) * 16));
+    }
   }
-};
-template <>
-struct ColPair<float> {
-  static __device__ __forceinline__ float2 get(const float* p) {
-    return *reinterpret_cast<const float2*>(p);
-  }
-};
+  if (bad) set_status(job.status, MEGAMOE_DEV_NONFINITE);
+}
 
-template <typename X>
-__global__ void __launch_bounds__(256)
-    k_mx_columns(const X* __restrict__ x, int64_t rows, int K, int64_t ld,
-                 uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int layout,
-                 uint32_t* status) {
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  X* tile = reinterpret_cast<X*>(s_raw);  // [kColRows][kColCols]
-  // [kColCols][kColRows / 2], 16-byte chunk q of column c at q ^ (c / 2 % 8),
-  // so that both the chunks written (one block of 32 columns) and the chunks
-  // read (eight blocks of a column) fall in different banks
-  uint8_t* s_codes = s_raw + kColRows * kColCols * sizeof(X);
-  constexpr int pitch = kColRows / 2;
+// Up to three matrices in one launch; tile t belongs to the last job whose
+// first tile is not past t.  WIDE: one of them may be fp32.
+template <bool WIDE>
+__global__ void __launch_bounds__(256, 3) k_mx_tiles(const __grid_constant__ MxTiles jobs) {
+  extern __shared__ __align__(16) uint8_t s_raw[];  // two tiles, then a tile's column codes
   pdl_wait();
   pdl_trigger();
-  const int64_t r0 = static_cast<int64_t>(blockIdx.x) * kColRows;
-  const int c0 = blockIdx.y * kColCols;
-  const int64_t padded = (rows + 31) / 32 * 32;
-  constexpr int per = 16 / sizeof(X);           // elements of a 16-byte load
-  constexpr int vecs = kColCols / per;          // loads of a tile row
-  constexpr int rounds = kColRows * vecs / 256;
-#pragma unroll
-  for (int i = 0; i < rounds; ++i) {
-    const int t = threadIdx.x + 256 * i;
-    const int r = t / vecs, c = (t % vecs) * per;
-    uint4 q = make_uint4(0u, 0u, 0u, 0u);
-    if (r0 + r < rows && c0 + c < K)
-      q = __ldg(reinterpret_cast<const uint4*>(x + (r0 + r) * ld + c0 + c));
-    *reinterpret_cast<uint4*>(tile + r * kColCols + c) = q;
-  }
-  __syncthreads();
-  const int pair = threadIdx.x & 31, blk = threadIdx.x >> 5;
-  const X* from = tile + blk * 32 * kColCols + 2 * pair;
-  uint32_t m0 = 0, m1 = 0;
-#pragma unroll 8
-  for (int i = 0; i < 32; ++i) {
-    const float2 v = ColPair<X>::get(from + i * kColCols);
-    m0 = max(m0, __float_as_uint(v.x) & 0x7fffffffu);
-    m1 = max(m1, __float_as_uint(v.y) & 0x7fffffffu);
-  }
-  const uint32_t b0 = mx_scale_byte(m0), b1 = mx_scale_byte(m1);
-  const float i0 = mx_inverse(b0), i1 = mx_inverse(b1);
-  uint32_t q0[4], q1[4];
-#pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float a[8], b[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 v = ColPair<X>::get(from + (8 * g + i) * kColCols);
-      a[i] = v.x;
-      b[i] = v.y;
-    }
-    q0[g] = mx_codes8(a, i0);
-    q1[g] = mx_codes8(b, i1);
-  }
-  uint8_t* to = s_codes + 2 * pair * pitch + ((blk ^ (pair & 7)) * 16);
-  *reinterpret_cast<uint4*>(to) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
-  *reinterpret_cast<uint4*>(to + pitch) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
-  const int64_t block = (r0 >> 5) + blk;
-  const int c = c0 + 2 * pair;
-  if (c < K) {
-    const bool in = block * 32 < rows;
-    if (in || (layout == MEGAMOE_SCALES_MMA && block < mx_atoms(padded) * 4)) {
-      scales[scale_offset(layout, c, block, padded)] = static_cast<uint8_t>(b0);
-      scales[scale_offset(layout, c + 1, block, padded)] = static_cast<uint8_t>(b1);
-      if (b0 == kMxNan || b1 == kMxNan) set_status(status, MEGAMOE_DEV_NONFINITE);
-    }
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kColCols * 8 / 256; ++i) {
-    const int t = threadIdx.x + 256 * i;
-    const int col = t >> 3, part = t & 7;
-    if (c0 + col < K && r0 + part * 32 < rows)
-      *reinterpret_cast<uint4*>(codes + (c0 + col) * (padded / 2) + r0 / 2 + part * 16) =
-          *reinterpret_cast<const uint4*>(s_codes + col * pitch + ((part ^ (col >> 1 & 7)) * 16));
+  auto with = [&](int tile, auto&& f) {  // f(job, row tile, column tile)
+    int j = 0;
+    while (j + 1 < jobs.count && tile >= jobs.job[j + 1].first) ++j;
+    const MxTile& job = jobs.job[j];
+    const int t = tile - job.first;
+    f(job, t / job.col_tiles, t % job.col_tiles);
+  };
+  auto load = [&](int tile, uint8_t* buf) {
+    with(tile, [&](const MxTile& job, int r, int c) {
+      if (WIDE && job.type == MEGAMOE_TYPE_F32) load_tile<float>(job, r, c, buf);
+      else load_tile<__half>(job, r, c, buf);  // any 2-byte type
+    });
+  };
+  int turn = 0;
+  if (static_cast<int>(blockIdx.x) < jobs.tiles) load(blockIdx.x, s_raw);
+  asm volatile("cp.async.commit_group;" ::: "memory");
+  for (int tile = blockIdx.x; tile < jobs.tiles; tile += gridDim.x, turn ^= 1) {
+    if (tile + static_cast<int>(gridDim.x) < jobs.tiles)
+      load(tile + gridDim.x, s_raw + (turn ^ 1) * kTileBytes);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    __syncthreads();
+    const uint8_t* buf = s_raw + turn * kTileBytes;
+    uint8_t* s_codes = s_raw + 2 * kTileBytes;
+    with(tile, [&](const MxTile& job, int r, int c) {
+      if (WIDE && job.type == MEGAMOE_TYPE_F32) encode_tile<float>(job, r, c, buf, s_codes);
+      else if (job.type == MEGAMOE_TYPE_F16) encode_tile<__half>(job, r, c, buf, s_codes);
+      else encode_tile<__nv_bfloat16>(job, r, c, buf, s_codes);
+    });
+    __syncthreads();  // the tile and the codes are free again
   }
 }
 
@@ -189,9 +308,11 @@ __global__ void __launch_bounds__(256)
     const int64_t t = w / steps;
     const int col = static_cast<int>(w - t * steps) * 256 + 8 * lane;
     const int my_dst = lane < k ? __ldg(slot_dst + t * k + lane) : -1;
+    Eight<__nv_bfloat16> e;
+    e.load(x + t * d + col);
+    const uint32_t byte = block_byte(e);
     float v[8];
-    mx_load8(x + t * d + col, v);
-    const uint32_t byte = mx_scale_byte(block_max(amax_bits8(v)));
+    e.values(v);
     const uint32_t c = mx_codes8(v, mx_inverse(byte));
     if (byte == kMxNan) set_status(status, MEGAMOE_DEV_NONFINITE);
     for (int j = 0; j < k; ++j) {
@@ -204,30 +325,46 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// E2M1 code -> value: 0, 0.5, or (1 + m / 2) 2^(e - 1).
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-  const uint32_t m = code & 7u;
-  const float v = m < 2u ? 0.5f * static_cast<float>(m)
-                         : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-  return (code & 8u) ? -v : v;
+// Two E2M1 codes (a byte, the even element low) -> two halves.
+__device__ __forceinline__ uint32_t e2m1x2_halves(uint32_t byte) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 t, u;\n\tmov.b16 {t, u}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, t;\n\t}"
+      : "=r"(r)
+      : "h"(static_cast<uint16_t>(byte)));
+  return r;
 }
 
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+// Eight codes times a block's scale -> 16 bytes of bf16 (exact: bf16 holds
+// every MXFP4 value).  The five exponent bits of a half moved to the place of
+// bf16's eight are the value times 2^-112; two multiplications by powers of two
+// bring it up and apply the scale.
+__device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t codes, uint32_t byte) {
+  const __nv_bfloat162 up = __float2bfloat162_rn(__uint_as_float((127u + 112u) << 23));
+  const __nv_bfloat162 s = __float2bfloat162_rn(mx_scale_value(byte));
   uint32_t u[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t*>(&h);
+    const uint32_t h = e2m1x2_halves(codes >> (8 * i) & 0xffu);
+    const uint32_t b = (h & 0x80008000u) | ((h & 0x7fff7fffu) >> 3);
+    const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up), s);
+    u[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
   *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+__device__ __forceinline__ void store_values(float* p, uint32_t codes, uint32_t byte) {
+  const float s = mx_scale_value(byte);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t a = e2m1x2_halves(codes >> (16 * i) & 0xffu);
+    const uint32_t b = e2m1x2_halves(codes >> (16 * i + 8) & 0xffu);
+    const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
+    const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
+    reinterpret_cast<float4*>(p)[i] = make_float4(fa.x * s, fa.y * s, fb.x * s, fb.y * s);
+  }
 }
 
-// The values: four bytes of codes in, eight elements out per thread.  bf16
-// holds every MXFP4 value exactly.
+// The values: four bytes of codes in, eight elements out per thread, four of
+// them at once; no division where the rows of out follow each other.
 template <typename O>
 __global__ void __launch_bounds__(256)
     k_mx_values(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
@@ -237,15 +374,29 @@ __global__ void __launch_bounds__(256)
   const int vecs = K / 8;
   const int64_t total = rows * vecs;
   const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += stride) {
-    const int64_t r = i / vecs;
-    const uint32_t c = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const float s = mx_scale_value(__ldg(scales + (i >> 2)));
-    float v[8];
+  constexpr int n = 4;
+  for (int64_t i0 = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i0 < total;
+       i0 += n * stride) {
+    uint32_t c[n], s[n];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = e2m1_value(c >> (4 * j)) * s;
-    store8(out + r * ld + (i - r * vecs) * 8, v);
+    for (int j = 0; j < n; ++j) {
+      const int64_t i = i0 + j * stride;
+      if (i < total) {
+        c[j] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+        s[j] = __ldg(scales + (i >> 2));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int64_t i = i0 + j * stride;
+      if (i >= total) break;
+      int64_t at = i * 8;
+      if (ld != K) {
+        const int64_t r = task_div(i, vecs);
+        at = r * ld + (i - r * vecs) * 8;
+      }
+      store_values(out + at, c[j], s[j]);
+    }
   }
 }
 
@@ -269,31 +420,62 @@ unsigned blocks_for(int64_t tasks, int64_t per_block) {
 }
 
 template <typename X>
-cudaError_t quantize_typed(const MxQuant& q, cudaStream_t s) {
-  const X* x = static_cast<const X*>(q.x);
-  if (!q.transpose) {
-    const int64_t tasks = q.rows * ((q.K + 255) / 256);
-    return launch_pdl(k_mx_rows<X>, dim3(blocks_for(tasks, 8)), dim3(256), 0, s, x, q.rows, q.K,
-                      q.ld, q.codes, q.scales, q.layout, q.status);
-  }
-  const size_t smem = kColRows * kColCols * sizeof(X) + kColCols * (kColRows / 2);
-  cudaError_t e = cudaFuncSetAttribute(k_mx_columns<X>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((q.rows + kColRows - 1) / kColRows),
-                  static_cast<unsigned>((q.K + kColCols - 1) / kColCols));
-  return launch_pdl(k_mx_columns<X>, grid, dim3(256), smem, s, x, q.rows, q.K, q.ld, q.codes,
-                    q.scales, q.layout, q.status);
+cudaError_t quantize_rows(const MxQuant& q, cudaStream_t s) {
+  const int64_t tasks = q.rows * ((q.K + 1023) / 1024);
+  // enough blocks for every task at small sizes, several tasks a warp at large ones
+  return launch_pdl(k_mx_rows<X>, dim3(blocks_for(tasks, 8)), dim3(256), 0, s,
+                    static_cast<const X*>(q.x), q.rows, q.K, q.ld, q.codes, q.scales, q.layout,
+                    q.status);
 }
 
 }  // namespace
 
+cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s) {
+  jobs.tiles = 0;
+  bool wide = false;
+  for (int j = 0; j < jobs.count; ++j) {
+    MxTile& t = jobs.job[j];
+    const int tall = t.type == MEGAMOE_TYPE_F32 ? kTileRows<float> : kTileRows<__half>;
+    wide |= t.type == MEGAMOE_TYPE_F32;
+    // a row's scales in the atom layout reach to whole K steps of 256
+    const int64_t cols = t.row_codes ? mx_atoms(t.K) * 128 : t.K;
+    t.col_tiles = static_cast<int>((cols + kTileCols - 1) / kTileCols);
+    t.first = jobs.tiles;
+    const bool steps = t.col_codes && t.col_layout == MEGAMOE_SCALES_MMA;  // and so do a column's
+    const int64_t rows = t.rows == 0 ? 0 : steps ? mx_atoms(t.rows) * 128 : t.rows;
+    const int64_t n = (rows + tall - 1) / tall * t.col_tiles;
+    if (jobs.tiles + n >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+    jobs.tiles += static_cast<int>(n);
+  }
+  if (jobs.tiles == 0) return cudaSuccess;
+  constexpr int smem = 2 * kTileBytes + kTileCodes;
+  auto kern = wide ? k_mx_tiles<true> : k_mx_tiles<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  // three blocks an SM by shared memory
+  return launch_pdl(kern, dim3(std::min(jobs.tiles, 3 * num_sms())), dim3(256), smem, s, jobs);
+}
+
 cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s) {
   if (q.rows == 0) return cudaSuccess;
+  if (q.transpose) {
+    MxTiles jobs{};
+    jobs.count = 1;
+    jobs.job[0].x = q.x;
+    jobs.job[0].type = q.type;
+    jobs.job[0].rows = q.rows;
+    jobs.job[0].ld = q.ld;
+    jobs.job[0].K = q.K;
+    jobs.job[0].col_codes = q.codes;
+    jobs.job[0].col_scales = q.scales;
+    jobs.job[0].col_layout = q.layout;
+    jobs.job[0].status = q.status;
+    return launch_mx_tiles(jobs, s);
+  }
   switch (q.type) {
-    case MEGAMOE_TYPE_BF16: return quantize_typed<__nv_bfloat16>(q, s);
-    case MEGAMOE_TYPE_F16: return quantize_typed<__half>(q, s);
-    default: return quantize_typed<float>(q, s);
+    case MEGAMOE_TYPE_BF16: return quantize_rows<__nv_bfloat16>(q, s);
+    case MEGAMOE_TYPE_F16: return quantize_rows<__half>(q, s);
+    default: return quantize_rows<float>(q, s);
   }
 }
 

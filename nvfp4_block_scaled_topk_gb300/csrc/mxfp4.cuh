@@ -38,13 +38,19 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
 }
 // Eight elements -> four bytes of codes (element 0 in the lowest nibble).
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
-  uint32_t c = 0;
-  if (inv != 0.f) {
+  float s[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      c |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-  }
-  return c;
+  for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+  uint32_t c;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(c)
+      : "f"(s[0]), "f"(s[1]), "f"(s[2]), "f"(s[3]), "f"(s[4]), "f"(s[5]), "f"(s[6]), "f"(s[7]));
+  return inv != 0.f ? c : 0u;
 }
 
 // Atoms along K of a matrix of row length K (a K step of 256 holds two).
@@ -64,31 +70,76 @@ __host__ __device__ __forceinline__ int64_t mx_routed_offset(int b) {
   return static_cast<int64_t>(b >> 3) * 16 + (b & 7);
 }
 
-// Eight consecutive elements as floats.
-__device__ __forceinline__ void mx_load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(u[i] << 16);
-    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+// Eight consecutive elements: their bits, the largest |x| in a form that
+// ordinary integer maxima keep ordered, and their values.
+template <typename X>
+struct Eight;
+template <typename X>
+struct Eight16 {  // 2-byte types: two magnitudes side by side in a word
+  uint4 q;
+  __device__ __forceinline__ void load(const X* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void clear() { q = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ uint32_t widest() const {
+    const uint32_t m = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(q.x & m, q.y & m), __vmaxu2(q.z & m, q.w & m));
   }
-}
-__device__ __forceinline__ void mx_load8(const __half* p, float (&v)[8]) {
-  const uint4 q = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
+  __device__ __forceinline__ static uint32_t wider(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+};
+template <>
+struct Eight<__nv_bfloat16> : Eight16<__nv_bfloat16> {
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) {  // as fp32
+    return max(m << 16, m & 0xffff0000u);
   }
-}
-__device__ __forceinline__ void mx_load8(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p));
-  const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Eight<__half> : Eight16<__half> {
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) {
+    const uint16_t h = static_cast<uint16_t>(max(m & 0xffffu, m >> 16));
+    return __float_as_uint(__half2float(__ushort_as_half(h)));
+  }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Eight<float> {
+  float v8[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldg(reinterpret_cast<const float4*>(p));
+    const float4 b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    v8[0] = a.x; v8[1] = a.y; v8[2] = a.z; v8[3] = a.w;
+    v8[4] = b.x; v8[5] = b.y; v8[6] = b.z; v8[7] = b.w;
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v8[i] = 0.f;
+  }
+  __device__ __forceinline__ uint32_t widest() const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v8[i]) & 0x7fffffffu);
+    return m;
+  }
+  __device__ __forceinline__ static uint32_t wider(uint32_t a, uint32_t b) { return max(a, b); }
+  __device__ __forceinline__ static uint32_t bits(uint32_t m) { return m; }
+  __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = v8[i];
+  }
+};
 
 }  // namespace megamoe
