@@ -30,6 +30,21 @@ __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
   return __bfloat162float(*p);
 }
 
+// One logit, or four on a 16-byte (bf16: 8-byte) boundary.
+__device__ __forceinline__ void load_logits(const float* p, float (&v)[1]) { v[0] = __ldg(p); }
+__device__ __forceinline__ void load_logits(const __nv_bfloat16* p, float (&v)[1]) {
+  v[0] = __bfloat162float(*p);
+}
+__device__ __forceinline__ void load_logits(const float* p, float (&v)[4]) {
+  const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+}
+__device__ __forceinline__ void load_logits(const __nv_bfloat16* p, float (&v)[4]) {
+  const uint2 q = __ldg(reinterpret_cast<const uint2*>(p));
+  v[0] = __uint_as_float(q.x << 16); v[1] = __uint_as_float(q.x & 0xffff0000u);
+  v[2] = __uint_as_float(q.y << 16); v[3] = __uint_as_float(q.y & 0xffff0000u);
+}
+
 // NaN -> -inf, +inf -> the largest float (so that exp(l - m) has a limit).
 __device__ __forceinline__ float clean_logit(float l) {
   return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
@@ -60,34 +75,57 @@ __device__ __forceinline__ float warp_max(float v) {
 
 constexpr int kWarps = 4;  // tokens per block
 
+// The experts that a lane holds: of its group, V consecutive ones at a time,
+// the group's lanes side by side.
+template <int V>
+__device__ __forceinline__ int lane_expert(int i, int sub, int lanes) {
+  return (i / V * lanes + sub) * V + i % V;
+}
+
 // One warp per token, everything in registers.  The 32 lanes are cut into one
-// run of lanes_per_group (a power of two) per group of experts; a lane holds
-// experts sub, sub + lanes_per_group, ... of its group (at most NV), so a
-// group's two largest scores are a shuffle reduction within its run, and
-// dropping a group empties its lanes.  A round of the top-k is two warp
-// reductions: the largest key, then the lowest expert that has it.
-template <typename L, int NV>
+// run of `lanes` (a power of two) per group of experts, so a group's two largest
+// scores are a shuffle reduction within its run, and dropping a group empties
+// its lanes.  The choice:
+//   - the k-th largest of the lanes' largest scores is a lower bound of the
+//     k-th largest score (k lanes have one at least as large), found by k warp
+//     maxima;
+//   - the scores from the bound on, few more than k, go to shared memory, one
+//     for each lane, and each lane counts those before its own (a larger score,
+//     or an equal one at a lower index): its slot.
+// More than 32 of them (ties) are taken one by one.  The work per token bounds
+// this kernel, not its bytes; at 16384 tokens of 384 experts in 8 groups, top-6,
+// with 16-byte loads of four experts, taking all by warp maxima took 30.2 us.
+// Scores for the choice use the hardware's exponential and reciprocal (within
+// 2^-20 of their value, the same for equal logits); the weights do not.
+template <typename L, int NV, int V>
 __global__ void __launch_bounds__(kWarps * 32)
     k_scored_router(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
-                    const float* __restrict__ bias, int softmax, int n_group, int lanes_per_group,
+                    const float* __restrict__ bias, int softmax, int n_group, int lanes,
                     int topk_group, int group_top, int k, int renormalize, float scale,
                     int32_t* __restrict__ ids, float* __restrict__ weights) {
+  __shared__ float s_score[kWarps][32];
+  __shared__ int s_id[kWarps][32];
   pdl_wait();
   pdl_trigger();
-  const int lane = threadIdx.x & 31;
-  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = static_cast<int64_t>(blockIdx.x) * kWarps + warp;
   if (t >= T) return;  // warp-uniform
   const L* row = logits + t * ld;
   const int size = E / n_group;
-  const int group = lane / lanes_per_group, sub = lane & (lanes_per_group - 1);
-  const bool mine = group < n_group;
+  const int group = lane / lanes, sub = lane & (lanes - 1);
   const int first = group * size;
+  const int mine = group < n_group ? size : 0;  // experts within reach of this lane
 
   float c[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = sub + i * lanes_per_group;
-    c[i] = mine && j < size ? clean_logit(load_logit(row + first + j)) : -INFINITY;
+  for (int i = 0; i < NV; i += V) {
+    const int j = lane_expert<V>(i, sub, lanes);
+    float v[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) v[u] = -INFINITY;
+    if (j < mine) load_logits(row + first + j, v);
+#pragma unroll
+    for (int u = 0; u < V; ++u) c[i + u] = clean_logit(v[u]);
   }
   float top = 0.f, total = 1.f;  // softmax: the largest logit, the sum of exp(l - top)
   if (softmax) {
@@ -101,69 +139,108 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int i = 0; i < NV; ++i) sum += expf(c[i] - top);
     total = warp_sum(sum);
   }
-  auto score = [&](float l) {
-    if (!softmax) return sigmoid(l);
-    return total > 0.f ? __fdiv_rn(expf(l - top), total) : 0.f;
-  };
-  uint32_t key[NV];
+  // scores plus bias; -inf: cannot be taken
+  const float inverse = total > 0.f ? __fdividef(1.f, total) : 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int j = sub + i * lanes_per_group;
-    key[i] = 0u;
-    if (c[i] > -INFINITY) {
-      const float s = score(c[i]);
-      key[i] = order_key(bias ? __fadd_rn(s, __ldg(bias + first + j)) : s);
+  for (int i = 0; i < NV; i += V) {
+    const int j = lane_expert<V>(i, sub, lanes);
+    float b[V];
+#pragma unroll
+    for (int u = 0; u < V; ++u) b[u] = 0.f;
+    if (bias && j < mine) load_logits(bias + first + j, b);
+#pragma unroll
+    for (int u = 0; u < V; ++u) {
+      const float l = c[i + u];
+      const float s = softmax ? __expf(l - top) * inverse : __fdividef(1.f, 1.f + __expf(-l));
+      const float v = s + b[u];
+      c[i + u] = l > -INFINITY && v > -INFINITY ? v : -INFINITY;
     }
   }
   if (n_group > 1) {
-    uint32_t a = 0u, b = 0u;  // the group's two largest keys
+    float a = -INFINITY, b = -INFINITY;  // the group's two largest
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      b = max(b, min(a, key[i]));
-      a = max(a, key[i]);
+      b = fmaxf(b, fminf(a, c[i]));
+      a = fmaxf(a, c[i]);
     }
-    for (int o = lanes_per_group >> 1; o > 0; o >>= 1) {
-      const uint32_t oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
-      b = max(max(b, ob), min(a, oa));
-      a = max(a, oa);
+    for (int o = lanes >> 1; o > 0; o >>= 1) {
+      const float oa = __shfl_xor_sync(kAll, a, o), ob = __shfl_xor_sync(kAll, b, o);
+      b = fmaxf(fmaxf(b, ob), fminf(a, oa));
+      a = fmaxf(a, oa);
     }
-    uint32_t g = a;  // the group's score as a key
-    if (group_top == 2 && b != 0u) g = order_key(__fadd_rn(key_value(a), key_value(b)));
-    // rank among the groups (before it: a higher score, or an equal one at a
-    // lower index); 0 keys (nothing to take) count as lowest
+    const float g = group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a;
     int rank = 0;
     for (int o = 0; o < n_group; ++o) {
-      const uint32_t og = __shfl_sync(kAll, g, o * lanes_per_group);
+      const float og = __shfl_sync(kAll, g, o * lanes);
       rank += og > g || (og == g && o < group);
     }
     if (rank >= topk_group) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) key[i] = 0u;
+      for (int i = 0; i < NV; ++i) c[i] = -INFINITY;
     }
   }
-  int my_id = -1;
-  for (int j = 0; j < k; ++j) {
-    uint32_t best = 0u;
-    int at = 0;
+  float most = c[0];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      if (key[i] > best) {  // experts ascend with i: the first of equals stays
-        best = key[i];
-        at = i;
-      }
+  for (int i = 1; i < NV; ++i) most = fmaxf(most, c[i]);
+  uint32_t key = order_key(most), bound = 0u;
+  for (int j = 0; j < k; ++j) {
+    bound = __reduce_max_sync(kAll, key);
+    if (bound == 0u) break;  // fewer than k lanes have any
+    if (key == bound) key = 0u;
+  }
+  const float least = bound == 0u ? -FLT_MAX : key_value(bound);
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const unsigned take = __ballot_sync(kAll, c[i] >= least);
+    if (take == 0u) continue;  // warp-uniform
+    const int at = n + __popc(take & ((1u << lane) - 1u));
+    if (c[i] >= least && at < 32) {
+      s_score[warp][at] = c[i];
+      s_id[warp][at] = first + lane_expert<V>(i, sub, lanes);
     }
-    const uint32_t m = __reduce_max_sync(kAll, best);
-    if (m == 0u) break;  // nothing left to take
-    const int e = best == m ? first + sub + at * lanes_per_group : 0x7fffffff;
-    const int won = __reduce_min_sync(kAll, e);
-    if (e == won) {
+    n += __popc(take);
+  }
+  __syncwarp();
+  int my_id = -1;
+  if (n <= 32) {
+    const float v = lane < n ? s_score[warp][lane] : -INFINITY;
+    const int e = lane < n ? s_id[warp][lane] : 0x7fffffff;
+    int slot = 0;
+    for (int j = 0; j < n; ++j) {
+      const float ov = __shfl_sync(kAll, v, j);
+      const int oe = __shfl_sync(kAll, e, j);
+      slot += ov > v || (ov == v && oe < e);
+    }
+    __syncwarp();
+    if (lane < n) s_id[warp][slot] = e;
+    __syncwarp();
+    if (lane < min(k, n)) my_id = s_id[warp][lane];
+  } else {
+    for (int j = 0; j < k; ++j) {
+      float best = -INFINITY;
+      int e = 0x7fffffff;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        if (c[i] > best) {  // experts ascend with i: the first of equals stays
+          best = c[i];
+          e = first + lane_expert<V>(i, sub, lanes);
+        }
+      }
+      const uint32_t mk = order_key(best), m = __reduce_max_sync(kAll, mk);
+      if (m == 0u) break;  // nothing left to take
+      const int won = __reduce_min_sync(kAll, mk == m ? e : 0x7fffffff);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (i == at) key[i] = 0u;
+        if (first + lane_expert<V>(i, sub, lanes) == won && mine) c[i] = -INFINITY;
+      if (lane == j) my_id = won;
     }
-    if (lane == j) my_id = won;
   }
-  float w = my_id >= 0 ? score(clean_logit(load_logit(row + my_id))) : 0.f;
+  float w = 0.f;
+  if (my_id >= 0) {
+    const float l = clean_logit(load_logit(row + my_id));
+    w = softmax ? __fdiv_rn(expf(l - top), total) : sigmoid(l);
+  }
   if (renormalize) {
     const float sum = warp_sum(w);
     w = sum > 0.f ? __fdiv_rn(w, sum) : 0.f;
@@ -254,20 +331,31 @@ template <typename L>
 cudaError_t launch_router_typed(const ScoredRouter& r, cudaStream_t stream) {
   int runs = 1;  // groups, up to a power of two
   while (runs < r.n_group) runs *= 2;
-  const int lanes = 32 / runs;
-  const int per_lane = (r.E / r.n_group + lanes - 1) / lanes;
+  const int lanes = 32 / runs, size = r.E / r.n_group;
   const dim3 grid(static_cast<unsigned>((r.T + kWarps - 1) / kWarps)), block(kWarps * 32);
   auto run = [&](auto kern) {
     return launch_pdl(kern, grid, block, 0, stream, static_cast<const L*>(r.logits), r.T, r.E, r.ld,
                       r.bias, r.softmax, r.n_group, lanes, r.topk_group, r.group_top, r.k,
                       r.renormalize, r.scale, r.ids, r.weights);
   };
-  if (per_lane <= 4) return run(k_scored_router<L, 4>);
-  if (per_lane <= 8) return run(k_scored_router<L, 8>);
-  if (per_lane <= 12) return run(k_scored_router<L, 12>);
-  if (per_lane <= 16) return run(k_scored_router<L, 16>);
-  if (per_lane <= 32) return run(k_scored_router<L, 32>);
-  return run(k_scored_router<L, 64>);
+  // four experts a load where groups, rows and pointers are whole fours
+  const bool fours = size % 4 == 0 && r.ld % 4 == 0 &&
+                     reinterpret_cast<uintptr_t>(r.logits) % (4 * sizeof(L)) == 0 &&
+                     reinterpret_cast<uintptr_t>(r.bias) % 16 == 0;
+  if (fours) {
+    const int per_lane = (size + 4 * lanes - 1) / (4 * lanes) * 4;
+    if (per_lane <= 4) return run(k_scored_router<L, 4, 4>);
+    if (per_lane <= 8) return run(k_scored_router<L, 8, 4>);
+    if (per_lane <= 12) return run(k_scored_router<L, 12, 4>);
+    if (per_lane <= 16) return run(k_scored_router<L, 16, 4>);
+    if (per_lane <= 32) return run(k_scored_router<L, 32, 4>);
+    return run(k_scored_router<L, 64, 4>);
+  }
+  const int per_lane = (size + lanes - 1) / lanes;
+  if (per_lane <= 4) return run(k_scored_router<L, 4, 1>);
+  if (per_lane <= 12) return run(k_scored_router<L, 12, 1>);
+  if (per_lane <= 32) return run(k_scored_router<L, 32, 1>);
+  return run(k_scored_router<L, 64, 1>);
 }
 
 template <typename L>
