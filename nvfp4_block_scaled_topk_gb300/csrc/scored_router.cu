@@ -50,6 +50,19 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
 }
 
+// The hardware's exponential and reciprocal, within 2^-22 + |x| 2^-24 and 2^-23
+// of their value (results below the smallest normal number are zero).
+__device__ __forceinline__ float fast_exp(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
+  return r;
+}
+__device__ __forceinline__ float fast_reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 __device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.f, 1.f + expf(-l)); }
 
 // Unsigned key in the order of the floats above -inf; 0 marks what cannot be taken.
@@ -103,8 +116,8 @@ __global__ void __launch_bounds__(kWarps * 32)
                     const float* __restrict__ bias, int softmax, int n_group, int lanes,
                     int topk_group, int group_top, int k, int renormalize, float scale,
                     int32_t* __restrict__ ids, float* __restrict__ weights) {
-  __shared__ float s_score[kWarps][32];
-  __shared__ int s_id[kWarps][32];
+  __shared__ float2 s_taken[kWarps][32];  // score, expert (as bits)
+  __shared__ int s_count[kWarps], s_id[kWarps][32];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -125,37 +138,48 @@ __global__ void __launch_bounds__(kWarps * 32)
     for (int u = 0; u < V; ++u) v[u] = -INFINITY;
     if (j < mine) load_logits(row + first + j, v);
 #pragma unroll
-    for (int u = 0; u < V; ++u) c[i + u] = clean_logit(v[u]);
+    for (int u = 0; u < V; ++u) c[i + u] = v[u];
   }
   float top = 0.f, total = 1.f;  // softmax: the largest logit, the sum of exp(l - top)
   if (softmax) {
     top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) top = fmaxf(top, c[i]);
+    for (int i = 0; i < NV; ++i) {
+      c[i] = clean_logit(c[i]);
+      top = fmaxf(top, c[i]);
+    }
     top = warp_max(top);
     if (top == -INFINITY) top = 0.f;  // no expert: every exp is 0
-    float sum = 0.f;
+    total = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) sum += expf(c[i] - top);
-    total = warp_sum(sum);
+    for (int i = 0; i < NV; ++i) total += expf(c[i] - top);
+    total = warp_sum(total);
+    const float inverse = total > 0.f ? fast_reciprocal(total) : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      c[i] = c[i] > -INFINITY ? fast_exp(c[i] - top) * inverse : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)  // NaN stays NaN
+      c[i] = c[i] > -INFINITY ? fast_reciprocal(1.f + fast_exp(-c[i])) : -INFINITY;
   }
   // scores plus bias; -inf: cannot be taken
-  const float inverse = total > 0.f ? __fdividef(1.f, total) : 0.f;
+  if (bias) {
 #pragma unroll
-  for (int i = 0; i < NV; i += V) {
-    const int j = lane_expert<V>(i, sub, lanes);
-    float b[V];
+    for (int i = 0; i < NV; i += V) {
+      const int j = lane_expert<V>(i, sub, lanes);
+      float b[V];
 #pragma unroll
-    for (int u = 0; u < V; ++u) b[u] = 0.f;
-    if (bias && j < mine) load_logits(bias + first + j, b);
+      for (int u = 0; u < V; ++u) b[u] = 0.f;
+      if (j < mine) load_logits(bias + first + j, b);
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const float l = c[i + u];
-      const float s = softmax ? __expf(l - top) * inverse : __fdividef(1.f, 1.f + __expf(-l));
-      const float v = s + b[u];
-      c[i + u] = l > -INFINITY && v > -INFINITY ? v : -INFINITY;
+      for (int u = 0; u < V; ++u) {
+        const float v = c[i + u] + b[u];
+        c[i + u] = v > -INFINITY ? v : -INFINITY;  // NaN too
+      }
     }
   }
+  if (lane == 0) s_count[warp] = 0;
   if (n_group > 1) {
     float a = -INFINITY, b = -INFINITY;  // the group's two largest
 #pragma unroll
@@ -170,6 +194,7 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
     const float g = group_top == 2 && b > -INFINITY ? __fadd_rn(a, b) : a;
     int rank = 0;
+#pragma unroll 4
     for (int o = 0; o < n_group; ++o) {
       const float og = __shfl_sync(kAll, g, o * lanes);
       rank += og > g || (og == g && o < group);
@@ -189,30 +214,28 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (key == bound) key = 0u;
   }
   const float least = bound == 0u ? -FLT_MAX : key_value(bound);
-  int n = 0;
+  __syncwarp();
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const unsigned take = __ballot_sync(kAll, c[i] >= least);
-    if (take == 0u) continue;  // warp-uniform
-    const int at = n + __popc(take & ((1u << lane) - 1u));
-    if (c[i] >= least && at < 32) {
-      s_score[warp][at] = c[i];
-      s_id[warp][at] = first + lane_expert<V>(i, sub, lanes);
+    if (c[i] >= least) {  // in any order: their slots do not depend on it
+      const int at = atomicAdd(&s_count[warp], 1);
+      if (at < 32)
+        s_taken[warp][at] =
+            make_float2(c[i], __int_as_float(first + lane_expert<V>(i, sub, lanes)));
     }
-    n += __popc(take);
   }
   __syncwarp();
+  const int n = s_count[warp];
   int my_id = -1;
   if (n <= 32) {
-    const float v = lane < n ? s_score[warp][lane] : -INFINITY;
-    const int e = lane < n ? s_id[warp][lane] : 0x7fffffff;
+    const float2 own = s_taken[warp][min(lane, max(n - 1, 0))];
+    const int e = __float_as_int(own.y);
     int slot = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
-      const float ov = __shfl_sync(kAll, v, j);
-      const int oe = __shfl_sync(kAll, e, j);
-      slot += ov > v || (ov == v && oe < e);
+      const float2 o = s_taken[warp][j];
+      slot += o.x > own.x || (o.x == own.x && __float_as_int(o.y) < e);
     }
-    __syncwarp();
     if (lane < n) s_id[warp][slot] = e;
     __syncwarp();
     if (lane < min(k, n)) my_id = s_id[warp][lane];
