@@ -65,6 +65,12 @@ struct LinearWs {
 LinearWs carve_linear(void* base, int64_t T, int K, int N) {
   Carver c{static_cast<uint8_t*>(base)};
   LinearWs w{};
+  if (mx_linear_few_fits(T, K, N)) {  // one launch, the status word alone
+    w.head = c.take(256);
+    w.status = reinterpret_cast<uint32_t*>(w.head);
+    w.bytes = c.off;
+    return w;
+  }
   w.head_bytes = 256 + 4 * static_cast<size_t>(mx_product_counters(T, N, K));
   w.head = c.take(w.head_bytes);
   w.status = reinterpret_cast<uint32_t*>(w.head);
@@ -355,7 +361,10 @@ megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K,
   const LinearWs wk = carve_linear(ws, T, K, N);
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = as_stream(stream);
-  cudaError_t e = cudaMemsetAsync(wk.head, 0, wk.head_bytes, s);
+  if (T > 0 && mx_linear_few_fits(T, K, N))
+    return cuda_status(launch_mx_linear_few(x, x_type, T, K, ld_x, w_codes, w_scales, N, out,
+                                              out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status, s));
+  cudaError_t e = cudaMemsetAsync(wk.head, 0, std::max<size_t>(wk.head_bytes, 256), s);
   if (e == cudaSuccess)
     e = launch_mx_quantize(quant_of(x, x_type, T, K, ld_x, false, wk.x, wk.status), s);
   if (e == cudaSuccess)

@@ -311,6 +311,11 @@ __device__ __forceinline__ uint32_t cluster_address(const void* p, uint32_t rank
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// tc_copy_atom_pair for a CTA on its own.
+__device__ __forceinline__ void tc_copy_atom(uint32_t taddr, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
+               : "memory");
+}
 // An atom of 512 bytes (128 rows x 4 block scales; descriptor of sdesc_atom)
 // from each CTA's shared memory into four columns of its tensor memory, in all
 // four lane quarters.  Runs in the tensor pipe in issue order with the MMAs.

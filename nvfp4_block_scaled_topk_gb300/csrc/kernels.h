@@ -229,6 +229,13 @@ size_t mx_product_bytes(int64_t R, int64_t C, int64_t K);
 int mx_product_counters(int64_t R, int64_t C, int64_t K);
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);
 
+// The MXFP4 linear for few tokens in one launch (clears *status first).
+bool mx_linear_few_fits(int64_t T, int64_t K, int64_t N);
+cudaError_t launch_mx_linear_few(const void* x, int x_type, int64_t T, int K, int64_t ld_x,
+                                 const uint8_t* codes, const uint8_t* scales, int N, void* out,
+                                 bool out_f32, int64_t ld_out, uint32_t* status,
+                                 cudaStream_t stream);
+
 // Shape and weight-pointer checks of megamoe_forward.
 megamoe_status check_forward_shape(const megamoe_weights* w, int T, int k, int pad);
 // Argument and shape checks of megamoe_forward that do not involve the

@@ -635,22 +635,43 @@ def _carve_views(ws, off, T, k, E, d, I, pad):
 # --------------------------------------------------------------------------
 # scored router
 # --------------------------------------------------------------------------
-def _dev_logits(t, name):
-    if not (t.is_cuda and t.dim() == 2 and t.dtype in (torch.float32, torch.bfloat16)
-            and (t.stride(1) == 1 or t.shape[1] <= 1)):
-        raise TypeError(f"{name} must be a CUDA float32 or bfloat16 matrix with unit column stride")
-    _on_current_device(t, name)
+# (the checks below are written for the few microseconds that a short kernel
+# takes: each attribute is asked for once)
+LOGIT_TYPES = {torch.float32: 1, torch.bfloat16: 0}
+
+
+def _matrix(t, types, name):
+    """(rows, columns, row stride, type code, stream) of a CUDA matrix of one of
+    `types` with unit column stride, on the current device."""
+    code = types.get(t.dtype)
+    if code is None or not t.is_cuda or t.dim() != 2:
+        raise TypeError(f"{name} must be a CUDA matrix of {', '.join(map(str, types))}")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise TypeError(f"{name} must have unit column stride")
+    if rows <= 1 and ld < cols:  # a matrix of one row may carry any stride
+        ld = cols
+    dev = t.get_device()
+    if dev != torch._C._cuda_getDevice():
+        _on_current_device(t, name)
+    return rows, cols, ld, code, torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _vector(t, n, name):
+    """Address of a float32 vector of n values (None: null)."""
+    if t is None:
+        return None
+    _dev(t, torch.float32, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} values")
+    return t.data_ptr()
 
 
 def _score(score):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
     return SCORES[score]
-
-
-def _row_stride(t):
-    """Elements between rows (a matrix of one row may carry any stride)."""
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
 
 
 def router_scored_topk(logits: torch.Tensor, k: int, score: str = "sigmoid", bias=None,
@@ -661,17 +682,13 @@ def router_scored_topk(logits: torch.Tensor, k: int, score: str = "sigmoid", bia
     within the topk_group groups (of n_group) whose group_top best experts sum
     highest, weighted by scale * score, renormalised over the k taken.  Slots
     without an expert to take get id -1 and weight 0."""
-    _dev_logits(logits, "logits")
-    T, E = logits.shape
-    if bias is not None:
-        _dev(bias, torch.float32, "bias")
-        if bias.numel() != E:
-            raise ValueError("bias must have one value per expert")
-    ids = torch.empty(T, k, dtype=torch.int32, device=logits.device)
-    w = torch.empty(T, k, dtype=torch.float32, device=logits.device)
+    T, E, ld, code, stream = _matrix(logits, LOGIT_TYPES, "logits")
+    dev = logits.device
+    ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = torch.empty((T, k), dtype=torch.float32, device=dev)
     _check("megamoe_router_scored_topk", load().megamoe_router_scored_topk(
-        _p(logits), TYPES[logits.dtype], T, E, _row_stride(logits), _p(bias), _score(score),
-        n_group, topk_group, group_top, k, renormalize, scale, _p(ids), _p(w), _stream()))
+        logits.data_ptr(), code, T, E, ld, _vector(bias, E, "bias"), _score(score), n_group,
+        topk_group, group_top, k, renormalize, scale, ids.data_ptr(), w.data_ptr(), stream))
     return ids, w
 
 
@@ -680,28 +697,23 @@ def router_scored_topk_backward(logits: torch.Tensor, ids: torch.Tensor,
                                 renormalize: bool = True, scale: float = 1.0):
     """Gradient [T, E] (of the logits' type) of router_scored_topk's weights
     with respect to the logits, for the ids it gave."""
-    _dev_logits(logits, "logits")
+    T, E, ld, code, stream = _matrix(logits, LOGIT_TYPES, "logits")
     _dev(ids, torch.int32, "ids")
     _dev(grad_weights, torch.float32, "grad_weights")
-    T, E = logits.shape
-    if ids.dim() != 2 or ids.shape[0] != T or grad_weights.shape != ids.shape:
+    shape = ids.shape
+    if len(shape) != 2 or shape[0] != T or grad_weights.shape != shape:
         raise ValueError("ids and grad_weights must be [T, k]")
-    out = torch.empty(T, E, dtype=logits.dtype, device=logits.device)
+    out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     _check("megamoe_router_scored_topk_backward", load().megamoe_router_scored_topk_backward(
-        _p(logits), TYPES[logits.dtype], T, E, _row_stride(logits), _p(ids), _p(grad_weights),
-        _score(score), ids.shape[1], renormalize, scale, _p(out), E, _stream()))
+        logits.data_ptr(), code, T, E, ld, ids.data_ptr(), grad_weights.data_ptr(), _score(score),
+        shape[1], renormalize, scale, out.data_ptr(), E, stream))
     return out
 
 
 # --------------------------------------------------------------------------
 # MXFP4: E2M1 codes, one power-of-two scale per 32 elements
 # --------------------------------------------------------------------------
-def _dev_float_rows(t, name):
-    if not (t.is_cuda and t.dtype in TYPES and t.dim() == 2
-            and (t.stride(1) == 1 or t.shape[1] <= 1)):
-        raise TypeError(f"{name} must be a CUDA bfloat16, float16 or float32 matrix with unit "
-                        "column stride")
-    _on_current_device(t, name)
+_BYTES = {torch.uint8: 0}
 
 
 def mx_atom_bytes(rows: int, K: int) -> int:
@@ -715,33 +727,34 @@ def quantize_mxfp4(x: torch.Tensor, transpose: bool = False, scale_layout=SCALES
     transpose those of x^T, quantised along the rows of x: codes [K, R / 2],
     scales [K, R / 32], R = rows up to a multiple of 32 (zeros past the last).
     With SCALES_MMA the scales are a buffer in the atom layout."""
-    _dev_float_rows(x, "x")
-    rows, K = x.shape
+    rows, K, ld, code, stream = _matrix(x, TYPES, "x")
     out_rows, out_k = (K, (rows + 31) // 32 * 32) if transpose else (rows, K)
-    codes = torch.empty(out_rows, out_k // 2, dtype=torch.uint8, device=x.device)
-    if scale_layout == SCALES_MMA:
-        scales = torch.empty(mx_atom_bytes(out_rows, out_k), dtype=torch.uint8, device=x.device)
-    else:
-        scales = torch.empty(out_rows, out_k // 32, dtype=torch.uint8, device=x.device)
+    dev = x.device
+    codes = torch.empty((out_rows, out_k // 2), dtype=torch.uint8, device=dev)
+    shape = (mx_atom_bytes(out_rows, out_k),) if scale_layout == SCALES_MMA else (out_rows,
+                                                                                  out_k // 32)
+    scales = torch.empty(shape, dtype=torch.uint8, device=dev)
     _check("megamoe_quantize_mxfp4", load().megamoe_quantize_mxfp4(
-        _p(x), TYPES[x.dtype], rows, K, _row_stride(x), transpose, _p(codes), _p(scales),
-        scale_layout, _p(status), _stream()))
+        x.data_ptr(), code, rows, K, ld, transpose, codes.data_ptr(), scales.data_ptr(),
+        scale_layout, _p(status), stream))
     return codes, scales
 
 
 def dequantize_mxfp4(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16):
     """The values of row-major codes [rows, K / 2] and scales [rows, K / 32]."""
-    _dev(codes, torch.uint8, "codes")
+    rows, half, ld, _, stream = _matrix(codes, _BYTES, "codes")
     _dev(scales, torch.uint8, "scales")
-    rows, half = codes.shape
+    if ld != half and rows > 1:
+        raise TypeError("codes must be contiguous")
     if scales.shape != (rows, half // 16):
         raise ValueError("scales must be [rows, K / 32]")
-    if dtype not in (torch.bfloat16, torch.float32):
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
         raise TypeError("dtype must be bfloat16 or float32")
-    out = torch.empty(rows, 2 * half, dtype=dtype, device=codes.device)
+    out = torch.empty((rows, 2 * half), dtype=dtype, device=codes.device)
     if rows and half:
         _check("megamoe_dequantize_mxfp4", load().megamoe_dequantize_mxfp4(
-            _p(codes), _p(scales), rows, 2 * half, _p(out), TYPES[dtype], 2 * half, _stream()))
+            codes.data_ptr(), scales.data_ptr(), rows, 2 * half, out.data_ptr(), TYPES[dtype],
+            2 * half, stream))
     return out
 
 
@@ -787,30 +800,41 @@ def _epi(dtype):
     return EPI_F32 if dtype == torch.float32 else EPI_BF16
 
 
+#: workspace bytes by shape (a call of the library each otherwise)
+_SIZES: dict = {}
+
+
 def linear_mxfp4_workspace_size(T: int, K: int, N: int) -> int:
-    return int(load().megamoe_linear_mxfp4_workspace_size(T, K, N))
+    size = _SIZES.get((T, K, N))
+    if size is None:
+        size = int(load().megamoe_linear_mxfp4_workspace_size(T, K, N))
+        if len(_SIZES) < 4096:
+            _SIZES[(T, K, N)] = size
+    return size
 
 
 def linear_mxfp4(x: torch.Tensor, w: MxLinearWeights, out_dtype=EPI_BF16, out=None, ws=None):
     """out [T, N] = MXFP4(x) @ w.T, in bf16 (EPI_BF16) or float32 (EPI_F32).
     Returns (out, ws); ws holds the status word in its first four bytes and may
     be passed again for calls of the same shape."""
-    _dev_float_rows(x, "x")
-    T, K = x.shape
+    T, K, ld, code, stream = _matrix(x, TYPES, "x")
+    N = w.N
     if K != w.K:
         raise ValueError("x and w disagree on K")
+    dev = x.device
     if ws is None:
-        ws = torch.empty(linear_mxfp4_workspace_size(T, K, w.N), dtype=torch.uint8,
-                         device=x.device)
+        ws = torch.empty((linear_mxfp4_workspace_size(T, K, N),), dtype=torch.uint8, device=dev)
     dt = torch.float32 if out_dtype == EPI_F32 else torch.bfloat16
+    ld_out = N
     if out is None:
-        out = torch.empty(T, w.N, dtype=dt, device=x.device)
-    elif out.shape != (T, w.N):
-        raise ValueError("out must be [T, N]")
-    _dev_rows(out, dt, "out")
+        out = torch.empty((T, N), dtype=dt, device=dev)
+    else:
+        rows, cols, ld_out, _, _ = _matrix(out, {dt: 0}, "out")
+        if rows != T or cols != N:
+            raise ValueError("out must be [T, N]")
     _check("megamoe_linear_mxfp4", load().megamoe_linear_mxfp4(
-        _p(x), TYPES[x.dtype], T, K, _row_stride(x), _p(w.codes), _p(w.scales), w.N, out_dtype,
-        _p(out), _row_stride(out), _p(ws), ws.numel(), _stream()))
+        x.data_ptr(), code, T, K, ld, w.codes.data_ptr(), w.scales.data_ptr(), N, out_dtype,
+        out.data_ptr(), ld_out, ws.data_ptr(), ws.numel(), stream))
     return out, ws
 
 
@@ -820,23 +844,22 @@ def linear_mxfp4_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tens
     """(grad_x [T, K], grad_w [N, K], ws) of the linear with master weight w
     [N, K]: grad_out, x and w are each quantised to MXFP4 along the dimension
     that their product sums over.  need_x / need_w false: that gradient is None."""
-    _dev_float_rows(grad_out, "grad_out")
-    _dev_float_rows(x, "x")
-    _dev_float_rows(w, "w")
-    T, N = grad_out.shape
-    K = x.shape[1]
-    if x.shape[0] != T or w.shape != (N, K):
+    T, N, ld_g, g_code, stream = _matrix(grad_out, TYPES, "grad_out")
+    xT, K, ld_x, x_code, _ = _matrix(x, TYPES, "x")
+    wN, wK, ld_w, w_code, _ = _matrix(w, TYPES, "w")
+    if xT != T or wN != N or wK != K:
         raise ValueError("grad_out [T, N], x [T, K] and w [N, K] disagree")
+    gx_epi, gw_epi = _epi(grad_x_dtype), _epi(grad_w_dtype)
+    dev = x.device
     lib = load()
     if ws is None:
-        ws = torch.empty(lib.megamoe_linear_mxfp4_backward_workspace_size(T, K, N),
-                         dtype=torch.uint8, device=x.device)
-    gx = torch.empty(T, K, dtype=grad_x_dtype, device=x.device) if need_x else None
-    gw = torch.empty(N, K, dtype=grad_w_dtype, device=x.device) if need_w else None
+        ws = torch.empty((lib.megamoe_linear_mxfp4_backward_workspace_size(T, K, N),),
+                         dtype=torch.uint8, device=dev)
+    gx = torch.empty((T, K), dtype=grad_x_dtype, device=dev) if need_x else None
+    gw = torch.empty((N, K), dtype=grad_w_dtype, device=dev) if need_w else None
     _check("megamoe_linear_mxfp4_backward", lib.megamoe_linear_mxfp4_backward(
-        _p(grad_out), TYPES[grad_out.dtype], _row_stride(grad_out), _p(x), TYPES[x.dtype],
-        _row_stride(x), _p(w), TYPES[w.dtype], _row_stride(w), T, K, N, _p(gx), _epi(grad_x_dtype),
-        K, _p(gw), _epi(grad_w_dtype), K, _p(ws), ws.numel(), _stream()))
+        grad_out.data_ptr(), g_code, ld_g, x.data_ptr(), x_code, ld_x, w.data_ptr(), w_code, ld_w,
+        T, K, N, _p(gx), gx_epi, K, _p(gw), gw_epi, K, ws.data_ptr(), ws.numel(), stream))
     return gx, gw, ws
 
 
@@ -921,17 +944,13 @@ class MxForward:
                     scale: float = 1.0, out=None):
         """The whole layer: router_scored_topk over logits [T, E], then the experts."""
         out = self._check_x(x, out)
-        _dev_logits(logits, "logits")
-        if logits.shape != (self.T, self.w.E):
+        T, E, ld, code, stream = _matrix(logits, LOGIT_TYPES, "logits")
+        if T != self.T or E != self.w.E:
             raise ValueError("logits must be [T, E]")
-        if bias is not None:
-            _dev(bias, torch.float32, "bias")
-            if bias.numel() != self.w.E:
-                raise ValueError("bias must have one value per expert")
         _check("megamoe_forward_mxfp4_from_logits", load().megamoe_forward_mxfp4_from_logits(
-            ctypes.byref(self.cw), _p(x), _p(logits), TYPES[logits.dtype], _row_stride(logits),
-            _p(bias), _score(score), n_group, topk_group, group_top, renormalize, scale, self.T,
-            self.k, self.pad, _p(out), self.ws_ptr, self.ws_bytes, _stream()))
+            ctypes.byref(self.cw), x.data_ptr(), logits.data_ptr(), code, ld,
+            _vector(bias, E, "bias"), _score(score), n_group, topk_group, group_top, renormalize,
+            scale, self.T, self.k, self.pad, out.data_ptr(), self.ws_ptr, self.ws_bytes, stream))
         return out[:self.T]
 
     def read_status(self) -> int:
