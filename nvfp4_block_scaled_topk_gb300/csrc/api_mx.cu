@@ -54,61 +54,33 @@ MxOperand take_operand(Carver& c, int64_t rows, int64_t K) {
 }
 
 struct LinearWs {
-  uint8_t* head;  // status word, then the products' counters: cleared first
-  size_t head_bytes;
   uint32_t* status;
-  uint32_t* counters;
   MxOperand x;
-  float* partial;
   size_t bytes;
 };
 LinearWs carve_linear(void* base, int64_t T, int K, int N) {
   Carver c{static_cast<uint8_t*>(base)};
   LinearWs w{};
-  if (mx_linear_few_fits(T, K, N)) {  // one launch, the status word alone
-    w.head = c.take(256);
-    w.status = reinterpret_cast<uint32_t*>(w.head);
-    w.bytes = c.off;
-    return w;
-  }
-  w.head_bytes = 256 + 4 * static_cast<size_t>(mx_product_counters(T, N, K));
-  w.head = c.take(w.head_bytes);
-  w.status = reinterpret_cast<uint32_t*>(w.head);
-  w.counters = w.head ? reinterpret_cast<uint32_t*>(w.head + 256) : nullptr;
-  w.x = take_operand(c, T, K);
-  w.partial = reinterpret_cast<float*>(c.take(mx_product_bytes(T, N, K)));
+  w.status = reinterpret_cast<uint32_t*>(c.take(256));
+  if (!mx_linear_few_fits(T, K, N)) w.x = take_operand(c, T, K);
   w.bytes = c.off;
   return w;
 }
 
 struct BackwardWs {
-  uint8_t* head;
-  size_t head_bytes;
   uint32_t* status;
-  uint32_t* counters_x;
-  uint32_t* counters_w;
   MxOperand dy, dy_t, x_t, w_t;
-  float* partial;
   size_t bytes;
 };
 BackwardWs carve_backward(void* base, int64_t T, int K, int N) {
   Carver c{static_cast<uint8_t*>(base)};
   BackwardWs w{};
   const int64_t R = (T + 31) / 32 * 32;
-  const int nx = mx_product_counters(T, K, N), nw = mx_product_counters(N, K, R);
-  w.head_bytes = 256 + 4 * static_cast<size_t>(nx + nw);
-  w.head = c.take(w.head_bytes);
-  w.status = reinterpret_cast<uint32_t*>(w.head);
-  if (w.head) {
-    w.counters_x = reinterpret_cast<uint32_t*>(w.head + 256);
-    w.counters_w = w.counters_x + nx;
-  }
+  w.status = reinterpret_cast<uint32_t*>(c.take(256));
   w.dy = take_operand(c, T, N);
   w.dy_t = take_operand(c, N, R);
   w.x_t = take_operand(c, K, R);
   w.w_t = take_operand(c, K, N);
-  w.partial = reinterpret_cast<float*>(
-      c.take(std::max(mx_product_bytes(T, K, N), mx_product_bytes(N, K, R))));
   w.bytes = c.off;
   return w;
 }
@@ -364,13 +336,12 @@ megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K,
   if (T > 0 && mx_linear_few_fits(T, K, N))
     return cuda_status(launch_mx_linear_few(x, x_type, T, K, ld_x, w_codes, w_scales, N, out,
                                               out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status, s));
-  cudaError_t e = cudaMemsetAsync(wk.head, 0, std::max<size_t>(wk.head_bytes, 256), s);
+  cudaError_t e = cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s);
   if (e == cudaSuccess)
     e = launch_mx_quantize(quant_of(x, x_type, T, K, ld_x, false, wk.x, wk.status), s);
   if (e == cudaSuccess)
     e = launch_mx_product(MxProduct{wk.x.codes, wk.x.scales, w_codes, w_scales, T, N, K, out,
-                                    out_dtype == MEGAMOE_EPI_F32, ld_out, wk.partial, wk.counters,
-                                    wk.status},
+                                    out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status},
                           s);
   return cuda_status(e);
 }
@@ -402,7 +373,7 @@ megamoe_status megamoe_linear_mxfp4_backward(
   const BackwardWs wk = carve_backward(ws, T, K, N);
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = as_stream(stream);
-  cudaError_t e = cudaMemsetAsync(wk.head, 0, wk.head_bytes, s);
+  cudaError_t e = cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s);
   if (e != cudaSuccess) return MEGAMOE_ERR_CUDA;
   if (T == 0) {  // a sum over nothing
     if (grad_w)
@@ -437,14 +408,13 @@ megamoe_status megamoe_linear_mxfp4_backward(
   e = launch_mx_tiles(jobs, s);
   if (grad_x && e == cudaSuccess)
     e = launch_mx_product(MxProduct{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N,
-                                    grad_x, grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.partial,
-                                    wk.counters_x, wk.status},
+                                    grad_x, grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status},
                           s);
   const int64_t R = (T + 31) / 32 * 32;
   if (grad_w && e == cudaSuccess)
     e = launch_mx_product(MxProduct{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K,
                                     R, grad_w, grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w,
-                                    wk.partial, wk.counters_w, wk.status},
+                                    wk.status},
                           s);
   return cuda_status(e);
 }

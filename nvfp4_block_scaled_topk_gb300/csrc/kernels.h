@@ -28,6 +28,27 @@ inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
+// The same with clusters of `cluster` blocks.
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                      int cluster, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 size_t route_smem_bytes(int E);
 // Routing over many blocks (three passes) from this many slots on, when the
 // caller passes a block_hist scratch of kRouteMaxBlocks * E ints.
@@ -221,12 +242,8 @@ struct MxProduct {
   void* out;
   bool out_f32;
   int64_t ld_out;
-  float* partial;      // mx_product_bytes
-  uint32_t* counters;  // mx_product_counters words, zero
   uint32_t* status;
 };
-size_t mx_product_bytes(int64_t R, int64_t C, int64_t K);
-int mx_product_counters(int64_t R, int64_t C, int64_t K);
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);
 
 // The MXFP4 linear for few tokens in one launch (clears *status first).

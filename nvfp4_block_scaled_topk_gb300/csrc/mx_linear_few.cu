@@ -305,21 +305,8 @@ cudaError_t launch_few(const FewArgs& a, const uint8_t* w_codes, cudaStream_t st
   const int smem = few_bytes(BN, a.K, a.cluster);
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * a.cluster));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = a.cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, codes, a);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>((a.N + 127) / 128 * a.cluster)),
+                            dim3(kThreads), smem, a.cluster, stream, codes, a);
 }
 
 template <typename X>
