@@ -406,16 +406,16 @@ megamoe_status megamoe_linear_mxfp4_backward(
   if (grad_w) add(x, x_type, T, K, ld_x, nullptr, &wk.x_t);
   if (grad_x) add(w, w_type, N, K, ld_w, nullptr, &wk.w_t);
   e = launch_mx_tiles(jobs, s);
-  if (grad_x && e == cudaSuccess)
-    e = launch_mx_product(MxProduct{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N,
-                                    grad_x, grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status},
-                          s);
   const int64_t R = (T + 31) / 32 * 32;
-  if (grad_w && e == cudaSuccess)
-    e = launch_mx_product(MxProduct{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K,
-                                    R, grad_w, grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w,
-                                    wk.status},
-                          s);
+  const MxProduct px{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N, grad_x,
+                     grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status};
+  const MxProduct pw{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K, R, grad_w,
+                     grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w, wk.status};
+  if (e == cudaSuccess) {
+    if (grad_x && grad_w) e = launch_mx_products(px, pw, s);
+    else if (grad_x) e = launch_mx_product(px, s);
+    else if (grad_w) e = launch_mx_product(pw, s);
+  }
   return cuda_status(e);
 }
 

@@ -245,6 +245,8 @@ struct MxProduct {
   uint32_t* status;
 };
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);
+// Two independent products, in one launch where their sizes allow it.
+cudaError_t launch_mx_products(const MxProduct& g, const MxProduct& h, cudaStream_t stream);
 
 // The MXFP4 linear for few tokens in one launch (clears *status first).
 bool mx_linear_few_fits(int64_t T, int64_t K, int64_t N);

@@ -34,7 +34,9 @@ struct MxGemmArgs {
   void* out;
   int64_t ld_out;
   int M, N, K;
+  int out_f32;  // else bf16
   int cluster;  // CTAs that share a tile's K range
+  int n_box;    // rows of an N-side box
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -69,7 +71,13 @@ __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float
 // start and end run under the other's products.
 //
 // FLIP: few output rows (tokens) are the N side, so that no M tile is mostly
-// empty, and the tile is stored transposed.
+// empty, and the tile is stored transposed.  Its box holds only the rows that
+// there are (up to eights): boxes that reach out of the matrix load more slowly
+// (1536 -> 24576 at 17 tokens took longer than at 64).
+//
+// One launch takes one product or two (a linear's two gradients), each split as
+// it would be alone: the launch's cluster is the larger of theirs, and the
+// smaller one's CTAs form groups within it.
 // ---------------------------------------------------------------------------
 template <int BN, bool FLIP>
 struct TileCfg {
@@ -82,7 +90,6 @@ struct TileCfg {
   static constexpr int OFF_SFM = OFF_N + N_TILE;
   static constexpr int OFF_SFN = OFF_SFM + SF;
   static constexpr int STAGE = OFF_SFN + SF;
-  static constexpr uint32_t TX = STAGE;
   static constexpr int COLS = BN + 32 <= 128 ? 128 : 256;  // tensor memory: a power of two
   static constexpr int SMEM = 1024 + STAGES * STAGE;
   // partial sums: rows of the output's row direction, padded against bank conflicts
@@ -97,10 +104,19 @@ struct TileCfg {
 struct TileMaps {
   CUtensorMap m, n, out;
 };
+struct TileJobs {
+  TileMaps maps[2];
+  MxGemmArgs args[2];
+  int first;    // the second product's first block, a multiple of cluster
+  int cluster;  // of the launch
+};
 
-template <int BN, bool FLIP, typename O>
-__global__ void __launch_bounds__(320, 2)
-    k_mx_gemm_tile(const __grid_constant__ TileMaps maps, const MxGemmArgs p) {
+template <int BN, bool FLIP>
+__global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__ TileJobs jobs) {
+  const bool second = static_cast<int>(blockIdx.x) >= jobs.first;
+  const TileMaps& maps = jobs.maps[second ? 1 : 0];
+  const MxGemmArgs& p = jobs.args[second ? 1 : 0];
+  const int block = blockIdx.x - (second ? jobs.first : 0);
   using C = TileCfg<BN, FLIP>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
@@ -113,11 +129,18 @@ __global__ void __launch_bounds__(320, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int S = p.cluster;
-  const int rank = S > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int MT = (p.M + 127) / 128;
-  const int tile = blockIdx.x / S, nt = tile / MT, mt = tile - nt * MT;
+  const int MT = (p.M + 127) / 128, NT = (p.N + BN - 1) / BN;
+  const int tile = block / S, rank = block - tile * S;  // rank within the tile's CTAs
+  const int nt = tile / MT, mt = tile - nt * MT;
   const int KT = (p.K + 255) / 256;
   const int k0 = rank * KT / S, k1 = (rank + 1) * KT / S;
+  if (tile >= MT * NT) {  // fills up the last cluster
+    pdl_wait();
+    pdl_trigger();
+    cluster_sync();
+    cluster_sync();
+    return;
+  }
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -159,7 +182,7 @@ __global__ void __launch_bounds__(320, 2)
           break;
         }
         uint8_t* sb = smem + stage * C::STAGE;
-        mbar_arrive_expect_tx(&full[stage], C::TX);
+        mbar_arrive_expect_tx(&full[stage], C::M_TILE + p.n_box * 128 + 2 * C::SF);
         tma_load_2d(sb, &maps.m, &full[stage], kt * 128, mt * 128, pol);
         tma_load_2d(sb + C::OFF_N, &maps.n, &full[stage], kt * 128, nt * BN, pol);
         bulk_load(sb + C::OFF_SFM, sfm + kt * C::SF, C::SF, &full[stage], pol);
@@ -251,34 +274,34 @@ __global__ void __launch_bounds__(320, 2)
         const int n = nt * BN + half * HALF + c;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          if (done && m < p.M && n + j < p.N)
-            store1(static_cast<O*>(p.out) + (n + j) * p.ld_out + m, __uint_as_float(v[j]));
+          if (done && m < p.M && n + j < p.N) {
+            const int64_t at = (n + j) * p.ld_out + m;
+            if (p.out_f32) store1(static_cast<float*>(p.out) + at, __uint_as_float(v[j]));
+            else store1(static_cast<__nv_bfloat16*>(p.out) + at, __uint_as_float(v[j]));
+          }
       }
     } else {
-      // 128-byte rows through shared memory and out by tensor map
+      // 128-byte rows through shared memory and out by tensor map: 64 columns
+      // of bf16 or 32 of fp32 at a time
       uint8_t* stg = smem + (warp - 2) * 4096;
-      constexpr bool F32 = sizeof(O) == 4;
-      constexpr int COLS = F32 ? 32 : 64;
       const int m = mt * 128 + quarter * 32, n = nt * BN + half * HALF;
+      uint32_t w[32];
 #pragma unroll
-      for (int c = 0; c < HALF; c += COLS) {
-        uint32_t w[32];
+      for (int c = 0; c < HALF; c += 32) {
+        uint32_t v[32];
+        tmem_ld_32x32b_x32(base + c, v);
+        tmem_ld_wait();
+        if (p.out_f32) {
 #pragma unroll
-        for (int i = 0; i < COLS; i += 32) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(base + c + i, v);
-          tmem_ld_wait();
-          if (F32) {
+          for (int j = 0; j < 32; ++j) w[j] = v[j];
+        } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = v[j];
-          } else {
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]),
-                                                             __uint_as_float(v[2 * j + 1]));
-              w[(F32 ? 0 : i / 2) + j] = *reinterpret_cast<const uint32_t*>(&h);
-            }
+          for (int j = 0; j < 16; ++j) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * j]),
+                                                           __uint_as_float(v[2 * j + 1]));
+            w[(c & 32) / 2 + j] = *reinterpret_cast<const uint32_t*>(&h);
           }
+          if ((c & 32) == 0) continue;  // half of the chunk's columns
         }
         if (lane == 0) bulk_store_wait_read();  // the chunk before has left
         __syncwarp();
@@ -288,7 +311,8 @@ __global__ void __launch_bounds__(320, 2)
               make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
         fence_async_shared();
         __syncwarp();
-        if (lane == 0 && done && m < p.M && n + c < p.N) tma_store_2d(&maps.out, stg, n + c, m);
+        const int at = n + (p.out_f32 ? c : c & ~63);
+        if (lane == 0 && done && m < p.M && at < p.N) tma_store_2d(&maps.out, stg, at, m);
       }
       if (lane == 0) bulk_store_wait();
       __syncwarp();
@@ -296,17 +320,17 @@ __global__ void __launch_bounds__(320, 2)
     tc_fence_before();
   }
   __syncthreads();
+  if (jobs.cluster > 1) cluster_sync();
   if (S > 1) {
-    cluster_sync();
+    const uint32_t group = cluster_rank() - rank;  // the tile's first CTA
     const float* part = reinterpret_cast<const float*>(smem);
-    O* out = static_cast<O*>(p.out);
     constexpr int quads = C::INNER / 4;
     const int first = rank * C::OUTER / S, last = (rank + 1) * C::OUTER / S;
     for (int i = first * quads + threadIdx.x; i < last * quads; i += C::THREADS) {
       const int o = i / quads, q = i % quads * 4;
       float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
       for (int r = 0; r < S; ++r) {
-        const float4 v = load_cluster4(part + o * C::PITCH + q, r);
+        const float4 v = load_cluster4(part + o * C::PITCH + q, group + r);
         sum.x += v.x;
         sum.y += v.y;
         sum.z += v.z;
@@ -314,33 +338,54 @@ __global__ void __launch_bounds__(320, 2)
       }
       // rows and columns of the output; whole fours along it
       const int r = (FLIP ? nt * BN : mt * 128) + o, c = (FLIP ? mt * 128 : nt * BN) + q;
-      if (r < (FLIP ? p.N : p.M) && c < (FLIP ? p.M : p.N)) store4(out + r * p.ld_out + c, sum);
+      if (r < (FLIP ? p.N : p.M) && c < (FLIP ? p.M : p.N)) {
+        if (p.out_f32) store4(static_cast<float*>(p.out) + r * p.ld_out + c, sum);
+        else store4(static_cast<__nv_bfloat16*>(p.out) + r * p.ld_out + c, sum);
+      }
     }
-    cluster_sync();  // no CTA leaves while another reads its sums
   }
+  if (jobs.cluster > 1) cluster_sync();  // no CTA leaves while another reads its sums
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::COLS);
   }
 }
 
-template <int BN, bool FLIP, typename O>
-cudaError_t launch_tile(const MxGemmArgs& a, const uint8_t* m_codes, const uint8_t* n_codes,
-                        int tiles, cudaStream_t stream) {
+// A product as its kernel sees it.
+struct MxJob {
+  MxGemmArgs a;
+  const uint8_t* m_codes;
+  const uint8_t* n_codes;
+  int tiles;
+};
+
+template <int BN, bool FLIP>
+cudaError_t launch_tiles(const MxJob* jobs, int count, cudaStream_t stream) {
   using C = TileCfg<BN, FLIP>;
-  TileMaps maps;
-  const uint64_t row = static_cast<uint64_t>(a.K) / 2, m = a.M, n = a.N;
-  const auto type = sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  if (!make_codes_map(&maps.m, m_codes, m, row, 128) || !make_codes_map(&maps.n, n_codes, n, row, BN) ||
-      !make_map(&maps.out, type, a.out, FLIP ? m : n, FLIP ? n : m,
-                static_cast<uint64_t>(a.ld_out) * sizeof(O), 128 / sizeof(O), 32,
-                CU_TENSOR_MAP_SWIZZLE_128B))
-    return cudaErrorInvalidValue;
-  auto kern = k_mx_gemm_tile<BN, FLIP, O>;
+  TileJobs t{};
+  t.cluster = jobs[0].a.cluster;
+  if (count == 2) t.cluster = std::max(t.cluster, jobs[1].a.cluster);
+  int blocks = 0;
+  for (int i = 0; i < count; ++i) {
+    const MxJob& j = jobs[i];
+    const uint64_t row = static_cast<uint64_t>(j.a.K) / 2, m = j.a.M, n = j.a.N;
+    const int size = j.a.out_f32 ? 4 : 2;
+    t.args[i] = j.a;
+    t.args[i].n_box = static_cast<int>(std::min<uint64_t>(BN, (n + 7) / 8 * 8));
+    if (!make_codes_map(&t.maps[i].m, j.m_codes, m, row, 128) ||
+        !make_codes_map(&t.maps[i].n, j.n_codes, n, row, t.args[i].n_box) ||
+        !make_map(&t.maps[i].out,
+                  size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  j.a.out, FLIP ? m : n, FLIP ? n : m, static_cast<uint64_t>(j.a.ld_out) * size,
+                  128 / size, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    blocks += (j.tiles * j.a.cluster + t.cluster - 1) / t.cluster * t.cluster;
+    if (i == 0) t.first = blocks;
+  }
+  auto kern = k_mx_gemm_tile<BN, FLIP>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl_cluster(kern, dim3(tiles * a.cluster), dim3(C::THREADS), C::SMEM, a.cluster,
-                            stream, maps, a);
+  return launch_pdl_cluster(kern, dim3(blocks), dim3(C::THREADS), C::SMEM, t.cluster, stream, t);
 }
 
 // ---------------------------------------------------------------------------
@@ -589,14 +634,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
 }
 
 template <typename O>
-cudaError_t launch_pair(const MxGemmArgs& a, const uint8_t* m_codes, const uint8_t* n_codes,
-                        int tiles, cudaStream_t stream) {
+cudaError_t launch_pair(const MxJob& j, cudaStream_t stream) {
+  const MxGemmArgs& a = j.a;
   PairMaps maps;
   const uint64_t row = static_cast<uint64_t>(a.K) / 2;
   const uint64_t sf_row = static_cast<uint64_t>(mx_atoms(a.K)) * 512;
   const uint64_t m = a.M, n = a.N;
-  if (!make_codes_map(&maps.m, m_codes, m, row, 128) ||
-      !make_codes_map(&maps.n, n_codes, n, row, 128) ||
+  if (!make_codes_map(&maps.m, j.m_codes, m, row, 128) ||
+      !make_codes_map(&maps.n, j.n_codes, n, row, 128) ||
       !make_map(&maps.sfm, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.m_sf, sf_row / 4, (m + 127) / 128,
                 sf_row, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !make_map(&maps.sfn, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.n_sf, sf_row / 4, (n + 127) / 128,
@@ -610,7 +655,7 @@ cudaError_t launch_pair(const MxGemmArgs& a, const uint8_t* m_codes, const uint8
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(2 * std::min(num_sms() / 2, tiles)), dim3(PairCfg::THREADS),
+  return launch_pdl(kern, dim3(2 * std::min(num_sms() / 2, j.tiles)), dim3(PairCfg::THREADS),
                     PairCfg::SMEM, stream, maps, a);
 }
 
@@ -620,6 +665,23 @@ struct MxPlan {
   bool flip;  // output rows on the N side (tiles of 128 x 64)
   int tiles, cluster;
 };
+
+// CTAs that share a tile's K range, so that idle SMs take part: the steps of the
+// slowest SM, about four steps' time of start and end, and two more for the sums
+// over a cluster.
+int pick_cluster(int64_t tiles, int64_t steps) {
+  const double sms = num_sms();
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= 8 && s <= steps; s *= 2) {
+    const double cost = std::max(1.0, tiles * s / sms) * steps / s + (s > 1 ? 6.0 : 4.0);
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
 
 MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
   MxPlan p{};
@@ -634,19 +696,27 @@ MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
     return p;
   }
   p.tiles = static_cast<int>(p.flip ? (C + 127) / 128 : (R + 127) / 128 * ((C + 127) / 128));
-  // idle SMs share the K ranges: steps of the slowest SM, and about four steps'
-  // time of start and end, two more for the sums over a cluster
-  const int steps = static_cast<int>((K + 255) / 256);
-  double least = 1e30;
-  for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-    const double cost = std::max(1.0, static_cast<double>(p.tiles) * s / sms) * steps / s +
-                        (s > 1 ? 6.0 : 4.0);
-    if (cost < least) {
-      least = cost;
-      p.cluster = s;
-    }
-  }
+  p.cluster = pick_cluster(p.tiles, (K + 255) / 256);
   return p;
+}
+
+MxJob job_of(const MxProduct& g, const MxPlan& p) {
+  MxJob j{};
+  j.m_codes = p.flip ? g.c_codes : g.r_codes;
+  j.n_codes = p.flip ? g.r_codes : g.c_codes;
+  j.tiles = p.tiles;
+  j.a.m_sf = p.flip ? g.c_scales : g.r_scales;
+  j.a.n_sf = p.flip ? g.r_scales : g.c_scales;
+  j.a.out = g.out;
+  j.a.ld_out = g.ld_out;
+  j.a.M = static_cast<int>(p.flip ? g.C : g.R);
+  j.a.N = static_cast<int>(p.flip ? g.R : g.C);
+  j.a.K = static_cast<int>(g.K);
+  j.a.out_f32 = g.out_f32;
+  j.a.cluster = p.cluster;
+  j.a.status = g.status;
+  j.a.wait_limit_ns = wait_limit_ns();
+  return j;
 }
 
 }  // namespace
@@ -654,26 +724,20 @@ MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
   if (g.R == 0 || g.C == 0) return cudaSuccess;
   const MxPlan p = plan_product(g.R, g.C, g.K);
-  const uint8_t* m_codes = p.flip ? g.c_codes : g.r_codes;
-  const uint8_t* n_codes = p.flip ? g.r_codes : g.c_codes;
-  MxGemmArgs a{};
-  a.m_sf = p.flip ? g.c_scales : g.r_scales;
-  a.n_sf = p.flip ? g.r_scales : g.c_scales;
-  a.out = g.out;
-  a.ld_out = g.ld_out;
-  a.M = static_cast<int>(p.flip ? g.C : g.R);
-  a.N = static_cast<int>(p.flip ? g.R : g.C);
-  a.K = static_cast<int>(g.K);
-  a.cluster = p.cluster;
-  a.status = g.status;
-  a.wait_limit_ns = wait_limit_ns();
-  auto run = [&](auto out) {
-    using O = decltype(out);
-    if (p.pair) return launch_pair<O>(a, m_codes, n_codes, p.tiles, stream);
-    return p.flip ? launch_tile<64, true, O>(a, m_codes, n_codes, p.tiles, stream)
-                  : launch_tile<128, false, O>(a, m_codes, n_codes, p.tiles, stream);
-  };
-  return g.out_f32 ? run(float{}) : run(__nv_bfloat16{});
+  const MxJob j = job_of(g, p);
+  if (p.pair)
+    return g.out_f32 ? launch_pair<float>(j, stream) : launch_pair<__nv_bfloat16>(j, stream);
+  return p.flip ? launch_tiles<64, true>(&j, 1, stream) : launch_tiles<128, false>(&j, 1, stream);
+}
+
+cudaError_t launch_mx_products(const MxProduct& g, const MxProduct& h, cudaStream_t stream) {
+  const MxPlan p = plan_product(g.R, g.C, g.K), q = plan_product(h.R, h.C, h.K);
+  if (p.pair || p.flip || q.pair || q.flip || g.R == 0 || h.R == 0) {
+    const cudaError_t e = launch_mx_product(g, stream);
+    return e != cudaSuccess ? e : launch_mx_product(h, stream);
+  }
+  const MxJob jobs[2] = {job_of(g, p), job_of(h, q)};
+  return launch_tiles<128, false>(jobs, 2, stream);
 }
 
 }  // namespace megamoe

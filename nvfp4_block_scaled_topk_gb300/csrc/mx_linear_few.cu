@@ -322,14 +322,14 @@ cudaError_t launch_typed(const FewArgs& a, const uint8_t* w_codes, bool f32, cud
 
 // Each CTA quantises the part of x that it needs, so an SM's share of that work
 // grows with T and with the K steps u of weights that it streams; beyond
-// T u = 100 + 3.5 u quantising once, in a kernel before the product, is faster.
+// T u = 100 + 4 u quantising once, in a kernel before the product, is faster.
 // Measured (this form / that form, us): 7168 -> 1536, u = 2.2: 10.0 / 12.4 at 32
 // tokens; 1536 -> 24576, u = 7.6: 13.9 / 14.4 at 16, 20.5 / 13.4 at 32;
 // 7168 -> 16384, u = 23.6: 20.3 / 20.6 at 8, 28.3 / 21.9 at 16.
 bool mx_linear_few_fits(int64_t T, int64_t K, int64_t N) {
   if (T > 32) return false;
   const double u = static_cast<double>((K + 255) / 256 * ((N + 127) / 128)) / num_sms();
-  return static_cast<double>(T) * u <= 100.0 + 3.5 * u &&
+  return static_cast<double>(T) * u <= 100.0 + 4.0 * u &&
          few_bytes(T <= 16 ? 16 : 32, K, few_cluster(N, K)) <= 226 * 1024;
 }
 
