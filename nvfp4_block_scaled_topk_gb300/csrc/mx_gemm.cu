@@ -666,15 +666,16 @@ struct MxPlan {
   int tiles, cluster;
 };
 
-// CTAs that share a tile's K range, so that idle SMs take part: the steps of the
-// slowest SM, about four steps' time of start and end, and two more for the sums
-// over a cluster.
-int pick_cluster(int64_t tiles, int64_t steps) {
-  const double sms = num_sms();
+// CTAs that share a tile's K range, where SMs would idle: a cluster's sums cost
+// as much as `sums` K steps, and more CTAs than SMs take turns.  Measured (us, 1
+// / 2 / 4 / 8 CTAs): 128 x 7168 -> 1536 15.5 / 14.4 / 12.4 / 12.4; 512 x 7168 ->
+// 2048 16.5 / 16.5 / 17.4 / 26.8; 333 x 1536 -> 2048 10.4 / 12.4 / 13.5 / 13.5;
+// flipped, 64 x 7168 -> 1536 16.5 / 14.0 / 11.8 / 11.2.
+int pick_cluster(int64_t tiles, int64_t steps, double sums) {
   int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= 8 && s <= steps; s *= 2) {
-    const double cost = std::max(1.0, tiles * s / sms) * steps / s + (s > 1 ? 6.0 : 4.0);
+  double least = static_cast<double>(steps);
+  for (int s = 2; s <= 8 && s <= steps && tiles * s <= num_sms(); s *= 2) {
+    const double cost = static_cast<double>(steps) / s + sums;
     if (cost < least) {
       least = cost;
       best = s;
@@ -685,18 +686,21 @@ int pick_cluster(int64_t tiles, int64_t steps) {
 
 MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
   MxPlan p{};
-  const int sms = num_sms();
   const int64_t pairs = (R + 255) / 256 * ((C + 255) / 256);
+  const int64_t tiles = (R + 127) / 128 * ((C + 127) / 128);
   p.flip = R <= 64;
   p.cluster = 1;
-  // pairs load a third less for the same product, but want a tile each
-  p.pair = !p.flip && pairs * 2 >= sms;
+  // A pair takes four tiles' worth in the time that an SM takes one of its own
+  // tiles (operands per product halved), so it is chosen where it has enough to
+  // do and pads to less than twice the tiles: 128 x 1536 -> 24576 took 24.8 us
+  // in pairs, half of them empty.
+  p.pair = !p.flip && pairs * 2 >= num_sms() && pairs * 4 < tiles * 2;
   if (p.pair) {
     p.tiles = static_cast<int>(pairs);
     return p;
   }
-  p.tiles = static_cast<int>(p.flip ? (C + 127) / 128 : (R + 127) / 128 * ((C + 127) / 128));
-  p.cluster = pick_cluster(p.tiles, (K + 255) / 256);
+  p.tiles = static_cast<int>(p.flip ? (C + 127) / 128 : tiles);
+  p.cluster = pick_cluster(p.tiles, (K + 255) / 256, p.flip ? 6.0 : 13.0);
   return p;
 }
 
