@@ -17,8 +17,9 @@
 // warp 1 tensor-memory allocator and MMA issuer, warps 2..7 quantise x, warps
 // 4..7 then drain the accumulator.
 //
-// 7168 -> 1536: 12.4 us before (status clear, quantiser and product, three
-// launches) at 1 to 32 tokens.
+// 7168 -> 1536 (5.8 MB of weights, 0.9 us at the copy's bandwidth): 4.7 us at one
+// token, 7.4 at 16, against 12.4 as three launches (status, quantiser, product);
+// 1536 -> 24576 (20 MB, 3.0 us): 4.5 us at one token.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -272,16 +273,18 @@ __global__ void __launch_bounds__(kThreads) k_mx_linear_few(const __grid_constan
   }
 }
 
-// CTAs of a cluster: the split that finishes first, counting for each CTA a
-// fixed cost of about two and a half K steps and that an SM takes its CTAs in
-// turn (the weights' stream bounds them together).
-int few_cluster(int64_t N, int64_t K) {
-  const int64_t mt = (N + 127) / 128, steps = (K + 255) / 256, sms = num_sms();
+// CTAs of a cluster, where SMs would idle: a K step of weights and of x's
+// quantisation (dearer with more tokens) against a cluster's start and sums,
+// about three and a half steps.  Measured (us, 1 / 2 / 4 / 8 CTAs) at one token:
+// 7168 -> 1536 9.0 / 7.1 / 5.6 / 4.7; 1024 -> 1024 3.3 / 4.0 / 3.8; more CTAs than
+// SMs: 1536 -> 24576 4.5 / 9.0 / 14.0.
+int few_cluster(int64_t T, int64_t N, int64_t K) {
+  const int64_t mt = (N + 127) / 128, steps = (K + 255) / 256;
+  const double step = 1.0 + static_cast<double>(T) / 8;
   int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= kMaxCluster && s <= steps; s *= 2) {
-    const double cost = static_cast<double>((mt * s + sms - 1) / sms) *
-                        (static_cast<double>(steps) / s + 2.5);
+  double least = step * steps;
+  for (int s = 2; s <= kMaxCluster && s <= steps && mt * s <= num_sms(); s *= 2) {
+    const double cost = step * steps / s + 3.5;
     if (cost < least) {
       least = cost;
       best = s;
@@ -320,17 +323,17 @@ cudaError_t launch_typed(const FewArgs& a, const uint8_t* w_codes, bool f32, cud
 
 }  // namespace
 
-// Each CTA quantises the part of x that it needs, so an SM's share of that work
-// grows with T and with the K steps u of weights that it streams; beyond
-// T u = 100 + 4 u quantising once, in a kernel before the product, is faster.
-// Measured (this form / that form, us): 7168 -> 1536, u = 2.2: 10.0 / 12.4 at 32
-// tokens; 1536 -> 24576, u = 7.6: 13.9 / 14.4 at 16, 20.5 / 13.4 at 32;
-// 7168 -> 16384, u = 23.6: 20.3 / 20.6 at 8, 28.3 / 21.9 at 16.
+// Each CTA quantises the part of x that it needs: T tokens by its K steps.
+// Beyond T (steps / cluster) = 90 + 4 steps, quantising once in a kernel before
+// the product is faster.  Measured (this form / that form, us): 7168 -> 1536 at 32
+// tokens 9.9 / 11; 1536 -> 24576 at 16 9.1 / 12.4; 2048 -> 7168 at 16 7.7 / 10.4, at
+// 32 11.3 / 10.4; 7168 -> 16384 at 8 20.3 / 20.6.
 bool mx_linear_few_fits(int64_t T, int64_t K, int64_t N) {
   if (T > 32) return false;
-  const double u = static_cast<double>((K + 255) / 256 * ((N + 127) / 128)) / num_sms();
-  return static_cast<double>(T) * u <= 100.0 + 4.0 * u &&
-         few_bytes(T <= 16 ? 16 : 32, K, few_cluster(N, K)) <= 226 * 1024;
+  const int64_t steps = (K + 255) / 256;
+  const int cluster = few_cluster(T, N, K);
+  return T * steps / cluster <= 90 + 4 * steps &&
+         few_bytes(T <= 16 ? 16 : 32, K, cluster) <= 226 * 1024;
 }
 
 cudaError_t launch_mx_linear_few(const void* x, int x_type, int64_t T, int K, int64_t ld_x,
@@ -339,7 +342,7 @@ cudaError_t launch_mx_linear_few(const void* x, int x_type, int64_t T, int K, in
                                  cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
   const FewArgs a{x,   ld_x,   static_cast<int>(T),  K,      N,
-                  scales, out, ld_out, few_cluster(N, K), status, wait_limit_ns()};
+                  scales, out, ld_out, few_cluster(T, N, K), status, wait_limit_ns()};
   switch (x_type) {
     case MEGAMOE_TYPE_BF16: return launch_typed<__nv_bfloat16>(a, codes, out_f32, stream);
     case MEGAMOE_TYPE_F16: return launch_typed<__half>(a, codes, out_f32, stream);
