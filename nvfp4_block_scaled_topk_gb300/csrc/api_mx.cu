@@ -55,6 +55,7 @@ MxOperand take_operand(Carver& c, int64_t rows, int64_t K) {
 
 struct LinearWs {
   uint32_t* status;
+  uint32_t* flags;  // of the quantising launch
   MxOperand x;
   size_t bytes;
 };
@@ -62,13 +63,17 @@ LinearWs carve_linear(void* base, int64_t T, int K, int N) {
   Carver c{static_cast<uint8_t*>(base)};
   LinearWs w{};
   w.status = reinterpret_cast<uint32_t*>(c.take(256));
-  if (!mx_linear_few_fits(T, K, N)) w.x = take_operand(c, T, K);
+  if (!mx_linear_few_fits(T, K, N)) {
+    w.flags = reinterpret_cast<uint32_t*>(c.take(4 * static_cast<size_t>(mx_flags_words())));
+    w.x = take_operand(c, T, K);
+  }
   w.bytes = c.off;
   return w;
 }
 
 struct BackwardWs {
   uint32_t* status;
+  uint32_t* flags;
   MxOperand dy, dy_t, x_t, w_t;
   size_t bytes;
 };
@@ -77,6 +82,7 @@ BackwardWs carve_backward(void* base, int64_t T, int K, int N) {
   BackwardWs w{};
   const int64_t R = (T + 31) / 32 * 32;
   w.status = reinterpret_cast<uint32_t*>(c.take(256));
+  w.flags = reinterpret_cast<uint32_t*>(c.take(4 * static_cast<size_t>(mx_flags_words())));
   w.dy = take_operand(c, T, N);
   w.dy_t = take_operand(c, N, R);
   w.x_t = take_operand(c, K, R);
@@ -94,8 +100,9 @@ bool linear_sizes_ok(int64_t T, int K, int N) {
 }
 
 MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool transpose,
-                 const MxOperand& o, uint32_t* status) {
-  return MxQuant{x, type, rows, ld, K, transpose, o.codes, o.scales, MEGAMOE_SCALES_MMA, status};
+                 const MxOperand& o, uint32_t* status, uint32_t* flags) {
+  return MxQuant{x, type, rows, ld, K, transpose, o.codes, o.scales, MEGAMOE_SCALES_MMA, status,
+                 flags};
 }
 
 // Workspace of the MXFP4 forward.
@@ -288,7 +295,7 @@ megamoe_status megamoe_quantize_mxfp4(const void* x, int x_type, int64_t rows, i
   if (rows > 0 && (!vectors_ok(x, ld, size) || !aligned(codes, 16)))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   return cuda_status(launch_mx_quantize(
-      MxQuant{x, x_type, rows, ld, K, transpose != 0, codes, scales, scale_layout, status},
+      MxQuant{x, x_type, rows, ld, K, transpose != 0, codes, scales, scale_layout, status, nullptr},
       as_stream(stream)));
 }
 
@@ -336,12 +343,14 @@ megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K,
   if (T > 0 && mx_linear_few_fits(T, K, N))
     return cuda_status(launch_mx_linear_few(x, x_type, T, K, ld_x, w_codes, w_scales, N, out,
                                               out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status, s));
-  cudaError_t e = cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s);
-  if (e == cudaSuccess)
-    e = launch_mx_quantize(quant_of(x, x_type, T, K, ld_x, false, wk.x, wk.status), s);
+  if (T == 0) return cuda_status(cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s));
+  int blocks = 0;
+  cudaError_t e = launch_mx_quantize(
+      quant_of(x, x_type, T, K, ld_x, false, wk.x, wk.status, wk.flags), s, &blocks);
   if (e == cudaSuccess)
     e = launch_mx_product(MxProduct{wk.x.codes, wk.x.scales, w_codes, w_scales, T, N, K, out,
-                                    out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status},
+                                    out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status, wk.flags,
+                                    blocks},
                           s);
   return cuda_status(e);
 }
@@ -373,10 +382,10 @@ megamoe_status megamoe_linear_mxfp4_backward(
   const BackwardWs wk = carve_backward(ws, T, K, N);
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
   cudaStream_t s = as_stream(stream);
-  cudaError_t e = cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s);
-  if (e != cudaSuccess) return MEGAMOE_ERR_CUDA;
-  if (T == 0) {  // a sum over nothing
-    if (grad_w)
+  cudaError_t e = cudaSuccess;
+  if (T == 0 || (!grad_x && !grad_w)) {  // sums over nothing
+    e = cudaMemsetAsync(wk.status, 0, sizeof(uint32_t), s);
+    if (e == cudaSuccess && grad_w)
       e = cudaMemset2DAsync(grad_w, ld_grad_w * gw_size, 0, K * gw_size, N, s);
     return cuda_status(e);
   }
@@ -399,18 +408,20 @@ megamoe_status megamoe_linear_mxfp4_backward(
       t.col_scales = col->scales;
     }
     t.col_layout = MEGAMOE_SCALES_MMA;
-    t.status = wk.status;
   };
-  if (grad_x || grad_w)
-    add(grad_out, grad_type, T, N, ld_grad, grad_x ? &wk.dy : nullptr, grad_w ? &wk.dy_t : nullptr);
+  jobs.status = wk.status;
+  jobs.flags = wk.flags;
+  add(grad_out, grad_type, T, N, ld_grad, grad_x ? &wk.dy : nullptr, grad_w ? &wk.dy_t : nullptr);
   if (grad_w) add(x, x_type, T, K, ld_x, nullptr, &wk.x_t);
   if (grad_x) add(w, w_type, N, K, ld_w, nullptr, &wk.w_t);
-  e = launch_mx_tiles(jobs, s);
+  int blocks = 0;
+  e = launch_mx_tiles(jobs, s, &blocks);
   const int64_t R = (T + 31) / 32 * 32;
   const MxProduct px{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N, grad_x,
-                     grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status};
+                     grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status, wk.flags, blocks};
   const MxProduct pw{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K, R, grad_w,
-                     grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w, wk.status};
+                     grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w, wk.status, wk.flags,
+                     grad_x ? 0 : blocks};
   if (e == cudaSuccess) {
     if (grad_x && grad_w) e = launch_mx_products(px, pw, s);
     else if (grad_x) e = launch_mx_product(px, s);

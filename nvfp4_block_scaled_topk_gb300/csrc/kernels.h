@@ -199,8 +199,10 @@ struct MxQuant {
   uint8_t* scales;
   int layout;  // MEGAMOE_SCALES_*
   uint32_t* status;
+  uint32_t* flags;  // one word a block for the product that follows, or null
 };
-cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s);
+// blocks (may be null): blocks of the launch, the words of flags.
+cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s, int* blocks = nullptr);
 // Matrices quantised tile by tile in one launch, each along its columns (codes
 // of x^T), along its rows (atom layout of the scales), or both from one read.
 struct MxTile {
@@ -213,15 +215,18 @@ struct MxTile {
   uint8_t* col_codes;  // null: not along the columns
   uint8_t* col_scales;
   int col_layout;
-  uint32_t* status;
   int first, col_tiles;  // set by the launch
 };
 struct MxTiles {
   MxTile job[3];
   int count;
+  uint32_t* status;
+  uint32_t* flags;  // as MxQuant::flags
   int tiles;  // set by the launch
 };
-cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s);
+// Most words that a quantising launch leaves in its flags.
+int mx_flags_words();
+cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s, int* blocks = nullptr);
 // x [T, d] bf16 into routed rows slot_dst[t k + j] (routed scale layout).
 cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t* slot_dst, int k,
                              uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s);
@@ -243,6 +248,9 @@ struct MxProduct {
   bool out_f32;
   int64_t ld_out;
   uint32_t* status;
+  // findings of the quantising launch before it, for the status word
+  const uint32_t* flags;
+  int flag_count;
 };
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);
 // Two independent products, in one launch where their sizes allow it.

@@ -38,6 +38,8 @@ struct MxGemmArgs {
   int cluster;  // CTAs that share a tile's K range
   int n_box;    // rows of an N-side box
   uint32_t* status;
+  const uint32_t* flags;  // of the quantising launch before it (collect_flags)
+  int flag_count;
   uint64_t wait_limit_ns;
 };
 
@@ -243,6 +245,7 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
     const int quarter = warp & 3, half = warp >= 6 ? 1 : 0;
     const int row = quarter * 32 + lane;
     constexpr int HALF = BN / 2;
+    if (block == 0) collect_flags(p.flags, p.flag_count, threadIdx.x - 64, 256, p.status);
     done = mbar_wait(&acc_full, 0, abort_flag, p.status, p.wait_limit_ns);
     tc_fence_after();
     const uint32_t base = tmem + half * HALF + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -479,7 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
     if (lane == 0) {
       // ------------------------------------------------------------ producer
       const uint64_t pol = policy_evict_normal();
-      int stage = 0, issued = 0;
+      int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
@@ -497,25 +500,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
           tma_load_2d_pair(sb + C::OFF_N, &maps.n, bar, kt * 128, n0 + rank * 128, pol);
           tma_load_2d_pair(sb + C::OFF_SFM, &maps.sfm, bar, kt * 256, m0 >> 7, pol);
           tma_load_2d_pair(sb + C::OFF_SFN, &maps.sfn, bar, kt * 256, n0 >> 7, pol);
-          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) {  // unwinding: let the copies in flight land first
-        if (rank == 0) {
-          for (int s = 0; s < STAGES && s < issued; ++s) {
-            const int i = issued - 1 - s;
-            mbar_drain(&full[i % STAGES], static_cast<uint32_t>(i / STAGES) & 1u);
-          }
-        } else {
-          // rank 1's complete on rank 0's barriers, which may have moved on:
-          // wait a time that no copy takes
-          const uint64_t t0 = globaltimer();
-          while (globaltimer() - t0 < 5000000) __nanosleep(1000);
-        }
+      if (!ok) {
+        // unwinding: let the copies in flight land first.  A stage's barrier
+        // counts both CTAs' copies and may never complete when one stopped
+        // before the other, so wait a time that no copy takes.
+        const uint64_t t0 = globaltimer();
+        while (globaltimer() - t0 < 5000000) __nanosleep(1000);
       }
     }
     __syncwarp();
@@ -578,6 +574,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
     uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
     constexpr bool F32 = sizeof(O) == 4;
     constexpr int COLS = F32 ? 32 : 64;  // columns of a staged chunk
+    if (blockIdx.x == 0) collect_flags(p.flags, p.flag_count, threadIdx.x - 64, 256, p.status);
     uint32_t acc_phase = 0;
     for (int q = first; q < total; q += step) {
       const int nt = q / MT, mt = q - nt * MT;
@@ -719,6 +716,8 @@ MxJob job_of(const MxProduct& g, const MxPlan& p) {
   j.a.out_f32 = g.out_f32;
   j.a.cluster = p.cluster;
   j.a.status = g.status;
+  j.a.flags = g.flags;
+  j.a.flag_count = g.flag_count;
   j.a.wait_limit_ns = wait_limit_ns();
   return j;
 }

@@ -45,7 +45,7 @@ constexpr int kRowSteps = 4;
 template <typename X>
 __global__ void __launch_bounds__(256)
     k_mx_rows(const X* __restrict__ x, int64_t rows, int K, int64_t ld, uint8_t* __restrict__ codes,
-              uint8_t* __restrict__ scales, int layout, uint32_t* status) {
+              uint8_t* __restrict__ scales, int layout, uint32_t* status, uint32_t* flags) {
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256)
     if (b < end) scales[scale_offset(layout, r, b, K)] = static_cast<uint8_t>(mine);
     bad |= mine == kMxNan;
   }
-  if (bad) set_status(status, MEGAMOE_DEV_NONFINITE);
+  report_nonfinite(bad, status, flags);
 }
 
 // Along columns: codes [K, R / 2] and scales of x^T, R = rows up to a multiple
@@ -146,7 +146,7 @@ __device__ __forceinline__ void load_tile(const MxTile& job, int row_tile, int c
 }
 
 template <typename X>
-__device__ __forceinline__ void encode_tile(const MxTile& job, int row_tile, int col_tile,
+__device__ __forceinline__ bool encode_tile(const MxTile& job, int row_tile, int col_tile,
                                             const uint8_t* buf, uint8_t* s_codes) {
   using W = Word<X>;
   const X* tile = reinterpret_cast<const X*>(buf);  // [kTileRows][kTileCols]
@@ -247,7 +247,7 @@ __device__ __forceinline__ void encode_tile(const MxTile& job, int row_tile, int
                                             ((part ^ (col / W::NC % blocks)) * 16));
     }
   }
-  if (bad) set_status(job.status, MEGAMOE_DEV_NONFINITE);
+  return bad;
 }
 
 // Up to three matrices in one launch; tile t belongs to the last job whose
@@ -271,6 +271,7 @@ __global__ void __launch_bounds__(256, 3) k_mx_tiles(const __grid_constant__ MxT
     });
   };
   int turn = 0;
+  bool bad = false;
   if (static_cast<int>(blockIdx.x) < jobs.tiles) load(blockIdx.x, s_raw);
   asm volatile("cp.async.commit_group;" ::: "memory");
   for (int tile = blockIdx.x; tile < jobs.tiles; tile += gridDim.x, turn ^= 1) {
@@ -282,12 +283,13 @@ __global__ void __launch_bounds__(256, 3) k_mx_tiles(const __grid_constant__ MxT
     const uint8_t* buf = s_raw + turn * kTileBytes;
     uint8_t* s_codes = s_raw + 2 * kTileBytes;
     with(tile, [&](const MxTile& job, int r, int c) {
-      if (WIDE && job.type == MEGAMOE_TYPE_F32) encode_tile<float>(job, r, c, buf, s_codes);
-      else if (job.type == MEGAMOE_TYPE_F16) encode_tile<__half>(job, r, c, buf, s_codes);
-      else encode_tile<__nv_bfloat16>(job, r, c, buf, s_codes);
+      if (WIDE && job.type == MEGAMOE_TYPE_F32) bad |= encode_tile<float>(job, r, c, buf, s_codes);
+      else if (job.type == MEGAMOE_TYPE_F16) bad |= encode_tile<__half>(job, r, c, buf, s_codes);
+      else bad |= encode_tile<__nv_bfloat16>(job, r, c, buf, s_codes);
     });
     __syncthreads();  // the tile and the codes are free again
   }
+  report_nonfinite(bad, jobs.status, jobs.flags);
 }
 
 // Token rows into their routed rows: slot j of token t goes to row
@@ -420,17 +422,19 @@ unsigned blocks_for(int64_t tasks, int64_t per_block) {
 }
 
 template <typename X>
-cudaError_t quantize_rows(const MxQuant& q, cudaStream_t s) {
+cudaError_t quantize_rows(const MxQuant& q, cudaStream_t s, int* blocks) {
   const int64_t tasks = q.rows * ((q.K + 1023) / 1024);
   // enough blocks for every task at small sizes, several tasks a warp at large ones
-  return launch_pdl(k_mx_rows<X>, dim3(blocks_for(tasks, 8)), dim3(256), 0, s,
+  const unsigned n = blocks_for(tasks, 8);
+  if (blocks) *blocks = static_cast<int>(n);
+  return launch_pdl(k_mx_rows<X>, dim3(n), dim3(256), 0, s,
                     static_cast<const X*>(q.x), q.rows, q.K, q.ld, q.codes, q.scales, q.layout,
-                    q.status);
+                    q.status, q.flags);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s) {
+cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s, int* blocks) {
   jobs.tiles = 0;
   bool wide = false;
   for (int j = 0; j < jobs.count; ++j) {
@@ -453,10 +457,14 @@ cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   // three blocks an SM by shared memory
-  return launch_pdl(kern, dim3(std::min(jobs.tiles, 3 * num_sms())), dim3(256), smem, s, jobs);
+  const int n = std::min(jobs.tiles, 3 * num_sms());
+  if (blocks) *blocks = n;
+  return launch_pdl(kern, dim3(n), dim3(256), smem, s, jobs);
 }
 
-cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s) {
+int mx_flags_words() { return num_sms() * 16; }
+
+cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s, int* blocks) {
   if (q.rows == 0) return cudaSuccess;
   if (q.transpose) {
     MxTiles jobs{};
@@ -469,13 +477,14 @@ cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s) {
     jobs.job[0].col_codes = q.codes;
     jobs.job[0].col_scales = q.scales;
     jobs.job[0].col_layout = q.layout;
-    jobs.job[0].status = q.status;
-    return launch_mx_tiles(jobs, s);
+    jobs.status = q.status;
+    jobs.flags = q.flags;
+    return launch_mx_tiles(jobs, s, blocks);
   }
   switch (q.type) {
-    case MEGAMOE_TYPE_BF16: return quantize_rows<__nv_bfloat16>(q, s);
-    case MEGAMOE_TYPE_F16: return quantize_rows<__half>(q, s);
-    default: return quantize_rows<float>(q, s);
+    case MEGAMOE_TYPE_BF16: return quantize_rows<__nv_bfloat16>(q, s, blocks);
+    case MEGAMOE_TYPE_F16: return quantize_rows<__half>(q, s, blocks);
+    default: return quantize_rows<float>(q, s, blocks);
   }
 }
 

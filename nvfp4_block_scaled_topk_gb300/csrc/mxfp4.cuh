@@ -53,6 +53,32 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
   return inv != 0.f ? c : 0u;
 }
 
+// What a quantising kernel found, for a status word.  Alone it sets the word
+// itself.  Ahead of a product (flags not null) its first block clears the word
+// and every block leaves its own finding in flags[block]; the product's first
+// block reads them (collect_flags) and sets the word, so that no other
+// operation has to clear it beforehand.
+__device__ __forceinline__ void report_nonfinite(bool bad, uint32_t* status, uint32_t* flags) {
+  if (!flags) {
+    if (bad) set_status(status, MEGAMOE_DEV_NONFINITE);
+    return;
+  }
+  const int any = __syncthreads_or(bad ? 1 : 0);
+  if (threadIdx.x == 0) {
+    flags[blockIdx.x] = any ? MEGAMOE_DEV_NONFINITE : 0u;
+    if (blockIdx.x == 0) *status = 0u;
+  }
+}
+
+// By whole warps, `threads` threads of which this is number `index`.
+__device__ __forceinline__ void collect_flags(const uint32_t* flags, int count, int index,
+                                              int threads, uint32_t* status) {
+  uint32_t bits = 0;
+  for (int i = index; i < count; i += threads) bits |= __ldcg(flags + i);
+  bits = __reduce_or_sync(0xffffffffu, bits);
+  if ((index & 31) == 0 && bits) set_status(status, bits);
+}
+
 // Atoms along K of a matrix of row length K (a K step of 256 holds two).
 __host__ __device__ __forceinline__ int64_t mx_atoms(int64_t K) { return (K + 255) / 256 * 2; }
 

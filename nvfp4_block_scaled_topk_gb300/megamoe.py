@@ -853,8 +853,12 @@ def linear_mxfp4_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tens
     dev = x.device
     lib = load()
     if ws is None:
-        ws = torch.empty((lib.megamoe_linear_mxfp4_backward_workspace_size(T, K, N),),
-                         dtype=torch.uint8, device=dev)
+        size = _SIZES.get(("backward", T, K, N))
+        if size is None:
+            size = int(lib.megamoe_linear_mxfp4_backward_workspace_size(T, K, N))
+            if len(_SIZES) < 4096:
+                _SIZES[("backward", T, K, N)] = size
+        ws = torch.empty((size,), dtype=torch.uint8, device=dev)
     gx = torch.empty((T, K), dtype=grad_x_dtype, device=dev) if need_x else None
     gw = torch.empty((N, K), dtype=grad_w_dtype, device=dev) if need_w else None
     _check("megamoe_linear_mxfp4_backward", lib.megamoe_linear_mxfp4_backward(

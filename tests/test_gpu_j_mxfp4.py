@@ -188,13 +188,47 @@ def test_linear_gradients_are_differences_where_rounding_is_exact(cuda_lib):
         assert loss(x, w + step[:N]) - loss(x, w) == gw[r, c].item()
 
 
-def test_non_finite_inputs_reach_the_output(cuda_lib):
-    x = _x(3, 64)
+# one launch; a tile a cluster, flipped and not; pairs of CTAs
+@pytest.mark.parametrize("T,K,N", [(3, 64, 32), (50, 2048, 96), (100, 64, 160), (4096, 64, 2560)])
+def test_non_finite_inputs_reach_the_output(cuda_lib, T, K, N):
+    x = _x(T, K)
     x[1, 3] = torch.inf
-    w = _x(32, 64, seed=1, wide=False)
-    out, ws = megamoe.linear_mxfp4(x.cuda(), megamoe.MxLinearWeights.quantize(w.cuda()))
-    assert torch.isnan(out[1]).all() and torch.isfinite(out[[0, 2]]).all()
+    w = _x(N, K, seed=1, wide=False).cuda()
+    out, ws = megamoe.linear_mxfp4(x.cuda(), megamoe.MxLinearWeights.quantize(w))
+    good = torch.ones(T, dtype=torch.bool)
+    good[1] = False
+    assert torch.isnan(out[1]).all() and torch.isfinite(out[good.cuda()]).all()
     assert ws[:4].view(torch.int32).item() == megamoe.DEV_NONFINITE
+    g = _x(T, N, seed=2).cuda()
+    gx, gw, ws = megamoe.linear_mxfp4_backward(g, x.cuda(), w)
+    assert torch.isfinite(gx).all() and torch.isnan(gw[:, 3]).all()
+    assert torch.isfinite(gw[:, 4:]).all()
+    assert ws[:4].view(torch.int32).item() == megamoe.DEV_NONFINITE
+    # the next call clears the word
+    x[1, 3] = 0
+    _, _, ws = megamoe.linear_mxfp4_backward(g, x.cuda(), w, ws=ws)
+    assert ws[:4].view(torch.int32).item() == 0
+
+
+@pytest.mark.parametrize("T,K,N", [(3, 2048, 96), (50, 2048, 96), (100, 512, 160), (4096, 512, 2560)])
+def test_waits_that_run_out_are_reported(cuda_lib, T, K, N):
+    """Under a limit of 100 ns a wait that the hardware does not end by itself
+    gives up: the kernel reports it and returns (or nothing had to give up, and
+    the result is right), and the next call is right."""
+    x, w = _x(T, K).cuda(), _x(N, K, seed=1, wide=False).cuda()
+    weights = megamoe.MxLinearWeights.quantize(w)
+    want, _ = megamoe.linear_mxfp4(x, weights)
+    torch.cuda.synchronize()
+    megamoe.set_wait_limit_ns(100)
+    try:
+        out, ws = megamoe.linear_mxfp4(x, weights)
+        torch.cuda.synchronize()
+        bits = ws[:4].view(torch.int32).item()
+        assert bits == megamoe.DEV_TIMEOUT or (bits == 0 and torch.equal(out, want))
+    finally:
+        megamoe.set_wait_limit_ns(0)
+    out, ws = megamoe.linear_mxfp4(x, weights, ws=ws)
+    assert ws[:4].view(torch.int32).item() == 0 and torch.equal(out, want)
 
 
 def _experts(E, d, I, seed):
