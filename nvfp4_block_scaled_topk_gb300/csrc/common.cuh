@@ -76,15 +76,33 @@ __device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without blocking (try_wait may suspend the thread for a while of the
+// hardware's choosing).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Wait until the phase with parity `parity` of `bar` has completed.  Returns
 // false if the abort flag was raised or the wait ran past `limit_ns` (in which
-// case the abort flag is raised here and `status` gets the TIMEOUT bit).
+// case the abort flag is raised here and `status` gets the TIMEOUT bit).  Limits
+// below kPreciseLimitNs are kept to by polling; above, the hardware's suspended
+// wait is cheaper.
+constexpr uint64_t kPreciseLimitNs = 1000 * 1000;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* status, uint64_t limit_ns = kWaitTimeoutNs) {
-  if (mbar_try_wait(bar, parity)) return true;
+  const bool precise = limit_ns < kPreciseLimitNs;
+  if (!precise && mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (precise ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
     if (globaltimer() - t0 > limit_ns) {
       *abort_flag = 1;

@@ -260,33 +260,37 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int piece = blockIdx.x; ok && piece < total; piece += gridDim.x) {
-        if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+    // -------------------------------------------------------------- MMA issuer
+    // (the whole warp, one lane of it issuing: elect_one)
+    const bool leader = elect_one();
+    const uint64_t w_desc = sdesc_sw128(smem_u32(smem)), t_desc = sdesc_at(w_desc, C::OFF_B);
+    int stage = 0, acc = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int piece = blockIdx.x; ok && piece < total; piece += gridDim.x) {
+      if (!mbar_wait(&acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+      tc_fence_after();
+      const uint32_t d_col = tmem + acc * C::ACC_COLS;
+      const int ks = piece - (piece / S) * S;
+      const int k0 = ks * KT / S, k1 = (ks + 1) * KT / S;
+      for (int kt = k0; kt < k1; ++kt) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
+            !mbar_wait(&sf_ready[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        const uint32_t d_col = tmem + acc * C::ACC_COLS;
-        const int ks = piece - (piece / S) * S;
-        const int k0 = ks * KT / S, k1 = (ks + 1) * KT / S;
-        for (int kt = k0; kt < k1; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
-              !mbar_wait(&sf_ready[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t* sb = smem + stage * C::STAGE;
-          const uint32_t sf_col = tmem + C::SF_COL0 + stage * C::SF_COLS;
-          const uint32_t sfa_col = sf_col + 16 * C::G;
+        const uint64_t wd = sdesc_at(w_desc, stage * C::STAGE);
+        const uint64_t td = sdesc_at(t_desc, stage * C::STAGE);
+        const uint32_t sf_col = tmem + C::SF_COL0 + stage * C::SF_COLS;
+        const uint32_t sfa_col = sf_col + 16 * C::G;
+        if (leader) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint64_t bdesc = sdesc_sw128(smem_u32(sb + C::OFF_B) + 32 * c);
+            const uint64_t bdesc = sdesc_at(td, 32 * c);
 #pragma unroll
             for (int g = 0; g < C::G; ++g) {
-              const uint64_t adesc = sdesc_sw128(smem_u32(sb + C::OFF_A + g * C::A_TILE) + 32 * c);
+              const uint64_t adesc = sdesc_at(wd, g * C::A_TILE + 32 * c);
               if (MX)
                 mma_mxf4(d_col + g * BN, adesc, bdesc, idesc_mxf4(128, BN, c & 1),
                          sf_col + 16 * g + 4 * (c >> 1), sfa_col + 4 * (c >> 1),
@@ -297,23 +301,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
           }
           tc_commit(&empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        tc_commit(&acc_full[acc]);
-        if (++acc == C::ACC_STAGES) {
-          acc = 0;
-          acc_phase ^= 1u;
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
         }
       }
-      // every MMA issued so far must finish before tensor memory is released
-      tc_commit(drain);
-      mbar_drain(drain, 0);
+      if (!ok) break;
+      if (leader) tc_commit(&acc_full[acc]);
+      __syncwarp();
+      if (++acc == C::ACC_STAGES) {
+        acc = 0;
+        acc_phase ^= 1u;
+      }
     }
+    // every MMA issued so far must finish before tensor memory is released
+    if (leader) tc_commit(drain);
     __syncwarp();
+    mbar_drain(drain, 0);
   } else if (warp >= kSfWarp0 && warp < kEpiWarp1) {
     // --------------------------------------------------------- scale writers
     // Weight atom of slice c: byte 16 i + 4 j + b = row 32 j + i, block 4c + b;

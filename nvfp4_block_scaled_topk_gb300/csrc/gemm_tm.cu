@@ -239,27 +239,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+    // -------------------------------------------------------------- MMA issuer
+    // (the whole warp, one lane of it issuing: elect_one)
+    const bool leader = elect_one();
+    const uint64_t t_desc = sdesc_sw128(smem_u32(smem));
+    int stage = 0;
+    uint32_t phase = 0, acc_phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+      tc_fence_after();
+      for (int kt = 0; kt < KT; ++kt) {
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
+            !mbar_wait(&sf_ready[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
         tc_fence_after();
-        for (int kt = 0; kt < KT; ++kt) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
-              !mbar_wait(&sf_ready[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint8_t* sb = smem + stage * C::STAGE;
-          const uint32_t sf_col = tmem + C::SF_COL0 + stage * C::SF_COLS;
+        const uint64_t td = sdesc_at(t_desc, stage * C::STAGE);
+        const uint32_t sf_col = tmem + C::SF_COL0 + stage * C::SF_COLS;
+        if (leader) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const uint64_t adesc = sdesc_sw128(smem_u32(sb + C::OFF_A) + 32 * c);
-            const uint64_t bdesc = sdesc_sw128(smem_u32(sb + C::OFF_B) + 32 * c);
+            const uint64_t adesc = sdesc_at(td, C::OFF_A + 32 * c);
+            const uint64_t bdesc = sdesc_at(td, C::OFF_B + 32 * c);
             if (C::MX)
               mma_mxf4(tmem, adesc, bdesc, idesc_mxf4(128, 256, c & 1), sf_col + 4 * (c >> 1),
                        sf_col + 16 + 8 * (c >> 1), (kt != 0 || c != 0) ? 1u : 0u);
@@ -268,20 +271,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                        (kt != 0 || c != 0) ? 1u : 0u);
           }
           tc_commit(&empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
         }
-        if (!ok) break;
-        tc_commit(acc_full);
-        acc_phase ^= 1u;
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // every MMA issued so far must finish before tensor memory is released
-      tc_commit(drain);
-      mbar_drain(drain, 0);
+      if (!ok) break;
+      if (leader) tc_commit(acc_full);
+      __syncwarp();
+      acc_phase ^= 1u;
     }
+    // every MMA issued so far must finish before tensor memory is released
+    if (leader) tc_commit(drain);
     __syncwarp();
+    mbar_drain(drain, 0);
   } else if (warp >= kSfWarp0 && warp < kEpiWarp1) {
     // --------------------------------------------------------- scale writers
     // Token scales arrive row-major (row n: 16 bytes = 4 slices x 4 blocks):

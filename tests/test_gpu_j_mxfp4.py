@@ -212,19 +212,17 @@ def test_non_finite_inputs_reach_the_output(cuda_lib, T, K, N):
 
 @pytest.mark.parametrize("T,K,N", [(3, 2048, 96), (50, 2048, 96), (100, 512, 160), (4096, 512, 2560)])
 def test_waits_that_run_out_are_reported(cuda_lib, T, K, N):
-    """Under a limit of 100 ns a wait that the hardware does not end by itself
-    gives up: the kernel reports it and returns (or nothing had to give up, and
-    the result is right), and the next call is right."""
+    """A limit that no load meets: the kernels give up, report it and return,
+    and the next call is right."""
     x, w = _x(T, K).cuda(), _x(N, K, seed=1, wide=False).cuda()
     weights = megamoe.MxLinearWeights.quantize(w)
     want, _ = megamoe.linear_mxfp4(x, weights)
     torch.cuda.synchronize()
     megamoe.set_wait_limit_ns(100)
     try:
-        out, ws = megamoe.linear_mxfp4(x, weights)
+        _, ws = megamoe.linear_mxfp4(x, weights)
         torch.cuda.synchronize()
-        bits = ws[:4].view(torch.int32).item()
-        assert bits == megamoe.DEV_TIMEOUT or (bits == 0 and torch.equal(out, want))
+        assert ws[:4].view(torch.int32).item() == megamoe.DEV_TIMEOUT
     finally:
         megamoe.set_wait_limit_ns(0)
     out, ws = megamoe.linear_mxfp4(x, weights, ws=ws)
