@@ -105,6 +105,17 @@ MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool 
                  flags};
 }
 
+// Large batches run on pairs of CTAs with 256-row tiles (mx_experts.cu): from
+// about this many rows an expert on.
+constexpr double kPairRows = 96.0;
+bool pair_experts(int T, int k, int E) {
+  return num_sms() >= 2 && static_cast<double>(T) * k / E >= kPairRows;
+}
+// Rows of an expert are padded to whole scale atoms of 128 rows there.
+int padding(int T, int k, int E, int pad) {
+  return pair_experts(T, k, E) ? (pad + 127) / 128 * 128 : pad;
+}
+
 // Workspace of the MXFP4 forward.
 struct ForwardWs {
   uint32_t* status;
@@ -114,7 +125,7 @@ struct ForwardWs {
   int32_t* slot_dst;
   int32_t* row_src;
   uint8_t* xq_codes;
-  uint8_t* xq_scales;  // routed layout, 16 bytes per K step of 256
+  uint8_t* xq_scales;  // routed layout, 16 bytes per K step of 256, or (pairs) atoms
   uint8_t* hq_codes;
   uint8_t* hq_scales;
   uint16_t* y;  // BFP16
@@ -129,7 +140,7 @@ ForwardWs carve_forward(void* base, int T, int k, int E, int d, int I, int pad) 
   Carver c{static_cast<uint8_t*>(base)};
   ForwardWs w{};
   const size_t slots = static_cast<size_t>(T) * k;
-  w.rows = megamoe_max_padded_rows(T, k, E, pad);
+  w.rows = megamoe_max_padded_rows(T, k, E, padding(T, k, E, pad));
   const size_t rows = static_cast<size_t>(w.rows);
   auto ints = [&](size_t n) { return reinterpret_cast<int32_t*>(c.take(4 * n)); };
   w.status = reinterpret_cast<uint32_t*>(c.take(256));
@@ -139,9 +150,11 @@ ForwardWs carve_forward(void* base, int T, int k, int E, int d, int I, int pad) 
   w.slot_dst = ints(slots);
   w.row_src = ints(rows);
   w.xq_codes = c.take(rows * (d / 2));
-  w.xq_scales = c.take(rows * (d / 16));
+  // (atoms take half of the routed layout's bytes, in whole groups of 128 rows)
+  const size_t whole = (rows + 127) / 128 * 128;
+  w.xq_scales = c.take(whole * (d / 16));
   w.hq_codes = c.take(rows * (I / 2));
-  w.hq_scales = c.take(rows * (I / 16));
+  w.hq_scales = c.take(whole * (I / 16));
   uint8_t* y = c.take(MEGAMOE_BFP16_BYTES(rows, d));
   w.y = reinterpret_cast<uint16_t*>(y);
   w.y_exp = y ? reinterpret_cast<int8_t*>(y + rows * d * 2) : nullptr;
@@ -184,6 +197,14 @@ megamoe_status check_mx_forward(const megamoe_mx_weights* w, const uint16_t* x, 
                               w->w13_scales,  none,      w->w2_codes,     w->w2_scales, none};
   megamoe_status st = check_forward_args(&shape, x, nullptr, nullptr, T, k, pad, out, true);
   if (st != MEGAMOE_OK) return st;
+  // weight blocks' rows are counted in 31 bits
+  const int64_t E = w->num_experts, d = w->hidden, I = w->intermediate;
+  if (E * 2 * I * (d / 256) >= (int64_t{1} << 31) || E * d * (I / 256) >= (int64_t{1} << 31))
+    return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  // and so are padded rows
+  if (megamoe_max_padded_rows(T, k, w->num_experts, padding(T, k, w->num_experts, pad)) >=
+      (int64_t{1} << 31))
+    return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   if (!ws || !aligned(ws, 256)) return MEGAMOE_ERR_INVALID_ARG;
   if (ws_bytes < megamoe_workspace_size_mxfp4(T, k, w->num_experts, w->hidden, w->intermediate, pad))
     return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
@@ -194,14 +215,47 @@ megamoe_status run_mx_forward(const megamoe_mx_weights* w, const uint16_t* x,
                               const int32_t* topk_ids, const float* topk_weights, int T, int k,
                               int pad, uint16_t* out, const ForwardWs& wk, cudaStream_t s) {
   const int E = w->num_experts, d = w->hidden, I = w->intermediate;
+  const bool pairs = pair_experts(T, k, E);
+  pad = padding(T, k, E, pad);
   // The routing clears the status word; no amax of x is needed, so there is
   // nothing between it and the quantiser.
   cudaError_t e = launch_route(topk_ids, T * k, E, pad, wk.counts, wk.offsets, wk.padded_offsets,
                                wk.row_src, wk.rows, wk.slot_dst, wk.status, wk.status, 1, s,
                                wk.route_hist);
   if (e == cudaSuccess)
-    e = launch_mx_routed(x, T, d, wk.slot_dst, k, wk.xq_codes, wk.xq_scales, wk.status, s);
+    e = launch_mx_routed(x, T, d, wk.slot_dst, k, pairs, wk.xq_codes, wk.xq_scales, wk.status, s);
   if (e != cudaSuccess) return MEGAMOE_ERR_CUDA;
+  if (pairs) {
+    MxExperts m{};
+    m.act_codes = wk.xq_codes;
+    m.act_scales = wk.xq_scales;
+    m.rows = wk.rows;
+    m.w_codes = w->w13_codes;
+    m.w_scales = w->w13_scales;
+    m.E = E;
+    m.N = 2 * I;
+    m.K = d;
+    m.offsets = wk.offsets;
+    m.padded_offsets = wk.padded_offsets;
+    m.h_codes = wk.hq_codes;
+    m.h_scales = wk.hq_scales;
+    m.status = wk.status;
+    e = launch_mx_experts(m, s);
+    if (e != cudaSuccess) return MEGAMOE_ERR_CUDA;
+    m.act_codes = wk.hq_codes;
+    m.act_scales = wk.hq_scales;
+    m.w_codes = w->w2_codes;
+    m.w_scales = w->w2_scales;
+    m.N = d;
+    m.K = I;
+    m.y = wk.y;
+    m.y_exp = wk.y_exp;
+    e = launch_mx_experts(m, s);
+    if (e == cudaSuccess)
+      e = launch_combine(wk.y, wk.y_exp, d, wk.rows, wk.slot_dst, topk_weights, T, k, d, out, false,
+                         s);
+    return cuda_status(e);
+  }
   const int tile_n = pick_tile_n(static_cast<double>(T) * k / E);
   GemmLaunch g{};
   g.mx = true;

@@ -227,9 +227,30 @@ struct MxTiles {
 // Most words that a quantising launch leaves in its flags.
 int mx_flags_words();
 cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s, int* blocks = nullptr);
-// x [T, d] bf16 into routed rows slot_dst[t k + j] (routed scale layout).
+// x [T, d] bf16 into routed rows slot_dst[t k + j] (routed scale layout, or atoms).
 cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t* slot_dst, int k,
-                             uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s);
+                             bool atoms, uint8_t* codes, uint8_t* scales, uint32_t* status,
+                             cudaStream_t s);
+// The routed experts' products on pairs of CTAs (large batches): experts' rows
+// start at multiples of 128, scales of rows in the atom layout.  y null: gate and
+// up (N = 2 I), SiLU * up quantised to h_codes and h_scales (atom layout); else
+// down (N = d), BFP16 y and its exponents.
+struct MxExperts {
+  const uint8_t* act_codes;
+  const uint8_t* act_scales;
+  int64_t rows;
+  const uint8_t* w_codes;
+  const uint8_t* w_scales;
+  int E, N, K;
+  const int32_t* offsets;  // complete before the kernel ahead of this one started
+  const int32_t* padded_offsets;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+  uint16_t* y;
+  int8_t* y_exp;
+  uint32_t* status;
+};
+cudaError_t launch_mx_experts(const MxExperts& g, cudaStream_t stream);
 // Row-major codes and scales -> values.
 cudaError_t launch_mx_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
                              void* out, bool f32, int64_t ld, cudaStream_t s);

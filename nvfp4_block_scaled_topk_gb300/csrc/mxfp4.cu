@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(256, 3) k_mx_tiles(const __grid_constant__ MxT
 // tasks of 256 elements as above; d is a multiple of 256.
 __global__ void __launch_bounds__(256)
     k_mx_routed(const __nv_bfloat16* __restrict__ x, int64_t T, int d,
-                const int32_t* __restrict__ slot_dst, int k, uint8_t* __restrict__ codes,
+                const int32_t* __restrict__ slot_dst, int k, int atoms, uint8_t* __restrict__ codes,
                 uint8_t* __restrict__ scales, uint32_t* status) {
   pdl_wait();
   pdl_trigger();
@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(256)
       if (dst < 0) continue;  // warp-uniform
       *reinterpret_cast<uint32_t*>(codes + dst * (d / 2) + col / 2) = c;
       if ((lane & 3) == 0)
-        scales[dst * (d / 16) + mx_routed_offset(col >> 5)] = static_cast<uint8_t>(byte);
+        scales[atoms ? mx_atom_offset(dst, col >> 5, d / 128)
+                     : dst * (d / 16) + mx_routed_offset(col >> 5)] = static_cast<uint8_t>(byte);
     }
   }
 }
@@ -489,11 +490,12 @@ cudaError_t launch_mx_quantize(const MxQuant& q, cudaStream_t s, int* blocks) {
 }
 
 cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t* slot_dst, int k,
-                             uint8_t* codes, uint8_t* scales, uint32_t* status, cudaStream_t s) {
+                             bool atoms, uint8_t* codes, uint8_t* scales, uint32_t* status,
+                             cudaStream_t s) {
   if (T == 0) return cudaSuccess;
   return launch_pdl(k_mx_routed, dim3(blocks_for(T * (d / 256), 8)), dim3(256), 0, s,
-                    reinterpret_cast<const __nv_bfloat16*>(x), T, d, slot_dst, k, codes, scales,
-                    status);
+                    reinterpret_cast<const __nv_bfloat16*>(x), T, d, slot_dst, k, atoms ? 1 : 0, codes,
+                    scales, status);
 }
 
 cudaError_t launch_mx_values(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K,
