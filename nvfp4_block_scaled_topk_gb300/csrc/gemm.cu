@@ -191,8 +191,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       // A weight tile read by one token tile is dead after it (evict first);
       // one that the expert's next token tiles re-read stays (evict normal).
       const uint64_t pol_w_once = policy_evict_first();
@@ -233,16 +235,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint8_t* sb = smem + stage * C::STAGE;
           // scales first, on their own barrier: the scale warps move them into
           // tensor memory while the codes are still landing
-          mbar_arrive_expect_tx(&sf_full[stage], C::SF_TX);
-          bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
-          if (C::G == 2)
-            bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
-          tma_load_2d(sb + C::OFF_SFA_RAW, &maps.scales, &sf_full[stage], kt * 16, a_row0, pol_a);
-          mbar_arrive_expect_tx(&full[stage], C::TX);
-          // the stage's weight blocks (gate then up for L1) are contiguous and
-          // pre-swizzled: one bulk copy
-          bulk_load(sb + C::OFF_A, wcod + kt * (C::G * 16384), C::G * C::A_TILE, &full[stage], pol_w);
-          tma_load_2d(sb + C::OFF_B, &maps.codes, &full[stage], kt * 128, a_row0, pol_a);
+          if (leader) {
+            mbar_arrive_expect_tx(&sf_full[stage], C::SF_TX);
+            bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
+            if (C::G == 2)
+              bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
+            tma_load_2d(sb + C::OFF_SFA_RAW, &maps.scales, &sf_full[stage], kt * 16, a_row0, pol_a);
+            mbar_arrive_expect_tx(&full[stage], C::TX);
+            // the stage's weight blocks (gate then up for L1) are contiguous and
+            // pre-swizzled: one bulk copy
+            bulk_load(sb + C::OFF_A, wcod + kt * (C::G * 16384), C::G * C::A_TILE, &full[stage], pol_w);
+            tma_load_2d(sb + C::OFF_B, &maps.codes, &full[stage], kt * 128, a_row0, pol_a);
+          }
+          __syncwarp();
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -708,6 +713,19 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint
   return enc(map, type, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
+                 uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[3] = {n0, n1, n2};
+  cuuint64_t strides[2] = {stride1, stride2};
+  cuuint32_t box[3] = {box0, box1, box2};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int num_sms() {

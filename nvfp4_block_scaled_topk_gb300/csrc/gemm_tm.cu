@@ -160,8 +160,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   const uint32_t tmem = *tmem_holder;
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       const uint64_t pol_w_once = policy_evict_first();
       const uint64_t pol_w_reused = policy_evict_normal();
       const uint64_t pol_a = policy_evict_last();
@@ -210,18 +212,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           uint8_t* sb = smem + stage * C::STAGE;
-          mbar_arrive_expect_tx(&sf_full[stage], C::SFW + box * 16);
-          bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
-          bulk_load(sb + C::OFF_SFW + C::SFG, sfw1 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
-          tma_load_2d(sb + C::OFF_SFA_RAW, map_s, &sf_full[stage], kt * 16, a_row0, pol_a);
-          mbar_arrive_expect_tx(&full[stage], C::B_TILE + box * 128);
-          if (C::SILU) {
-            bulk_load(sb + C::OFF_B, wc0 + kt * 32768, 32768, &full[stage], pol_w);
-          } else {
-            bulk_load(sb + C::OFF_B, wc0 + kt * 16384, 16384, &full[stage], pol_w);
-            bulk_load(sb + C::OFF_B + 16384, wc1 + kt * 16384, 16384, &full[stage], pol_w);
+          if (leader) {
+            mbar_arrive_expect_tx(&sf_full[stage], C::SFW + box * 16);
+            bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
+            bulk_load(sb + C::OFF_SFW + C::SFG, sfw1 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
+            tma_load_2d(sb + C::OFF_SFA_RAW, map_s, &sf_full[stage], kt * 16, a_row0, pol_a);
+            mbar_arrive_expect_tx(&full[stage], C::B_TILE + box * 128);
+            if (C::SILU) {
+              bulk_load(sb + C::OFF_B, wc0 + kt * 32768, 32768, &full[stage], pol_w);
+            } else {
+              bulk_load(sb + C::OFF_B, wc0 + kt * 16384, 16384, &full[stage], pol_w);
+              bulk_load(sb + C::OFF_B + 16384, wc1 + kt * 16384, 16384, &full[stage], pol_w);
+            }
+            tma_load_2d(sb + C::OFF_A, map_c, &full[stage], kt * 128, a_row0, pol_a);
           }
-          tma_load_2d(sb + C::OFF_A, map_c, &full[stage], kt * 128, a_row0, pol_a);
+          __syncwarp();
           ++issued;
           if (++stage == STAGES) {
             stage = 0;

@@ -170,6 +170,10 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint
               uint64_t rows, uint64_t stride, uint32_t box_cols, uint32_t box_rows,
               CUtensorMapSwizzle swizzle);
 
+// 3-D map of 32-bit words.
+bool make_map_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
+                 uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2);
+
 // Scored router (grouped top-k over sigmoid or softmax scores) and its gradient.
 struct ScoredRouter {
   const void* logits;  // [T, ld], fp32 or bf16

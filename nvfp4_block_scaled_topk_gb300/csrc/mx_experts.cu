@@ -154,8 +154,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       const uint64_t pol_w_once = policy_evict_first(), pol_w_again = policy_evict_normal();
       const uint64_t pol_t = policy_evict_last();
       int stage = 0, e_lo = 0;
@@ -172,23 +174,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         const uint32_t bytes = 2 * C::STAGE - (both ? 0 : C::TILE + C::SF);
         const uint64_t pol_w = ti.ntiles > 1 ? pol_w_again : pol_w_once;
         // this CTA's block of 128 weight rows at K step 0 (gate and up blocks
-        // are neighbours), and the 128-row groups of the tile's scales
-        const int g0 = SILU ? ti.e * (p.N / 128) + ti.mt : ti.e * (p.N / 128) + 2 * ti.mt;
-        const int g1 = SILU ? g0 + p.N / 256 : g0 + 1;
-        const int blk = SILU ? (ti.e * MT + ti.mt) * KT * 2 + rank : (g0 + rank) * KT;
+        // are neighbours), and the tile's two 128-row groups of scales: groups
+        // mt of the expert's gate and up rows, or two neighbours
+        const int sf_y = SILU ? ti.mt : ti.e * (p.N / 128) + 2 * ti.mt, sf_z = SILU ? 2 * ti.e : 0;
+        const int blk = SILU ? (ti.e * MT + ti.mt) * KT * 2 + rank : (sf_y + rank) * KT;
         for (int kt = 0; kt < KT; ++kt) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
             break;
           }
           uint8_t* sb = smem + stage * C::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
-          const uint32_t bar = cluster_address(&full[stage], 0);
-          tma_load_2d_pair(sb + C::OFF_W, &maps.w, bar, 0, (blk + (SILU ? 2 : 1) * kt) * 128, pol_w);
-          if (mine) tma_load_2d_pair(sb, &maps.tok, bar, kt * 128, row0, pol_t);
-          if (mine) tma_load_2d_pair(sb + C::OFF_SFT, &maps.tok_sf, bar, kt * 256, row0 >> 7, pol_t);
-          tma_load_2d_pair(sb + C::OFF_SFW, &maps.w_sf, bar, kt * 256, g0, pol_w);
-          tma_load_2d_pair(sb + C::OFF_SFW + C::SF, &maps.w_sf, bar, kt * 256, g1, pol_w);
+          if (leader) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], bytes);
+            const uint32_t bar = cluster_address(&full[stage], 0);
+            tma_load_2d_pair(sb + C::OFF_W, &maps.w, bar, 0, (blk + (SILU ? 2 : 1) * kt) * 128, pol_w);
+            if (mine) {
+              tma_load_2d_pair(sb, &maps.tok, bar, kt * 128, row0, pol_t);
+              tma_load_2d_pair(sb + C::OFF_SFT, &maps.tok_sf, bar, kt * 256, row0 >> 7, pol_t);
+            }
+            tma_load_3d_pair(sb + C::OFF_SFW, &maps.w_sf, bar, kt * 256, sf_y, sf_z, pol_w);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
@@ -391,8 +397,10 @@ cudaError_t launch_typed(const MxExperts& g, cudaStream_t stream) {
       // packed blocks of 128 rows x 128 bytes, swizzled already
       !make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w_codes, 128, groups * KT * 128, 128, 128,
                 128, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_map(&maps.w_sf, CU_TENSOR_MAP_DATA_TYPE_UINT32, g.w_scales, sf_row / 4, groups, sf_row,
-                256, 1, CU_TENSOR_MAP_SWIZZLE_NONE))
+      // [2 E][I / 128] groups of gate and up rows, two of the first; or all groups, two of them
+      !make_map_3d(&maps.w_sf, g.w_scales, sf_row / 4, SILU ? g.N / 256 : groups,
+                   SILU ? 2 * static_cast<uint64_t>(g.E) : 1, sf_row,
+                   SILU ? sf_row * (g.N / 256) : sf_row * groups, 256, SILU ? 1 : 2, SILU ? 2 : 1))
     return cudaErrorInvalidValue;
   if (SILU) maps.y = maps.tok;  // not used
   else if (!make_map(&maps.y, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.y, g.N, rows,

@@ -169,8 +169,10 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
 
   bool done = true;
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       const uint64_t pol = policy_evict_normal();
       const int64_t atoms = mx_atoms(p.K);
       const uint8_t* sfm = p.m_sf + mt * atoms * 512;
@@ -184,11 +186,14 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
           break;
         }
         uint8_t* sb = smem + stage * C::STAGE;
-        mbar_arrive_expect_tx(&full[stage], C::M_TILE + p.n_box * 128 + 2 * C::SF);
-        tma_load_2d(sb, &maps.m, &full[stage], kt * 128, mt * 128, pol);
-        tma_load_2d(sb + C::OFF_N, &maps.n, &full[stage], kt * 128, nt * BN, pol);
-        bulk_load(sb + C::OFF_SFM, sfm + kt * C::SF, C::SF, &full[stage], pol);
-        bulk_load(sb + C::OFF_SFN, sfn + kt * C::SF, C::SF, &full[stage], pol);
+        if (leader) {
+          mbar_arrive_expect_tx(&full[stage], C::M_TILE + p.n_box * 128 + 2 * C::SF);
+          tma_load_2d(sb, &maps.m, &full[stage], kt * 128, mt * 128, pol);
+          tma_load_2d(sb + C::OFF_N, &maps.n, &full[stage], kt * 128, nt * BN, pol);
+          bulk_load(sb + C::OFF_SFM, sfm + kt * C::SF, C::SF, &full[stage], pol);
+          bulk_load(sb + C::OFF_SFN, sfn + kt * C::SF, C::SF, &full[stage], pol);
+        }
+        __syncwarp();
         ++issued;
         if (++stage == STAGES) {
           stage = 0;
@@ -479,8 +484,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
   pdl_trigger();
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------------------ producer
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       const uint64_t pol = policy_evict_normal();
       int stage = 0;
       uint32_t phase = 0;
@@ -494,12 +501,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
             break;
           }
           uint8_t* sb = smem + stage * C::STAGE;
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::TX);
-          const uint32_t bar = cluster_address(&full[stage], 0);
-          tma_load_2d_pair(sb, &maps.m, bar, kt * 128, m0, pol);
-          tma_load_2d_pair(sb + C::OFF_N, &maps.n, bar, kt * 128, n0 + rank * 128, pol);
-          tma_load_2d_pair(sb + C::OFF_SFM, &maps.sfm, bar, kt * 256, m0 >> 7, pol);
-          tma_load_2d_pair(sb + C::OFF_SFN, &maps.sfn, bar, kt * 256, n0 >> 7, pol);
+          if (leader) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], C::TX);
+            const uint32_t bar = cluster_address(&full[stage], 0);
+            tma_load_2d_pair(sb, &maps.m, bar, kt * 128, m0, pol);
+            tma_load_2d_pair(sb + C::OFF_N, &maps.n, bar, kt * 128, n0 + rank * 128, pol);
+            tma_load_2d_pair(sb + C::OFF_SFM, &maps.sfm, bar, kt * 256, m0 >> 7, pol);
+            tma_load_2d_pair(sb + C::OFF_SFN, &maps.sfn, bar, kt * 256, n0 >> 7, pol);
+          }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;

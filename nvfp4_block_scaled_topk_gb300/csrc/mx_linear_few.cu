@@ -119,8 +119,10 @@ __global__ void __launch_bounds__(kThreads) k_mx_linear_few(const __grid_constan
   const uint32_t tmem = tmem_holder;
 
   if (warp == 0) {
-    if (lane == 0) {
+    {
       // ------------------------------------------------ producer of the weights
+      // (the whole warp, one lane of it issuing: elect_one)
+      const bool leader = elect_one();
       const uint64_t pol = policy_evict_first();
       const uint8_t* sf = p.w_sf + mt * mx_atoms(p.K) * 512;
       int stage = 0, issued = 0;
@@ -132,9 +134,12 @@ __global__ void __launch_bounds__(kThreads) k_mx_linear_few(const __grid_constan
           break;
         }
         uint8_t* sb = smem + stage * kStage;
-        mbar_arrive_expect_tx(&full[stage], kStage);
-        tma_load_2d(sb, &codes, &full[stage], kt * 128, mt * 128, pol);
-        bulk_load(sb + 128 * 128, sf + static_cast<int64_t>(kt) * kSf, kSf, &full[stage], pol);
+        if (leader) {
+          mbar_arrive_expect_tx(&full[stage], kStage);
+          tma_load_2d(sb, &codes, &full[stage], kt * 128, mt * 128, pol);
+          bulk_load(sb + 128 * 128, sf + static_cast<int64_t>(kt) * kSf, kSf, &full[stage], pol);
+        }
+        __syncwarp();
         ++issued;
         if (++stage == kStages) {
           stage = 0;
@@ -323,16 +328,18 @@ cudaError_t launch_typed(const FewArgs& a, const uint8_t* w_codes, bool f32, cud
 
 }  // namespace
 
-// Each CTA quantises the part of x that it needs: T tokens by its K steps.
-// Beyond T (steps / cluster) = 90 + 4 steps, quantising once in a kernel before
-// the product is faster.  Measured (this form / that form, us): 7168 -> 1536 at 32
-// tokens 9.9 / 11; 1536 -> 24576 at 16 9.1 / 12.4; 2048 -> 7168 at 16 7.7 / 10.4, at
-// 32 11.3 / 10.4; 7168 -> 16384 at 8 20.3 / 20.6.
+// Each CTA quantises the part of x that it needs: T tokens by its q K steps.
+// Beyond T = 3.6 + 40 / q, quantising once in a kernel before the product is
+// faster.  Measured (this form / that form, us): 7168 -> 1536 (q = 4) at 12 tokens
+// 6.3 / 7.2, at 17 7.8 / 7.2; 1536 -> 24576 (q = 6) at 12 8.1 / 8.6, at 17 10.7 / 8.6;
+// 7168 -> 16384 (q = 28) at 4 16.2 / 16.9, at 8 20.3 / 16.9; 2048 -> 7168 (q = 4) at
+// 12 6.5 / 7.1, at 16 7.7 / 7.1.
 bool mx_linear_few_fits(int64_t T, int64_t K, int64_t N) {
   if (T > 32) return false;
   const int64_t steps = (K + 255) / 256;
   const int cluster = few_cluster(T, N, K);
-  return T * steps / cluster <= 90 + 4 * steps &&
+  const int64_t q = (steps + cluster - 1) / cluster;
+  return static_cast<double>(T) <= 3.6 + 40.0 / static_cast<double>(q) &&
          few_bytes(T <= 16 ? 16 : 32, K, cluster) <= 226 * 1024;
 }
 

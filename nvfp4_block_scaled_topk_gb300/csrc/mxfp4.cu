@@ -293,8 +293,10 @@ __global__ void __launch_bounds__(256, 3) k_mx_tiles(const __grid_constant__ MxT
 }
 
 // Token rows into their routed rows: slot j of token t goes to row
-// slot_dst[t k + j] (skipped when negative).  A row is encoded once.  Warp
-// tasks of 256 elements as above; d is a multiple of 256.
+// slot_dst[t k + j] (skipped when negative).  A row is encoded once.  A lane takes
+// a whole block of 32 elements, so that a copy of 1024 elements is one 16-byte
+// store of codes a lane and one word of scales for every four; d is a multiple
+// of 256.
 __global__ void __launch_bounds__(256)
     k_mx_routed(const __nv_bfloat16* __restrict__ x, int64_t T, int d,
                 const int32_t* __restrict__ slot_dst, int k, int atoms, uint8_t* __restrict__ codes,
@@ -302,30 +304,48 @@ __global__ void __launch_bounds__(256)
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31;
-  const int steps = d / 256;
-  const int64_t tasks = T * steps;
+  const int blocks = d / 32, groups = (blocks + 31) / 32;
+  const int64_t tasks = T * groups;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  bool bad = false;
   for (int64_t w = blockIdx.x * static_cast<int64_t>(blockDim.x >> 5) + (threadIdx.x >> 5);
        w < tasks; w += warps) {
-    const int64_t t = w / steps;
-    const int col = static_cast<int>(w - t * steps) * 256 + 8 * lane;
+    const int64_t t = task_div(w, groups);
+    const int b = static_cast<int>(w - t * groups) * 32 + lane;
+    const bool in = b < blocks;  // by fours: blocks is a multiple of eight
     const int my_dst = lane < k ? __ldg(slot_dst + t * k + lane) : -1;
-    Eight<__nv_bfloat16> e;
-    e.load(x + t * d + col);
-    const uint32_t byte = block_byte(e);
-    float v[8];
-    e.values(v);
-    const uint32_t c = mx_codes8(v, mx_inverse(byte));
-    if (byte == kMxNan) set_status(status, MEGAMOE_DEV_NONFINITE);
+    Eight<__nv_bfloat16> e[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (in) e[i].load(x + t * d + 32 * b + 8 * i);
+      else e[i].clear();
+    }
+    uint32_t m = e[0].widest();
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = Eight<__nv_bfloat16>::wider(m, e[i].widest());
+    const uint32_t byte = mx_scale_byte(Eight<__nv_bfloat16>::bits(m));
+    const float inv = mx_inverse(byte);
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[8];
+      e[i].values(v);
+      c[i] = mx_codes8(v, inv);
+    }
+    bad |= byte == kMxNan;
+    // lane 4 i: the scale bytes of blocks 4 i .. 4 i + 3
+    uint32_t word = byte | (__shfl_down_sync(kAll, byte, 1) << 8);
+    word |= __shfl_down_sync(kAll, word, 2) << 16;
     for (int j = 0; j < k; ++j) {
       const int64_t dst = __shfl_sync(kAll, my_dst, j);
-      if (dst < 0) continue;  // warp-uniform
-      *reinterpret_cast<uint32_t*>(codes + dst * (d / 2) + col / 2) = c;
+      if (dst < 0 || !in) continue;
+      *reinterpret_cast<uint4*>(codes + dst * (d / 2) + 16 * b) = make_uint4(c[0], c[1], c[2], c[3]);
       if ((lane & 3) == 0)
-        scales[atoms ? mx_atom_offset(dst, col >> 5, d / 128)
-                     : dst * (d / 16) + mx_routed_offset(col >> 5)] = static_cast<uint8_t>(byte);
+        *reinterpret_cast<uint32_t*>(scales + (atoms ? mx_atom_offset(dst, b, d / 128)
+                                                     : dst * (d / 16) + mx_routed_offset(b))) = word;
     }
   }
+  if (bad) set_status(status, MEGAMOE_DEV_NONFINITE);
 }
 
 // Two E2M1 codes (a byte, the even element low) -> two halves.
@@ -493,7 +513,7 @@ cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t*
                              bool atoms, uint8_t* codes, uint8_t* scales, uint32_t* status,
                              cudaStream_t s) {
   if (T == 0) return cudaSuccess;
-  return launch_pdl(k_mx_routed, dim3(blocks_for(T * (d / 256), 8)), dim3(256), 0, s,
+  return launch_pdl(k_mx_routed, dim3(blocks_for(T * ((d + 1023) / 1024), 8)), dim3(256), 0, s,
                     reinterpret_cast<const __nv_bfloat16*>(x), T, d, slot_dst, k, atoms ? 1 : 0, codes,
                     scales, status);
 }
