@@ -301,3 +301,26 @@ def test_experts_bad_id_is_flagged_and_graph_replay_matches(cuda_lib):
     bad[1, 1] = 8
     fwd(x, bad, w)
     assert fwd.read_status() == megamoe.DEV_BAD_EXPERT_ID
+
+
+@pytest.mark.parametrize("T", [6, 300])
+def test_non_finite_experts_reach_their_tokens_alone(cuda_lib, T):
+    """Inf in one token and NaN scales in one expert's down rows: only the
+    outputs that use them are not finite (small and large batches)."""
+    E, k, d, I = 8, 3, 256, 256
+    weights, values = _experts(E, d, I, 11)
+    rng = np.random.default_rng(T)
+    x = torch.tensor(rng.standard_normal((T, d)), dtype=torch.bfloat16)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    w = rng.random((T, k)).astype(np.float32) + 0.1
+    fwd = megamoe.MxForward(weights, T, k)
+    want = fwd(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()).clone()
+    x[2, 7] = torch.inf
+    got = fwd(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+    assert fwd.read_status() == megamoe.DEV_NONFINITE
+    keep = torch.ones(T, dtype=torch.bool)
+    keep[2] = False
+    assert torch.isnan(got[2]).all() and torch.isfinite(got[keep.cuda()]).all()
+    # a group of 16 rows that holds the token is stored as fp16: its other rows
+    # carry that rounding
+    assert_close_bf16(_np(got)[keep.numpy()], _np(want)[keep.numpy()], what="other tokens")
