@@ -105,9 +105,11 @@ MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool 
                  flags};
 }
 
-// Large batches run on pairs of CTAs with 256-row tiles (mx_experts.cu): from
-// about this many rows an expert on.
-constexpr double kPairRows = 96.0;
+// Large batches run on pairs of CTAs with 256-row tiles (mx_experts.cu), from
+// about this many rows an expert on: below, most experts' rows fit one 128-row
+// tile of the single CTAs.  48 experts (single / pairs, us): 106 rows an expert
+// 224 / 236, 128 rows 258 / 245, 160 rows 328 / 263.
+constexpr double kPairRows = 115.0;
 bool pair_experts(int T, int k, int E) {
   return num_sms() >= 2 && static_cast<double>(T) * k / E >= kPairRows;
 }

@@ -245,7 +245,8 @@ def _experts(E, d, I, seed):
 # the framework's bound for a forward (helpers.py) holds
 @pytest.mark.parametrize("T,E,k,d,I,pad", [(1, 8, 2, 256, 256, 32), (64, 8, 2, 256, 512, 32),
                                            (5, 33, 8, 512, 256, 128), (300, 8, 3, 256, 256, 32),
-                                           (700, 8, 2, 512, 768, 64), (130, 3, 1, 256, 256, 32)])
+                                           (700, 8, 2, 512, 768, 64), (130, 3, 1, 256, 256, 32),
+                                           (331, 8, 3, 256, 512, 96)])
 def test_experts(cuda_lib, T, E, k, d, I, pad):
     weights, values = _experts(E, d, I, T)
     rng = np.random.default_rng(T + E)
@@ -303,7 +304,7 @@ def test_experts_bad_id_is_flagged_and_graph_replay_matches(cuda_lib):
     assert fwd.read_status() == megamoe.DEV_BAD_EXPERT_ID
 
 
-@pytest.mark.parametrize("T", [6, 300])
+@pytest.mark.parametrize("T", [6, 300, 400])
 def test_non_finite_experts_reach_their_tokens_alone(cuda_lib, T):
     """Inf in one token and NaN scales in one expert's down rows: only the
     outputs that use them are not finite (small and large batches)."""
