@@ -91,12 +91,12 @@ BackwardWs carve_backward(void* base, int64_t T, int K, int N) {
   return w;
 }
 
-// Rows and columns of the products are int; the quantisers' tiles (of 128 x 64
-// at least) are counted in 31 bits over all three matrices.
+// Rows and columns of the products are int, their tiles (of 128 x 128) and the
+// quantisers' (of 128 x 64 at least, over all three matrices) counted in 31 bits.
 bool linear_sizes_ok(int64_t T, int K, int N) {
   if (K % 32 != 0 || N % 32 != 0 || T >= (int64_t{1} << 30)) return false;
-  const int64_t tall = (T + 127) / 128, k = K / 64 + 4, n = N / 64 + 4;
-  return tall * (k + n) + (N / 128 + 1) * k < (int64_t{1} << 30);
+  const int64_t t = T / 128 + 1, k = K / 128 + 1, n = N / 128 + 1, most = int64_t{1} << 28;
+  return t * k < most && t * n < most && n * k < most;
 }
 
 MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool transpose,
