@@ -4,7 +4,7 @@
 // features of one token: 128-bit loads of each routed row of y (up to eight
 // slots' loads in flight at once), fp32 sums in ascending j, one bf16
 // rounding, 64-bit stores.  y is fp32 (megamoe_combine), or (the forward)
-// BFP16, then one thread per 8 features (k_combine_bfp16).  An expert-parallel
+// BFP16, then a warp per 256 features (k_combine_bfp16).  An expert-parallel
 // shard writes the fp32 sum of its own slots instead, and the shards' sums
 // are added and rounded once after the exchange (k_round_bf16).
 #include <cuda_bf16.h>
@@ -79,83 +79,128 @@ __global__ void __launch_bounds__(256) k_round_bf16(const float4* __restrict__ i
   }
 }
 
-// The combine over a BFP16 y: one thread per 8 consecutive features of one
-// token, which are one exponent group of each routed row.  Per slot one
-// 16-byte load of values and one exponent byte, up to eight slots in flight;
-// the slot's power of two is folded into its weight (w * 2^s is exact), so
-// each element costs a byte permute, an exact subtraction and one fused
-// multiply-add into the fp32 sum (the same sum as decoding first), in
-// ascending j; one bf16 rounding, two 8-byte stores (or the fp32 sum of a
-// shard's slots).
-template <bool F32_OUT>
+// a * b + c and a + b of two floats each, every element rounded as alone.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t d) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
+  return r;
+}
+
+// The combine over a BFP16 y: a warp takes 256 consecutive features of a token,
+// a lane eight of them, which are one exponent group of each routed row.  Per
+// slot one 16-byte load of values and one exponent byte, the loads of SLOTS
+// slots in flight; the slot's power of two is folded into its weight (w * 2^s is
+// exact), so each element costs a byte permute and, two elements at a time, an
+// exact subtraction and a fused multiply-add into the fp32 sum (the same sum as
+// decoding first), in ascending j; one bf16 rounding (or the fp32 sum of a
+// shard's slots).  Resident warps count for more than slots in flight: eight at
+// a time (80 registers) took 46.2 us for 2003 tokens of 6 slots and 7168
+// features, six 40.7, four (64 registers) 39.7, three 38.1 (5.3 TB/s), two 41.2;
+// for 8 slots four took 45.4 and three 49.7.  So three or four, whichever leaves
+// fewer places empty in the last round.
+template <int SLOTS, bool F32_OUT>
 __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restrict__ y,
                                                        const int8_t* __restrict__ y_exp,
                                                        int64_t ld_y, int64_t y_rows,
                                                        const int32_t* __restrict__ slot_dst,
                                                        const float* __restrict__ w, int T, int k,
-                                                       int d, void* __restrict__ out) {
+                                                       int d, bool out16,
+                                                       void* __restrict__ out) {
   pdl_wait();
   pdl_trigger();
-  const int vecs = d / 8;
-  const int64_t total = static_cast<int64_t>(T) * vecs;
-  for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int t = (i >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(vecs))
-                                 : static_cast<int>(i / vecs);
-    const int v = static_cast<int>(i - static_cast<int64_t>(t) * vecs);
-    float acc[8];
+  const int vecs = d / 8, lane = threadIdx.x & 31;
+  const int per = (vecs + 31) / 32;  // warp tasks of a token
+  const int64_t total = static_cast<int64_t>(T) * per;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
+  const uint64_t bias = pair(-12615680.f, -12615680.f);  // as in bfp16_offset_value
+  for (int64_t i = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5; i < total;
+       i += warps) {
+    const int t = (i >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per))
+                                 : static_cast<int>(i / per);
+    const int v = static_cast<int>(i - static_cast<int64_t>(t) * per) * 32 + lane;
+    if (v < vecs) {
+      uint64_t acc[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-      int r[8];
-      float wt[8];
+      for (int e = 0; e < 4; ++e) acc[e] = 0;
+      for (int j0 = 0; j0 < k; j0 += SLOTS) {
+        int r[SLOTS];
+        float wt[SLOTS];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[j] = j0 + j < k ? __ldg(slot_dst + static_cast<int64_t>(t) * k + j0 + j) : -1;
-        if (r[j] >= y_rows) r[j] = -1;  // outside y: skipped like a -1 slot
-        wt[j] = j0 + j < k ? __ldg(w + static_cast<int64_t>(t) * k + j0 + j) : 0.f;
+        for (int j = 0; j < SLOTS; ++j) {
+          r[j] = -1;
+          if (j0 + j >= k) continue;
+          r[j] = __ldg(slot_dst + static_cast<int64_t>(t) * k + j0 + j);
+          wt[j] = __ldg(w + static_cast<int64_t>(t) * k + j0 + j);
+          if (r[j] >= y_rows) r[j] = -1;  // outside y: skipped like a -1 slot
+        }
+        uint4 qv[SLOTS];
+        int sv[SLOTS];
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+          if (r[j] >= 0) {
+            qv[j] = __ldg(reinterpret_cast<const uint4*>(y + r[j] * ld_y) + v);
+            sv[j] = __ldg(y_exp + (r[j] >> 4) * (ld_y / 8) + v);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < SLOTS; ++j) {
+          if (r[j] < 0) continue;
+          const uint32_t qw[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
+          if (sv[j] == kBfp16NonFinite) {  // a group holding Inf or NaN: fp16 values
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              acc[e] = fma2(pair(wt[j], wt[j]),
+                            pair(bfp16_decode(qw[e], false, sv[j]), bfp16_decode(qw[e], true, sv[j])),
+                            acc[e]);
+            continue;
+          }
+          const float wp = wt[j] * bfp16_pow2(sv[j]);
+          const uint64_t wp2 = pair(wp, wp);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            acc[e] = fma2(wp2,
+                          add2(pair(__uint_as_float(__byte_perm(qw[e], 0x4B40u, 0x5410u)),
+                                    __uint_as_float(__byte_perm(qw[e], 0x4B40u, 0x5432u))),
+                               bias),
+                          acc[e]);
+        }
       }
-      uint4 qv[8];
-      int sv[8];
+      if (F32_OUT) {  // the sum before its rounding (one shard's share of the output)
+        float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + static_cast<int64_t>(t) * d + 8 * v);
+        const float2 a0 = unpair(acc[0]), a1 = unpair(acc[1]), a2 = unpair(acc[2]), a3 = unpair(acc[3]);
+        __stcs(o, make_float4(a0.x, a0.y, a1.x, a1.y));
+        __stcs(o + 1, make_float4(a2.x, a2.y, a3.x, a3.y));
+      } else {
+        uint32_t pk[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (r[j] >= 0) {
-          qv[j] = __ldg(reinterpret_cast<const uint4*>(y + r[j] * ld_y) + v);
-          sv[j] = __ldg(y_exp + (r[j] >> 4) * (ld_y / 8) + v);
+        for (int e = 0; e < 4; ++e) {
+          const float2 a = unpair(acc[e]);
+          const __nv_bfloat162 b2 = __floats2bfloat162_rn(a.x, a.y);
+          pk[e] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        uint16_t* o = static_cast<uint16_t*>(out) + static_cast<int64_t>(t) * d + 8 * v;
+        if (out16) {
+          *reinterpret_cast<uint4*>(o) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         } else {
-          qv[j] = make_uint4(0u, 0u, 0u, 0u);
-          sv[j] = 0;
+          reinterpret_cast<uint2*>(o)[0] = make_uint2(pk[0], pk[1]);
+          reinterpret_cast<uint2*>(o)[1] = make_uint2(pk[2], pk[3]);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (r[j] < 0) continue;
-        const uint32_t qw[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
-        if (sv[j] == kBfp16NonFinite) {  // a group holding Inf or NaN: fp16 values
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            acc[e] = fmaf(wt[j], bfp16_decode(qw[e >> 1], e & 1, sv[j]), acc[e]);
-          continue;
-        }
-        const float wp = wt[j] * bfp16_pow2(sv[j]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = fmaf(wp, bfp16_offset_value(qw[e >> 1], e & 1), acc[e]);
-      }
-    }
-    if (F32_OUT) {  // the sum before its rounding (one shard's share of the output)
-      float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + static_cast<int64_t>(t) * d + 8 * v);
-      __stcs(o, make_float4(acc[0], acc[1], acc[2], acc[3]));
-      __stcs(o + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
-    } else {
-      uint32_t pk[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * e], acc[2 * e + 1]);
-        pk[e] = *reinterpret_cast<const uint32_t*>(&b2);
-      }
-      uint2* o = reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + static_cast<int64_t>(t) * d + 8 * v);
-      o[0] = make_uint2(pk[0], pk[1]);
-      o[1] = make_uint2(pk[2], pk[3]);
     }
   }
 }
@@ -171,15 +216,16 @@ cudaError_t launch_combine(const void* y, const int8_t* y_exp, int64_t ld_y, int
                            const int32_t* slot_dst, const float* w, int T, int k, int d,
                            void* out, bool out_f32, cudaStream_t stream) {
   if (y_exp) {
-    const int64_t tasks = static_cast<int64_t>(T) * (d / 8);
-    if (tasks == 0) return cudaSuccess;
-    const dim3 grid(stream_blocks(tasks));
+    if (T == 0) return cudaSuccess;
+    const int vecs = d / 8;
+    const dim3 grid(stream_blocks(static_cast<int64_t>(T) * ((vecs + 31) / 32) * 32));
     const uint16_t* yq = static_cast<const uint16_t*>(y);
-    if (out_f32)
-      return launch_pdl(k_combine_bfp16<true>, grid, dim3(256), 0, stream, yq, y_exp, ld_y,
-                        y_rows, slot_dst, w, T, k, d, out);
-    return launch_pdl(k_combine_bfp16<false>, grid, dim3(256), 0, stream, yq, y_exp, ld_y,
-                      y_rows, slot_dst, w, T, k, d, out);
+    const bool out16 = reinterpret_cast<uintptr_t>(out) % 16 == 0;
+    const bool threes = (k + 2) / 3 * 3 < (k + 3) / 4 * 4;
+    auto kern = threes ? (out_f32 ? k_combine_bfp16<3, true> : k_combine_bfp16<3, false>)
+                       : (out_f32 ? k_combine_bfp16<4, true> : k_combine_bfp16<4, false>);
+    return launch_pdl(kern, grid, dim3(256), 0, stream, yq, y_exp, ld_y, y_rows, slot_dst, w, T, k, d,
+                      out16, out);
   }
   // an fp32 y (megamoe_combine) always gives the bf16 output
   if (out_f32) return cudaErrorInvalidValue;
