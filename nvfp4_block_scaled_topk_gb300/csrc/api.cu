@@ -416,7 +416,7 @@ cudaError_t forward_l1(const megamoe_weights* w, const uint16_t* x, const int32_
     StageRange r("megamoe.route");
     e = launch_route(topk_ids, T * k, E, pad, wk.counts, wk.offsets, wk.padded_offsets,
                      wk.row_src, wk.rows, wk.slot_dst, wk.status, wk.status, 6, s,
-                     wk.route_hist);
+                     T * k >= kRouteMultiMinSlots ? wk.route_hist : nullptr);
     if (e != cudaSuccess) return e;
     StageRange ra("megamoe.amax_x");
     e = launch_amax(x, T, d, d, wk.amax_x, wk.status, false, s);

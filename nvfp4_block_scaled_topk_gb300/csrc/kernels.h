@@ -50,12 +50,15 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
 }
 
 size_t route_smem_bytes(int E);
-// Routing over many blocks (three passes) from this many slots on, when the
-// caller passes a block_hist scratch of kRouteMaxBlocks * E ints.
+// Routing over many blocks (three passes) when the caller passes a block_hist
+// scratch of kRouteMaxBlocks * E ints: megamoe_forward from this many slots on
+// (its workspace holds the scratch from there), the MXFP4 forward from
+// kMxRouteMultiMinSlots (api_mx.cu).
 constexpr int kRouteMultiMinSlots = 16384;
 constexpr int kRouteMaxBlocks = 256;
 // zero_words (may be null): n_zero 32-bit words cleared before anything else
 // (the forward's status word and amax accumulators).
+// row_src may be null: it is not written then.
 cudaError_t launch_route(const int32_t* ids, int n_slots, int E, int pad, int32_t* counts,
                          int32_t* offsets, int32_t* padded_offsets, int32_t* row_src,
                          int64_t row_capacity, int32_t* slot_dst, uint32_t* status,

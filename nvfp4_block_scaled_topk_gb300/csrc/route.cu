@@ -146,7 +146,7 @@ __device__ void route_block(const int32_t* ids, int n_slots, int E, int pad,
         const unsigned lower = peers & ((1u << lane) - 1u);
         const int rank = hist[warp * E + e] + __popc(lower);
         const int row = s_poff[e] + rank;
-        row_src[row] = s;
+        if (row_src) row_src[row] = s;
         slot_dst[s] = row;
       } else {
         slot_dst[s] = -1;
@@ -160,6 +160,7 @@ __device__ void route_block(const int32_t* ids, int n_slots, int E, int pad,
   }
 
   // padding rows of every expert, then everything past the last expert
+  if (!row_src) return;
   for (int e = tid; e < E; e += kRouteThreads) {
     for (int r = s_poff[e] + s_cnt[e]; r < s_poff[e + 1]; ++r) row_src[r] = -1;
   }
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1)
       if (e >= 0) {
         const unsigned lower = peers & ((1u << lane) - 1u);
         const int row = s_poff[e] + whist[warp * E + e] + __popc(lower);
-        row_src[row] = sv;
+        if (row_src) row_src[row] = sv;
         slot_dst[sv] = row;
       } else {
         slot_dst[sv] = -1;
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(kRouteThreads, 1)
   }
   // padding rows of every expert, then everything past the last expert,
   // spread over the blocks
+  if (!row_src) return;
   const int gtid = blockIdx.x * kRouteThreads + tid;
   const int gthreads = gridDim.x * kRouteThreads;
   for (int e = gtid; e < E; e += gthreads) {
@@ -442,7 +444,7 @@ cudaError_t launch_route(const int32_t* ids, int n_slots, int E, int pad, int32_
                          uint32_t* zero_words, int n_zero, cudaStream_t stream,
                          int32_t* block_hist) {
   const size_t smem = route_smem_bytes(E);
-  if (block_hist && n_slots >= kRouteMultiMinSlots) {
+  if (block_hist) {
     // chunks of at least 1024 slots, one per block, at most one block per SM
     const int blocks_max = std::min(kRouteMaxBlocks, num_sms());
     int chunk = (n_slots + blocks_max - 1) / blocks_max;
