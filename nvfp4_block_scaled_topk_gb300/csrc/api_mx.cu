@@ -410,7 +410,7 @@ megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K,
   if (e == cudaSuccess)
     e = launch_mx_product(MxProduct{wk.x.codes, wk.x.scales, w_codes, w_scales, T, N, K, out,
                                     out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status, wk.flags,
-                                    blocks},
+                                    blocks, false},
                           s);
   return cuda_status(e);
 }
@@ -478,10 +478,11 @@ megamoe_status megamoe_linear_mxfp4_backward(
   e = launch_mx_tiles(jobs, s, &blocks);
   const int64_t R = (T + 31) / 32 * 32;
   const MxProduct px{wk.dy.codes, wk.dy.scales, wk.w_t.codes, wk.w_t.scales, T, K, N, grad_x,
-                     grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status, wk.flags, blocks};
+                     grad_x_dtype == MEGAMOE_EPI_F32, ld_grad_x, wk.status, wk.flags, blocks,
+                     true};
   const MxProduct pw{wk.dy_t.codes, wk.dy_t.scales, wk.x_t.codes, wk.x_t.scales, N, K, R, grad_w,
                      grad_w_dtype == MEGAMOE_EPI_F32, ld_grad_w, wk.status, wk.flags,
-                     grad_x ? 0 : blocks};
+                     grad_x ? 0 : blocks, true};
   if (e == cudaSuccess) {
     if (grad_x && grad_w) e = launch_mx_products(px, pw, s);
     else if (grad_x) e = launch_mx_product(px, s);

@@ -401,21 +401,37 @@ cudaError_t launch_tiles(const MxJob* jobs, int count, cudaStream_t stream) {
 //
 // A stage of one CTA (a K step of 256) is 128 rows of each operand: 32 KB for
 // 128 x 256 of output, where a CTA on its own loads 48 KB for the same.  All
-// eight copies of a stage complete on one barrier of rank 0, whose one thread
+// eight copies of a stage complete on one barrier of rank 0, whose issuing warp
 // then copies the scales into tensor memory (tcgen05.cp, in order with the MMAs
 // and hidden behind them: measured 128.4 cycles an MMA with and 128.3 without)
 // and issues the MMAs of both CTAs.  Commits free the stage, and hand over the
-// accumulator, in both.  The accumulator leaves tensor memory for registers
-// before anything is stored, so the next tile's MMAs run under the stores,
-// which go through shared memory as 128-byte rows by tensor map.
+// accumulator, in both.
+//
+// Tensor memory holds two accumulators that have 48 of their 256 columns in
+// common: a tile's products start as soon as those have been read from the one
+// before, and the rest is read, rounded and stored meanwhile.  Stores go out as
+// 128-byte rows through 1 KB of shared memory a warp, by ordinary stores: stores
+// by tensor map go through the same unit as the loads, which then stand behind
+// them (1200 cycles at an issue that takes 130).  Eight rows at a time spread them
+// over the tile better than 32 (8192 x 2048 -> 7168 44.5 us against 47.6).
+//
+// Tiles go in bands of four rows of tiles where there are more than 16, so that
+// those in work at a time share few rows of either operand and find them in L2:
+// 16384 x 7168 -> 7168 250 us with one band, 238 with bands of eight rows, 235 of
+// four; with 16 rows of tiles one band is as good (66.6 against 67.2).
+//
+// 16384 x 7168 -> 7168 takes 220 us (7.65 PFLOP/s of the MMAs' 10), 4096 x 1536 ->
+// 24576 63 us (201 MB of output alone are 30): with every operand load left out
+// 214 and 60, so the tensor cores and, at short K, a tile's start and end bound it.
 // ---------------------------------------------------------------------------
 struct PairMaps {
-  CUtensorMap m, n, sfm, sfn, out;
+  CUtensorMap m, n, sfm, sfn;
 };
 
+template <int S>
 struct PairCfg {
   static constexpr int THREADS = 320;  // producer, MMA issuer, 8 epilogue warps
-  static constexpr int STAGES = 5;
+  static constexpr int STAGES = S;
   static constexpr int TILE = 128 * 128;  // a CTA's rows of either operand
   static constexpr int SF = 1024;
   static constexpr int OFF_N = TILE;
@@ -424,8 +440,11 @@ struct PairCfg {
   static constexpr int STAGE = OFF_SFN + 2 * SF;
   static constexpr uint32_t TX = 2 * STAGE;  // both CTAs
   static constexpr int SF_COLS = 8 + 16;
-  static constexpr int SF_COL0 = 256;  // two sets, taken in turn
-  static constexpr int STG = 32 * 128;  // 32 rows x 128 bytes per epilogue warp
+  // tensor memory: accumulators in turn at columns 0 and 208 (48 in common), then
+  // two sets of scales, in turn
+  static constexpr int ACC1 = 208;
+  static constexpr int SF_COL0 = 464;
+  static constexpr int STG = 8 * 128;  // 8 rows x 128 bytes per epilogue warp
   static constexpr int STG_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = STG_OFF + kEpiWarps * STG;
   static constexpr int SMEM = 1024 + BAR_OFF + 256;
@@ -433,10 +452,18 @@ struct PairCfg {
   static_assert(STAGE % 1024 == 0, "128-byte swizzle atoms");
 };
 
-template <typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
+// Tile q: bands of `tall` rows of tiles, column by column within a band.
+__device__ __forceinline__ void pair_tile(int q, int tall, int MT, int NT, int* mt, int* nt) {
+  const int band = q / (tall * NT), r = q - band * tall * NT;
+  const int rows = min(tall, MT - band * tall);
+  *nt = r / rows;
+  *mt = band * tall + r - *nt * rows;
+}
+
+template <typename O, int S>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS, 1)
     k_mx_gemm_pair(const __grid_constant__ PairMaps maps, const MxGemmArgs p) {
-  using C = PairCfg;
+  using C = PairCfg<S>;
   constexpr int STAGES = C::STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -454,6 +481,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
   const int MT = (p.M + 255) / 256, NT = (p.N + 255) / 256;
   const int KT = (p.K + 255) / 256;
   const int total = MT * NT;
+  const int tall = MT > 16 ? 4 : MT;  // rows of tiles in a band
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
 
   if (warp == 0 && lane == 0) {
@@ -461,7 +489,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
     prefetch_tensormap(&maps.n);
     prefetch_tensormap(&maps.sfm);
     prefetch_tensormap(&maps.sfn);
-    prefetch_tensormap(&maps.out);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -493,7 +520,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
-        const int nt = q / MT, mt = q - nt * MT;
+        int mt, nt;
+        pair_tile(q, tall, MT, NT, &mt, &nt);
         const int m0 = mt * 256 + rank * 128, n0 = nt * 256;
         for (int kt = 0; kt < KT; ++kt) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
@@ -535,8 +563,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
-        if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
-        tc_fence_after();
+        const uint32_t acc = tmem + acc_phase * C::ACC1;
         for (int kt = 0; kt < KT; ++kt) {
           if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
@@ -554,9 +581,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
               tc_copy_atom_pair(sf + 8 + 8 * h, sdesc_at(sd, C::SF + 512 * h));
               tc_copy_atom_pair(sf + 12 + 8 * h, sdesc_at(sd, 2 * C::SF + 512 * h));
             }
+          }
+          __syncwarp();
+          if (kt == 0) {
+            if (!mbar_wait(acc_empty, acc_phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+          }
+          if (leader) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              mma_mxf4_pair(tmem, sdesc_at(cd, 32 * c), sdesc_at(cd, C::OFF_N + 32 * c),
+              mma_mxf4_pair(acc, sdesc_at(cd, 32 * c), sdesc_at(cd, C::OFF_N + 32 * c),
                             idesc_mxf4(256, 256, c & 1), sf + 4 * (c >> 1), sf + 8 + 8 * (c >> 1),
                             (kt != 0 || c != 0) ? 1u : 0u);
             tc_commit_pair(&empty[stage]);
@@ -587,49 +624,72 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
     if (blockIdx.x == 0) collect_flags(p.flags, p.flag_count, threadIdx.x - 64, 256, p.status);
     uint32_t acc_phase = 0;
     for (int q = first; q < total; q += step) {
-      const int nt = q / MT, mt = q - nt * MT;
+      int mt, nt;
+      pair_tile(q, tall, MT, NT, &mt, &nt);
       if (!mbar_wait(acc_full, acc_phase, abort_flag, p.status, p.wait_limit_ns)) break;
       tc_fence_after();
-      const uint32_t base = tmem + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t base =
+          tmem + acc_phase * C::ACC1 + half * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
       const int m = mt * 256 + rank * 128 + quarter * 32, c0 = nt * 256 + half * 128;
-      uint32_t v[F32 ? 128 : 64];  // this lane's row: 128 values
+      // The next tile's products may start once the columns that the two
+      // accumulators share have been read: the last of this one at column 0 (the
+      // second half's), the first of the other.  The half without them lets go
+      // at once: it has read the whole tile before.
+      const bool shares = half != static_cast<int>(acc_phase);
+      auto let_go = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
+      };
+      if (!shares) let_go();
+      acc_phase ^= 1u;
+      constexpr int per = 16 / sizeof(O);
+      const int piece = lane & 7;
+      O* out = static_cast<O*>(p.out) + static_cast<int64_t>(m) * p.ld_out + c0 + piece * per;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {  // 64 columns, the shared ones first
+        const int at = 64 * (part ^ half);
+        uint32_t u[64];  // this lane's row
+        tmem_ld_32x32b_x32(base + at, u);
+        tmem_ld_32x32b_x32(base + at + 32, u + 32);
+        tmem_ld_wait();
+        if (part == 0 && shares) let_go();
+        if (m >= p.M) continue;  // warp-uniform
+        if (!F32) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        if (F32) {
-          tmem_ld_32x32b_x32(base + 32 * c, v + 32 * (F32 ? c : 0));
-        } else {
-          uint32_t u[32];
-          tmem_ld_32x32b_x32(base + 32 * c, u);
-          tmem_ld_wait();
+          for (int j = 0; j < 32; ++j) {
+            const __nv_bfloat162 h2 = __floats2bfloat162_rn(__uint_as_float(u[2 * j]),
+                                                            __uint_as_float(u[2 * j + 1]));
+            u[j] = *reinterpret_cast<const uint32_t*>(&h2);
+          }
+        }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(u[2 * j]),
-                                                           __uint_as_float(u[2 * j + 1]));
-            v[16 * c + j] = *reinterpret_cast<const uint32_t*>(&h);
+        for (int c = 0; c < 64 / COLS; ++c) {
+          const int col = at + c * COLS;
+          const bool in = c0 + col + piece * per < p.N;
+#pragma unroll 1
+          for (int g = 0; g < 4; ++g) {  // 8 rows
+            __syncwarp();
+            if (lane >> 3 == g) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
+                *reinterpret_cast<uint4*>(stg + piece * 128 + ((j ^ piece) * 16)) =
+                    make_uint4(u[32 * c + 4 * j], u[32 * c + 4 * j + 1], u[32 * c + 4 * j + 2],
+                               u[32 * c + 4 * j + 3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ r) * 16));
+              if (in && m + 8 * g + r < p.M)
+                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(8 * g + r) * p.ld_out + col) = x;
+            }
           }
         }
       }
-      if (F32) tmem_ld_wait();
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
-      acc_phase ^= 1u;
-      if (m >= p.M) continue;  // warp-uniform
-#pragma unroll
-      for (int c = 0; c < 128 / COLS; ++c) {
-        if (lane == 0) bulk_store_wait_read();  // the chunk before has left
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
-          *reinterpret_cast<uint4*>(stg + lane * 128 + ((j ^ (lane & 7)) * 16)) =
-              make_uint4(v[32 * c + 4 * j], v[32 * c + 4 * j + 1], v[32 * c + 4 * j + 2],
-                         v[32 * c + 4 * j + 3]);
-        fence_async_shared();
-        __syncwarp();
-        if (lane == 0 && c0 + c * COLS < p.N) tma_store_2d(&maps.out, stg, c0 + c * COLS, m);
-      }
     }
-    if (lane == 0) bulk_store_wait();
     __syncwarp();
   }
   __syncthreads();
@@ -640,7 +700,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg::THREADS, 1)
   }
 }
 
-template <typename O>
+template <typename O, int S>
 cudaError_t launch_pair(const MxJob& j, cudaStream_t stream) {
   const MxGemmArgs& a = j.a;
   PairMaps maps;
@@ -652,18 +712,14 @@ cudaError_t launch_pair(const MxJob& j, cudaStream_t stream) {
       !make_map(&maps.sfm, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.m_sf, sf_row / 4, (m + 127) / 128,
                 sf_row, 256, 1, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !make_map(&maps.sfn, CU_TENSOR_MAP_DATA_TYPE_UINT32, a.n_sf, sf_row / 4, (n + 127) / 128,
-                sf_row, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE) ||
-      !make_map(&maps.out,
-                sizeof(O) == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                a.out, n, m, static_cast<uint64_t>(a.ld_out) * sizeof(O), 128 / sizeof(O), 32,
-                CU_TENSOR_MAP_SWIZZLE_128B))
+                sf_row, 256, 2, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
-  auto kern = k_mx_gemm_pair<O>;
+  auto kern = k_mx_gemm_pair<O, S>;
   cudaError_t e =
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg::SMEM);
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PairCfg<S>::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(2 * std::min(num_sms() / 2, j.tiles)), dim3(PairCfg::THREADS),
-                    PairCfg::SMEM, stream, maps, a);
+  return launch_pdl(kern, dim3(2 * std::min(num_sms() / 2, j.tiles)), dim3(PairCfg<S>::THREADS),
+                    PairCfg<S>::SMEM, stream, maps, a);
 }
 
 // How a product of R x C with K steps KT runs.
@@ -738,8 +794,17 @@ cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
   if (g.R == 0 || g.C == 0) return cudaSuccess;
   const MxPlan p = plan_product(g.R, g.C, g.K);
   const MxJob j = job_of(g, p);
-  if (p.pair)
-    return g.out_f32 ? launch_pair<float>(j, stream) : launch_pair<__nv_bfloat16>(j, stream);
+  if (p.pair) {
+    // Six stages cover more of what a load waits for and of a tile's turn, worth
+    // most where tiles are short or the SM's memory is all shared memory already;
+    // five leave an SM's split of shared memory and cache where the rows' quantiser
+    // runs well, so that the two overlap.  Six / five (us): 4096 x 1536 -> 24576
+    // 63.3 / 65.7, the gradients of 8192 x 7168 -> 2048 134.7 / 137.2 with their
+    // quantiser; 8192 x 2048 -> 7168 46.3 / 44.3, 8192 x 4096 -> 4096 49.6 / 46.6.
+    const bool deep = g.K <= 7 * 256 || g.after_tiles;
+    if (g.out_f32) return deep ? launch_pair<float, 6>(j, stream) : launch_pair<float, 5>(j, stream);
+    return deep ? launch_pair<__nv_bfloat16, 6>(j, stream) : launch_pair<__nv_bfloat16, 5>(j, stream);
+  }
   return p.flip ? launch_tiles<64, true>(&j, 1, stream) : launch_tiles<128, false>(&j, 1, stream);
 }
 

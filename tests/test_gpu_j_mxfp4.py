@@ -147,6 +147,47 @@ def test_linear_large_tiles(cuda_lib, T, K, N):
     assert ((out - want).abs() <= bound).all()
 
 
+@pytest.mark.parametrize("T,K,N", [(4400, 320, 1312), (4700, 2080, 1536)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_linear_bands_of_large_tiles(cuda_lib, T, K, N, dtype):
+    """More than 16 rows of 256-row tiles, the last band of them and the last row
+    of a tile not full, a ragged last K step; the bounds of the test above, with
+    the output's own rounding."""
+    x, w = _x(T, K, seed=1).cuda(), _x(N, K, seed=2, wide=False).cuda()
+    weights = megamoe.MxLinearWeights.quantize(w)
+    epi = megamoe.EPI_F32 if dtype == torch.float32 else megamoe.EPI_BF16
+    wide = torch.full((T + 1, N + 8), 5.0, dtype=dtype, device="cuda")
+    out, _ = megamoe.linear_mxfp4(x, weights, out_dtype=epi, out=wide[:T, :N])
+    xq = megamoe.dequantize_mxfp4(*megamoe.quantize_mxfp4(x), dtype=torch.float32)
+    wq = megamoe.dequantize_mxfp4(*megamoe.quantize_mxfp4(w), dtype=torch.float32)
+    want = xq @ wq.t()
+    bound = 2 * (K / 64 + 18) * U * (xq.abs() @ wq.abs().t())
+    if dtype == torch.bfloat16:
+        bound = bound + 2.0 ** -8 * (want.abs() + bound)
+    assert ((out.float() - want).abs() <= bound).all()
+    assert (wide[T] == 5).all() and (wide[:, N:] == 5).all()
+
+
+def test_large_gradients(cuda_lib):
+    """Both gradients on pairs of CTAs, a number of tokens that fills no K step."""
+    T, K, N = 2600, 4160, 2080
+    x, w, g = _x(T, K, seed=3).cuda(), _x(N, K, seed=4, wide=False).cuda(), _x(T, N, seed=5).cuda()
+
+    def values(v, transpose=False):
+        return megamoe.dequantize_mxfp4(*megamoe.quantize_mxfp4(v, transpose=transpose),
+                                        dtype=torch.float32)
+
+    for gx_dt, gw_dt in ((torch.bfloat16, torch.float32), (torch.float32, torch.bfloat16)):
+        gx, gw, ws = megamoe.linear_mxfp4_backward(g, x, w, gx_dt, gw_dt)
+        assert ws[:4].view(torch.int32).item() == 0
+        for got, a, b in ((gx, values(g), values(w, True)), (gw, values(g, True), values(x, True))):
+            want = a @ b.t()
+            bound = 2 * (a.shape[1] / 64 + 18) * U * (a.abs() @ b.abs().t())
+            if got.dtype == torch.bfloat16:
+                bound = bound + 2.0 ** -8 * (want.abs() + bound)
+            assert ((got.float() - want).abs() <= bound).all()
+
+
 @pytest.mark.parametrize("T,K,N", [(1, 32, 32), (33, 96, 160), (64, 1536, 256), (333, 512, 800),
                                    (31, 2048, 96), (1000, 288, 480)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -264,6 +305,25 @@ def test_experts(cuda_lib, T, E, k, d, I, pad):
     assert_close_bf16(_np(out), want, what="mxfp4 experts")
     if T > 2:
         assert not out[1].any()
+
+
+@pytest.mark.parametrize("T,E,k", [(1024, 48, 4), (1023, 48, 4), (700, 64, 6), (2100, 8, 2),
+                                   (300, 16, 16)])
+def test_experts_routed_over_many_blocks(cuda_lib, T, E, k):
+    """Around and past the number of slots from which the routing takes several
+    blocks, on single CTAs and on pairs; one expert without rows; 16 slots."""
+    weights, values = _experts(E, 256, 256, E)
+    rng = np.random.default_rng(T)
+    x = torch.tensor(rng.standard_normal((T, 256)) * 0.5, dtype=torch.bfloat16)
+    ids = np.stack([rng.permutation(E)[:k] for _ in range(T)]).astype(np.int32)
+    ids[ids == 3] = -1
+    w = rng.random((T, k)).astype(np.float32)
+    fwd = megamoe.MxForward(weights, T, k)
+    out = fwd(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda())
+    assert fwd.read_status() == 0
+    want = mx.forward(_np(x), ids, w.astype(np.float64), values["w13"], values["w2"])
+    assert_close_bf16(_np(out), want, what="mxfp4 experts")
+    assert torch.equal(out, fwd(x.cuda(), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()))
 
 
 @pytest.mark.parametrize("T,dtype", [(1, torch.float32), (40, torch.bfloat16), (600, torch.float32)])
