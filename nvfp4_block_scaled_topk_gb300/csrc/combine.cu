@@ -79,28 +79,6 @@ __global__ void __launch_bounds__(256) k_round_bf16(const float4* __restrict__ i
   }
 }
 
-// a * b + c and a + b of two floats each, every element rounded as alone.
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pair(float lo, float hi) {
-  uint64_t d;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-  return d;
-}
-__device__ __forceinline__ float2 unpair(uint64_t d) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(d));
-  return r;
-}
-
 // The combine over a BFP16 y: a warp takes 256 consecutive features of a token,
 // a lane eight of them, which are one exponent group of each routed row.  Per
 // slot one 16-byte load of values and one exponent byte, the loads of SLOTS
@@ -127,7 +105,7 @@ __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restric
   const int per = (vecs + 31) / 32;  // warp tasks of a token
   const int64_t total = static_cast<int64_t>(T) * per;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x >> 5);
-  const uint64_t bias = pair(-12615680.f, -12615680.f);  // as in bfp16_offset_value
+  const uint64_t bias = pack2(-12615680.f, -12615680.f);  // as in bfp16_offset_value
   for (int64_t i = (blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x) >> 5; i < total;
        i += warps) {
     const int t = (i >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(i) / static_cast<uint32_t>(per))
@@ -164,17 +142,17 @@ __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restric
           if (sv[j] == kBfp16NonFinite) {  // a group holding Inf or NaN: fp16 values
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              acc[e] = fma2(pair(wt[j], wt[j]),
-                            pair(bfp16_decode(qw[e], false, sv[j]), bfp16_decode(qw[e], true, sv[j])),
+              acc[e] = fma2(pack2(wt[j], wt[j]),
+                            pack2(bfp16_decode(qw[e], false, sv[j]), bfp16_decode(qw[e], true, sv[j])),
                             acc[e]);
             continue;
           }
           const float wp = wt[j] * bfp16_pow2(sv[j]);
-          const uint64_t wp2 = pair(wp, wp);
+          const uint64_t wp2 = pack2(wp, wp);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             acc[e] = fma2(wp2,
-                          add2(pair(__uint_as_float(__byte_perm(qw[e], 0x4B40u, 0x5410u)),
+                          add2(pack2(__uint_as_float(__byte_perm(qw[e], 0x4B40u, 0x5410u)),
                                     __uint_as_float(__byte_perm(qw[e], 0x4B40u, 0x5432u))),
                                bias),
                           acc[e]);
@@ -182,14 +160,14 @@ __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restric
       }
       if (F32_OUT) {  // the sum before its rounding (one shard's share of the output)
         float4* o = reinterpret_cast<float4*>(static_cast<float*>(out) + static_cast<int64_t>(t) * d + 8 * v);
-        const float2 a0 = unpair(acc[0]), a1 = unpair(acc[1]), a2 = unpair(acc[2]), a3 = unpair(acc[3]);
+        const float2 a0 = unpack2(acc[0]), a1 = unpack2(acc[1]), a2 = unpack2(acc[2]), a3 = unpack2(acc[3]);
         __stcs(o, make_float4(a0.x, a0.y, a1.x, a1.y));
         __stcs(o + 1, make_float4(a2.x, a2.y, a3.x, a3.y));
       } else {
         uint32_t pk[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 a = unpair(acc[e]);
+          const float2 a = unpack2(acc[e]);
           const __nv_bfloat162 b2 = __floats2bfloat162_rn(a.x, a.y);
           pk[e] = *reinterpret_cast<const uint32_t*>(&b2);
         }

@@ -109,8 +109,8 @@ struct Word {
   static constexpr int NC = 2;
   uint32_t u;
   __device__ __forceinline__ void load(const X* p) { u = *reinterpret_cast<const uint32_t*>(p); }
-  // bit patterns of non-negative values order as the values do
-  __device__ __forceinline__ void widen(Word v) { u = __vmaxu2(u, v.u & 0x7fff7fffu); }
+  // (the sign bits of what comes out are of no use)
+  __device__ __forceinline__ void widen(Word v) { u = wider_pair<X>(u, v.u); }
   __device__ __forceinline__ float value(int c) const;
 };
 template <>
@@ -126,6 +126,7 @@ struct Word<float> {
   static constexpr int NC = 1;
   uint32_t u;
   __device__ __forceinline__ void load(const float* p) { u = *reinterpret_cast<const uint32_t*>(p); }
+  // bit patterns of non-negative values order as the values do
   __device__ __forceinline__ void widen(Word v) { u = max(u, v.u & 0x7fffffffu); }
   __device__ __forceinline__ float value(int) const { return __uint_as_float(u); }
 };
@@ -135,18 +136,22 @@ template <typename X>
 __device__ __forceinline__ void load_tile(const MxTile& job, int row_tile, int col_tile,
                                           uint8_t* buf) {
   constexpr int per = 16 / sizeof(X), vecs = kTileCols / per;
+  constexpr int rise = kTileThreads / vecs;  // rows between a thread's copies
+  const int64_t r0 = static_cast<int64_t>(row_tile) * kTileRows<X> + threadIdx.x / vecs;
+  const int c0 = col_tile * kTileCols + threadIdx.x % vecs * per;
   const X* x = static_cast<const X*>(job.x);
-  const int64_t r0 = static_cast<int64_t>(row_tile) * kTileRows<X>;
-  const int c0 = col_tile * kTileCols;
+  const X* from = x + r0 * job.ld + c0;
+  const int64_t hop = rise * job.ld;
+  const int64_t left = job.rows - r0;
+  const int here = c0 >= job.K ? 0 : left > kTileRows<X> ? kTileRows<X> : static_cast<int>(left);
+  const uint32_t to = smem_u32(buf + 16 * threadIdx.x);
 #pragma unroll
   for (int i = 0; i < kTileBytes / 16 / kTileThreads; ++i) {
-    const int t = threadIdx.x + kTileThreads * i;
-    const int r = t / vecs, c = t % vecs * per;
-    const bool in = r0 + r < job.rows && c0 + c < job.K;
-    const X* from = in ? x + (r0 + r) * job.ld + c0 + c : x;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(buf + 16 * t)),
-                 "l"(from), "r"(in ? 16 : 0)
+    const bool in = i * rise < here;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 16 * kTileThreads * i),
+                 "l"(in ? from : x), "r"(in ? 16 : 0)
                  : "memory");
+    from += hop;
   }
 }
 
@@ -221,7 +226,7 @@ __device__ __forceinline__ bool encode_tile(const MxTile& job, int row_tile, int
     const int64_t block = r0 / 32 + blk;
 #pragma unroll
     for (int c = 0; c < W::NC; ++c) {
-      const uint32_t byte = mx_scale_byte(__float_as_uint(m.value(c)));
+      const uint32_t byte = mx_scale_byte(__float_as_uint(m.value(c)) & 0x7fffffffu);
       const float inv = mx_inverse(byte);
       uint32_t q[4];
 #pragma unroll

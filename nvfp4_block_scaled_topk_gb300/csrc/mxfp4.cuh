@@ -40,7 +40,11 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
   float s[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s[i] = v[i] * inv;
+  for (int i = 0; i < 8; i += 2) {
+    const float2 p = unpack2(mul2(pack2(v[i], v[i + 1]), pack2(inv, inv)));
+    s[i] = p.x;
+    s[i + 1] = p.y;
+  }
   uint32_t c;
   asm("{\n\t.reg .b8 a, b, c, d;\n\t"
       "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
@@ -96,6 +100,23 @@ __host__ __device__ __forceinline__ int64_t mx_routed_offset(int b) {
   return static_cast<int64_t>(b >> 3) * 16 + (b & 7);
 }
 
+// The larger magnitudes of two pairs of 2-byte elements; NaN if either is.  The
+// sign bits are of no use.
+template <typename X>
+__device__ __forceinline__ uint32_t wider_pair(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t wider_pair<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+template <>
+__device__ __forceinline__ uint32_t wider_pair<__half>(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+
 // Eight consecutive elements: their bits, the largest |x| in a form that
 // ordinary integer maxima keep ordered, and their values.
 template <typename X>
@@ -106,8 +127,7 @@ struct Eight16 {  // 2-byte types: two magnitudes side by side in a word
   __device__ __forceinline__ void load(const X* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void clear() { q = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ uint32_t widest() const {
-    const uint32_t m = 0x7fff7fffu;
-    return __vmaxu2(__vmaxu2(q.x & m, q.y & m), __vmaxu2(q.z & m, q.w & m));
+    return wider_pair<X>(wider_pair<X>(q.x, q.y), wider_pair<X>(q.z, q.w)) & 0x7fff7fffu;
   }
   __device__ __forceinline__ static uint32_t wider(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 };
