@@ -92,10 +92,12 @@ __global__ void __launch_bounds__(256)
 // columns a thread takes 32 rows of two neighbouring columns into registers (a
 // 2-byte type: one 32-bit word per row, the warp's words consecutive; fp32: one
 // column), and their codes go out through shared memory as 64-byte (fp32: 32-byte)
-// runs.  What bounds it is the alternation of copies, encoding and barriers in a
-// block, so six small blocks an SM beat three large ones: 8195 x 7168 bf16 along
-// columns 29.5 us (5.0 TB/s) against 30.9 with 256 threads, fp32 of 8192 rows 42.5
-// (6.3 TB/s) against 45.2.
+// runs.  Instructions bound it (65 to 70 % of the issue slots), so a thread's
+// copies and stores walk pointers and magnitudes and products go two an
+// instruction; six blocks of 128 threads an SM, whose copies, encoding and barriers
+// overlap, beat three of 256 (29.5 us against 30.9 before that).  8195 x 7168 bf16
+// along columns 28.5 us (5.2 TB/s), 16384 rows 54 (5.5 TB/s), 8192 x 7168 fp32 43.5
+// (6.1 TB/s).
 constexpr int kTileCols = 64;
 constexpr int kTileThreads = 128;
 constexpr int kTileBytes = 128 * kTileThreads;  // of x in a tile, for every type
@@ -174,27 +176,24 @@ __device__ __forceinline__ bool encode_tile(const MxTile& job, int row_tile, int
       const int t = threadIdx.x + kTileThreads * i;
       const int r = t / vecs, col = c0 + t % vecs * per;
       const X* e = tile + t * per;
-      float v[per];
-      uint32_t m = 0;
       const uint4 q = *reinterpret_cast<const uint4*>(e);
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float e8[8] = {};
+      W word, most;
+      most.u = 0;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        W word;
         word.u = w[j];
+        most.widen(word);
 #pragma unroll
-        for (int c = 0; c < W::NC; ++c) {
-          v[W::NC * j + c] = word.value(c);
-          m = max(m, __float_as_uint(v[W::NC * j + c]) & 0x7fffffffu);
-        }
+        for (int c = 0; c < W::NC; ++c) e8[W::NC * j + c] = word.value(c);
       }
+      uint32_t m = __float_as_uint(most.value(0)) & 0x7fffffffu;
+      if (W::NC == 2) m = max(m, __float_as_uint(most.value(1)) & 0x7fffffffu);
       // the lanes of a row's block of 32 are neighbours
 #pragma unroll
       for (int o = 1; o < 32 / per; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
       const uint32_t byte = mx_scale_byte(m);
-      float e8[8] = {};
-#pragma unroll
-      for (int j = 0; j < per; ++j) e8[j] = v[j];
       const uint32_t code = mx_codes8(e8, mx_inverse(byte));
       if (r0 + r < rows) {
         if (col < K) {
@@ -223,7 +222,7 @@ __device__ __forceinline__ bool encode_tile(const MxTile& job, int row_tile, int
       v[i].load(from + i * kTileCols);
       m.widen(v[i]);
     }
-    const int64_t block = r0 / 32 + blk;
+    uint32_t bytes[W::NC];
 #pragma unroll
     for (int c = 0; c < W::NC; ++c) {
       const uint32_t byte = mx_scale_byte(__float_as_uint(m.value(c)) & 0x7fffffffu);
@@ -239,22 +238,32 @@ __device__ __forceinline__ bool encode_tile(const MxTile& job, int row_tile, int
       const int col = W::NC * across + c;
       *reinterpret_cast<uint4*>(s_codes + col * (16 * blocks) +
                                 ((blk ^ (across % blocks)) * 16)) = make_uint4(q[0], q[1], q[2], q[3]);
-      if (c0 + col < K && (block * 32 < rows || (job.col_layout == MEGAMOE_SCALES_MMA &&
-                                                 block < mx_atoms(padded) * 4))) {
-        job.col_scales[scale_offset(job.col_layout, c0 + col, block, padded)] =
-            static_cast<uint8_t>(byte);
-        bad |= byte == kMxNan;
+      bytes[c] = byte;
+    }
+    const int64_t block = r0 / 32 + blk;
+    const bool atom = job.col_layout == MEGAMOE_SCALES_MMA;
+    const bool stored = block * 32 < rows || (atom && block < mx_atoms(padded) * 4);
+    // two neighbouring columns, of which the first is even: rows of one atom
+    uint8_t* scale = job.col_scales + scale_offset(job.col_layout, c0 + W::NC * across, block, padded);
+#pragma unroll
+    for (int c = 0; c < W::NC; ++c) {
+      if (c0 + W::NC * across + c < K && stored) {
+        scale[c * (atom ? 16 : padded / 32)] = static_cast<uint8_t>(bytes[c]);
+        bad |= bytes[c] == kMxNan;
       }
     }
     __syncthreads();
+    constexpr int hop = kTileThreads / blocks;  // columns between a thread's chunks
+    const int part = threadIdx.x % blocks, col0 = threadIdx.x / blocks;
+    uint8_t* to = job.col_codes + (c0 + col0) * (padded / 2) + r0 / 2 + part * 16;
+    const bool in = r0 + part * 32 < rows;
 #pragma unroll
-    for (int i = 0; i < kTileCols * blocks / kTileThreads; ++i) {
-      const int t = threadIdx.x + kTileThreads * i;
-      const int col = t / blocks, part = t % blocks;
-      if (c0 + col < K && r0 + part * 32 < rows)
-        *reinterpret_cast<uint4*>(job.col_codes + (c0 + col) * (padded / 2) + r0 / 2 + part * 16) =
-            *reinterpret_cast<const uint4*>(s_codes + col * (16 * blocks) +
-                                            ((part ^ (col / W::NC % blocks)) * 16));
+    for (int i = 0; i < kTileCols / hop; ++i) {
+      const int col = col0 + hop * i;
+      if (in && c0 + col < K)
+        *reinterpret_cast<uint4*>(to) = *reinterpret_cast<const uint4*>(
+            s_codes + col * (16 * blocks) + ((part ^ (col / W::NC % blocks)) * 16));
+      to += hop * (padded / 2);
     }
   }
   return bad;
