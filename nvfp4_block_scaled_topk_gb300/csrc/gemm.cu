@@ -14,14 +14,18 @@
 // per K step into two TMEM ranges), so SiLU(gate) * up is a per-lane epilogue.
 //
 // Roles (448 threads, one CTA per SM, grid = number of SMs):
-//   warp 0      producer (one lane): per stage, the weights' block-scale atoms
+//   warp 0      producer: per stage, the weights' block-scale atoms
 //               (bulk copies) and the token tile's row-major block scales
 //               (tensor map) on one barrier, then the stage's weight codes
 //               (one bulk copy of pre-swizzled blocks) and token codes
 //               (tensor map, 128-byte swizzle) on another, into a
 //               STAGES-deep ring;
-//   warp 1      TMEM allocator; one lane issues tcgen05.mma and commits
-//               stage-free / accumulator-ready;
+//   warp 1      TMEM allocator; issues tcgen05.mma and commits stage-free /
+//               accumulator-ready;
+//               (both run as whole warps with one elected lane issuing: a
+//               branch taken by one lane alone spent 700 cycles a stage on
+//               descriptors that a converged warp keeps in uniform registers;
+//               48 experts, 8192 tokens 1507 -> 1381 us)
 //   warps 2..5, 10..13  epilogue, two warps per 32-lane TMEM quarter taking
 //               alternate 16-column chunks: tcgen05.ld, alpha scaling,
 //               SiLU * up -> bf16 + amax (L1), bf16, or fp32 (L2), staged
@@ -30,9 +34,16 @@
 //               scales into its own 32-lane quarter of tensor memory with
 //               tcgen05.st (every quarter holds the same copy, the layout the
 //               block-scaled MMA reads).  Scales do not go through the tensor
-//               pipe (a tcgen05.cp costs about as much as an MMA), and the
+//               pipe (a tcgen05.cp costs about as much as an MMA of few
+//               tokens; it hides behind one of N = 256, see mx_gemm.cu), and the
 //               token tile's first row always lands in the first scale
 //               column whatever row the tile starts at.
+// MXFP4 operands (MX instantiations, for up to about 115 rows an expert) have one
+// power-of-two scale per 32 elements: half as many scale atoms, each serving two
+// MMAs by its scale id, no global scales, and SiLU * up is quantised to MXFP4 in
+// the epilogue, where a warp holds whole blocks of 32 features.  Bound by HBM:
+// 8 tokens over 48 experts of 7168 x 2048 (33 of them used) 119 us for the layer,
+// 6.3 TB/s of weights.
 // Split-K (kEpiPartial* instantiations, used by the dense linear when it has
 // fewer tiles than SMs): each tile's K range is cut into pieces whose fp32
 // partial sums go to planes that k_splitk_finish adds in a fixed order.

@@ -16,9 +16,14 @@
 // expert.  A tile of at most 128 rows leaves the second CTA without rows of its
 // own: it loads its half of the weights and stores nothing.
 //
-// What bounds it: what an SM takes in, about 50 bytes a cycle, 35 KB a K step
-// (700 cycles against the MMAs' 513); one CTA on 128 x 256 takes 51 KB for half
-// the product.
+// What bounds it: at some 250 rows an expert the weights from HBM.  48 experts of
+// 7168 x 2048, 2003 tokens of 6 slots: gate and up 148 us for 0.81 GB (81 % of the
+// measured copy rate, the MMAs busy for 76 %), down 100 us for 0.52 GB and y.  At
+// 1024 rows what an SM takes in: 35 KB a K step (one CTA on 128 x 256 takes 51 KB
+// for half the product), 600 to 700 cycles against the MMAs' 513.  Measured and
+// not kept here: the accumulators with columns in common, the ordinary stores and
+// the sixth stage of mx_gemm.cu (316 against 315 us for the layer), and tiles of
+// at most 128 rows shared between the two CTAs (314.5 against 313).
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -106,8 +106,9 @@ __device__ __forceinline__ int lane_expert(int i, int sub, int lanes) {
 //     for each lane, and each lane counts those before its own (a larger score,
 //     or an equal one at a lower index): its slot.
 // More than 32 of them (ties) are taken one by one.  The work per token bounds
-// this kernel, not its bytes; at 16384 tokens of 384 experts in 8 groups, top-6,
-// with 16-byte loads of four experts, taking all by warp maxima took 30.2 us.
+// this kernel, not its bytes: 16384 tokens of 384 fp32 logits in 8 groups, top-6,
+// take 14.4 us (1.8 TB/s, 75 % of the issue slots), with all of the k taken by
+// warp maxima instead 30.2 us.  One token takes 2 us, a launch's latency.
 // Scores for the choice use the hardware's exponential and reciprocal (within
 // 2^-20 of their value, the same for equal logits); the weights do not.
 template <typename L, int NV, int V>
@@ -286,7 +287,8 @@ __device__ __forceinline__ void store_grad(__nv_bfloat16* p, float v) { *p = __f
 //   softmax                dl_e = s_e (g_e - sum_i g_i s_i) for every expert
 // In the first three only the taken experts have a gradient and only their
 // logits are read: the row is filled with zeros and the k values stored over
-// them after a warp barrier.
+// them after a warp barrier.  Bound by those stores: 16384 tokens of 384 experts
+// 6.2 us (25 MB written, 4.1 TB/s, most of it into L2).
 template <typename L>
 __global__ void __launch_bounds__(kWarps * 32)
     k_scored_router_backward(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
