@@ -414,10 +414,12 @@ cudaError_t launch_tiles(const MxJob* jobs, int count, cudaStream_t stream) {
 // Tensor memory holds two accumulators that have 48 of their 256 columns in
 // common: a tile's products start as soon as those have been read from the one
 // before, and the rest is read, rounded and stored meanwhile.  Stores go out as
-// 128-byte rows through 1 KB of shared memory a warp, by ordinary stores: stores
-// by tensor map go through the same unit as the loads, which then stand behind
-// them (1200 cycles at an issue that takes 130).  Eight rows at a time spread them
-// over the tile better than 32 (8192 x 2048 -> 7168 44.5 us against 47.6).
+// 128-byte rows through 2 KB of shared memory a warp, 16 rows at a time, by
+// ordinary stores: stores by tensor map go through the same unit as the loads,
+// which then stand behind them (1200 cycles at an issue that takes 130).  4096 x
+// 1536 -> 24576 takes 60.3 us so, 63.2 with 8 rows at a time, 66 with 32 rows and
+// the five stages that leave room for them, 71 with a lane storing its own row in
+// sectors of 32 bytes.
 //
 // Tiles go in bands of four rows of tiles where there are more than 16, so that
 // those in work at a time share few rows of either operand and find them in L2:
@@ -425,8 +427,11 @@ cudaError_t launch_tiles(const MxJob* jobs, int count, cudaStream_t stream) {
 // four; with 16 rows of tiles one band is as good (66.6 against 67.2).
 //
 // 16384 x 7168 -> 7168 takes 220 us (7.65 PFLOP/s of the MMAs' 10), 4096 x 1536 ->
-// 24576 63 us (201 MB of output alone are 30): with every operand load left out
-// 214 and 60, so the tensor cores and, at short K, a tile's start and end bound it.
+// 24576 60 us (201 MB of output alone are 30).  What bounds it: at long K the MMAs
+// and the loads that they wait for (214 us with every operand load left out); at
+// 6 and 8 K steps the epilogue, 4800 cycles a tile against the MMAs' 3100, which
+// reads tensor memory and stages through shared memory under the MMAs' own use of
+// both.
 // ---------------------------------------------------------------------------
 struct PairMaps {
   CUtensorMap m, n, sfm, sfn;
@@ -448,10 +453,10 @@ struct PairCfg {
   // two sets of scales, in turn
   static constexpr int ACC1 = 208;
   static constexpr int SF_COL0 = 464;
-  static constexpr int STG = 8 * 128;  // 8 rows x 128 bytes per epilogue warp
+  static constexpr int STG = 16 * 128;  // 16 rows x 128 bytes per epilogue warp
   static constexpr int STG_OFF = STAGES * STAGE;
   static constexpr int BAR_OFF = STG_OFF + kEpiWarps * STG;
-  static constexpr int SMEM = 1024 + BAR_OFF + 256;
+  static constexpr int SMEM = 768 + BAR_OFF + 256;  // from a multiple of 256 up to one of 1024
   static_assert(SMEM <= 232448, "shared memory budget");
   static_assert(STAGE % 1024 == 0, "128-byte swizzle atoms");
 };
@@ -469,9 +474,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS,
     k_mx_gemm_pair(const __grid_constant__ PairMaps maps, const MxGemmArgs p) {
   using C = PairCfg<S>;
   constexpr int STAGES = C::STAGES;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(256) uint8_t smem_pair[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+      (reinterpret_cast<uintptr_t>(smem_pair) + 1023) & ~static_cast<uintptr_t>(1023));
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // rank 0's
   uint64_t* empty = full + STAGES;
   uint64_t* acc_full = empty + STAGES;
@@ -672,22 +677,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS,
           const int col = at + c * COLS;
           const bool in = c0 + col + piece * per < p.N;
 #pragma unroll 1
-          for (int g = 0; g < 4; ++g) {  // 8 rows
+          for (int g = 0; g < 2; ++g) {  // 16 rows
             __syncwarp();
-            if (lane >> 3 == g) {
+            if (lane >> 4 == g) {
 #pragma unroll
               for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
-                *reinterpret_cast<uint4*>(stg + piece * 128 + ((j ^ piece) * 16)) =
+                *reinterpret_cast<uint4*>(stg + (lane & 15) * 128 + ((j ^ piece) * 16)) =
                     make_uint4(u[32 * c + 4 * j], u[32 * c + 4 * j + 1], u[32 * c + 4 * j + 2],
                                u[32 * c + 4 * j + 3]);
             }
             __syncwarp();
+            uint4 x[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 4; ++i) {
               const int r = 4 * i + (lane >> 3);
-              const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ r) * 16));
-              if (in && m + 8 * g + r < p.M)
-                *reinterpret_cast<uint4*>(out + static_cast<int64_t>(8 * g + r) * p.ld_out + col) = x;
+              x[i] = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) * 16));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 16 * g + 4 * i + (lane >> 3);
+              if (in && m + r < p.M)
+                __stcs(reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * p.ld_out + col), x[i]);
             }
           }
         }
@@ -804,7 +814,8 @@ cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
     // five leave an SM's split of shared memory and cache where the rows' quantiser
     // runs well, so that the two overlap.  Six / five (us): 4096 x 1536 -> 24576
     // 63.3 / 65.7, the gradients of 8192 x 7168 -> 2048 134.7 / 137.2 with their
-    // quantiser; 8192 x 2048 -> 7168 46.3 / 44.3, 8192 x 4096 -> 4096 49.6 / 46.6.
+    // quantiser; 8192 x 2048 -> 7168 46.3 / 44.3, 8192 x 4096 -> 4096 49.6 / 46.6
+    // (all with 8 rows staged at a time).
     const bool deep = g.K <= 7 * 256 || g.after_tiles;
     if (g.out_f32) return deep ? launch_pair<float, 6>(j, stream) : launch_pair<float, 5>(j, stream);
     return deep ? launch_pair<__nv_bfloat16, 6>(j, stream) : launch_pair<__nv_bfloat16, 5>(j, stream);
