@@ -87,20 +87,20 @@ __global__ void __launch_bounds__(256)
 
 // Along columns: codes [K, R / 2] and scales of x^T, R = rows up to a multiple
 // of 32 (elements past the last row count as zeros); on request the rows' own
-// codes and scales from the same read of x.  A block walks over tiles of 128
-// rows (fp32: 64) x 64 columns, the next one on its way into shared memory
+// codes and scales from the same read of x.  A block walks over tiles of 256
+// rows (fp32: 128) x 64 columns, the next one on its way into shared memory
 // (16-byte asynchronous copies) while it encodes the present one.  Down the
 // columns a thread takes 32 rows of two neighbouring columns into registers (a
 // 2-byte type: one 32-bit word per row, the warp's words consecutive; fp32: one
-// column), and their codes go out through shared memory as 64-byte (fp32: 32-byte)
+// column), and their codes go out through shared memory as 128-byte (fp32: 64-byte)
 // runs.  Instructions bound it (65 to 70 % of the issue slots), so a thread's
 // copies and stores walk pointers and magnitudes and products go two an
-// instruction; six blocks of 128 threads an SM, whose copies, encoding and barriers
-// overlap, beat three of 256 (29.5 us against 30.9 before that).  8195 x 7168 bf16
-// along columns 28.5 us (5.2 TB/s), 16384 rows 54 (5.5 TB/s), 8192 x 7168 fp32 43.5
-// (6.1 TB/s).
+// instruction.  8195 x 7168 bf16 along columns 29.7 us (5.0 TB/s), 16384 rows 57
+// (5.2 TB/s), 8192 x 7168 fp32 42 (6.3 TB/s).  Six blocks of 128 threads an SM
+// instead of three of 256 are 4 % faster on their own, but their 64-byte runs cost
+// the reader of the codes more (quantised and read back 55.5 us against 54.9).
 constexpr int kTileCols = 64;
-constexpr int kTileThreads = 128;
+constexpr int kTileThreads = 256;
 constexpr int kTileBytes = 128 * kTileThreads;  // of x in a tile, for every type
 template <typename X>
 constexpr int kTileRows = kTileBytes / kTileCols / static_cast<int>(sizeof(X));
@@ -394,7 +394,7 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t codes, u
     const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up), s);
     u[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
 }
 __device__ __forceinline__ void store_values(float* p, uint32_t codes, uint32_t byte) {
   const float s = mx_scale_value(byte);
@@ -404,13 +404,15 @@ __device__ __forceinline__ void store_values(float* p, uint32_t codes, uint32_t 
     const uint32_t b = e2m1x2_halves(codes >> (16 * i + 8) & 0xffu);
     const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
     const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    reinterpret_cast<float4*>(p)[i] = make_float4(fa.x * s, fa.y * s, fb.x * s, fb.y * s);
+    __stcs(reinterpret_cast<float4*>(p) + i, make_float4(fa.x * s, fa.y * s, fb.x * s, fb.y * s));
   }
 }
 
 // The values: four bytes of codes in, eight elements out per thread, four of
 // them at once; no division where the rows of out follow each other.  Bound by
-// HBM: 8195 x 7168 to bf16 24.8 us (6.0 TB/s).
+// HBM: 8195 x 7168 to bf16 21.4 us (6.9 TB/s).  The values are not read again here,
+// so they are stored to leave L2 first: 4 us less for the call that quantises the
+// next matrix and reads its codes back.
 template <typename O>
 __global__ void __launch_bounds__(256)
     k_mx_values(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
@@ -500,7 +502,7 @@ cudaError_t launch_mx_tiles(MxTiles jobs, cudaStream_t s, int* blocks) {
   auto kern = wide ? k_mx_tiles<true> : k_mx_tiles<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  // six blocks an SM by shared memory
+  // three blocks an SM by shared memory
   const int n = std::min(jobs.tiles, 768 / kTileThreads * num_sms());
   if (blocks) *blocks = n;
   return launch_pdl(kern, dim3(n), dim3(kTileThreads), smem, s, jobs);
