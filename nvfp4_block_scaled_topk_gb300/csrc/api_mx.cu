@@ -107,9 +107,11 @@ MxQuant quant_of(const void* x, int type, int64_t rows, int K, int64_t ld, bool 
 
 // Large batches run on pairs of CTAs with 256-row tiles (mx_experts.cu), from
 // about this many rows an expert on: below, most experts' rows fit one 128-row
-// tile of the single CTAs.  48 experts (single / pairs, us): 106 rows an expert
-// 224 / 236, 128 rows 258 / 245, 160 rows 328 / 263.
-constexpr double kPairRows = 115.0;
+// tile of the single CTAs.  Single / pairs, us, at 90, 110 and 130 rows an expert:
+// 48 experts of 7168 x 2048 with even loads 211 / 224, 223 / 232, 259 / 239, with
+// uneven ones (weights of 1 / rank^0.3) 218 / 224, 236 / 234, 256 / 241; 64 experts
+// of 2048 x 1024 even 65 / 66, 70 / 69, 93 / 72, uneven 68 / 67, 78 / 73, 84 / 75.
+constexpr double kPairRows = 105.0;
 bool pair_experts(int T, int k, int E) {
   return num_sms() >= 2 && static_cast<double>(T) * k / E >= kPairRows;
 }

@@ -38,7 +38,7 @@
 //               tokens; it hides behind one of N = 256, see mx_gemm.cu), and the
 //               token tile's first row always lands in the first scale
 //               column whatever row the tile starts at.
-// MXFP4 operands (MX instantiations, for up to about 115 rows an expert) have one
+// MXFP4 operands (MX instantiations, for up to about 105 rows an expert) have one
 // power-of-two scale per 32 elements: half as many scale atoms, each serving two
 // MMAs by its scale id, no global scales, and SiLU * up is quantised to MXFP4 in
 // the epilogue, where a warp holds whole blocks of 32 features.  Bound by HBM:
