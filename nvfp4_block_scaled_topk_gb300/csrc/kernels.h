@@ -279,7 +279,8 @@ struct MxProduct {
   // findings of the quantising launch before it, for the status word
   const uint32_t* flags;
   int flag_count;
-  // the launch before it ran with all of an SM's shared memory (k_mx_tiles)
+  // one of a linear's gradients: the launch before it ran with all of an SM's
+  // shared memory (k_mx_tiles), and the other one may share the launch
   bool after_tiles;
 };
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream);

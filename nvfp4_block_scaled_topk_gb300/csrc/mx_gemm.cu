@@ -761,17 +761,25 @@ int pick_cluster(int64_t tiles, int64_t steps, double sums) {
   return best;
 }
 
-MxPlan plan_product(int64_t R, int64_t C, int64_t K) {
+MxPlan plan_product(const MxProduct& g) {
+  const int64_t R = g.R, C = g.C, K = g.K;
   MxPlan p{};
   const int64_t pairs = (R + 255) / 256 * ((C + 255) / 256);
   const int64_t tiles = (R + 127) / 128 * ((C + 127) / 128);
   p.flip = R <= 64;
   p.cluster = 1;
   // A pair takes four tiles' worth in the time that an SM takes one of its own
-  // tiles (operands per product halved), so it is chosen where it has enough to
-  // do and pads to less than twice the tiles: 128 x 1536 -> 24576 took 24.8 us
-  // in pairs, half of them empty.
-  p.pair = !p.flip && pairs * 2 >= num_sms() && pairs * 4 < tiles * 2;
+  // tiles (operands per product halved), so it is chosen where half of the pairs
+  // have work and it pads to less than twice the tiles: 128 x 1536 -> 24576 took
+  // 24.8 us in pairs, half of them empty.  Single / pairs (us, with the
+  // quantiser): 75 pairs 3815 x 5664 -> 1248 39.6 / 27.4; 64 2048 x 4096 -> 2048
+  // 15.7 / 14.0; 48 1536 x 7168 -> 2048 19.8 / 18.1; 40 1280 x 4096 -> 2048 14.5 /
+  // 12.9, 1280 x 1536 -> 2048 9.4 / 9.7; 32 1024 x 7168 -> 2048 15.0 / 16.3.
+  // A linear's two gradients go in one launch of single CTAs where neither fills
+  // the pairs, so for them all pairs have to have work: 570 x 320 -> 8384 22.4 us
+  // in one launch, 28.9 with one of them in 66 pairs.
+  const int64_t least = g.after_tiles ? num_sms() / 2 : num_sms() / 4;
+  p.pair = !p.flip && pairs >= least && pairs * 4 < tiles * 2;
   if (p.pair) {
     p.tiles = static_cast<int>(pairs);
     return p;
@@ -806,7 +814,7 @@ MxJob job_of(const MxProduct& g, const MxPlan& p) {
 
 cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
   if (g.R == 0 || g.C == 0) return cudaSuccess;
-  const MxPlan p = plan_product(g.R, g.C, g.K);
+  const MxPlan p = plan_product(g);
   const MxJob j = job_of(g, p);
   if (p.pair) {
     // Six stages cover more of what a load waits for and of a tile's turn, worth
@@ -824,7 +832,7 @@ cudaError_t launch_mx_product(const MxProduct& g, cudaStream_t stream) {
 }
 
 cudaError_t launch_mx_products(const MxProduct& g, const MxProduct& h, cudaStream_t stream) {
-  const MxPlan p = plan_product(g.R, g.C, g.K), q = plan_product(h.R, h.C, h.K);
+  const MxPlan p = plan_product(g), q = plan_product(h);
   if (p.pair || p.flip || q.pair || q.flip || g.R == 0 || h.R == 0) {
     const cudaError_t e = launch_mx_product(g, stream);
     return e != cudaSuccess ? e : launch_mx_product(h, stream);
