@@ -90,23 +90,31 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// Wait until the phase with parity `parity` of `bar` has completed.  Returns
-// false if the abort flag was raised or the wait ran past `limit_ns` (in which
-// case the abort flag is raised here and `status` gets the TIMEOUT bit).  Limits
-// below kPreciseLimitNs are kept to by polling; above, the hardware's suspended
-// wait is cheaper.
+// By a whole converged warp: wait until the phase with parity `parity` of `bar`
+// has completed.  Returns false if the abort flag was raised or the wait ran past
+// `limit_ns` (in which case the abort flag is raised here and `status` gets the
+// TIMEOUT bit).  The warp decides as one: what follows a wait (tcgen05.ld and st,
+// elect.sync, __syncwarp) needs all of its lanes, and near the limit some of them
+// could find the phase complete and others the time up.  Limits below
+// kPreciseLimitNs are kept to by polling; above, the hardware's suspended wait is
+// cheaper.
 constexpr uint64_t kPreciseLimitNs = 1000 * 1000;
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* status, uint64_t limit_ns = kWaitTimeoutNs) {
+  constexpr unsigned all = 0xffffffffu;
   const bool precise = limit_ns < kPreciseLimitNs;
-  if (!precise && mbar_try_wait(bar, parity)) return true;
+  if (!precise && __all_sync(all, mbar_try_wait(bar, parity))) return true;
   const uint64_t t0 = globaltimer();
   while (true) {
-    if (precise ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
-    if (*abort_flag) return false;
-    if (globaltimer() - t0 > limit_ns) {
-      *abort_flag = 1;
-      set_status(status, MEGAMOE_DEV_TIMEOUT);
+    if (__all_sync(all, precise ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)))
+      return true;
+    const bool aborted = *abort_flag != 0, late = globaltimer() - t0 > limit_ns;
+    if (__any_sync(all, aborted || late)) {
+      if (!aborted && late) {
+        *abort_flag = 1;
+        set_status(status, MEGAMOE_DEV_TIMEOUT);
+      }
+      __syncwarp();
       return false;
     }
   }

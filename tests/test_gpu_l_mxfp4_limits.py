@@ -1,0 +1,36 @@
+"""Waits that run out in the MXFP4 products: the kernel gives up as whole warps,
+lets its copies land, reports MEGAMOE_DEV_TIMEOUT and returns, and the next call
+is right."""
+
+import numpy as np
+import pytest
+import torch
+
+from nvfp4_block_scaled_topk_gb300 import megamoe
+
+pytestmark = pytest.mark.gpu
+
+LIMIT_NS = 100  # less than any load takes
+
+
+def _normal(rows, cols, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(rows, cols, generator=g) * scale).to(torch.bfloat16).cuda()
+
+
+# both products in one launch of single CTAs; in clusters of their own; on pairs
+@pytest.mark.parametrize("T,K,N", [(333, 512, 800), (7000, 256, 256), (2600, 4160, 2080)])
+def test_gradients(cuda_lib, T, K, N):
+    x, w, g = _normal(T, K, 1), _normal(N, K, 2, 0.02), _normal(T, N, 3)
+    want_x, want_w, _ = megamoe.linear_mxfp4_backward(g, x, w)
+    torch.cuda.synchronize()
+    megamoe.set_wait_limit_ns(LIMIT_NS)
+    try:
+        _, _, ws = megamoe.linear_mxfp4_backward(g, x, w)
+        torch.cuda.synchronize()
+        assert ws[:4].view(torch.int32).item() == megamoe.DEV_TIMEOUT
+    finally:
+        megamoe.set_wait_limit_ns(0)
+    got_x, got_w, ws = megamoe.linear_mxfp4_backward(g, x, w, ws=ws)
+    assert ws[:4].view(torch.int32).item() == 0
+    assert torch.equal(got_x, want_x) and torch.equal(got_w, want_w)
