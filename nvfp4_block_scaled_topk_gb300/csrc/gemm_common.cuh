@@ -146,6 +146,39 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// A producer's last act, for each of its ring's barriers (issue i went to slot
+// i % stages): the copies into the last `stages` slots have landed.  On an ordinary
+// way out they are about to be used anyhow; when another warp has given up on a
+// wait after all of them were issued, nothing else keeps the block from leaving its
+// shared memory to the next one with copies still on their way into it.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int issued) {
+  for (int s = 0; s < stages && s < issued; ++s) {
+    const int i = issued - 1 - s;
+    mbar_drain(&full[i % stages], static_cast<uint32_t>(i / stages) & 1u);
+  }
+}
+
+// The same for a pair of CTAs, whose copies all complete on rank 0's barriers.  A
+// barrier counts both CTAs' copies and may never complete when one stopped before
+// the other, so the wait is one that no copy takes: at most kPairDrainNs, and all
+// of it in a CTA that gave up.  Rank 1, which cannot wait on the barriers, leaves
+// with rank 0 (cluster_sync).
+constexpr uint64_t kPairDrainNs = 5000000;
+__device__ __forceinline__ void drain_pair_copies(uint64_t* full, int stages, int issued, int rank,
+                                                  bool gave_up) {
+  const uint64_t t0 = globaltimer();
+  if (gave_up) {
+    while (globaltimer() - t0 < kPairDrainNs) __nanosleep(1000);
+    return;
+  }
+  for (int s = 0; rank == 0 && s < stages && s < issued; ++s) {
+    const int i = issued - 1 - s;
+    while (!mbar_test_wait(&full[i % stages], static_cast<uint32_t>(i / stages) & 1u) &&
+           globaltimer() - t0 < kPairDrainNs)
+      __nanosleep(100);
+  }
+}
+
 // Grid-wide arrival of this CTA (thread 0 only), then a bounded wait until
 // `expected` CTAs have arrived.  The fence before the arrival publishes this
 // CTA's earlier writes (ordered before by the caller's __syncthreads); the

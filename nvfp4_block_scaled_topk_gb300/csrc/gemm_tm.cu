@@ -237,13 +237,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
         }
       }
-      if (!ok) {  // unwinding: let every copy already in flight land first
-        for (int s = 0; s < STAGES && s < issued; ++s) {
-          const uint32_t parity = static_cast<uint32_t>((issued - 1 - s) / STAGES) & 1u;
-          mbar_drain(&full[s], parity);
-          mbar_drain(&sf_full[s], parity);
-        }
-      }
+      drain_copies(full, STAGES, issued);
+      drain_copies(sf_full, STAGES, issued);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -165,7 +165,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       const bool leader = elect_one();
       const uint64_t pol_w_once = policy_evict_first(), pol_w_again = policy_evict_normal();
       const uint64_t pol_t = policy_evict_last();
-      int stage = 0, e_lo = 0;
+      int stage = 0, issued = 0, e_lo = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int tile = first; ok && tile < total; tile += step) {
@@ -200,19 +200,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             tma_load_3d_pair(sb + C::OFF_SFW, &maps.w_sf, bar, kt * 256, sf_y, sf_z, pol_w);
           }
           __syncwarp();
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) {
-        // unwinding: let the copies in flight land first.  A stage's barrier
-        // counts both CTAs' copies and may never complete when one stopped
-        // before the other, so wait a time that no copy takes.
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 5000000) __nanosleep(1000);
-      }
+      drain_pair_copies(full, STAGES, issued, rank, !ok);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -183,12 +183,8 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
       const uint8_t* sfn = p.n_sf + (nt * BN >> 7) * atoms * 512;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
-      bool ok = true;
       for (int kt = k0; kt < k1; ++kt) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
         uint8_t* sb = smem + stage * C::STAGE;
         if (leader) {
           mbar_arrive_expect_tx(&full[stage], C::M_TILE + p.n_box * 128 + 2 * C::SF);
@@ -204,12 +200,7 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
           phase ^= 1u;
         }
       }
-      if (!ok) {  // unwinding: let every copy already in flight land first
-        for (int s = 0; s < STAGES && s < issued; ++s) {
-          const int i = issued - 1 - s;
-          mbar_drain(&full[i % STAGES], static_cast<uint32_t>(i / STAGES) & 1u);
-        }
-      }
+      drain_copies(full, STAGES, issued);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -525,7 +516,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS,
       // (the whole warp, one lane of it issuing: elect_one)
       const bool leader = elect_one();
       const uint64_t pol = policy_evict_normal();
-      int stage = 0;
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
@@ -547,19 +538,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS,
             tma_load_2d_pair(sb + C::OFF_SFN, &maps.sfn, bar, kt * 256, n0 >> 7, pol);
           }
           __syncwarp();
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      if (!ok) {
-        // unwinding: let the copies in flight land first.  A stage's barrier
-        // counts both CTAs' copies and may never complete when one stopped
-        // before the other, so wait a time that no copy takes.
-        const uint64_t t0 = globaltimer();
-        while (globaltimer() - t0 < 5000000) __nanosleep(1000);
-      }
+      drain_pair_copies(full, STAGES, issued, rank, !ok);
     }
     __syncwarp();
   } else if (warp == 1) {

@@ -127,12 +127,8 @@ __global__ void __launch_bounds__(kThreads) k_mx_linear_few(const __grid_constan
       const uint8_t* sf = p.w_sf + mt * mx_atoms(p.K) * 512;
       int stage = 0, issued = 0;
       uint32_t phase = 0;
-      bool ok = true;
       for (int kt = k0; kt < k1; ++kt) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
         uint8_t* sb = smem + stage * kStage;
         if (leader) {
           mbar_arrive_expect_tx(&full[stage], kStage);
@@ -146,12 +142,7 @@ __global__ void __launch_bounds__(kThreads) k_mx_linear_few(const __grid_constan
           phase ^= 1u;
         }
       }
-      if (!ok) {  // unwinding: let every copy already in flight land first
-        for (int s = 0; s < kStages && s < issued; ++s) {
-          const int i = issued - 1 - s;
-          mbar_drain(&full[i % kStages], static_cast<uint32_t>(i / kStages) & 1u);
-        }
-      }
+      drain_copies(full, kStages, issued);
     }
     __syncwarp();
   } else if (warp == 1) {
