@@ -693,6 +693,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<S>::THREADS,
     __syncwarp();
   }
   __syncthreads();
+  // rank 0's commits arrive on rank 1's barriers too: none is on its way after the last
+  if (warp == 1) mbar_drain(drain, 0);
+  __syncwarp();
   cluster_sync();  // neither CTA leaves while the other still reaches into it
   if (warp == 1) {
     tc_fence_after();
