@@ -717,9 +717,14 @@ typedef struct megamoe_mx_weights {
 /*
  * megamoe_forward_mxfp4 -- the routed-expert forward with MXFP4 weights and
  * activations: route -> quantise x into routed rows -> L1 grouped GEMM with
- * SiLU(gate)*up, quantised to MXFP4 in its epilogue -> L2 grouped GEMM into a
- * BFP16 y -> top-k weighted combine.  Arguments, shapes and errors as
- * megamoe_forward; workspace of megamoe_workspace_size_mxfp4 bytes.
+ * SiLU(gate)*up, quantised to MXFP4 in its epilogue -> L2 grouped GEMM into y
+ * -> top-k weighted combine in fp32, rounded once to bf16.  Arguments, shapes and
+ * errors as megamoe_forward; workspace of megamoe_workspace_size_mxfp4 bytes.
+ *
+ * y, the down product of each slot between the fp32 sum and the combine, is held
+ * in 16 bits: one power-of-two exponent for 32 neighbouring columns of a row, so
+ * that a value is off by at most 2^-15 of the largest of the 32 and no token
+ * depends on another.  Inf and NaN are kept and leave the others as they are.
  */
 size_t megamoe_workspace_size_mxfp4(int T, int k, int E, int d, int I, int pad);
 megamoe_status megamoe_forward_mxfp4(const megamoe_mx_weights* w, const uint16_t* x,

@@ -137,7 +137,7 @@ struct ForwardWs {
   uint8_t* xq_scales;  // routed layout, 16 bytes per K step of 256, or (pairs) atoms
   uint8_t* hq_codes;
   uint8_t* hq_scales;
-  uint16_t* y;  // BFP16
+  uint16_t* y;  // BFP16 by rows: one exponent word per 32 columns of a row
   int8_t* y_exp;
   int32_t* r_ids;
   float* r_w;
@@ -163,7 +163,7 @@ ForwardWs carve_forward(void* base, int T, int k, int E, int d, int I, int pad) 
   w.xq_scales = c.take(whole * (d / 16));
   w.hq_codes = c.take(rows * (I / 2));
   w.hq_scales = c.take(whole * (I / 16));
-  uint8_t* y = c.take(MEGAMOE_BFP16_BYTES(rows, d));
+  uint8_t* y = c.take(rows * d * 2 + rows * (d / 32) * 2);
   w.y = reinterpret_cast<uint16_t*>(y);
   w.y_exp = y ? reinterpret_cast<int8_t*>(y + rows * d * 2) : nullptr;
   w.r_ids = ints(slots);
@@ -261,7 +261,7 @@ megamoe_status run_mx_forward(const megamoe_mx_weights* w, const uint16_t* x,
     e = launch_mx_experts(m, s);
     if (e == cudaSuccess)
       e = launch_combine(wk.y, wk.y_exp, d, wk.rows, wk.slot_dst, topk_weights, T, k, d, out, false,
-                         s);
+                         s, true);
     return cuda_status(e);
   }
   const int tile_n = pick_tile_n(static_cast<double>(T) * k / E);
@@ -300,7 +300,8 @@ megamoe_status run_mx_forward(const megamoe_mx_weights* w, const uint16_t* x,
   g.tile_n = tile_n;
   e = launch_grouped_gemm(g, s);
   if (e == cudaSuccess)
-    e = launch_combine(wk.y, wk.y_exp, d, wk.rows, wk.slot_dst, topk_weights, T, k, d, out, false, s);
+    e = launch_combine(wk.y, wk.y_exp, d, wk.rows, wk.slot_dst, topk_weights, T, k, d, out, false, s,
+                       true);
   return cuda_status(e);
 }
 

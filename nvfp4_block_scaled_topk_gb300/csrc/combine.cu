@@ -81,7 +81,8 @@ __global__ void __launch_bounds__(256) k_round_bf16(const float4* __restrict__ i
 
 // The combine over a BFP16 y: a warp takes 256 consecutive features of a token,
 // a lane eight of them, which are one exponent group of each routed row.  Per
-// slot one 16-byte load of values and one exponent byte, the loads of SLOTS
+// slot one 16-byte load of values and one exponent byte (BY_ROW: BFP16 by rows, one
+// exponent word for four lanes), the loads of SLOTS
 // slots in flight; the slot's power of two is folded into its weight (w * 2^s is
 // exact), so each element costs a byte permute and, two elements at a time, an
 // exact subtraction and a fused multiply-add into the fp32 sum (the same sum as
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(256) k_round_bf16(const float4* __restrict__ i
 // features, six 40.7, four (64 registers) 39.7, three 38.1 (5.3 TB/s), two 41.2;
 // for 8 slots four took 45.4 and three 49.7.  So three or four, whichever leaves
 // fewer places empty in the last round.
-template <int SLOTS, bool F32_OUT>
+template <int SLOTS, bool F32_OUT, bool BY_ROW>
 __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restrict__ y,
                                                        const int8_t* __restrict__ y_exp,
                                                        int64_t ld_y, int64_t y_rows,
@@ -132,22 +133,26 @@ __global__ void __launch_bounds__(256) k_combine_bfp16(const uint16_t* __restric
         for (int j = 0; j < SLOTS; ++j) {
           if (r[j] >= 0) {
             qv[j] = __ldg(reinterpret_cast<const uint4*>(y + r[j] * ld_y) + v);
-            sv[j] = __ldg(y_exp + (r[j] >> 4) * (ld_y / 8) + v);
+            sv[j] = BY_ROW ? __ldg(reinterpret_cast<const uint16_t*>(y_exp) +
+                                   r[j] * (ld_y / kRowGroup) + v / (kRowGroup / 8))
+                           : __ldg(y_exp + (r[j] >> 4) * (ld_y / 8) + v);
           }
         }
 #pragma unroll
         for (int j = 0; j < SLOTS; ++j) {
           if (r[j] < 0) continue;
           const uint32_t qw[4] = {qv[j].x, qv[j].y, qv[j].z, qv[j].w};
-          if (sv[j] == kBfp16NonFinite) {  // a group holding Inf or NaN: fp16 values
+          const int s = BY_ROW ? bfp16_row_exponent(sv[j]) : sv[j];
+          if (BY_ROW ? (sv[j] & kRowSpecial) != 0 : s == kBfp16NonFinite) {  // a group holding Inf or NaN
+            auto value = [&](int e, bool hi) {
+              return BY_ROW ? bfp16_special_decode(qw[e], hi, s) : bfp16_decode(qw[e], hi, s);
+            };
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              acc[e] = fma2(pack2(wt[j], wt[j]),
-                            pack2(bfp16_decode(qw[e], false, sv[j]), bfp16_decode(qw[e], true, sv[j])),
-                            acc[e]);
+              acc[e] = fma2(pack2(wt[j], wt[j]), pack2(value(e, false), value(e, true)), acc[e]);
             continue;
           }
-          const float wp = wt[j] * bfp16_pow2(sv[j]);
+          const float wp = wt[j] * bfp16_pow2(s);
           const uint64_t wp2 = pack2(wp, wp);
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -192,7 +197,7 @@ static unsigned stream_blocks(int64_t tasks) {
 
 cudaError_t launch_combine(const void* y, const int8_t* y_exp, int64_t ld_y, int64_t y_rows,
                            const int32_t* slot_dst, const float* w, int T, int k, int d,
-                           void* out, bool out_f32, cudaStream_t stream) {
+                           void* out, bool out_f32, cudaStream_t stream, bool by_row) {
   if (y_exp) {
     if (T == 0) return cudaSuccess;
     const int vecs = d / 8;
@@ -200,8 +205,11 @@ cudaError_t launch_combine(const void* y, const int8_t* y_exp, int64_t ld_y, int
     const uint16_t* yq = static_cast<const uint16_t*>(y);
     const bool out16 = reinterpret_cast<uintptr_t>(out) % 16 == 0;
     const bool threes = (k + 2) / 3 * 3 < (k + 3) / 4 * 4;
-    auto kern = threes ? (out_f32 ? k_combine_bfp16<3, true> : k_combine_bfp16<3, false>)
-                       : (out_f32 ? k_combine_bfp16<4, true> : k_combine_bfp16<4, false>);
+    if (by_row && out_f32) return cudaErrorInvalidValue;  // no shards of the MXFP4 forward
+    auto kern = by_row    ? (threes ? k_combine_bfp16<3, false, true> : k_combine_bfp16<4, false, true>)
+                : out_f32 ? (threes ? k_combine_bfp16<3, true, false> : k_combine_bfp16<4, true, false>)
+                          : (threes ? k_combine_bfp16<3, false, false>
+                                    : k_combine_bfp16<4, false, false>);
     return launch_pdl(kern, grid, dim3(256), 0, stream, yq, y_exp, ld_y, y_rows, slot_dst, w, T, k, d,
                       out16, out);
   }

@@ -496,6 +496,36 @@ __device__ __forceinline__ float bfp16_decode(uint32_t word, bool hi, int s) {
   return bfp16_offset_value(word, hi) * bfp16_pow2(s);
 }
 
+// BFP16 by rows (the MXFP4 forward): one 16-bit exponent word per 32 neighbouring
+// columns of a row, [rows, ld / 32] of them, so that what a token's row holds depends
+// on no other token.  A value is off by at most half a unit, 2^-15 of its group's
+// largest.  Word: the exponent in its low byte, kRowSpecial when the group holds Inf
+// or NaN; those are then the stored values 65535 (Inf), 1 (-Inf) and 0 (NaN), and
+// the group's finite values, whose exponent keeps them off these three, are as exact
+// as without them.
+constexpr int kRowGroup = 32;
+constexpr uint32_t kRowSpecial = 0x100;
+__device__ __forceinline__ int bfp16_row_exponent(uint32_t word) {
+  return static_cast<int8_t>(word & 0xffu);
+}
+// Word of a group that holds Inf or NaN, from the bits of its largest finite |v|.
+__device__ __forceinline__ uint32_t bfp16_special_word(uint32_t mbits) {
+  const int s = bfp16_exponent(mbits);
+  const bool high = __uint_as_float(mbits) * bfp16_pow2(-s) >= 32766.5f;
+  return kRowSpecial | (static_cast<uint32_t>(high ? s + 1 : s) & 0xffu);
+}
+// A value of such a group, scaled by sc = 2^-exponent.
+__device__ __forceinline__ uint32_t bfp16_special_value(float v, float sc) {
+  if (fabsf(v) < INFINITY) return bfp16_round_int(v * sc);
+  return v > 0.f ? 65535u : v < 0.f ? 1u : 0u;
+}
+__device__ __forceinline__ float bfp16_special_decode(uint32_t word, bool hi, int s) {
+  const uint32_t u = hi ? word >> 16 : word & 0xffffu;
+  if (u == 0u) return __uint_as_float(0x7fffffffu);
+  if (u == 1u || u == 65535u) return u == 1u ? -INFINITY : INFINITY;
+  return bfp16_offset_value(word, hi) * bfp16_pow2(s);
+}
+
 // ---------------------------------------------------------------------------
 // Two floats an instruction, every element rounded as alone
 // ---------------------------------------------------------------------------

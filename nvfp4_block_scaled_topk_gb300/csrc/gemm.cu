@@ -541,6 +541,46 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                   reinterpret_cast<const uint4*>(stg)[lane];
             __syncwarp();
           }
+        } else if (C::BFP16 && MX) {
+          tmem_ld_wait();
+          // BFP16 by rows: the warp's lanes hold one group of 32 columns of each
+          // token, whose largest value is one warp reduction; lane j turns that of
+          // token j into an exponent for all
+          uint32_t mine = 0u;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, g[j] & 0x7fffffffu);
+            if (lane == j) mine = m;
+          }
+          uint32_t word = static_cast<uint32_t>(bfp16_exponent(mine)) & 0xffu;
+          if (__any_sync(0xffffffffu, lane < rows && mine >= 0x7f800000u)) {
+            // Inf or NaN: the exponent of the others
+            uint32_t finite = 0u;
+#pragma unroll 1
+            for (int j = 0; j < 16; ++j) {
+              uint32_t b = 0u;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i == j) b = g[i] & 0x7fffffffu;
+              const uint32_t m = __reduce_max_sync(0xffffffffu, b < 0x7f800000u ? b : 0u);
+              if (lane == j) finite = m;
+            }
+            if (mine >= 0x7f800000u) word = bfp16_special_word(finite);
+          }
+          const float own_scale = bfp16_pow2(-bfp16_row_exponent(word));
+          uint16_t* q = reinterpret_cast<uint16_t*>(p.out) + (row0 + n0) * p.ld_out + f0 + lane;
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float v = __uint_as_float(g[j]), sc = __shfl_sync(0xffffffffu, own_scale, j);
+            if (j < rows)
+              q[j * p.ld_out] = fabsf(v) < INFINITY
+                                    ? bfp16_round_int(v * sc)
+                                    : static_cast<uint16_t>(bfp16_special_value(v, sc));
+          }
+          if (lane < rows)
+            reinterpret_cast<uint16_t*>(
+                p.out_exp)[(row0 + n0 + lane) * (p.ld_out / kRowGroup) + f0 / kRowGroup] =
+                static_cast<uint16_t>(word);
         } else if (C::BFP16) {
           tmem_ld_wait();
           // rows row0 + n0 .. + 15 (16-aligned: pads and tiles are multiples

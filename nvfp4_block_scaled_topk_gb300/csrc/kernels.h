@@ -145,7 +145,7 @@ struct GemmLaunch {
   // MXFP4 operands: w_scales atoms of 128 rows x 4 blocks of 32, act_scales in
   // the routed layout (16 bytes per K step of 256, eight used), no global
   // scales; SILU_MUL writes rq_codes and rq_scales (routed layout) instead of
-  // out, BFP16 as for NVFP4; no split
+  // out, BFP16 is by rows; no split
   bool mx = false;
 };
 // Split-K choice for a GEMM of about `tiles` whole-K tiles of KT K steps: the
@@ -241,7 +241,7 @@ cudaError_t launch_mx_routed(const uint16_t* x, int64_t T, int d, const int32_t*
 // The routed experts' products on pairs of CTAs (large batches): experts' rows
 // start at multiples of 128, scales of rows in the atom layout.  y null: gate and
 // up (N = 2 I), SiLU * up quantised to h_codes and h_scales (atom layout); else
-// down (N = d), BFP16 y and its exponents.
+// down (N = d), y in BFP16 by rows and its exponents.
 struct MxExperts {
   const uint8_t* act_codes;
   const uint8_t* act_scales;
@@ -308,11 +308,12 @@ int num_sms();
 // out: bf16 [T, d] (one rounding of the fp32 sum), or with out_f32 the fp32
 // sum itself.
 // y fp32 [*, ld_y] (y_exp null) or BFP16 (uint16 values at y, exponents
-// [rows / 16, ld_y / 8] at y_exp)
+// [rows / 16, ld_y / 8] at y_exp), or with by_row BFP16 by rows (exponent
+// words, 16 bits, [rows, ld_y / 32])
 // (y_rows: rows of a BFP16 y; slots at or past it are skipped)
 cudaError_t launch_combine(const void* y, const int8_t* y_exp, int64_t ld_y, int64_t y_rows,
                            const int32_t* slot_dst, const float* w, int T, int k, int d,
-                           void* out, bool out_f32, cudaStream_t stream);
+                           void* out, bool out_f32, cudaStream_t stream, bool by_row = false);
 // Non-finite scan of a forward's stage outputs (MEGAMOE_STAGE_* bits in
 // *flags, cleared first); valid rows only, every output row.
 cudaError_t launch_stage_scan(const int32_t* row_src, const int32_t* padded_total,

@@ -8,8 +8,9 @@
 //                 is then in one thread, which quantises its blocks of 32
 //                 features to MXFP4 (codes row-major, scales in the atom layout
 //                 that the down product reads)
-//   down:         256 output features; y in BFP16 (one exponent per 16 rows x 8
-//                 columns), through shared memory as 128-byte rows by tensor map
+//   down:         256 output features; y in BFP16 by rows (one exponent word per
+//                 32 columns of a row, all in one lane), through shared memory as
+//                 128-byte rows by tensor map
 //
 // Experts' rows start at multiples of 128 (the caller pads so), so that a CTA's
 // 128 rows are whole scale atoms and the rows of a stored box belong to one
@@ -25,7 +26,6 @@
 // the sixth stage of mx_gemm.cu (316 against 315 us for the layer), and tiles of
 // at most 128 rows shared between the two CTAs (314.5 against 313).
 #include <cuda.h>
-#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -49,7 +49,7 @@ struct PairArgs {
   int E, N, K;  // N: weight rows of an expert
   uint8_t* h_codes;   // gate and up: [rows, N / 4]
   uint8_t* h_scales;  // atom layout of [rows, N / 2]
-  int8_t* y_exp;      // down: [rows / 16, N / 8]
+  uint16_t* y_exp;    // down: [rows, N / 32]
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -327,55 +327,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
           *reinterpret_cast<uint16_t*>(p.h_scales + mx_atom_offset(row0 + lane, f >> 5, mx_atoms(I))) =
               static_cast<uint16_t>(bytes);
       } else {
-        // Groups of 16 rows (half a warp) x 8 columns share an exponent: 16 of
-        // them here.  Each exchange of the reduction hands half of the groups
-        // over, so 15 shuffles leave lane g (and 16 + g) with the largest value
-        // of group g, which it turns into an exponent for all.  (Group by group,
-        // 64 shuffles in chains, took 6200 cycles of a tile's 9100.)
-        uint32_t m[16];
-#pragma unroll
-        for (int g = 0; g < 16; ++g) {
-          m[g] = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) m[g] = max(m[g], v[8 * g + j] & 0x7fffffffu);
-          if (!valid) m[g] = 0;  // rows that are not the expert's take no part
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-          const bool high = (lane & o) != 0;
-#pragma unroll
-          for (int i = 0; i < o; ++i) {
-            const uint32_t keep = high ? m[i + o] : m[i], give = high ? m[i] : m[i + o];
-            m[i] = max(keep, __shfl_xor_sync(0xffffffffu, give, o));
-          }
-        }
-        const int own = bfp16_exponent(m[0]);
+        // BFP16 by rows: this lane's row has four groups of 32 columns here.  The low
+        // 16 bits of x + 1.5 * 2^23 + 2^15 are rint(x) + 32768 (x is exact, so the
+        // fused sum rounds once, as bfp16_round_int does).
         const int c0 = ti.mt * 256 + half * 128;
-        p.y_exp[((row0 + (lane & 16)) >> 4) * (p.N / 8) + c0 / 8 + (lane & 15)] =
-            static_cast<int8_t>(own);
-        const float own_scale = own == kBfp16NonFinite ? 0.f : bfp16_pow2(-own);
-        const bool odd = __any_sync(0xffffffffu, own == kBfp16NonFinite);
-        uint32_t w[64];
+        uint32_t w[64], words[2] = {0, 0};
 #pragma unroll
-        for (int g = 0; g < 16; ++g) {
-          const float sc = __shfl_sync(0xffffffffu, own_scale, (lane & 16) | g);
-          // the low 16 bits of x + 1.5 * 2^23 + 2^15 are rint(x) + 32768 (x is
-          // exact, so the fused sum rounds once, as bfp16_round_int does)
+        for (int g = 0; g < 4; ++g) {
+          uint32_t m = 0;
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[4 * g + j] = __byte_perm(
-                __float_as_uint(__fmaf_rn(__uint_as_float(v[8 * g + 2 * j]), sc, 12615680.f)),
-                __float_as_uint(__fmaf_rn(__uint_as_float(v[8 * g + 2 * j + 1]), sc, 12615680.f)),
-                0x5410);
-          if (odd && sc == 0.f) {  // a group holding Inf or NaN: fp16 bits
+          for (int j = 0; j < 32; ++j) m = max(m, v[32 * g + j] & 0x7fffffffu);
+          uint32_t word = static_cast<uint32_t>(bfp16_exponent(m)) & 0xffu;
+          if (m < 0x7f800000u || !valid) {
+            const float sc = bfp16_pow2(-bfp16_row_exponent(word));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const __half2 h = __floats2half2_rn(__uint_as_float(v[8 * g + 2 * j]),
-                                                  __uint_as_float(v[8 * g + 2 * j + 1]));
-              w[4 * g + j] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int j = 0; j < 16; ++j)
+              w[16 * g + j] = __byte_perm(
+                  __float_as_uint(__fmaf_rn(__uint_as_float(v[32 * g + 2 * j]), sc, 12615680.f)),
+                  __float_as_uint(__fmaf_rn(__uint_as_float(v[32 * g + 2 * j + 1]), sc, 12615680.f)),
+                  0x5410);
+          } else {  // Inf or NaN: the exponent of the others
+            m = 0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const uint32_t b = v[32 * g + j] & 0x7fffffffu;
+              m = b < 0x7f800000u ? max(m, b) : m;
             }
+            word = bfp16_special_word(m);
+            const float sc = bfp16_pow2(-bfp16_row_exponent(word));
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[16 * g + j] = bfp16_special_value(__uint_as_float(v[32 * g + 2 * j]), sc) |
+                              bfp16_special_value(__uint_as_float(v[32 * g + 2 * j + 1]), sc) << 16;
           }
+          words[g >> 1] |= word << (16 * (g & 1));
         }
+        if (valid)
+          *reinterpret_cast<uint2*>(p.y_exp + (row0 + lane) * (p.N / kRowGroup) + c0 / kRowGroup) =
+              make_uint2(words[0], words[1]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {  // 64 columns
           if (lane == 0) bulk_store_wait_read();  // the chunk before has left
@@ -428,7 +417,8 @@ cudaError_t launch_typed(const MxExperts& g, cudaStream_t stream) {
                      static_cast<uint64_t>(g.N) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const PairArgs a{g.offsets,  g.padded_offsets, g.E,     g.N,      g.K,
-                   g.h_codes,  g.h_scales,       g.y_exp, g.status, wait_limit_ns()};
+                   g.h_codes,  g.h_scales,       reinterpret_cast<uint16_t*>(g.y_exp),
+                   g.status,   wait_limit_ns()};
   auto kern = k_mx_experts_pair<SILU>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
