@@ -2,7 +2,8 @@
 // that moves the choice but not the weights, groups of experts, top-k, and
 // the gradient of the weights with respect to the logits.
 //
-//   s_e = 1 / (1 + exp(-l_e))           or exp(l_e - m) / sum_i exp(l_i - m)
+//   s_e = 1 / (1 + exp(-l_e))           or exp(l_e - m) / sum_i exp(l_i - m), in
+//                                       fp32 to a few units, subnormal ones too
 //   c_e = s_e + bias_e                  (an fp32 add)
 //   a group's score is the sum of its group_top (1 or 2) largest c; the
 //   topk_group groups of highest score stay; the k experts of largest c among
@@ -50,20 +51,22 @@ __device__ __forceinline__ float clean_logit(float l) {
   return l > -INFINITY ? fminf(l, FLT_MAX) : -INFINITY;
 }
 
-// The hardware's exponential and reciprocal, within 2^-22 + |x| 2^-24 and 2^-23
-// of their value (results below the smallest normal number are zero).
-__device__ __forceinline__ float fast_exp(float x) {
+// 1 / d for d in [1, 2]: the hardware's reciprocal, off by up to one unit, and a
+// step of Newton's method, which leaves it within 2^-22 units of half a unit, so the
+// order of two different d is kept.  (16384 tokens of 384 logits take 16.6 us with it,
+// 18.7 with a correctly rounded reciprocal called for each score.)
+__device__ __forceinline__ float reciprocal(float d) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x * 1.44269504088896341f));
-  return r;
-}
-__device__ __forceinline__ float fast_reciprocal(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(d));
+  return __fmaf_rn(r, __fmaf_rn(-d, r, 1.f), r);
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return __fdiv_rn(1.f, 1.f + expf(-l)); }
+// The exponential is taken of -|l|, so that neither end overflows: a negative
+// logit's score keeps its bits down to the subnormal numbers.
+__device__ __forceinline__ float sigmoid(float l) {
+  const float e = expf(-fabsf(l)), r = reciprocal(1.f + e);
+  return l >= 0.f ? r : e * r;
+}
 
 // Unsigned key in the order of the floats above -inf; 0 marks what cannot be taken.
 __device__ __forceinline__ uint32_t order_key(float c) {
@@ -107,10 +110,9 @@ __device__ __forceinline__ int lane_expert(int i, int sub, int lanes) {
 //     or an equal one at a lower index): its slot.
 // More than 32 of them (ties) are taken one by one.  The work per token bounds
 // this kernel, not its bytes: 16384 tokens of 384 fp32 logits in 8 groups, top-6,
-// take 14.4 us (1.8 TB/s, 75 % of the issue slots), with all of the k taken by
-// warp maxima instead 30.2 us.  One token takes 2 us, a launch's latency.
-// Scores for the choice use the hardware's exponential and reciprocal (within
-// 2^-20 of their value, the same for equal logits); the weights do not.
+// take 16.6 us (1.5 TB/s); with the scores by the hardware's exponential alone, off
+// by up to 2^-18 and none below the smallest normal number, 14.5, and then with all
+// of the k taken by warp maxima 30.2.  One token takes 3.9 us, a launch's latency.
 template <typename L, int NV, int V>
 __global__ void __launch_bounds__(kWarps * 32)
     k_scored_router(const L* __restrict__ logits, int64_t T, int E, int64_t ld,
@@ -153,16 +155,19 @@ __global__ void __launch_bounds__(kWarps * 32)
     if (top == -INFINITY) top = 0.f;  // no expert: every exp is 0
     total = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) total += expf(c[i] - top);
+    for (int i = 0; i < NV; ++i) {
+      const float e = expf(c[i] - top);
+      total += e;
+      c[i] = c[i] > -INFINITY ? e : -INFINITY;
+    }
     total = warp_sum(total);
-    const float inverse = total > 0.f ? fast_reciprocal(total) : 0.f;
+    const float inverse = total > 0.f ? __frcp_rn(total) : 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      c[i] = c[i] > -INFINITY ? fast_exp(c[i] - top) * inverse : -INFINITY;
+    for (int i = 0; i < NV; ++i) c[i] = c[i] > -INFINITY ? c[i] * inverse : -INFINITY;
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)  // NaN stays NaN
-      c[i] = c[i] > -INFINITY ? fast_reciprocal(1.f + fast_exp(-c[i])) : -INFINITY;
+    for (int i = 0; i < NV; ++i)  // NaN becomes -inf: not taken
+      c[i] = c[i] > -INFINITY ? sigmoid(c[i]) : -INFINITY;
   }
   // scores plus bias; -inf: cannot be taken
   if (bias) {
