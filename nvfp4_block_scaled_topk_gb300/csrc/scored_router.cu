@@ -67,6 +67,8 @@ __device__ __forceinline__ float sigmoid(float l) {
   const float e = expf(-fabsf(l)), r = reciprocal(1.f + e);
   return l >= 0.f ? r : e * r;
 }
+// 1 - s, whose bits 1 - (s rounded) would lose.
+__device__ __forceinline__ float sigmoid_rest(float l) { return sigmoid(-l); }
 
 // Unsigned key in the order of the floats above -inf; 0 marks what cannot be taken.
 __device__ __forceinline__ uint32_t order_key(float c) {
@@ -334,10 +336,9 @@ __global__ void __launch_bounds__(kWarps * 32)
     const float sum = warp_sum(s);
     const float p = sum > 0.f ? __fdiv_rn(s, sum) : 0.f;
     dl = p * (g - warp_sum(g * p));
-    if (!softmax) dl *= 1.f - s;
+    if (!softmax) dl *= sigmoid_rest(l);
   } else {
-    const float s = sigmoid(l);
-    dl = g * s * (1.f - s);
+    dl = g * sigmoid(l) * sigmoid_rest(l);
   }
   if (dense) {
     for (int e = lane; e < E; e += 32) {

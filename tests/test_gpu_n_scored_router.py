@@ -115,3 +115,31 @@ def test_scores_keep_the_order_of_the_logits(cuda_lib):
     assert (w[:, :-1] >= w[:, 1:]).all() and before.all()
     want = 1 / (1 + np.exp(-taken.astype(np.float64)))
     assert (np.abs(w - want) <= 4 * U * want).all()
+
+
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_gradient_of_confident_scores(cuda_lib, renormalize):
+    """1 - s of logits of 10 to 40 is e^-l, not what is left of s after its rounding."""
+    rng = np.random.default_rng(8)
+    l = rng.uniform(10, 40, (50, 12)).astype(np.float32)
+    l[1::2] *= -1
+    l[::5, 3] *= -1
+    ids, _ = megamoe.router_scored_topk(torch.from_numpy(l).cuda(), 6)
+    g = rng.standard_normal((50, 6)).astype(np.float32)
+    got = megamoe.router_scored_topk_backward(torch.from_numpy(l).cuda(), ids,
+                                              torch.from_numpy(g).cuda(), renormalize=renormalize,
+                                              scale=2.5)
+    at = ids.cpu().numpy()
+    x, g = np.take_along_axis(l, at, 1).astype(np.float64), g.astype(np.float64)
+    e = np.exp(-np.abs(x))
+    s, rest = np.where(x >= 0, 1, e) / (1 + e), np.where(x >= 0, e, 1) / (1 + e)
+    if renormalize:
+        p = s / s.sum(1, keepdims=True)
+        factor, dl = p * rest, p * rest * (g - (g * p).sum(1, keepdims=True))
+    else:
+        factor, dl = s * rest, s * rest * g
+    want, bound = np.zeros(l.shape), np.zeros(l.shape)
+    np.put_along_axis(want, at, 2.5 * dl, 1)
+    most = np.abs(g).max(1, keepdims=True)
+    np.put_along_axis(bound, at, (64 + 2 * 40) * U * 2.5 * most * factor, 1)
+    assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
