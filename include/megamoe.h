@@ -573,7 +573,9 @@ megamoe_status megamoe_forward_static(const megamoe_weights* w, const uint16_t* 
  *     its group_top (1 or 2) largest c, and the topk_group groups of highest
  *     score stay;
  *   - the k experts of largest c among them, in descending order;
- *   - w_j = scale * s_j / sum_i s_i (renormalize), or scale * s_j.
+ *   - w_j = scale * s_j / sum_i s_i (renormalize), or scale * s_j.  Softmax shares
+ *     are taken of the logits, so they hold where the scores are 0 in fp32;
+ *     sigmoid scores that are all 0 in fp32 (logits below -103) give weights 0.
  * Ties, of groups and of experts, go to the lower index.  An expert whose
  * logit or c is NaN or -inf scores 0 and is never taken; slots left over get
  * id -1 and weight 0 (the forward skips them).  +inf counts as the largest

@@ -268,8 +268,11 @@ __global__ void __launch_bounds__(kWarps * 32)
     }
   }
   float w = 0.f;
-  if (my_id >= 0) {
-    const float l = clean_logit(load_logit(row + my_id));
+  const float l = my_id >= 0 ? clean_logit(load_logit(row + my_id)) : -INFINITY;
+  if (softmax && renormalize) {  // shares of the taken: the sum over all experts cancels
+    const float most = warp_max(l);
+    w = my_id >= 0 ? expf(l - most) : 0.f;
+  } else if (my_id >= 0) {
     w = softmax ? __fdiv_rn(expf(l - top), total) : sigmoid(l);
   }
   if (renormalize) {

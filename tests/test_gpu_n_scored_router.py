@@ -143,3 +143,30 @@ def test_gradient_of_confident_scores(cuda_lib, renormalize):
     most = np.abs(g).max(1, keepdims=True)
     np.put_along_axis(bound, at, (64 + 2 * 40) * U * 2.5 * most * factor, 1)
     assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_renormalised_softmax_far_below_the_top(cuda_lib, dtype):
+    """The bias takes experts whose softmax scores are nothing in fp32: their weights
+    are shares of one another all the same, and the gradient is that of these."""
+    rng = np.random.default_rng(9)
+    T, E, k = 40, 24, 4
+    l = torch.tensor(rng.uniform(-60, 60, (T, E)), dtype=dtype)
+    l[:, :8] -= 130  # 70 and more below the others
+    l[0, :8] = -float(np.finfo(np.float32).max) if dtype == torch.float32 else -3e38
+    bias = np.where(np.arange(E) < 8, 4 + np.arange(E) / 8, 0)
+    kw = dict(score="softmax", scale=2.5)
+    ids, w = megamoe.router_scored_topk(l.cuda(), k, bias=torch.tensor(bias, dtype=torch.float32).cuda(),
+                                        **kw)
+    assert (ids.cpu().numpy() == [7, 6, 5, 4]).all()
+    g = torch.tensor(rng.standard_normal((T, k)), dtype=torch.float32)
+    got = megamoe.router_scored_topk_backward(l.cuda(), ids, g.cuda(), **kw)
+    x, gd = l[:, [7, 6, 5, 4]].double().numpy(), g.double().numpy()
+    p = np.exp(x - x.max(1, keepdims=True))
+    p = p / p.sum(1, keepdims=True)
+    assert (np.abs(w.double().cpu().numpy() - 2.5 * p) <= (24 + 120) * U * 2.5 * p + 1e-44).all()
+    want = np.zeros((T, E))
+    want[:, [7, 6, 5, 4]] = 2.5 * p * (gd - (gd * p).sum(1, keepdims=True))
+    bound = (64 + 2 * 120) * U * 2.5 * np.abs(gd).max(1, keepdims=True) + np.abs(want) * (
+        2.0 ** -8 if dtype == torch.bfloat16 else 0)
+    assert (np.abs(got.double().cpu().numpy() - want) <= bound).all()
