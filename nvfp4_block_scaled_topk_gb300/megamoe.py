@@ -668,6 +668,13 @@ def _vector(t, n, name):
     return t.data_ptr()
 
 
+def _workspace(ws, device):
+    """Bytes of a caller's workspace, which the library writes from its address on."""
+    if not (ws.is_cuda and ws.is_contiguous()) or ws.get_device() != device:
+        raise TypeError("ws must be a contiguous CUDA tensor on the inputs' device")
+    return ws.numel() * ws.element_size()
+
+
 def _score(score):
     if score not in SCORES:
         raise ValueError(f"score must be one of {sorted(SCORES)}")
@@ -728,6 +735,10 @@ def quantize_mxfp4(x: torch.Tensor, transpose: bool = False, scale_layout=SCALES
     scales [K, R / 32], R = rows up to a multiple of 32 (zeros past the last).
     With SCALES_MMA the scales are a buffer in the atom layout."""
     rows, K, ld, code, stream = _matrix(x, TYPES, "x")
+    if status is not None:
+        _dev(status, torch.int32, "status")
+        if status.numel() < 1:
+            raise ValueError("status must hold a word")
     out_rows, out_k = (K, (rows + 31) // 32 * 32) if transpose else (rows, K)
     dev = x.device
     codes = torch.empty((out_rows, out_k // 2), dtype=torch.uint8, device=dev)
@@ -778,6 +789,13 @@ class MxLinearWeights:
     codes: torch.Tensor
     scales: torch.Tensor  # atom layout
 
+    def __post_init__(self):
+        _dev(self.codes, torch.uint8, "codes")
+        _dev(self.scales, torch.uint8, "scales")
+        if (self.codes.numel() != self.N * (self.K // 2)
+                or self.scales.numel() != mx_atom_bytes(self.N, self.K)):
+            raise ValueError("codes and scales must be those of [N, K]")
+
     @classmethod
     def prepare(cls, codes: torch.Tensor, scales: torch.Tensor) -> "MxLinearWeights":
         """From row-major codes [N, K / 2] and scales [N, K / 32]."""
@@ -821,9 +839,12 @@ def linear_mxfp4(x: torch.Tensor, w: MxLinearWeights, out_dtype=EPI_BF16, out=No
     N = w.N
     if K != w.K:
         raise ValueError("x and w disagree on K")
+    if w.codes.get_device() != x.get_device():
+        raise ValueError("x and w must be on one device")
     dev = x.device
     if ws is None:
         ws = torch.empty((linear_mxfp4_workspace_size(T, K, N),), dtype=torch.uint8, device=dev)
+    ws_bytes = _workspace(ws, x.get_device())
     dt = torch.float32 if out_dtype == EPI_F32 else torch.bfloat16
     ld_out = N
     if out is None:
@@ -834,7 +855,7 @@ def linear_mxfp4(x: torch.Tensor, w: MxLinearWeights, out_dtype=EPI_BF16, out=No
             raise ValueError("out must be [T, N]")
     _check("megamoe_linear_mxfp4", load().megamoe_linear_mxfp4(
         x.data_ptr(), code, T, K, ld, w.codes.data_ptr(), w.scales.data_ptr(), N, out_dtype,
-        out.data_ptr(), ld_out, ws.data_ptr(), ws.numel(), stream))
+        out.data_ptr(), ld_out, ws.data_ptr(), ws_bytes, stream))
     return out, ws
 
 
@@ -859,11 +880,12 @@ def linear_mxfp4_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Tens
             if len(_SIZES) < 4096:
                 _SIZES[("backward", T, K, N)] = size
         ws = torch.empty((size,), dtype=torch.uint8, device=dev)
+    ws_bytes = _workspace(ws, x.get_device())
     gx = torch.empty((T, K), dtype=grad_x_dtype, device=dev) if need_x else None
     gw = torch.empty((N, K), dtype=grad_w_dtype, device=dev) if need_w else None
     _check("megamoe_linear_mxfp4_backward", lib.megamoe_linear_mxfp4_backward(
         grad_out.data_ptr(), g_code, ld_g, x.data_ptr(), x_code, ld_x, w.data_ptr(), w_code, ld_w,
-        T, K, N, _p(gx), gx_epi, K, _p(gw), gw_epi, K, ws.data_ptr(), ws.numel(), stream))
+        T, K, N, _p(gx), gx_epi, K, _p(gw), gw_epi, K, ws.data_ptr(), ws_bytes, stream))
     return gx, gw, ws
 
 
@@ -885,6 +907,16 @@ class MxWeights:
     w13_scales: torch.Tensor  # atom layout
     w2_codes: torch.Tensor
     w2_scales: torch.Tensor  # atom layout
+
+    def __post_init__(self):
+        for name, n in (("w13_codes", self.E * self.I * self.d),
+                        ("w13_scales", mx_atom_bytes(self.E * 2 * self.I, self.d)),
+                        ("w2_codes", self.E * self.d * self.I // 2),
+                        ("w2_scales", mx_atom_bytes(self.E * self.d, self.I))):
+            t = getattr(self, name)
+            _dev(t, torch.uint8, name)
+            if t.numel() != n:
+                raise ValueError(f"{name} must be those of E, d and I")
 
     @classmethod
     def prepare(cls, w: dict) -> "MxWeights":
@@ -914,7 +946,9 @@ class MxForward:
         self.w = weights
         self.cw = weights.cstruct()
         self.T, self.k, self.pad = T, k, pad
-        dev = device or weights.w13_codes.device
+        dev = torch.device(device or weights.w13_codes.device)
+        if dev.type != "cuda" or dev.index not in (None, weights.w13_codes.get_device()):
+            raise ValueError("device must be that of the weights")
         self.ws_bytes = int(load().megamoe_workspace_size_mxfp4(T, k, weights.E, weights.d,
                                                                 weights.I, pad))
         self.ws = torch.empty(self.ws_bytes + 256, dtype=torch.uint8, device=dev)
@@ -926,6 +960,8 @@ class MxForward:
         _dev(x, torch.bfloat16, "x")
         if x.shape != (self.T, self.w.d):
             raise ValueError("x must be [T, d] of the shape this object was built for")
+        if x.get_device() != self.ws.get_device():
+            raise ValueError("x must be on the weights' device")
         out = self.out if out is None else out
         _dev(out, torch.bfloat16, "out")
         if out.dim() != 2 or out.shape[0] < self.T or out.shape[1] != self.w.d:
