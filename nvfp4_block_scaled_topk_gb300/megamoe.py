@@ -447,7 +447,7 @@ class Forward:
 
     @property
     def ws_ptr(self):
-        return self.ws.data_ptr() + self.ws_off
+        return ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
 
     def status_tensor(self):
         return self.ws[self.ws_off:self.ws_off + 4].view(torch.int32)
@@ -523,7 +523,7 @@ class ShardForward:
 
     @property
     def ws_ptr(self):
-        return self.ws.data_ptr() + self.ws_off
+        return ctypes.c_void_p(self.ws.data_ptr() + self.ws_off)
 
     def amax_h(self) -> torch.Tensor:
         """The shard's amax(h) after begin(): a device float [1] view into the
