@@ -128,10 +128,19 @@ def _p(t):
     return None if t is None else t.data_ptr()
 
 
+def _raw_stream_of():
+    """device -> handle of its current stream: torch's internal function, which saves
+    the 3 us (a short kernel's own time) that building the Stream object takes, or
+    the public one in a torch without it."""
+    return (getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            or (lambda device: torch.cuda.current_stream(device).cuda_stream))
+
+
+_raw_stream = _raw_stream_of()
+
+
 def _stream():
-    # the handle of torch.cuda.current_stream(), without the 3 us that building
-    # the Stream object around it takes (a short kernel's own time)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _on_current_device(t, name):
@@ -653,9 +662,8 @@ def _matrix(t, types, name):
     if rows <= 1 and ld < cols:  # a matrix of one row may carry any stride
         ld = cols
     dev = t.get_device()
-    if dev != torch._C._cuda_getDevice():
-        _on_current_device(t, name)
-    return rows, cols, ld, code, torch._C._cuda_getCurrentRawStream(dev)
+    _on_current_device(t, name)
+    return rows, cols, ld, code, _raw_stream(dev)
 
 
 def _vector(t, n, name):

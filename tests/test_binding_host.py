@@ -14,3 +14,12 @@ def test_workspace_addresses_are_ctypes_pointers(kind):
     fwd.ws, fwd.ws_off = torch.empty(512, dtype=torch.uint8), 64
     assert isinstance(fwd.ws_ptr, ctypes.c_void_p)
     assert fwd.ws_ptr.value == fwd.ws.data_ptr() + 64
+
+
+def test_streams_without_the_internal_function(monkeypatch):
+    class Stream:
+        cuda_stream = 1234
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream)
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert megamoe._raw_stream_of()(0) == 1234
