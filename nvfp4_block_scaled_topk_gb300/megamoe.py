@@ -659,7 +659,7 @@ def _matrix(t, types, name):
     ld, unit = t.stride()
     if unit != 1 and cols > 1:
         raise TypeError(f"{name} must have unit column stride")
-    if rows <= 1 and ld < cols:  # a matrix of one row may carry any stride
+    if rows <= 1:  # the stride of a lone row, which may be anything, leads nowhere
         ld = cols
     dev = t.get_device()
     _on_current_device(t, name)

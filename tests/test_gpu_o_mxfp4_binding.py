@@ -77,3 +77,23 @@ def test_status_words(cuda_lib):
             megamoe.quantize_mxfp4(_x(), status=status)
     with pytest.raises(ValueError):
         megamoe.quantize_mxfp4(_x(), status=torch.zeros(0, dtype=torch.int32, device="cuda"))
+
+
+def test_one_row_of_any_stride(cuda_lib):
+    """A row cut out of a matrix whose own rows are not on 16-byte boundaries."""
+    x = torch.randn(1, K + 8, device="cuda").to(torch.bfloat16)
+    odd = x.as_strided((1, K), (K + 1, 1))
+    flat = odd.clone(memory_format=torch.contiguous_format)
+    w = megamoe.MxLinearWeights.quantize(torch.randn(N, K, device="cuda"))
+    out = torch.empty(1, N + 8, dtype=torch.bfloat16, device="cuda").as_strided((1, N), (N + 1, 1))
+    want = megamoe.linear_mxfp4(flat, w)[0]
+    assert torch.equal(megamoe.linear_mxfp4(odd, w)[0], want)
+    assert torch.equal(megamoe.linear_mxfp4(flat, w, out=out)[0], want)
+    for transpose in (False, True):
+        for got, ref in zip(megamoe.quantize_mxfp4(odd, transpose),
+                            megamoe.quantize_mxfp4(flat, transpose)):
+            assert torch.equal(got, ref)
+    g, m = torch.randn(1, N, device="cuda"), torch.randn(N, K, device="cuda")
+    for got, ref in zip(megamoe.linear_mxfp4_backward(g, odd, m)[:2],
+                        megamoe.linear_mxfp4_backward(g, flat, m)[:2]):
+        assert torch.equal(got, ref)
