@@ -244,18 +244,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           uint8_t* sb = smem + stage * C::STAGE;
+          const int64_t step = kt;  // offsets of a long row pass 32 bits
           // scales first, on their own barrier: the scale warps move them into
           // tensor memory while the codes are still landing
           if (leader) {
             mbar_arrive_expect_tx(&sf_full[stage], C::SF_TX);
-            bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
+            bulk_load(sb + C::OFF_SFW, sfw0 + step * C::SFW, C::SFW, &sf_full[stage], pol_w);
             if (C::G == 2)
-              bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + kt * C::SFW, C::SFW, &sf_full[stage], pol_w);
+              bulk_load(sb + C::OFF_SFW + C::SFW, sfw1 + step * C::SFW, C::SFW, &sf_full[stage], pol_w);
             tma_load_2d(sb + C::OFF_SFA_RAW, &maps.scales, &sf_full[stage], kt * 16, a_row0, pol_a);
             mbar_arrive_expect_tx(&full[stage], C::TX);
             // the stage's weight blocks (gate then up for L1) are contiguous and
             // pre-swizzled: one bulk copy
-            bulk_load(sb + C::OFF_A, wcod + kt * (C::G * 16384), C::G * C::A_TILE, &full[stage], pol_w);
+            bulk_load(sb + C::OFF_A, wcod + step * (C::G * 16384), C::G * C::A_TILE, &full[stage], pol_w);
             tma_load_2d(sb + C::OFF_B, &maps.codes, &full[stage], kt * 128, a_row0, pol_a);
           }
           __syncwarp();

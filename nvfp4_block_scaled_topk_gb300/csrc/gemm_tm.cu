@@ -215,17 +215,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             break;
           }
           uint8_t* sb = smem + stage * C::STAGE;
+          const int64_t step = kt;  // offsets of a long row pass 32 bits
           if (leader) {
             mbar_arrive_expect_tx(&sf_full[stage], C::SFW + box * 16);
-            bulk_load(sb + C::OFF_SFW, sfw0 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
-            bulk_load(sb + C::OFF_SFW + C::SFG, sfw1 + kt * C::SFG, C::SFG, &sf_full[stage], pol_w);
+            bulk_load(sb + C::OFF_SFW, sfw0 + step * C::SFG, C::SFG, &sf_full[stage], pol_w);
+            bulk_load(sb + C::OFF_SFW + C::SFG, sfw1 + step * C::SFG, C::SFG, &sf_full[stage], pol_w);
             tma_load_2d(sb + C::OFF_SFA_RAW, map_s, &sf_full[stage], kt * 16, a_row0, pol_a);
             mbar_arrive_expect_tx(&full[stage], C::B_TILE + box * 128);
             if (C::SILU) {
-              bulk_load(sb + C::OFF_B, wc0 + kt * 32768, 32768, &full[stage], pol_w);
+              bulk_load(sb + C::OFF_B, wc0 + step * 32768, 32768, &full[stage], pol_w);
             } else {
-              bulk_load(sb + C::OFF_B, wc0 + kt * 16384, 16384, &full[stage], pol_w);
-              bulk_load(sb + C::OFF_B + 16384, wc1 + kt * 16384, 16384, &full[stage], pol_w);
+              bulk_load(sb + C::OFF_B, wc0 + step * 16384, 16384, &full[stage], pol_w);
+              bulk_load(sb + C::OFF_B + 16384, wc1 + step * 16384, 16384, &full[stage], pol_w);
             }
             tma_load_2d(sb + C::OFF_A, map_c, &full[stage], kt * 128, a_row0, pol_a);
           }

@@ -190,8 +190,8 @@ __global__ void __launch_bounds__(320, 2) k_mx_gemm_tile(const __grid_constant__
           mbar_arrive_expect_tx(&full[stage], C::M_TILE + p.n_box * 128 + 2 * C::SF);
           tma_load_2d(sb, &maps.m, &full[stage], kt * 128, mt * 128, pol);
           tma_load_2d(sb + C::OFF_N, &maps.n, &full[stage], kt * 128, nt * BN, pol);
-          bulk_load(sb + C::OFF_SFM, sfm + kt * C::SF, C::SF, &full[stage], pol);
-          bulk_load(sb + C::OFF_SFN, sfn + kt * C::SF, C::SF, &full[stage], pol);
+          bulk_load(sb + C::OFF_SFM, sfm + static_cast<int64_t>(kt) * C::SF, C::SF, &full[stage], pol);
+          bulk_load(sb + C::OFF_SFN, sfn + static_cast<int64_t>(kt) * C::SF, C::SF, &full[stage], pol);
         }
         __syncwarp();
         ++issued;
