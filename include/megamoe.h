@@ -642,8 +642,8 @@ megamoe_status megamoe_router_scored_topk_backward(
  *                [K, R], R = rows up to a multiple of 32 (the last block's
  *                missing elements count as zeros)
  *   status       device status word or null
- * Requires K a multiple of 32, ld * element size a multiple of 16, x and codes
- * 16-byte aligned.
+ * Requires K a multiple of 32 below 2^30, rows < 2^31, ld * element size a multiple
+ * of 16, x and codes 16-byte aligned.
  */
 megamoe_status megamoe_quantize_mxfp4(const void* x, int x_type, int64_t rows, int K, int64_t ld,
                                       int transpose, uint8_t* codes, uint8_t* scales,
@@ -669,8 +669,8 @@ megamoe_status megamoe_swizzle_scales_mxfp4(const uint8_t* src, int64_t rows, in
  *   out       [T, N] bf16 (MEGAMOE_EPI_BF16) or fp32 (MEGAMOE_EPI_F32)
  *   ws        at least megamoe_linear_mxfp4_workspace_size(T, K, N) bytes,
  *             256-byte aligned; its first 4 bytes are the status word
- * Requires K and N multiples of 32, pointers 16-byte aligned and rows on
- * 16-byte boundaries.
+ * Requires K and N multiples of 32, T, K and N below 2^30, pointers 16-byte aligned
+ * and rows on 16-byte boundaries.
  */
 size_t megamoe_linear_mxfp4_workspace_size(int64_t T, int K, int N);
 megamoe_status megamoe_linear_mxfp4(const void* x, int x_type, int64_t T, int K, int64_t ld_x,

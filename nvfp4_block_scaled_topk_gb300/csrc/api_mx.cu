@@ -93,8 +93,10 @@ BackwardWs carve_backward(void* base, int64_t T, int K, int N) {
 
 // Rows and columns of the products are int, their tiles (of 128 x 128) and the
 // quantisers' (of 128 x 64 at least, over all three matrices) counted in 31 bits.
+constexpr int kMaxColumns = 1 << 30;  // columns rounded up to whole steps stay in 31 bits
 bool linear_sizes_ok(int64_t T, int K, int N) {
-  if (K % 32 != 0 || N % 32 != 0 || T >= (int64_t{1} << 30)) return false;
+  if (K % 32 != 0 || N % 32 != 0 || T >= (int64_t{1} << 30) || K >= kMaxColumns || N >= kMaxColumns)
+    return false;
   const int64_t t = T / 128 + 1, k = K / 128 + 1, n = N / 128 + 1, most = int64_t{1} << 28;
   return t * k < most && t * n < most && n * k < most;
 }
@@ -350,7 +352,8 @@ megamoe_status megamoe_quantize_mxfp4(const void* x, int x_type, int64_t rows, i
   if (rows < 0 || K <= 0 || ld < K || !size) return MEGAMOE_ERR_INVALID_ARG;
   if (scale_layout != MEGAMOE_SCALES_ROWMAJOR && scale_layout != MEGAMOE_SCALES_MMA)
     return MEGAMOE_ERR_INVALID_ARG;
-  if (K % 32 != 0 || rows >= (int64_t{1} << 31)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  if (K % 32 != 0 || K >= kMaxColumns || rows >= (int64_t{1} << 31))
+    return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   // the tiles of a transposed launch are counted in 31 bits
   if (transpose && (rows + 127) / 128 * ((K + 63) / 64) >= (int64_t{1} << 30))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
