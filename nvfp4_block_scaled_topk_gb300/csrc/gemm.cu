@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
                 const float gv = __uint_as_float(g[h8 + j]), uv = __uint_as_float(u[h8 + j]);
-                const float hv = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+                const float hv = silu_mul(gv, uv);
                 const uint32_t byte = mx_scale_byte(
                     __reduce_max_sync(0xffffffffu, __float_as_uint(hv) & 0x7fffffffu));
                 if (lane == j) mine = byte;

@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float gv = __uint_as_float(g[j]), uv = __uint_as_float(u[j]);
-              hv[i + j] = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+              hv[i + j] = silu_mul(gv, uv);
               m = max(m, __float_as_uint(hv[i + j]) & 0x7fffffffu);
             }
           }

@@ -304,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float gv = __uint_as_float(v[32 * b + j]), uv = __uint_as_float(v[64 + 32 * b + j]);
-            hv[j] = __fdividef(gv, 1.0f + __expf(-gv)) * uv;
+            hv[j] = silu_mul(gv, uv);
             m = max(m, __float_as_uint(hv[j]) & 0x7fffffffu);
           }
           const uint32_t byte = mx_scale_byte(m);

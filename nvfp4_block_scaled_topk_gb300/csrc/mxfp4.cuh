@@ -36,6 +36,15 @@ __device__ __forceinline__ float mx_scale_value(uint32_t byte) {
   return byte == kMxNan ? __uint_as_float(0x7fffffffu)
                         : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
 }
+// SiLU(g) * u to a few units of fp32 at every g: the exponential is taken of -|g|
+// (the short form of it, __expf, is off by |g| units more), and the hardware's
+// reciprocal of a number in [1, 2] by one.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  const float e = expf(-fabsf(g));
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * (g >= 0.f ? r : e * r) * u;
+}
 // Eight elements -> four bytes of codes (element 0 in the lowest nibble).
 __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8], float inv) {
   float s[8];
