@@ -97,8 +97,10 @@ __global__ void __launch_bounds__(256)
 // copies and stores walk pointers and magnitudes and products go two an
 // instruction.  8195 x 7168 bf16 along columns 29.7 us (5.0 TB/s), 16384 rows 57
 // (5.2 TB/s), 8192 x 7168 fp32 42 (6.3 TB/s).  Six blocks of 128 threads an SM
-// instead of three of 256 are 4 % faster on their own, but their 64-byte runs cost
-// the reader of the codes more (quantised and read back 55.5 us against 54.9).
+// instead of three of 256, whose runs are 64 bytes long, are 1 to 4 % faster on bf16
+// alone (8195 x 7168 29.8 us against 31.0 in a graph), 3 to 4 % slower on fp32, and
+// leave a linear's gradients, which read the codes, as they are (8192 x 7168 -> 2048
+// 124.3 against 124.5, 4096 x 2048 -> 7168 82.8 against 82.4).
 constexpr int kTileCols = 64;
 constexpr int kTileThreads = 256;
 constexpr int kTileBytes = 128 * kTileThreads;  // of x in a tile, for every type
@@ -394,7 +396,7 @@ __device__ __forceinline__ void store_values(__nv_bfloat16* p, uint32_t codes, u
     const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&b), up), s);
     u[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  __stcs(reinterpret_cast<uint4*>(p), make_uint4(u[0], u[1], u[2], u[3]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
 }
 __device__ __forceinline__ void store_values(float* p, uint32_t codes, uint32_t byte) {
   const float s = mx_scale_value(byte);
@@ -404,15 +406,16 @@ __device__ __forceinline__ void store_values(float* p, uint32_t codes, uint32_t 
     const uint32_t b = e2m1x2_halves(codes >> (16 * i + 8) & 0xffu);
     const float2 fa = __half22float2(*reinterpret_cast<const __half2*>(&a));
     const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&b));
-    __stcs(reinterpret_cast<float4*>(p) + i, make_float4(fa.x * s, fa.y * s, fb.x * s, fb.y * s));
+    reinterpret_cast<float4*>(p)[i] = make_float4(fa.x * s, fa.y * s, fb.x * s, fb.y * s);
   }
 }
 
 // The values: four bytes of codes in, eight elements out per thread, four of
 // them at once; no division where the rows of out follow each other.  Bound by
-// HBM: 8195 x 7168 to bf16 21.4 us (6.9 TB/s).  The values are not read again here,
-// so they are stored to leave L2 first: 4 us less for the call that quantises the
-// next matrix and reads its codes back.
+// HBM: 8195 x 7168 to bf16 24.8 us, 16384 rows 48.0 (6.3 TB/s).  Ordinary stores:
+// what is read next are the values.  Stored to leave L2 first they took 21.7 and 50.7
+// us by themselves, but with a pass over them after it 60.4 against 58.9 and 118
+// against 115.6, and at 512 to 2048 rows 3 to 6 % more by themselves too.
 template <typename O>
 __global__ void __launch_bounds__(256)
     k_mx_values(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales, int64_t rows,
