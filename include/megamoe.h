@@ -576,10 +576,10 @@ megamoe_status megamoe_forward_static(const megamoe_weights* w, const uint16_t* 
  *   - w_j = scale * s_j / sum_i s_i (renormalize), or scale * s_j.  Softmax shares
  *     are taken of the logits, so they hold where the scores are 0 in fp32;
  *     sigmoid scores that are all 0 in fp32 (logits below -103) give weights 0.
- * Ties, of groups and of experts, go to the lower index.  An expert whose
- * logit or c is NaN or -inf scores 0 and is never taken; slots left over get
- * id -1 and weight 0 (the forward skips them).  +inf counts as the largest
- * float.
+ * Ties, of groups and of experts, go to the lower index.  An expert whose logit
+ * is NaN or -inf scores 0; neither it nor one whose c is NaN or -inf is ever
+ * taken; slots left over get id -1 and weight 0 (the forward skips them).  +inf
+ * counts as the largest float.
  * ------------------------------------------------------------------------ */
 
 /* Element types. */

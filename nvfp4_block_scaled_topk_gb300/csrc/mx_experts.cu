@@ -18,8 +18,8 @@
 // own: it loads its half of the weights and stores nothing.
 //
 // What bounds it: at some 250 rows an expert the weights from HBM.  48 experts of
-// 7168 x 2048, 2003 tokens of 6 slots: gate and up 148 us for 0.81 GB (81 % of the
-// measured copy rate, the MMAs busy for 76 %), down 100 us for 0.52 GB and y.  At
+// 7168 x 2048, 2003 tokens of 6 slots: gate and up 150 us for 0.81 GB (80 % of the
+// measured copy rate, the MMAs busy for 76 %), down 100 us for 0.39 GB and y.  At
 // 1024 rows what an SM takes in: 35 KB a K step (one CTA on 128 x 256 takes 51 KB
 // for half the product), 600 to 700 cycles against the MMAs' 513.  Measured and
 // not kept here: the accumulators with columns in common, the ordinary stores and

@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(256)
 // column), and their codes go out through shared memory as 128-byte (fp32: 64-byte)
 // runs.  Instructions bound it (65 to 70 % of the issue slots), so a thread's
 // copies and stores walk pointers and magnitudes and products go two an
-// instruction.  8195 x 7168 bf16 along columns 29.7 us (5.0 TB/s), 16384 rows 57
+// instruction.  8195 x 7168 bf16 along columns 30 to 31 us (4.8 TB/s), 16384 rows 57
 // (5.2 TB/s), 8192 x 7168 fp32 42 (6.3 TB/s).  Six blocks of 128 threads an SM
 // instead of three of 256, whose runs are 64 bytes long, are 1 to 4 % faster on bf16
 // alone (8195 x 7168 29.8 us against 31.0 in a graph), 3 to 4 % slower on fp32, and
