@@ -74,6 +74,7 @@ typedef enum megamoe_status {
 #define MEGAMOE_DEV_BAD_EXPERT_ID 0x1u /* a topk id >= E was seen (slot skipped) */
 #define MEGAMOE_DEV_NONFINITE 0x2u     /* the amax of an input was not finite    */
 #define MEGAMOE_DEV_TIMEOUT 0x4u       /* a bounded device wait gave up          */
+#define MEGAMOE_DEV_BAD_OFFSETS 0x8u   /* rows of an expert outside the matrix   */
 
 /* Scale layouts. */
 #define MEGAMOE_SCALES_ROWMAJOR 0 /* [rows, K/16] bytes                         */
@@ -586,6 +587,7 @@ megamoe_status megamoe_forward_static(const megamoe_weights* w, const uint16_t* 
 #define MEGAMOE_TYPE_BF16 0
 #define MEGAMOE_TYPE_F32 1
 #define MEGAMOE_TYPE_F16 2
+#define MEGAMOE_TYPE_I8 3 /* codes of the 8-bit integer linear */
 
 /* Scores. */
 #define MEGAMOE_SCORE_SIGMOID 0
@@ -744,6 +746,136 @@ megamoe_status megamoe_forward_mxfp4_from_logits(
     int64_t ld_logits, const float* bias, int score, int n_group, int topk_group, int group_top,
     int renormalize, double scale, int T, int k, int pad, uint16_t* out, void* ws, size_t ws_bytes,
     megamoe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Experts in 16 bits: products grouped by expert, the activation between them
+ * and the movement of rows, with the gradients that training needs.  Types are
+ * MEGAMOE_TYPE_BF16 or MEGAMOE_TYPE_F16 (one of them for all operands of a
+ * call); sums are fp32, each output rounded once.  Row matrices may have any row
+ * stride that keeps rows on 16-byte boundaries; widths are multiples of 8.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * megamoe_grouped_linear -- out[r, n] = sum_k x[r, k] w[e, n, k] for the rows r of
+ * each expert e: offsets[e + 1] - offsets[e] of them from padded_offsets[e] on, as
+ * megamoe_route_permute gives both with any pad (padded_offsets null: from
+ * offsets[e] on, which is pad 1).  Any counts, none among them.
+ *   x        [rows, K], row stride ld_x; w [E, N, K]
+ *   out      [rows, N] of `type` or MEGAMOE_TYPE_F32, row stride ld_out; rows of no
+ *            expert are left as they are
+ *   status   device status word or null: MEGAMOE_DEV_BAD_OFFSETS where an expert's
+ *            rows are not all inside the matrix (those outside are left out)
+ * An expert's product does not depend on other experts' rows, on rows of no expert
+ * or on the order of the launch.
+ * Requires K and N multiples of 8, 1 <= E <= 1024, rows < 2^31, pointers 16-byte
+ * and rows 16-byte aligned.
+ */
+megamoe_status megamoe_grouped_linear(const void* x, int type, int64_t rows, int64_t ld_x,
+                                      const void* w, int E, int N, int K, const int32_t* offsets,
+                                      const int32_t* padded_offsets, int out_type, void* out,
+                                      int64_t ld_out, uint32_t* status, megamoe_stream_t stream);
+
+/*
+ * megamoe_grouped_linear_backward -- its gradients:
+ *   grad_x [rows, K]  grad_x[r, k] = sum_n grad_out[r, n] w[e, n, k], of `type`; rows
+ *                     of no expert are left as they are
+ *   grad_w [E, N, K]  grad_w[e, n, k] = sum_r grad_out[r, n] x[r, k] over e's rows, of
+ *                     `type` or MEGAMOE_TYPE_F32; zeros for an expert without rows
+ * Either may be null and is then not computed (w may then be null for grad_x, x for
+ * grad_w).
+ */
+megamoe_status megamoe_grouped_linear_backward(
+    const void* grad_out, int64_t ld_grad, const void* x, int64_t ld_x, const void* w, int type,
+    int64_t rows, int E, int N, int K, const int32_t* offsets, const int32_t* padded_offsets,
+    void* grad_x, int64_t ld_grad_x, int grad_w_type, void* grad_w, uint32_t* status,
+    megamoe_stream_t stream);
+
+/*
+ * megamoe_silu_mul -- out[r, i] = g / (1 + exp(-g)) * u with g = a[r, i] and u =
+ * a[r, I + i]; a [rows, 2 I], out [rows, I].  live_rows (device int32, may be null):
+ * rows from *live_rows on are neither read nor written (offsets + E with pad 1).
+ * megamoe_silu_mul_backward -- grad_a [rows, 2 I] from grad [rows, I]: of g
+ * grad u s (1 + g (1 - s)), of u grad g s, with s = 1 / (1 + exp(-g)).
+ */
+megamoe_status megamoe_silu_mul(const void* a, int type, int64_t rows, int I, int64_t ld_a,
+                                const int32_t* live_rows, void* out, int64_t ld_out,
+                                megamoe_stream_t stream);
+megamoe_status megamoe_silu_mul_backward(const void* grad, int64_t ld_grad, const void* a, int type,
+                                         int64_t rows, int I, int64_t ld_a,
+                                         const int32_t* live_rows, void* grad_a, int64_t ld_grad_a,
+                                         megamoe_stream_t stream);
+
+/*
+ * megamoe_gather_rows -- tokens into the experts' order: out[r] = x[row_src[r] / k], zeros
+ * where row_src[r] < 0 (row_src as megamoe_route_permute gives it; a source past the
+ * T tokens counts as none).  Its gradient with respect to x is
+ * megamoe_combine_rows of the rows' gradients without weights.
+ *   x [T, d], row_src [rows], out [rows, d]
+ */
+megamoe_status megamoe_gather_rows(const void* x, int type, int64_t T, int d, int64_t ld_x,
+                                   const int32_t* row_src, int64_t rows, int k, void* out,
+                                   int64_t ld_out, megamoe_stream_t stream);
+
+/*
+ * megamoe_combine_rows -- out[t] = sum_j topk_weights[t, j] y[slot_dst[t k + j]] in
+ * ascending j, one rounding at the end; slots whose row is negative or past the
+ * matrix are skipped; topk_weights null: all 1.
+ *   y [rows, d], slot_dst [T, k], topk_weights [T, k], out [T, d] of `type`
+ */
+megamoe_status megamoe_combine_rows(const void* y, int type, int64_t rows, int64_t ld_y,
+                                    const int32_t* slot_dst, const float* topk_weights, int64_t T,
+                                    int k, int d, void* out, int64_t ld_out,
+                                    megamoe_stream_t stream);
+
+/*
+ * megamoe_combine_rows_backward -- its gradients for slot_dst whose rows are all
+ * different, as megamoe_route_permute gives them:
+ *   grad_y [rows, d]           grad_y[slot_dst[t k + j]] = topk_weights[t, j]
+ *                              grad_out[t], of `type`; rows of no slot are left
+ *   grad_topk_weights [T, k]   sum_i grad_out[t, i] y[slot_dst[t k + j], i], 0 for a
+ *                              skipped slot; may be null (y may then be null)
+ */
+megamoe_status megamoe_combine_rows_backward(const void* grad_out, int64_t ld_grad, const void* y,
+                                             int type, int64_t rows, int64_t ld_y,
+                                             const int32_t* slot_dst, const float* topk_weights,
+                                             int64_t T, int k, int d, void* grad_y,
+                                             int64_t ld_grad_y, float* grad_topk_weights,
+                                             megamoe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Linear in 8-bit integers: a scale for each token (row of x) and one for each
+ * output channel (row of w), symmetric, integers -127 .. 127 (-128 is taken as it
+ * is where the caller brings it).
+ *   scale[t] = amax_t / 127 (correctly rounded), code = rint(127 x / amax_t), ties to
+ *   even, decided as in exact arithmetic.  A row of zeros has scale 0.  A row that
+ *   holds Inf or NaN gets scale NaN and codes 0, and MEGAMOE_DEV_NONFINITE is set.
+ * ------------------------------------------------------------------------ */
+
+/* x [rows, K] of MEGAMOE_TYPE_BF16, F16 or F32 -> codes int8 [rows, K], scales [rows];
+ * status: device status word or null.  Requires K a multiple of 16, x and codes
+ * 16-byte aligned, rows of x on 16-byte boundaries. */
+megamoe_status megamoe_quantize_int8(const void* x, int x_type, int64_t rows, int K, int64_t ld,
+                                     int8_t* codes, float* scales, uint32_t* status,
+                                     megamoe_stream_t stream);
+
+/*
+ * megamoe_linear_int8 -- out[t, n] = (sum_k q_x[t, k] w_codes[n, k]) s_x[t] w_scales[n].
+ *   x         [T, K], row stride ld_x: BF16, F16 or F32, quantised here as above, or
+ *             MEGAMOE_TYPE_I8 codes with x_scales [T] (null otherwise)
+ *   w_codes   int8 [N, K], w_scales float [N]
+ *   out       [T, N] bf16 (MEGAMOE_EPI_BF16) or fp32 (MEGAMOE_EPI_F32)
+ *   ws        at least megamoe_linear_int8_workspace_size(T, K, N) bytes, 256-byte
+ *             aligned; its first 4 bytes are the status word
+ * The integers' sum is exact while sum |q_x q_w| < 2^24, fp32 past that.
+ * Requires K a multiple of 16, N of 8, T, K and N below 2^30, pointers 16-byte
+ * aligned (scales 4-byte) and rows on 16-byte boundaries.
+ */
+size_t megamoe_linear_int8_workspace_size(int64_t T, int K, int N);
+megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, int64_t ld_x,
+                                   const float* x_scales, const int8_t* w_codes,
+                                   const float* w_scales, int N, int out_dtype, void* out,
+                                   int64_t ld_out, void* ws, size_t ws_bytes,
+                                   megamoe_stream_t stream);
 
 #ifdef __cplusplus
 }

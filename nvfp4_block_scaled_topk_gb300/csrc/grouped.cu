@@ -1,0 +1,626 @@
+// Products of 16-bit operands grouped by expert, on tcgen05 tensor cores with
+// fp32 accumulation: rows lie in the order of their experts, expert e's are
+// [start_e, start_e + count_e), any count.
+//
+//   forward:      out[r, n]     = sum_k x[r, k] w[e, n, k]
+//   grad of x:    grad_x[r, k]  = sum_n grad_out[r, n] w[e, n, k]
+//   grad of w:    grad_w[e,n,k] = sum_r grad_out[r, n] x[r, k]
+//
+// A pair of CTAs (tcgen05.mma cta_group::2) works on a tile.  In the first two
+// the weights are the MMA's M side (256 features) and the rows its N side: N is
+// the tile's row count rounded up to 16, so an expert with one row pays for 16
+// and one with 300 for two tiles of 160, where rows on M would pay for 512.
+// The gradient of w sums over rows; its tile is 256 x 256 of one expert.
+//
+// Operands come by tensor map in the 128-byte swizzle, 64 elements of the
+// summed dimension a stage.  Where that dimension is contiguous (x and w of the
+// forward, grad_out of grad_x) boxes are K-major; w in grad_x and both operands
+// of grad_w are read as they lie, MN-major (64 x 64 boxes, one after another).
+//
+// Ends.  Features and columns past the matrix read as zeros and are not
+// stored.  Rows past an expert's last belong to the next one: as N columns they
+// are computed and not stored; where they are summed over (grad_w) one warp of
+// each CTA overwrites them with zeros in shared memory before the MMAs read
+// them, in both operands, since 0 * Inf is not 0.
+//
+// Tensor memory holds two accumulators of 256 columns: a tile is read, rounded
+// and stored under the next one's products.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace megamoe {
+
+namespace {
+
+enum Mode { kForward, kGradX, kGradW };
+
+struct GroupedMaps {
+  CUtensorMap m, n;  // the MMA's M and N side
+};
+
+struct GroupedArgs {
+  const int32_t* offsets;
+  const int32_t* padded_offsets;
+  int64_t rows;  // of the row matrices
+  int E;
+  int F;    // features on the M side (N, K or N)
+  int G;    // grad_w: columns on the N side (K)
+  int sum;  // forward, grad_x: length of the sums (K or N)
+  void* out;
+  int64_t ld_out;
+  uint32_t idesc;  // instruction descriptor without N
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct Cfg {
+  static constexpr int THREADS = 352;  // producer, MMA issuer, 8 epilogue warps, tail warp
+  static constexpr int STAGES = 6;
+  static constexpr int TILE = 128 * 128;  // a CTA's part of either operand
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int STG = 2048;  // staged output of an epilogue warp
+  static constexpr int STG_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = STG_OFF + kEpiWarps * STG;
+  static constexpr int RANGE_OFF = BAR_OFF + 256;  // experts' rows, first tiles
+  static constexpr int TOFF_OFF = RANGE_OFF + 8 * MEGAMOE_MAX_EXPERTS;
+  static constexpr int SMEM = 1024 + TOFF_OFF + 4 * (MEGAMOE_MAX_EXPERTS + 1);
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// kind::f16 over the pair: rows 0 .. 127 of A and D in rank 0's memory, 128 ..
+// 255 in rank 1's, half of B's rows in each.
+__device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// MN-major operand in the 128-byte swizzle: atoms of 64 elements x 8 steps of
+// the summed dimension (1024 bytes), atoms along that dimension 1024 bytes
+// apart, the next 64 elements 8 KB on.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>(8192 >> 4) << 16;
+  d |= static_cast<uint64_t>(1024 >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;  // descriptor version
+  d |= static_cast<uint64_t>(2) << 61;  // 128-byte swizzle
+  return d;
+}
+
+// Rows of an expert, kept inside the matrix whatever the offsets say.
+struct Range {
+  int start, count;
+};
+
+// An expert's rows in tiles of equal size, a multiple of 16 up to 256.
+__device__ __forceinline__ int tile_rows(int count) {
+  const int tiles = (count + 255) / 256;
+  return tiles ? ((count + tiles - 1) / tiles + 15) / 16 * 16 : 16;
+}
+
+// Experts' rows, and s_toff[e] = first tile of expert e, s_toff[E] = all tiles
+// (forward, grad_x).  All threads.
+__device__ void build_tables(const GroupedArgs& p, int MT, Range* s_range, int* s_toff,
+                             int* s_scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.E + Cfg::THREADS - 1) / Cfg::THREADS;
+  const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
+  int sum = 0;
+  bool bad = false;
+  for (int e = e0; e < e1; ++e) {
+    const int64_t o0 = __ldcg(p.offsets + e), o1 = __ldcg(p.offsets + e + 1);
+    const int64_t s = p.padded_offsets ? __ldcg(p.padded_offsets + e) : o0;
+    const int64_t start = min(max(s, int64_t{0}), p.rows);
+    const int64_t count = max(min(s + o1 - o0, p.rows) - start, int64_t{0});
+    bad |= start != s || count != o1 - o0;
+    s_range[e] = {static_cast<int>(start), static_cast<int>(count)};
+    const int rows = tile_rows(static_cast<int>(count));
+    s_toff[e] = (static_cast<int>(count) + rows - 1) / rows * MT;
+    sum += s_toff[e];
+  }
+  if (bad && blockIdx.x == 0) set_status(p.status, MEGAMOE_DEV_BAD_OFFSETS);
+  int x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) s_scan[warp] = x;
+  __syncthreads();
+  int base = x - sum;
+  for (int w = 0; w < warp; ++w) base += s_scan[w];
+  for (int e = e0; e < e1; ++e) {
+    const int t = s_toff[e];
+    s_toff[e] = base;
+    base += t;
+  }
+  if (tid == Cfg::THREADS - 1) s_toff[p.E] = base;
+  __syncthreads();
+}
+
+// A tile as every role sees it.
+struct Tile {
+  int e;
+  int m0;     // first feature
+  int n0;     // first row (forward, grad_x) or column (grad_w)
+  int rows;   // rows: of the tile, or those that are summed over
+  int start;  // grad_w: the expert's first row
+  int n;      // the MMA's N
+  int steps;  // stages of the sum
+  bool again;  // the weights are read by other tiles, too
+};
+template <Mode MODE>
+__device__ __forceinline__ Tile decode(const GroupedArgs& p, int q, const Range* s_range,
+                                       const int* s_toff, int MT, int NT, int* e_lo) {
+  Tile t;
+  if (MODE == kGradW) {
+    t.e = q / (MT * NT);
+    const int local = q - t.e * MT * NT, mt = local / NT;
+    const Range r = s_range[t.e];
+    t.m0 = mt * 256;
+    t.n0 = (local - mt * NT) * 256;
+    t.start = r.start;
+    t.rows = r.count;
+    t.n = 256;
+    t.steps = (r.count + 63) / 64;
+    t.again = true;
+  } else {
+    const TileInfo ti = decode_tile(q, s_toff, p.E, MT, *e_lo);
+    *e_lo = ti.e;
+    const Range r = s_range[ti.e];
+    const int per = tile_rows(r.count);
+    t.e = ti.e;
+    t.m0 = ti.mt * 256;
+    t.n0 = r.start + ti.nt * per;
+    t.start = r.start;
+    t.rows = min(per, r.count - ti.nt * per);
+    t.n = (t.rows + 15) / 16 * 16;
+    t.steps = (p.sum + 63) / 64;
+    t.again = ti.ntiles > 1;
+  }
+  return t;
+}
+
+__device__ __forceinline__ void store_rounded(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_rounded(float v, __half* p) { *p = __float2half_rn(v); }
+__device__ __forceinline__ void store_rounded(float v, float* p) { *p = v; }
+__device__ __forceinline__ uint32_t round_pair(float a, float b, const __nv_bfloat16*) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t round_pair(float a, float b, const __half*) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t round_pair(float, float, const float*) { return 0; }
+
+template <Mode MODE, typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+    k_grouped_pair(const __grid_constant__ GroupedMaps maps, const GroupedArgs p) {
+  using C = Cfg;
+  constexpr int STAGES = C::STAGES;
+  constexpr bool M_MN = MODE != kForward;  // the M side is read MN-major
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + STAGES;
+  uint64_t* ready = empty + STAGES;  // grad_w: rank 0's, after both tail warps
+  uint64_t* acc_full = ready + STAGES;
+  uint64_t* acc_empty = acc_full + 2;  // rank 0's: the epilogue warps of both
+  uint64_t* drain = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  Range* s_range = reinterpret_cast<Range*>(smem + C::RANGE_OFF);
+  int* s_toff = reinterpret_cast<int*>(smem + C::TOFF_OFF);
+  __shared__ int s_scan[C::THREADS / 32];
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int MT = (p.F + 255) / 256, NT = MODE == kGradW ? (p.G + 255) / 256 : 1;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.m);
+    prefetch_tensormap(&maps.n);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&ready[s], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there before either is arrived on
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_trigger();
+  build_tables(p, MT, s_range, s_toff, s_scan);
+  const int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    // (the whole warp, one lane of it issuing: elect_one)
+    const bool leader = elect_one();
+    const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
+    int stage = 0, issued = 0, e_lo = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int q = first; ok && q < total; q += step) {
+      const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+      const int m0 = t.m0 + rank * 128;
+      const int boxes = (t.n / 2 + 31) / 32;  // of 32 rows: this CTA's half of N
+      const int r0 = t.n0 + rank * (t.n / 2);
+      const uint64_t pol_m = t.again ? pol_again : pol_once;
+      for (int i = 0; i < t.steps; ++i) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sm = smem + stage * C::STAGE;
+        uint8_t* sn = sm + C::TILE;
+        if (leader) {
+          if (MODE == kGradW) {  // each CTA's copies complete on its own barrier
+            mbar_arrive_expect_tx(&full[stage], C::STAGE);
+            const int r = t.start + i * 64, n0 = t.n0 + rank * 128;
+            tma_load_2d(sm, &maps.m, &full[stage], m0, r, pol_again);
+            tma_load_2d(sm + 8192, &maps.m, &full[stage], m0 + 64, r, pol_again);
+            tma_load_2d(sn, &maps.n, &full[stage], n0, r, pol_again);
+            tma_load_2d(sn + 8192, &maps.n, &full[stage], n0 + 64, r, pol_again);
+          } else {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + boxes * 4096));
+            const uint32_t bar = cluster_address(&full[stage], 0);
+            if (M_MN) {
+              tma_load_3d_pair(sm, &maps.m, bar, m0, i * 64, t.e, pol_m);
+              tma_load_3d_pair(sm + 8192, &maps.m, bar, m0 + 64, i * 64, t.e, pol_m);
+            } else {
+              tma_load_3d_pair(sm, &maps.m, bar, i * 64, m0, t.e, pol_m);
+            }
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d_pair(sn + b * 4096, &maps.n, bar, i * 64, r0 + b * 32, pol_again);
+          }
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    if (MODE == kGradW) drain_copies(full, STAGES, issued);
+    else drain_pair_copies(full, STAGES, issued, rank, !ok);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint64_t dm = M_MN ? sdesc_mn(smem_u32(smem)) : sdesc_sw128(smem_u32(smem));
+      const uint64_t dn = MODE == kGradW ? sdesc_mn(smem_u32(smem) + C::TILE)
+                                         : sdesc_sw128(smem_u32(smem) + C::TILE);
+      // 16 of the summed dimension: 32 bytes of a row, or 16 rows of 128 bytes
+      constexpr uint32_t AM = M_MN ? 2048 : 32, AN = MODE == kGradW ? 2048 : 32;
+      int stage = 0, tiles = 0, e_lo = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int q = first; ok && q < total; q += step) {
+        const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+        if (t.steps == 0) continue;
+        const uint32_t buf = tiles & 1, acc = tmem + buf * 256;
+        const uint32_t idesc = p.idesc | static_cast<uint32_t>(t.n >> 3) << 17;
+        if (!mbar_wait(&acc_empty[buf], (tiles >> 1 & 1) ^ 1u, abort_flag, p.status,
+                       p.wait_limit_ns))
+          break;
+        ++tiles;
+        tc_fence_after();
+        for (int i = 0; i < t.steps; ++i) {
+          uint64_t* bar = MODE == kGradW ? &ready[stage] : &full[stage];
+          if (!mbar_wait(bar, phase, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          if (MODE == kGradW) fence_cluster();
+          tc_fence_after();
+          const uint64_t cm = sdesc_at(dm, stage * C::STAGE), cn = sdesc_at(dn, stage * C::STAGE);
+          // sixteens of the last stage that hold nothing are left out
+          const int left = (MODE == kGradW ? t.rows : p.sum) - i * 64;
+          if (leader) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              if (16 * c < left)
+                mma_f16_pair(acc, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
+                             (i != 0 || c != 0) ? 1u : 0u);
+            tc_commit_pair(&empty[stage]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair(&acc_full[buf]);
+        __syncwarp();
+      }
+      // every MMA issued so far must finish before tensor memory is released
+      if (leader) tc_commit_pair(drain);
+      __syncwarp();
+      mbar_drain(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    if (MODE == kGradW) {
+      // ---------------------------------------------------------- tail warp
+      // hands every stage on to the MMAs; in an expert's last one the rows past
+      // its end become zeros first, up to the sixteen that are read
+      int stage = 0, e_lo = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int q = first; ok && q < total; q += step) {
+        const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+        for (int i = 0; i < t.steps; ++i) {
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          const int left = t.rows - i * 64;
+          if (left < 64 && (left & 15) != 0) {
+            uint8_t* sb = smem + stage * C::STAGE;
+            const int end = (left + 15) / 16 * 16;  // rows of 128 bytes in each of four boxes
+            for (int v = left * 8 + lane; v < end * 8; v += 32)
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
+            fence_async_shared();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(&ready[stage], 0);
+          __syncwarp();
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3;
+    const int half = warp >= 6 ? 1 : 0;
+    uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
+    constexpr int SIZE = sizeof(O), PER = 16 / SIZE;  // elements of 16 bytes
+    O* out = static_cast<O*>(p.out);
+    int tiles = 0, e_lo = 0;
+    for (int q = first; q < total; q += step) {
+      const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+      const int m = t.m0 + rank * 128 + quarter * 32;  // this warp's first feature
+      const uint32_t buf = tiles & 1;
+      const bool some = t.steps != 0;
+      if (some) {
+        if (!mbar_wait(&acc_full[buf], tiles >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) break;
+        tc_fence_after();
+        ++tiles;
+      }
+      const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+      auto let_go = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], 0);
+      };
+      if (MODE != kGradW) {
+        // A lane has a feature, a column is a row of the output: 64 or 128 bytes
+        // of 32 features of a row at a time through shared memory.  The two warps
+        // of a quarter take chunks of 32 rows in turn.
+        constexpr int ROWS = C::STG / (32 * SIZE);  // staged at a time
+        constexpr int LANES = 32 / PER;             // lanes of a row's 16-byte pieces
+        const int chunks = (t.rows + 31) / 32;
+        const int piece = lane % LANES;
+        const bool in = m + piece * PER < p.F;
+        for (int c = half; c < chunks; c += 2) {
+          uint32_t v[32];
+          tmem_ld_32x32b_x32(base + 32 * c, v);
+          tmem_ld_wait();
+          if (m >= p.F) continue;  // warp-uniform
+#pragma unroll
+          for (int g = 0; g < 32 / ROWS; ++g) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j)
+              store_rounded(__uint_as_float(v[g * ROWS + j]), reinterpret_cast<O*>(stg) + j * 32 + lane);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < ROWS * LANES / 32; ++j) {
+              const int r = j * (32 / LANES) + lane / LANES;
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
+              const int row = 32 * c + g * ROWS + r;
+              if (in && row < t.rows)
+                *reinterpret_cast<uint4*>(out + (t.n0 + static_cast<int64_t>(row)) * p.ld_out + m +
+                                          piece * PER) = x;
+            }
+          }
+        }
+        let_go();
+      } else {
+        // A lane has a row of the output: 128-byte pieces of 16 rows at a time.
+        constexpr int COLS = 128 / SIZE;
+        const int c0 = t.n0 + half * 128, piece = lane & 7;
+        O* at = out + (static_cast<int64_t>(t.e) * p.F + m) * p.ld_out + c0 + piece * PER;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += COLS) {
+          uint32_t u[COLS];
+          if (some) {
+            tmem_ld_32x32b_x32(base + half * 128 + c, u);
+            if (COLS == 64) tmem_ld_32x32b_x32(base + half * 128 + c + 32, u + COLS - 32);
+            tmem_ld_wait();
+            if (c + COLS == 128) let_go();
+          } else {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) u[j] = 0;
+          }
+          if (m >= p.F || c0 + c >= p.G) continue;  // warp-uniform
+          if (SIZE == 2) {
+#pragma unroll
+            for (int j = 0; j < COLS / 2; ++j)
+              u[j] = round_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]),
+                                static_cast<const O*>(nullptr));
+          }
+          const bool in = c0 + c + piece * PER < p.G;
+#pragma unroll 1
+          for (int g = 0; g < 2; ++g) {  // 16 rows
+            __syncwarp();
+            if (lane >> 4 == g) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
+                *reinterpret_cast<uint4*>(stg + (lane & 15) * 128 + ((j ^ piece) * 16)) =
+                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 4 * i + (lane >> 3);
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) * 16));
+              if (in && m + 16 * g + r < p.F)
+                __stcs(reinterpret_cast<uint4*>(at + static_cast<int64_t>(16 * g + r) * p.ld_out + c), x);
+            }
+          }
+        }
+      }
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  // rank 0's commits arrive on rank 1's barriers too: none is on its way after the last
+  if (warp == 1) mbar_drain(drain, 0);
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves while the other still reaches into it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <Mode MODE, typename O>
+cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t tiles,
+                         cudaStream_t stream) {
+  auto kern = k_grouped_pair<MODE, O>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
+                    stream, maps, a);
+}
+
+template <Mode MODE>
+cudaError_t launch_mode(const GroupedMaps& maps, const GroupedArgs& a, int out_type, int64_t tiles,
+                        cudaStream_t stream) {
+  if (out_type == MEGAMOE_TYPE_F32) return launch_typed<MODE, float>(maps, a, tiles, stream);
+  if (out_type == MEGAMOE_TYPE_F16) return launch_typed<MODE, __half>(maps, a, tiles, stream);
+  return launch_typed<MODE, __nv_bfloat16>(maps, a, tiles, stream);
+}
+
+// [E, N, K] weights, boxes of 64 x `rows`.
+bool weight_map(CUtensorMap* map, const Grouped& g, uint32_t rows) {
+  const uint64_t row = static_cast<uint64_t>(g.K) * 2;
+  return make_map_3d(map, g.w, g.K, g.N, g.E, row, row * g.N, 64, rows, 1,
+                     CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+bool rows_map(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t ld,
+              uint32_t box) {
+  return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, base, cols, rows,
+                  static_cast<uint64_t>(ld) * 2, 64, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// Instruction descriptor (kind::f16) without N: fp32 sums, M = 256, MN-major sides.
+uint32_t idesc_f16(int type, bool m_mn, bool n_mn) {
+  const uint32_t format = type == MEGAMOE_TYPE_BF16 ? 1u : 0u;
+  return (1u << 4) | format << 7 | format << 10 | (m_mn ? 1u << 15 : 0u) | (n_mn ? 1u << 16 : 0u) |
+         (256u >> 4) << 24;
+}
+
+GroupedArgs args_of(const Grouped& g) {
+  GroupedArgs a{};
+  a.offsets = g.offsets;
+  a.padded_offsets = g.padded_offsets;
+  a.rows = g.rows;
+  a.E = g.E;
+  a.status = g.status;
+  a.wait_limit_ns = wait_limit_ns();
+  return a;
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_forward(const Grouped& g, void* out, int out_type, int64_t ld_out,
+                                   cudaStream_t stream) {
+  if (g.rows == 0) return cudaSuccess;
+  GroupedMaps maps;
+  if (!weight_map(&maps.m, g, 128) || !rows_map(&maps.n, g.x, g.K, g.rows, g.ld_x, 32))
+    return cudaErrorInvalidValue;
+  GroupedArgs a = args_of(g);
+  a.F = g.N;
+  a.sum = g.K;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.idesc = idesc_f16(g.type, false, false);
+  return launch_mode<kForward>(maps, a, out_type, grouped_tiles(g.rows, g.E, g.N), stream);
+}
+
+cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, cudaStream_t stream) {
+  if (g.rows == 0) return cudaSuccess;
+  GroupedMaps maps;
+  if (!weight_map(&maps.m, g, 64) || !rows_map(&maps.n, g.grad, g.N, g.rows, g.ld_grad, 32))
+    return cudaErrorInvalidValue;
+  GroupedArgs a = args_of(g);
+  a.F = g.K;
+  a.sum = g.N;
+  a.out = out;
+  a.ld_out = ld_out;
+  a.idesc = idesc_f16(g.type, true, false);
+  const int64_t tiles = grouped_tiles(g.rows, g.E, g.K);
+  return g.type == MEGAMOE_TYPE_F16 ? launch_typed<kGradX, __half>(maps, a, tiles, stream)
+                                    : launch_typed<kGradX, __nv_bfloat16>(maps, a, tiles, stream);
+}
+
+cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream) {
+  GroupedArgs a = args_of(g);
+  a.F = g.N;
+  a.G = g.K;
+  a.out = out;
+  a.ld_out = g.K;
+  a.idesc = idesc_f16(g.type, true, true);
+  if (g.rows == 0)  // nothing to add up
+    return cudaMemsetAsync(out, 0, static_cast<size_t>(g.E) * g.N * g.K *
+                                       (out_type == MEGAMOE_TYPE_F32 ? 4 : 2), stream);
+  GroupedMaps maps;
+  if (!rows_map(&maps.m, g.grad, g.N, g.rows, g.ld_grad, 64) ||
+      !rows_map(&maps.n, g.x, g.K, g.rows, g.ld_x, 64))
+    return cudaErrorInvalidValue;
+  const int64_t tiles = static_cast<int64_t>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256);
+  return launch_mode<kGradW>(maps, a, out_type, tiles, stream);
+}
+
+}  // namespace megamoe

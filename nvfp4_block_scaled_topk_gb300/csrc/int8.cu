@@ -1,0 +1,585 @@
+// Linear in 8-bit integers: y[t, n] = (sum_k q_x[t, k] q_w[n, k]) s_x[t] s_w[n].
+//
+// A token's scale is amax / 127 (rounded to fp32) and its integers
+// rint(127 x / amax), ties to even, decided as in exact arithmetic.
+//
+// The tensor cores of sm_103a have no integer kind.  An 8-bit integer is exact in
+// fp16 and a product of two in fp32, so the integers are multiplied as fp16
+// (kind::f16) and the sum is exact up to 2^24, that is while sum |q_x q_w| stays
+// below it, and rounded to fp32 at each of the K / 16 additions past that.
+//
+// Weights stay in memory as bytes.  A pair of CTAs has 256 features on the MMA's
+// M side: four warps of each read a stage's bytes from shared memory, widen them
+// in registers (a byte with its sign bit flipped under 0x64 is the fp16 value 1024
+// + 128 + q) and put them into tensor memory, from where the MMA takes its A
+// operand; the tokens' integers come as fp16 by tensor map.  Per 128 of K a CTA
+// so takes in 16 KB of weights and up to 32 KB of tokens.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "gemm_common.cuh"
+#include "kernels.h"
+
+namespace megamoe {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Quantisation of tokens: a block a row
+// ---------------------------------------------------------------------------
+constexpr int kQuantThreads = 256;
+constexpr int kHeld = 4;  // eights of elements a thread keeps between the two passes
+
+// Eight elements as fp32.
+template <typename X>
+__device__ __forceinline__ void load8(const X* p, float (&v)[8]);
+template <>
+__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// rint(127 x / amax) as in exact arithmetic, |x| <= amax.  The fast product with
+// 127 / amax is off by at most 2^-22 of the quotient; only where that could
+// change the integer (the fraction within 2^-13 of a half, or an amax whose
+// inverse is no normal number) is the quotient taken in 64 bits.  There 127 x is
+// exact, and a quotient of two fp32 numbers that is no half is at least 2^-33 of
+// its size away from one.
+__device__ __forceinline__ int quantised(float x, float amax, float inv) {
+  const float t = x * inv, r = rintf(t);
+  if (fabsf(fabsf(t - r) - 0.5f) > 0x1p-13f && inv < INFINITY && amax < 0x1p120f)
+    return static_cast<int>(r);
+  return static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+}
+
+template <typename X>
+__global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant p) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float s_amax[kQuantThreads / 32];
+  const int vecs = p.K / 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const X* row = static_cast<const X*>(p.x) + t * p.ld;
+    float v[kHeld][8];
+    // the largest magnitude by its bits: NaN and Inf compare as the largest
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int i = threadIdx.x + h * kQuantThreads;
+      if (i >= vecs) break;
+      load8(row + i * 8, v[h]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[h][j]) & 0x7fffffffu);
+    }
+    for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
+      float u[8];
+      load8(row + static_cast<int64_t>(i) * 8, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(u[j]) & 0x7fffffffu);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    __syncthreads();  // the row before has been read
+    if (lane == 0) s_amax[warp] = __uint_as_float(m);
+    __syncthreads();
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, __float_as_uint(s_amax[i]));
+    const bool finite = m < 0x7f800000u;
+    const float amax = __uint_as_float(m);
+    const float inv = 127.f / amax;
+    const bool zero = !finite || m == 0;
+    if (threadIdx.x == 0) {
+      p.scales[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
+      if (!finite && !p.clear) set_status(p.status, MEGAMOE_DEV_NONFINITE);
+    }
+    auto put = [&](int i, const float (&u)[8]) {
+      int q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) q[j] = zero ? 0 : quantised(u[j], amax, inv);
+      const int64_t at = t * p.K + static_cast<int64_t>(i) * 8;
+      if (p.half) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __half2 h = __halves2half2(__int2half_rn(q[2 * j]), __int2half_rn(q[2 * j + 1]));
+          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(p.half + at) = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        uint32_t w[2] = {0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j >> 2] |= static_cast<uint32_t>(q[j] & 0xff) << (8 * (j & 3));
+        *reinterpret_cast<uint2*>(p.codes + at) = make_uint2(w[0], w[1]);
+      }
+    };
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int i = threadIdx.x + h * kQuantThreads;
+      if (i >= vecs) break;
+      put(i, v[h]);
+    }
+    for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
+      float u[8];
+      load8(row + static_cast<int64_t>(i) * 8, u);
+      put(i, u);
+    }
+  }
+}
+
+// Four integers -> four fp16 values: with its sign bit flipped a byte is q + 128,
+// and under 0x64 the fp16 number 1024 + 128 + q, of which 1152 is taken off exactly.
+__device__ __forceinline__ void widen4(uint32_t bytes, uint32_t* lo, uint32_t* hi) {
+  const uint32_t u = bytes ^ 0x80808080u;
+  const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+  uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+  const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+  const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+  *lo = *reinterpret_cast<const uint32_t*>(&x);
+  *hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
+// Integers that the caller brings, as fp16, and their scales.
+__global__ void __launch_bounds__(kQuantThreads) k_int8_widen(const Int8Quant p) {
+  pdl_wait();
+  pdl_trigger();
+  if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
+  const int vecs = p.K / 16;
+  const int64_t total = p.T * vecs;
+  for (int64_t i = blockIdx.x * int64_t{kQuantThreads} + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * kQuantThreads) {
+    const int64_t t = i / vecs;
+    const int v = static_cast<int>(i - t * vecs);
+    if (v == 0) p.scales[t] = __ldg(p.x_scales + t);
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.x) + t * p.ld) + v);
+    uint4 a, b;
+    widen4(q.x, &a.x, &a.y);
+    widen4(q.y, &a.z, &a.w);
+    widen4(q.z, &b.x, &b.y);
+    widen4(q.w, &b.z, &b.w);
+    uint4* to = reinterpret_cast<uint4*>(p.half + t * p.K + static_cast<int64_t>(v) * 16);
+    to[0] = a;
+    to[1] = b;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The product on pairs of CTAs
+// ---------------------------------------------------------------------------
+struct Int8Maps {
+  CUtensorMap w, x;
+};
+
+struct Int8Args {
+  const float* x_scales;
+  const float* w_scales;
+  int T, N, K;
+  int per;  // tokens of a tile, a multiple of 16 up to 256
+  void* out;
+  int64_t ld_out;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+};
+
+struct Cfg {
+  static constexpr int THREADS = 448;  // producer, MMA issuer, 8 epilogue warps, 4 that widen
+  static constexpr int STAGES = 4;     // of 128 of K
+  static constexpr int W = 128 * 128;  // a CTA's bytes of weights
+  static constexpr int X = 128 * 128;  // its tokens' fp16, 64 of K
+  static constexpr int STAGE = W + 2 * X;
+  static constexpr int STG = 2048;  // staged output of an epilogue warp
+  static constexpr int STG_OFF = STAGES * STAGE;
+  static constexpr int BAR_OFF = STG_OFF + kEpiWarps * STG;
+  static constexpr int SMEM = 1024 + BAR_OFF + 256;
+  // tensor memory: accumulators in turn at columns 0 and 128 (128 in common), then
+  // two buffers of widened weights
+  static constexpr int ACC1 = 128;
+  static constexpr int A_COL0 = 384;
+  static constexpr int A_COLS = 64;
+  static_assert(SMEM <= 232448, "shared memory budget");
+};
+
+// kind::f16 over the pair with A in each CTA's tensor memory (its 128 rows).
+__device__ __forceinline__ void mma_f16_pair_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+      "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+
+__device__ __forceinline__ void store_rounded(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void store_rounded(float v, float* p) { *p = v; }
+
+// Tile q: bands of eight tiles of tokens, feature tile by feature tile within a
+// band, so that tiles in work at a time share few rows of either operand.
+__device__ __forceinline__ void int8_tile(int q, int MT, int NT, int* mt, int* nt) {
+  const int band = q / (8 * MT), r = q - band * 8 * MT;
+  const int wide = min(8, NT - band * 8);
+  *mt = r / wide;
+  *nt = band * 8 + r - *mt * wide;
+}
+
+template <typename O>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+    k_int8_pair(const __grid_constant__ Int8Maps maps, const Int8Args p) {
+  using C = Cfg;
+  constexpr int STAGES = C::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* empty = full + STAGES;
+  uint64_t* a_full = empty + STAGES;  // rank 0's: the widening warps of both
+  uint64_t* a_empty = a_full + 2;
+  uint64_t* acc_full = a_empty + 2;
+  uint64_t* acc_empty = acc_full + 1;  // rank 0's: the epilogue warps of both
+  uint64_t* drain = acc_empty + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_rank());
+  const int MT = (p.N + 255) / 256, NT = (p.T + p.per - 1) / p.per;
+  const int KT = (p.K + 127) / 128;
+  const int total = MT * NT;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
+
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&maps.w);
+    prefetch_tensormap(&maps.x);
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&a_full[i], 8);
+      mbar_init(&a_empty[i], 1);
+    }
+    mbar_init(acc_full, 1);
+    mbar_init(acc_empty, 2 * kEpiWarps);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_holder, 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there before either is arrived on
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  pdl_wait();
+  pdl_trigger();
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- producer
+    // (the whole warp, one lane of it issuing: elect_one); each CTA's copies
+    // complete on its own barrier
+    const bool leader = elect_one();
+    const uint64_t pol_w = NT > 1 ? policy_evict_normal() : policy_evict_first();
+    const uint64_t pol_x = policy_evict_normal();
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int q = first; ok && q < total; q += step) {
+      int mt, nt;
+      int8_tile(q, MT, NT, &mt, &nt);
+      const int rows = min(p.per, p.T - nt * p.per), half = (rows + 15) / 16 * 8;
+      const int boxes = (half + 31) / 32, t0 = nt * p.per + rank * half;
+      const int m0 = mt * 256 + rank * 128;
+      for (int i = 0; i < KT; ++i) {
+        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sw = smem + stage * C::STAGE;
+        uint8_t* sx = sw + C::W;
+        if (leader) {
+          mbar_arrive_expect_tx(&full[stage], C::W + 2 * boxes * 4096);
+          tma_load_2d(sw, &maps.w, &full[stage], i * 128, m0, pol_w);
+          for (int h = 0; h < 2; ++h)
+            for (int b = 0; b < boxes; ++b)
+              tma_load_2d(sx + h * C::X + b * 4096, &maps.x, &full[stage], i * 128 + h * 64,
+                          t0 + b * 32, pol_x);
+        }
+        __syncwarp();
+        ++issued;
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    drain_copies(full, STAGES, issued);
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      // ---------------------------------------------------------- MMA issuer
+      const bool leader = elect_one();
+      const uint64_t dx = sdesc_sw128(smem_u32(smem) + C::W);
+      // fp16 operands, K-major, fp32 sums, M = 256
+      constexpr uint32_t idesc0 = (1u << 4) | (256u >> 4) << 24;
+      int stage = 0, tiles = 0, steps = 0;
+      bool ok = true;
+      for (int q = first; ok && q < total; q += step, ++tiles) {
+        int mt, nt;
+        int8_tile(q, MT, NT, &mt, &nt);
+        const int n = (min(p.per, p.T - nt * p.per) + 15) / 16 * 16;
+        const uint32_t idesc = idesc0 | static_cast<uint32_t>(n >> 3) << 17;
+        const uint32_t acc = tmem + (tiles & 1) * C::ACC1;
+        for (int i = 0; i < KT; ++i, ++steps) {
+          const int buf = steps & 1;
+          if (!mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
+              (i == 0 && !mbar_wait(acc_empty, (tiles & 1) ^ 1u, abort_flag, p.status,
+                                    p.wait_limit_ns))) {
+            ok = false;
+            break;
+          }
+          fence_cluster();
+          tc_fence_after();
+          const uint64_t cx = sdesc_at(dx, stage * C::STAGE);
+          const uint32_t a = tmem + C::A_COL0 + buf * C::A_COLS;
+          const int left = p.K - i * 128;  // a multiple of 16
+          if (leader) {
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              if (16 * c < left)
+                mma_f16_pair_ts(acc, a + 8 * c, sdesc_at(cx, (c >> 2) * C::X + 32 * (c & 3)), idesc,
+                                (i != 0 || c != 0) ? 1u : 0u);
+            tc_commit_pair(&empty[stage]);
+            tc_commit_pair(&a_empty[buf]);
+          }
+          __syncwarp();
+          if (++stage == STAGES) stage = 0;
+        }
+        if (!ok) break;
+        if (leader) tc_commit_pair(acc_full);
+        __syncwarp();
+      }
+      // every MMA issued so far must finish before tensor memory is released
+      if (leader) tc_commit_pair(drain);
+      __syncwarp();
+      mbar_drain(drain, 0);
+    }
+    __syncwarp();
+  } else if (warp >= 10) {
+    // ---------------------------------------------------------- widening warps
+    // A lane has a row of 128 bytes; its 16-byte piece j is at j ^ (row % 8).
+    const int quarter = warp & 3;
+    const uint32_t to = tmem + C::A_COL0 + (static_cast<uint32_t>(quarter * 32) << 16);
+    int stage = 0, steps = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int q = first; ok && q < total; q += step) {
+      for (int i = 0; i < KT; ++i, ++steps) {
+        const int buf = steps & 1;
+        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        const uint4* row = reinterpret_cast<const uint4*>(smem + stage * C::STAGE +
+                                                          (quarter * 32 + lane) * 128);
+        uint32_t v[64];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint4 b = row[j ^ (lane & 7)];
+          widen4(b.x, &v[8 * j], &v[8 * j + 1]);
+          widen4(b.y, &v[8 * j + 2], &v[8 * j + 3]);
+          widen4(b.z, &v[8 * j + 4], &v[8 * j + 5]);
+          widen4(b.w, &v[8 * j + 6], &v[8 * j + 7]);
+        }
+        if (!mbar_wait(&a_empty[buf], (steps >> 1 & 1) ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        tmem_st_32x32b_x32(to + buf * C::A_COLS, v);
+        tmem_st_32x32b_x32(to + buf * C::A_COLS + 32, v + 32);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(&a_full[buf], 0);
+        __syncwarp();
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    // A lane has a feature, a column is a token: 64 or 128 bytes of 32 features of
+    // a token at a time through shared memory.  The two warps of a quarter take
+    // chunks of 32 tokens in turn, those first whose columns the next tile's
+    // accumulator shares; its products may start once they have been read.
+    const int quarter = warp & 3;
+    const int half = warp >= 6 ? 1 : 0;
+    uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
+    constexpr int SIZE = sizeof(O), PER = 16 / SIZE;
+    constexpr int ROWS = C::STG / (32 * SIZE);  // staged at a time
+    constexpr int LANES = 32 / PER;             // lanes of a token's 16-byte pieces
+    const int piece = lane % LANES;
+    O* out = static_cast<O*>(p.out);
+    int tiles = 0;
+    bool bad = false;
+    for (int q = first; q < total; q += step, ++tiles) {
+      int mt, nt;
+      int8_tile(q, MT, NT, &mt, &nt);
+      const int rows = min(p.per, p.T - nt * p.per), t0 = nt * p.per;
+      const int m = mt * 256 + rank * 128 + quarter * 32;  // this warp's first feature
+      const float sw = m + lane < p.N ? __ldg(p.w_scales + m + lane) : 0.f;
+      if (!mbar_wait(acc_full, tiles & 1, abort_flag, p.status, p.wait_limit_ns)) break;
+      tc_fence_after();
+      const uint32_t base =
+          tmem + (tiles & 1) * C::ACC1 + (static_cast<uint32_t>(quarter * 32) << 16);
+      const bool in = m + piece * PER < p.N;
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part) {  // 128 tokens, the shared columns first
+        const int c0 = ((tiles & 1) ^ part ^ 1) * 128 + half * 32;
+        uint32_t v[2][32];
+        if (c0 < rows) tmem_ld_32x32b_x32(base + c0, v[0]);
+        if (c0 + 64 < rows) tmem_ld_32x32b_x32(base + c0 + 64, v[1]);
+        tmem_ld_wait();
+        if (part == 0) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
+        }
+        if (m >= p.N) continue;  // warp-uniform
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = c0 + 64 * h;
+          if (c >= rows) continue;
+          const float4* xs = reinterpret_cast<const float4*>(p.x_scales + t0 + c);
+#pragma unroll
+          for (int g = 0; g < 32 / ROWS; ++g) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < ROWS; j += 4) {
+              const float4 s = __ldg(xs + (g * ROWS + j) / 4);
+              const float sx[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                store_rounded(__uint_as_float(v[h][g * ROWS + j + i]) * sx[i] * sw,
+                              reinterpret_cast<O*>(stg) + (j + i) * 32 + lane);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < ROWS * LANES / 32; ++j) {
+              const int r = j * (32 / LANES) + lane / LANES;
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
+              const int row = c + g * ROWS + r;
+              if (in && row < rows)
+                *reinterpret_cast<uint4*>(out + (t0 + static_cast<int64_t>(row)) * p.ld_out + m +
+                                          piece * PER) = x;
+            }
+          }
+          if (mt == 0 && c + lane < rows) {  // once for each token
+            const float s = __ldg(p.x_scales + t0 + c + lane);
+            bad |= !(s <= 0x1.fffffep127f);
+          }
+        }
+      }
+    }
+    if (bad) set_status(p.status, MEGAMOE_DEV_NONFINITE);
+    __syncwarp();
+  }
+  __syncthreads();
+  // rank 0's commits arrive on rank 1's barriers too: none is on its way after the last
+  if (warp == 1) mbar_drain(drain, 0);
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves while the other still reaches into it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename O>
+cudaError_t launch_pair(const Int8Maps& maps, const Int8Args& a, int64_t tiles, cudaStream_t stream) {
+  auto kern = k_int8_pair<O>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
+  if (e != cudaSuccess) return e;
+  const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
+  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
+                    stream, maps, a);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_quantize(const Int8Quant& q, cudaStream_t stream) {
+  if (q.T == 0) return cudaSuccess;
+  const int64_t most = static_cast<int64_t>(num_sms()) * 16;
+  if (q.type == MEGAMOE_TYPE_I8) {
+    const int64_t blocks = (q.T * (q.K / 16) + kQuantThreads - 1) / kQuantThreads;
+    return launch_pdl(k_int8_widen, dim3(static_cast<unsigned>(std::min(blocks, most))),
+                      dim3(kQuantThreads), 0, stream, q);
+  }
+  auto kern = q.type == MEGAMOE_TYPE_F32   ? k_int8_quantize<float>
+              : q.type == MEGAMOE_TYPE_F16 ? k_int8_quantize<__half>
+                                           : k_int8_quantize<__nv_bfloat16>;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(std::min(q.T, most))), dim3(kQuantThreads), 0,
+                    stream, q);
+}
+
+cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {
+  if (g.T == 0) return cudaSuccess;
+  Int8Maps maps;
+  if (!make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w, g.K, g.N, g.K, 128, 128,
+                CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.x, g.K, g.T,
+                static_cast<uint64_t>(g.K) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  const int64_t nt = (g.T + 255) / 256;
+  const int per = static_cast<int>(((g.T + nt - 1) / nt + 15) / 16 * 16);
+  const Int8Args a{g.x_scales, g.w_scales, static_cast<int>(g.T), g.N, g.K, per, g.out, g.ld_out,
+                   g.status, wait_limit_ns()};
+  const int64_t tiles = nt * ((g.N + 255) / 256);
+  return g.out_f32 ? launch_pair<float>(maps, a, tiles, stream)
+                   : launch_pair<__nv_bfloat16>(maps, a, tiles, stream);
+}
+
+}  // namespace megamoe

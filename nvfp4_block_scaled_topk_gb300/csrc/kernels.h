@@ -173,9 +173,11 @@ bool make_map(CUtensorMap* map, CUtensorMapDataType type, const void* base, uint
               uint64_t rows, uint64_t stride, uint32_t box_cols, uint32_t box_rows,
               CUtensorMapSwizzle swizzle);
 
-// 3-D map of 32-bit words.
+// 3-D map, strides in bytes.
 bool make_map_3d(CUtensorMap* map, const void* base, uint64_t n0, uint64_t n1, uint64_t n2,
-                 uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2);
+                 uint64_t stride1, uint64_t stride2, uint32_t box0, uint32_t box1, uint32_t box2,
+                 CUtensorMapDataType type = CU_TENSOR_MAP_DATA_TYPE_UINT32,
+                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // Scored router (grouped top-k over sigmoid or softmax scores) and its gradient.
 struct ScoredRouter {
@@ -293,6 +295,90 @@ cudaError_t launch_mx_linear_few(const void* x, int x_type, int64_t T, int K, in
                                  const uint8_t* codes, const uint8_t* scales, int N, void* out,
                                  bool out_f32, int64_t ld_out, uint32_t* status,
                                  cudaStream_t stream);
+
+// Products of 16-bit operands grouped by expert (grouped.cu): x [rows, K], grad
+// [rows, N] in the experts' order, w [E, N, K].
+struct Grouped {
+  const void* x;
+  const void* grad;
+  const void* w;
+  int type;  // MEGAMOE_TYPE_BF16 or _F16
+  int64_t rows, ld_x, ld_grad;
+  int E, N, K;
+  const int32_t* offsets;
+  const int32_t* padded_offsets;  // null: the same
+  uint32_t* status;
+};
+cudaError_t launch_grouped_forward(const Grouped& g, void* out, int out_type, int64_t ld_out,
+                                   cudaStream_t stream);
+cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, cudaStream_t stream);
+cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream);
+// Most tiles of the first two with `features` columns of output (counted in 31 bits).
+inline int64_t grouped_tiles(int64_t rows, int E, int features) {
+  return (rows / 256 + (rows < E ? rows : E)) * ((features + int64_t{255}) / 256);
+}
+
+// 8-bit integer linear (int8.cu).  x [T, K] of any MEGAMOE_TYPE_*; as I8 with
+// x_scales [T].
+struct Int8Quant {
+  const void* x;
+  int type;
+  const float* x_scales;
+  int64_t T, ld;
+  int K;
+  int8_t* codes;   // [T, K], or
+  uint16_t* half;  // the integers as fp16, [T, K]
+  float* scales;
+  uint32_t* status;  // NONFINITE is set here unless clear
+  bool clear;  // status = 0 (the product that follows sets what it finds)
+};
+cudaError_t launch_int8_quantize(const Int8Quant& q, cudaStream_t stream);
+struct Int8Product {
+  const uint16_t* x;  // fp16 integers [T, K]
+  const float* x_scales;  // readable up to a multiple of 64
+  int64_t T;
+  const int8_t* w;  // [N, K]
+  const float* w_scales;
+  int N, K;
+  void* out;
+  bool out_f32;
+  int64_t ld_out;
+  uint32_t* status;
+};
+cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream);
+
+// The gated activation and the movement of rows (rows.cu); 16-bit elements,
+// widths multiples of 8.
+struct Silu {
+  const void* a;  // [rows, 2 I]: gate, up
+  const void* grad;  // [rows, I], backward only
+  int type;
+  int64_t rows, ld_a, ld_grad, ld_out;
+  int I;
+  const int32_t* live_rows;  // may be null
+  void* out;  // [rows, I], or backward [rows, 2 I]
+};
+cudaError_t launch_silu(const Silu& a, cudaStream_t stream);
+cudaError_t launch_silu_backward(const Silu& a, cudaStream_t stream);
+cudaError_t launch_gather_rows(const void* x, int64_t T, int d, int64_t ld_x,
+                               const int32_t* row_src, int64_t rows, int k, void* out,
+                               int64_t ld_out, cudaStream_t stream);
+struct CombineRows {
+  const void* y;
+  int type;
+  int64_t rows, ld_y;
+  const int32_t* slot_dst;
+  const float* weights;  // null: all one
+  int64_t T;
+  int k, d;
+  const void* grad;  // backward: [T, d]
+  int64_t ld_grad;
+  void* out;  // [T, d], or backward the gradient of y
+  int64_t ld_out;
+  float* grad_weights;  // backward, may be null
+};
+cudaError_t launch_combine_rows(const CombineRows& c, cudaStream_t stream);
+cudaError_t launch_combine_rows_backward(const CombineRows& c, cudaStream_t stream);
 
 // Shape and weight-pointer checks of megamoe_forward.
 megamoe_status check_forward_shape(const megamoe_weights* w, int T, int k, int pad);
