@@ -160,6 +160,8 @@ struct Tile {
   int start;  // grad_w: the expert's first row
   int n;      // the MMA's N
   int steps;  // stages of the sum
+  // grad_w: a stage whose last sixteen rows are not all the expert's
+  __device__ bool ragged_at(int i) const { return i == steps - 1 && (rows & 15) != 0; }
   bool again;  // the weights are read by other tiles, too
 };
 template <Mode MODE>
@@ -213,13 +215,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   using C = Cfg;
   constexpr int STAGES = C::STAGES;
   constexpr bool M_MN = MODE != kForward;  // the M side is read MN-major
+  // Sums in tensor memory drop what lies past their last bit: at 2048, 4096 and
+  // 16384 rows in one go the gradient of w was off by 2.1e-6, 4.4e-6 and 1.9e-5 of
+  // its size, always towards zero.  For fp32 results the sum is taken in parts of
+  // SEG stages, and the epilogue adds the parts up in registers, rounding to nearest.
+  // A 16-bit result is rounded to 2^-9 or 2^-12 of its size and takes one part.
+  constexpr bool FOLD = sizeof(O) == 4;
+  constexpr int SEG = FOLD ? 8 : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // rank 0's
   uint64_t* empty = full + STAGES;
-  uint64_t* ready = empty + STAGES;  // grad_w: rank 0's, after both tail warps
-  uint64_t* acc_full = ready + STAGES;
+  uint64_t* tail = empty + STAGES;  // grad_w: this CTA's copies of an expert's last stage
+  uint64_t* acc_full = tail + STAGES;
   uint64_t* acc_empty = acc_full + 2;  // rank 0's: the epilogue warps of both
   uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -238,9 +247,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // rank 0's producer twice, or both tail warps
       mbar_init(&empty[s], 1);
-      mbar_init(&ready[s], 2);
+      mbar_init(&tail[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&acc_full[i], 1);
@@ -284,15 +293,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         uint8_t* sm = smem + stage * C::STAGE;
         uint8_t* sn = sm + C::TILE;
         if (leader) {
-          if (MODE == kGradW) {  // each CTA's copies complete on its own barrier
-            mbar_arrive_expect_tx(&full[stage], C::STAGE);
+          const bool ragged = MODE == kGradW && t.ragged_at(i);
+          if (rank == 0 && !ragged) {
+            mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + (MODE == kGradW ? C::TILE : boxes * 4096)));
+            mbar_arrive(&full[stage]);
+          }
+          if (MODE == kGradW) {
             const int r = t.start + i * 64, n0 = t.n0 + rank * 128;
-            tma_load_2d(sm, &maps.m, &full[stage], m0, r, pol_again);
-            tma_load_2d(sm + 8192, &maps.m, &full[stage], m0 + 64, r, pol_again);
-            tma_load_2d(sn, &maps.n, &full[stage], n0, r, pol_again);
-            tma_load_2d(sn + 8192, &maps.n, &full[stage], n0 + 64, r, pol_again);
+            uint32_t bar = cluster_address(&full[stage], 0);
+            if (ragged) {
+              mbar_arrive_expect_tx(&tail[stage], C::STAGE);
+              bar = cluster_address(&tail[stage], rank);
+            }
+            tma_load_2d_pair(sm, &maps.m, bar, m0, r, pol_again);
+            tma_load_2d_pair(sm + 8192, &maps.m, bar, m0 + 64, r, pol_again);
+            tma_load_2d_pair(sn, &maps.n, bar, n0, r, pol_again);
+            tma_load_2d_pair(sn + 8192, &maps.n, bar, n0 + 64, r, pol_again);
           } else {
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + boxes * 4096));
             const uint32_t bar = cluster_address(&full[stage], 0);
             if (M_MN) {
               tma_load_3d_pair(sm, &maps.m, bar, m0, i * 64, t.e, pol_m);
@@ -312,8 +329,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         }
       }
     }
-    if (MODE == kGradW) drain_copies(full, STAGES, issued);
-    else drain_pair_copies(full, STAGES, issued, rank, !ok);
+    drain_pair_copies(full, STAGES, issued, rank, !ok);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -324,26 +340,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                                          : sdesc_sw128(smem_u32(smem) + C::TILE);
       // 16 of the summed dimension: 32 bytes of a row, or 16 rows of 128 bytes
       constexpr uint32_t AM = M_MN ? 2048 : 32, AN = MODE == kGradW ? 2048 : 32;
-      int stage = 0, tiles = 0, e_lo = 0;
+      int stage = 0, parts = 0, e_lo = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
         const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
-        if (t.steps == 0) continue;
-        const uint32_t buf = tiles & 1, acc = tmem + buf * 256;
         const uint32_t idesc = p.idesc | static_cast<uint32_t>(t.n >> 3) << 17;
-        if (!mbar_wait(&acc_empty[buf], (tiles >> 1 & 1) ^ 1u, abort_flag, p.status,
-                       p.wait_limit_ns))
-          break;
-        ++tiles;
-        tc_fence_after();
+        uint32_t buf = 0;
         for (int i = 0; i < t.steps; ++i) {
-          uint64_t* bar = MODE == kGradW ? &ready[stage] : &full[stage];
-          if (!mbar_wait(bar, phase, abort_flag, p.status, p.wait_limit_ns)) {
+          if (i % SEG == 0) {
+            buf = parts & 1;
+            if (!mbar_wait(&acc_empty[buf], (parts >> 1 & 1) ^ 1u, abort_flag, p.status,
+                           p.wait_limit_ns)) {
+              ok = false;
+              break;
+            }
+            ++parts;
+          }
+          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
             break;
           }
-          if (MODE == kGradW) fence_cluster();
           tc_fence_after();
           const uint64_t cm = sdesc_at(dm, stage * C::STAGE), cn = sdesc_at(dn, stage * C::STAGE);
           // sixteens of the last stage that hold nothing are left out
@@ -352,9 +369,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
             for (int c = 0; c < 4; ++c)
               if (16 * c < left)
-                mma_f16_pair(acc, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
-                             (i != 0 || c != 0) ? 1u : 0u);
+                mma_f16_pair(tmem + buf * 256, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
+                             (i % SEG != 0 || c != 0) ? 1u : 0u);
             tc_commit_pair(&empty[stage]);
+            if (i % SEG == SEG - 1 || i == t.steps - 1) tc_commit_pair(&acc_full[buf]);
           }
           __syncwarp();
           if (++stage == STAGES) {
@@ -362,9 +380,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        if (leader) tc_commit_pair(&acc_full[buf]);
-        __syncwarp();
       }
       // every MMA issued so far must finish before tensor memory is released
       if (leader) tc_commit_pair(drain);
@@ -375,36 +390,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   } else if (warp == 10) {
     if (MODE == kGradW) {
       // ---------------------------------------------------------- tail warp
-      // hands every stage on to the MMAs; in an expert's last one the rows past
-      // its end become zeros first, up to the sixteen that are read
-      int stage = 0, e_lo = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int q = first; ok && q < total; q += step) {
+      // in an expert's last stage the rows past its end become zeros, up to the
+      // sixteen that are read; the other stages go from the copies to the MMAs
+      int at = 0, e_lo = 0;
+      uint32_t phases = 0;  // a bit for each stage's barrier
+      for (int q = first; q < total; q += step) {
         const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
-        for (int i = 0; i < t.steps; ++i) {
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
-            ok = false;
-            break;
-          }
-          const int left = t.rows - i * 64;
-          if (left < 64 && (left & 15) != 0) {
-            uint8_t* sb = smem + stage * C::STAGE;
-            const int end = (left + 15) / 16 * 16;  // rows of 128 bytes in each of four boxes
-            for (int v = left * 8 + lane; v < end * 8; v += 32)
+        at = (at + t.steps) % STAGES;
+        if (!t.ragged_at(t.steps - 1)) continue;
+        const int stage = (at + STAGES - 1) % STAGES;
+        if (!mbar_wait(&tail[stage], phases >> stage & 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+        phases ^= 1u << stage;
+        uint8_t* sb = smem + stage * C::STAGE;
+        const int left = t.rows - (t.steps - 1) * 64;
+        const int end = (left + 15) / 16 * 16;  // rows of 128 bytes in each of four boxes
+        for (int v = left * 8 + lane; v < end * 8; v += 32)
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
-            fence_async_shared();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(&ready[stage], 0);
-          __syncwarp();
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+          for (int b = 0; b < 4; ++b)
+            *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(&full[stage], 0);
+        __syncwarp();
       }
     }
   } else {
@@ -414,82 +421,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
     constexpr int SIZE = sizeof(O), PER = 16 / SIZE;  // elements of 16 bytes
     O* out = static_cast<O*>(p.out);
-    int tiles = 0, e_lo = 0;
-    for (int q = first; q < total; q += step) {
+    int parts = 0, e_lo = 0;
+    bool ok = true;
+    for (int q = first; ok && q < total; q += step) {
       const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
       const int m = t.m0 + rank * 128 + quarter * 32;  // this warp's first feature
-      const uint32_t buf = tiles & 1;
-      const bool some = t.steps != 0;
-      if (some) {
-        if (!mbar_wait(&acc_full[buf], tiles >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) break;
-        tc_fence_after();
-        ++tiles;
-      }
-      const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      auto let_go = [&]() {
+      // chunks of 32 columns: the two warps of a quarter take them in turn, or
+      // (grad_w) half of the columns each
+      const int chunks = MODE == kGradW ? 8 : (t.rows + 31) / 32;
+      auto chunk_of = [&](int c) { return MODE == kGradW ? half * 4 + c : half + 2 * c; };
+      auto let_go = [&](uint32_t buf) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], 0);
       };
+      float sum[FOLD ? 4 : 1][32];
+      const int last = t.steps == 0 ? 0 : (t.steps - 1) / SEG;  // parts before the last
+      if (FOLD) {
+#pragma unroll
+        for (int c = 0; c < 4 * FOLD; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
+        for (int i = 0; i < last; ++i, ++parts) {
+          const uint32_t buf = parts & 1;
+          if (!mbar_wait(&acc_full[buf], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int at = chunk_of(c);
+            if (at >= chunks) continue;
+            uint32_t v[32];
+            tmem_ld_32x32b_x32(base + 32 * at, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[c * FOLD][j] += __uint_as_float(v[j]);
+          }
+          let_go(buf);
+        }
+        if (!ok) break;
+      }
+      const uint32_t buf = parts & 1;
+      if (t.steps != 0) {
+        if (!mbar_wait(&acc_full[buf], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) break;
+        tc_fence_after();
+        ++parts;
+      }
+      const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+      // a chunk of the last part, and the parts before it
+      auto load = [&](int c, float* v) {
+        uint32_t u[32];
+        tmem_ld_32x32b_x32(base + 32 * chunk_of(c), u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+          v[j] = FOLD ? sum[c * FOLD][j] + __uint_as_float(u[j]) : __uint_as_float(u[j]);
+      };
       if (MODE != kGradW) {
         // A lane has a feature, a column is a row of the output: 64 or 128 bytes
-        // of 32 features of a row at a time through shared memory.  The two warps
-        // of a quarter take chunks of 32 rows in turn.
+        // of 32 features of a row at a time through shared memory.
         constexpr int ROWS = C::STG / (32 * SIZE);  // staged at a time
         constexpr int LANES = 32 / PER;             // lanes of a row's 16-byte pieces
-        const int chunks = (t.rows + 31) / 32;
         const int piece = lane % LANES;
         const bool in = m + piece * PER < p.F;
-        for (int c = half; c < chunks; c += 2) {
-          uint32_t v[32];
-          tmem_ld_32x32b_x32(base + 32 * c, v);
-          tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (chunk_of(c) >= chunks) continue;
+          float v[32];
+          load(c, v);
           if (m >= p.F) continue;  // warp-uniform
 #pragma unroll
           for (int g = 0; g < 32 / ROWS; ++g) {
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < ROWS; ++j)
-              store_rounded(__uint_as_float(v[g * ROWS + j]), reinterpret_cast<O*>(stg) + j * 32 + lane);
+              store_rounded(v[g * ROWS + j], reinterpret_cast<O*>(stg) + j * 32 + lane);
             __syncwarp();
 #pragma unroll
             for (int j = 0; j < ROWS * LANES / 32; ++j) {
               const int r = j * (32 / LANES) + lane / LANES;
               const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
-              const int row = 32 * c + g * ROWS + r;
+              const int row = 32 * chunk_of(c) + g * ROWS + r;
               if (in && row < t.rows)
                 *reinterpret_cast<uint4*>(out + (t.n0 + static_cast<int64_t>(row)) * p.ld_out + m +
                                           piece * PER) = x;
             }
           }
         }
-        let_go();
+        let_go(buf);
       } else {
         // A lane has a row of the output: 128-byte pieces of 16 rows at a time.
-        constexpr int COLS = 128 / SIZE;
+        constexpr int CH = SIZE == 4 ? 1 : 2;  // chunks of such a piece
         const int c0 = t.n0 + half * 128, piece = lane & 7;
         O* at = out + (static_cast<int64_t>(t.e) * p.F + m) * p.ld_out + c0 + piece * PER;
-#pragma unroll 1
-        for (int c = 0; c < 128; c += COLS) {
-          uint32_t u[COLS];
-          if (some) {
-            tmem_ld_32x32b_x32(base + half * 128 + c, u);
-            if (COLS == 64) tmem_ld_32x32b_x32(base + half * 128 + c + 32, u + COLS - 32);
-            tmem_ld_wait();
-            if (c + COLS == 128) let_go();
+#pragma unroll
+        for (int c = 0; c < 4; c += CH) {
+          float v[32 * CH];
+          if (t.steps != 0) {
+            load(c, v);
+            if (CH == 2) load(c + CH - 1, v + 32 * (CH - 1));
+            if (c + CH == 4) let_go(buf);
           } else {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) u[j] = 0;
+            for (int j = 0; j < 32 * CH; ++j) v[j] = 0.f;
           }
-          if (m >= p.F || c0 + c >= p.G) continue;  // warp-uniform
-          if (SIZE == 2) {
+          if (m >= p.F || c0 + 32 * c >= p.G) continue;  // warp-uniform
+          uint32_t u[32];
 #pragma unroll
-            for (int j = 0; j < COLS / 2; ++j)
-              u[j] = round_pair(__uint_as_float(u[2 * j]), __uint_as_float(u[2 * j + 1]),
-                                static_cast<const O*>(nullptr));
-          }
-          const bool in = c0 + c + piece * PER < p.G;
-#pragma unroll 1
+          for (int j = 0; j < 32; ++j)
+            u[j] = CH == 1 ? __float_as_uint(v[j])
+                           : round_pair(v[2 * j % (32 * CH)], v[(2 * j + 1) % (32 * CH)],
+                                        static_cast<const O*>(nullptr));
+          const bool in = c0 + 32 * c + piece * PER < p.G;
+#pragma unroll
           for (int g = 0; g < 2; ++g) {  // 16 rows
             __syncwarp();
             if (lane >> 4 == g) {
@@ -504,7 +551,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
               const int r = 4 * i + (lane >> 3);
               const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) * 16));
               if (in && m + 16 * g + r < p.F)
-                __stcs(reinterpret_cast<uint4*>(at + static_cast<int64_t>(16 * g + r) * p.ld_out + c), x);
+                __stcs(reinterpret_cast<uint4*>(at + static_cast<int64_t>(16 * g + r) * p.ld_out + 32 * c), x);
             }
           }
         }

@@ -35,13 +35,20 @@ namespace {
 constexpr int kQuantThreads = 256;
 constexpr int kHeld = 4;  // eights of elements a thread keeps between the two passes
 
-// Eight elements as fp32.
+// Eight elements as they lie, and as fp32.
 template <typename X>
-__device__ __forceinline__ void load8(const X* p, float (&v)[8]);
+struct Eight {
+  uint4 q[sizeof(X) / 2];
+  __device__ void load(const X* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i)
+      q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  __device__ void values(float (&v)[8]) const;
+};
 template <>
-__device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void Eight<__nv_bfloat16>::values(float (&v)[8]) const {
+  const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     v[2 * i] = __uint_as_float(u[i] << 16);
@@ -49,9 +56,8 @@ __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, flo
   }
 }
 template <>
-__device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+__device__ __forceinline__ void Eight<__half>::values(float (&v)[8]) const {
+  const uint32_t u[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
@@ -60,96 +66,116 @@ __device__ __forceinline__ void load8<__half>(const __half* p, float (&v)[8]) {
   }
 }
 template <>
-__device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+__device__ __forceinline__ void Eight<float>::values(float (&v)[8]) const {
+  const uint32_t u[8] = {q[0].x, q[0].y, q[0].z, q[0].w, q[1].x, q[1].y, q[1].z, q[1].w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
+}
+// Largest magnitude of eight, as bits: NaN and Inf compare as the largest.
+template <typename X>
+__device__ __forceinline__ uint32_t largest(const Eight<X>& e) {
+  float v[8];
+  e.values(v);
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  return m;
 }
 
-// rint(127 x / amax) as in exact arithmetic, |x| <= amax.  The fast product with
-// 127 / amax is off by at most 2^-22 of the quotient; only where that could
-// change the integer (the fraction within 2^-13 of a half, or an amax whose
-// inverse is no normal number) is the quotient taken in 64 bits.  There 127 x is
-// exact, and a quotient of two fp32 numbers that is no half is at least 2^-33 of
-// its size away from one.
-__device__ __forceinline__ int quantised(float x, float amax, float inv) {
-  const float t = x * inv, r = rintf(t);
-  if (fabsf(fabsf(t - r) - 0.5f) > 0x1p-13f && inv < INFINITY && amax < 0x1p120f)
-    return static_cast<int>(r);
-  return static_cast<int>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+__device__ __noinline__ float exact_quotient(float x, float amax) {
+  return static_cast<float>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+}
+
+// rint(127 x / amax) of eight as in exact arithmetic, |x| <= amax.  The product
+// with 127 / amax is off by at most 2^-22 of the quotient; only where that could
+// change an integer (a fraction within 2^-13 of a half, or an amax whose inverse is
+// no normal number) is the quotient taken in 64 bits.  There 127 x is exact, and a
+// quotient of two fp32 numbers that is no half is at least 2^-33 of its size away
+// from one.
+__device__ __forceinline__ void quantised(const float (&x)[8], float amax, float inv, bool plain,
+                                          float (&q)[8]) {
+  float off = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float t = x[j] * inv;
+    q[j] = __fsub_rn(__fadd_rn(t, 12582912.f), 12582912.f);  // 1.5 * 2^23: to the nearest integer
+    off = fmaxf(off, fabsf(t - q[j]));
+  }
+  if (plain && off < 0.5f - 0x1p-13f) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (!plain || !(fabsf(x[j] * inv - q[j]) < 0.5f - 0x1p-13f)) q[j] = exact_quotient(x[j], amax);
 }
 
 template <typename X>
 __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float s_amax[kQuantThreads / 32];
+  __shared__ uint32_t s_amax[2][kQuantThreads / 32];
   const int vecs = p.K / 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (p.clear && blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0u;
-  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+  int turn = 0;
+  for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x, turn ^= 1) {
     const X* row = static_cast<const X*>(p.x) + t * p.ld;
-    float v[kHeld][8];
-    // the largest magnitude by its bits: NaN and Inf compare as the largest
+    Eight<X> held[kHeld];
     uint32_t m = 0;
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       const int i = threadIdx.x + h * kQuantThreads;
-      if (i >= vecs) break;
-      load8(row + i * 8, v[h]);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[h][j]) & 0x7fffffffu);
+      if (i < vecs) held[h].load(row + i * 8);
     }
-    for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
-      float u[8];
-      load8(row + static_cast<int64_t>(i) * 8, u);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(u[j]) & 0x7fffffffu);
+    for (int h = 0; h < kHeld; ++h)
+      if (threadIdx.x + h * kQuantThreads < vecs) m = max(m, largest(held[h]));
+    for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
+      Eight<X> e;
+      e.load(row + static_cast<int64_t>(i) * 8);
+      m = max(m, largest(e));
     }
     m = __reduce_max_sync(0xffffffffu, m);
-    __syncthreads();  // the row before has been read
-    if (lane == 0) s_amax[warp] = __uint_as_float(m);
+    if (lane == 0) s_amax[turn][warp] = m;  // two sets in turn: one barrier a row
     __syncthreads();
-    m = 0;
 #pragma unroll
-    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, __float_as_uint(s_amax[i]));
+    for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, s_amax[turn][i]);
     const bool finite = m < 0x7f800000u;
     const float amax = __uint_as_float(m);
     const float inv = 127.f / amax;
     const bool zero = !finite || m == 0;
+    const bool plain = inv < INFINITY && amax < 0x1p120f;
     if (threadIdx.x == 0) {
       p.scales[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
       if (!finite && !p.clear) set_status(p.status, MEGAMOE_DEV_NONFINITE);
     }
-    auto put = [&](int i, const float (&u)[8]) {
-      int q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = zero ? 0 : quantised(u[j], amax, inv);
+    auto put = [&](int i, const Eight<X>& e) {
+      float v[8], q[8];
+      e.values(v);
+      if (!zero) quantised(v, amax, inv, plain, q);
       const int64_t at = t * p.K + static_cast<int64_t>(i) * 8;
       if (p.half) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const __half2 h = __halves2half2(__int2half_rn(q[2 * j]), __int2half_rn(q[2 * j + 1]));
-          w[j] = *reinterpret_cast<const uint32_t*>(&h);
+          const __half2 h = __floats2half2_rn(q[2 * j], q[2 * j + 1]);
+          w[j] = zero ? 0u : *reinterpret_cast<const uint32_t*>(&h);
         }
         *reinterpret_cast<uint4*>(p.half + at) = make_uint4(w[0], w[1], w[2], w[3]);
       } else {
         uint32_t w[2] = {0, 0};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w[j >> 2] |= static_cast<uint32_t>(q[j] & 0xff) << (8 * (j & 3));
+        for (int j = 0; j < 8; ++j)
+          w[j >> 2] |= zero ? 0u : static_cast<uint32_t>(__float2int_rn(q[j]) & 0xff) << (8 * (j & 3));
         *reinterpret_cast<uint2*>(p.codes + at) = make_uint2(w[0], w[1]);
       }
     };
 #pragma unroll
     for (int h = 0; h < kHeld; ++h) {
       const int i = threadIdx.x + h * kQuantThreads;
-      if (i >= vecs) break;
-      put(i, v[h]);
+      if (i < vecs) put(i, held[h]);
     }
     for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
-      float u[8];
-      load8(row + static_cast<int64_t>(i) * 8, u);
-      put(i, u);
+      Eight<X> e;
+      e.load(row + static_cast<int64_t>(i) * 8);
+      put(i, e);
     }
   }
 }
@@ -269,8 +295,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);
-  uint64_t* empty = full + STAGES;
+  uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + C::BAR_OFF);  // this CTA's weights
+  uint64_t* x_full = w_full + STAGES;  // rank 0's: the tokens of both
+  uint64_t* empty = x_full + STAGES;
   uint64_t* a_full = empty + STAGES;  // rank 0's: the widening warps of both
   uint64_t* a_empty = a_full + 2;
   uint64_t* acc_full = a_empty + 2;
@@ -292,7 +319,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&w_full[s], 1);
+      mbar_init(&x_full[s], 1);
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -316,8 +344,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    // (the whole warp, one lane of it issuing: elect_one); each CTA's copies
-    // complete on its own barrier
+    // (the whole warp, one lane of it issuing: elect_one).  Weights are waited for
+    // by this CTA's own warps, tokens by rank 0's MMAs.
     const bool leader = elect_one();
     const uint64_t pol_w = NT > 1 ? policy_evict_normal() : policy_evict_first();
     const uint64_t pol_x = policy_evict_normal();
@@ -338,12 +366,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         uint8_t* sw = smem + stage * C::STAGE;
         uint8_t* sx = sw + C::W;
         if (leader) {
-          mbar_arrive_expect_tx(&full[stage], C::W + 2 * boxes * 4096);
-          tma_load_2d(sw, &maps.w, &full[stage], i * 128, m0, pol_w);
+          mbar_arrive_expect_tx(&w_full[stage], C::W);
+          tma_load_2d(sw, &maps.w, &w_full[stage], i * 128, m0, pol_w);
+          if (rank == 0) mbar_arrive_expect_tx(&x_full[stage], 4 * boxes * 4096);
+          const uint32_t bar = cluster_address(&x_full[stage], 0);
           for (int h = 0; h < 2; ++h)
             for (int b = 0; b < boxes; ++b)
-              tma_load_2d(sx + h * C::X + b * 4096, &maps.x, &full[stage], i * 128 + h * 64,
-                          t0 + b * 32, pol_x);
+              tma_load_2d_pair(sx + h * C::X + b * 4096, &maps.x, bar, i * 128 + h * 64,
+                               t0 + b * 32, pol_x);
         }
         __syncwarp();
         ++issued;
@@ -353,7 +383,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         }
       }
     }
-    drain_copies(full, STAGES, issued);
+    drain_copies(w_full, STAGES, issued);
+    drain_pair_copies(x_full, STAGES, issued, rank, !ok);
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -363,6 +394,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       // fp16 operands, K-major, fp32 sums, M = 256
       constexpr uint32_t idesc0 = (1u << 4) | (256u >> 4) << 24;
       int stage = 0, tiles = 0, steps = 0;
+      uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step, ++tiles) {
         int mt, nt;
@@ -372,13 +404,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         const uint32_t acc = tmem + (tiles & 1) * C::ACC1;
         for (int i = 0; i < KT; ++i, ++steps) {
           const int buf = steps & 1;
-          if (!mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
+          if (!mbar_wait(&x_full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
+              !mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
               (i == 0 && !mbar_wait(acc_empty, (tiles & 1) ^ 1u, abort_flag, p.status,
                                     p.wait_limit_ns))) {
             ok = false;
             break;
           }
-          fence_cluster();
           tc_fence_after();
           const uint64_t cx = sdesc_at(dx, stage * C::STAGE);
           const uint32_t a = tmem + C::A_COL0 + buf * C::A_COLS;
@@ -393,7 +425,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             tc_commit_pair(&a_empty[buf]);
           }
           __syncwarp();
-          if (++stage == STAGES) stage = 0;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
         if (!ok) break;
         if (leader) tc_commit_pair(acc_full);
@@ -416,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     for (int q = first; ok && q < total; q += step) {
       for (int i = 0; i < KT; ++i, ++steps) {
         const int buf = steps & 1;
-        if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+        if (!mbar_wait(&w_full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
           ok = false;
           break;
         }
@@ -441,7 +476,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(&a_full[buf], 0);
+        if (lane == 0) mbar_arrive_cluster_relaxed(&a_full[buf], 0);
         __syncwarp();
         if (++stage == STAGES) {
           stage = 0;
