@@ -51,8 +51,8 @@ struct GroupedArgs {
   const int32_t* padded_offsets;
   int64_t rows;  // of the row matrices
   int E;
-  int F;    // features on the M side (N, K or N)
-  int G;    // grad_w: columns on the N side (K)
+  int F;    // features on the M side (N, K or K)
+  int G;    // grad_w: features on the N side (N)
   int sum;  // forward, grad_x: length of the sums (K or N)
   void* out;
   int64_t ld_out;
@@ -155,7 +155,7 @@ __device__ void build_tables(const GroupedArgs& p, int MT, Range* s_range, int* 
 struct Tile {
   int e;
   int m0;     // first feature
-  int n0;     // first row (forward, grad_x) or column (grad_w)
+  int n0;     // first row, or (grad_w) first feature of the N side
   int rows;   // rows: of the tile, or those that are summed over
   int start;  // grad_w: the expert's first row
   int n;      // the MMA's N
@@ -198,17 +198,6 @@ __device__ __forceinline__ Tile decode(const GroupedArgs& p, int q, const Range*
 
 __device__ __forceinline__ void store_rounded(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_rounded(float v, __half* p) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void store_rounded(float v, float* p) { *p = v; }
-__device__ __forceinline__ uint32_t round_pair(float a, float b, const __nv_bfloat16*) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t round_pair(float a, float b, const __half*) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t round_pair(float, float, const float*) { return 0; }
-
 template <Mode MODE, typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     k_grouped_pair(const __grid_constant__ GroupedMaps maps, const GroupedArgs p) {
@@ -419,30 +408,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     const int quarter = warp & 3;
     const int half = warp >= 6 ? 1 : 0;
     uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
-    constexpr int SIZE = sizeof(O), PER = 16 / SIZE;  // elements of 16 bytes
+    // A lane has a feature, a column is a row of the output.  The two warps of a
+    // quarter take chunks of 32 columns in turn.
     O* out = static_cast<O*>(p.out);
     int parts = 0, e_lo = 0;
     bool ok = true;
     for (int q = first; ok && q < total; q += step) {
       const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
       const int m = t.m0 + rank * 128 + quarter * 32;  // this warp's first feature
-      // chunks of 32 columns: the two warps of a quarter take them in turn, or
-      // (grad_w) half of the columns each
-      const int chunks = MODE == kGradW ? 8 : (t.rows + 31) / 32;
-      auto chunk_of = [&](int c) { return MODE == kGradW ? half * 4 + c : half + 2 * c; };
+      // rows of the output: the tile's, or (grad_w) features of the other side
+      const int rows = MODE == kGradW ? min(256, p.G - t.n0) : t.rows;
+      const int chunks = (rows + 31) / 32;
+      const int64_t row0 = (MODE == kGradW ? static_cast<int64_t>(t.e) * p.G : 0) + t.n0;
+      O* at = out + row0 * p.ld_out + m;
+      auto chunk_of = [&](int c) { return half + 2 * c; };
       auto let_go = [&](uint32_t buf) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], 0);
       };
       float sum[FOLD ? 4 : 1][32];
-      const int last = t.steps == 0 ? 0 : (t.steps - 1) / SEG;  // parts before the last
-      if (FOLD) {
+      if (FOLD) {  // the parts, and the accumulator's back before anything is stored
 #pragma unroll
         for (int c = 0; c < 4 * FOLD; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-        for (int i = 0; i < last; ++i, ++parts) {
+        for (int i = 0; i < t.steps; i += SEG, ++parts) {
           const uint32_t buf = parts & 1;
           if (!mbar_wait(&acc_full[buf], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
@@ -452,108 +443,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
           const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int at = chunk_of(c);
-            if (at >= chunks) continue;
+            if (chunk_of(c) >= chunks) continue;
             uint32_t v[32];
-            tmem_ld_32x32b_x32(base + 32 * at, v);
+            tmem_ld_32x32b_x32(base + 32 * chunk_of(c), v);
             tmem_ld_wait();
 #pragma unroll
             for (int j = 0; j < 32; ++j) sum[c * FOLD][j] += __uint_as_float(v[j]);
           }
           let_go(buf);
         }
-        if (!ok) break;
-      }
-      const uint32_t buf = parts & 1;
-      if (t.steps != 0) {
-        if (!mbar_wait(&acc_full[buf], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) break;
+      } else if (t.steps != 0) {
+        ok = mbar_wait(&acc_full[parts & 1], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns);
         tc_fence_after();
-        ++parts;
       }
-      const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-      // a chunk of the last part, and the parts before it
-      auto load = [&](int c, float* v) {
-        uint32_t u[32];
-        tmem_ld_32x32b_x32(base + 32 * chunk_of(c), u);
-        tmem_ld_wait();
+      if (!ok) break;
+      if constexpr (FOLD) {
+        // fp32: 32 features of a row are 128 bytes as they lie
+        if (m + lane < p.F) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          v[j] = FOLD ? sum[c * FOLD][j] + __uint_as_float(u[j]) : __uint_as_float(u[j]);
-      };
-      if (MODE != kGradW) {
-        // A lane has a feature, a column is a row of the output: 64 or 128 bytes
-        // of 32 features of a row at a time through shared memory.
-        constexpr int ROWS = C::STG / (32 * SIZE);  // staged at a time
-        constexpr int LANES = 32 / PER;             // lanes of a row's 16-byte pieces
-        const int piece = lane % LANES;
-        const bool in = m + piece * PER < p.F;
+          for (int c = 0; c < 4; ++c) {
+            float* to = at + 32 * chunk_of(c) * p.ld_out + lane;
+#pragma unroll
+            for (int j = 0; j < 32; ++j, to += p.ld_out)
+              if (32 * chunk_of(c) + j < rows) __stcs(to, sum[c][j]);
+          }
+        }
+        __syncwarp();
+      } else {
+        // 16 bits: 64 bytes of 32 features of a row, through shared memory
+        const uint32_t buf = parts & 1;
+        const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+        const int piece = lane & 3;
+        const bool in = m + piece * 8 < p.F;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (chunk_of(c) >= chunks) continue;
-          float v[32];
-          load(c, v);
-          if (m >= p.F) continue;  // warp-uniform
-#pragma unroll
-          for (int g = 0; g < 32 / ROWS; ++g) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < ROWS; ++j)
-              store_rounded(v[g * ROWS + j], reinterpret_cast<O*>(stg) + j * 32 + lane);
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < ROWS * LANES / 32; ++j) {
-              const int r = j * (32 / LANES) + lane / LANES;
-              const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
-              const int row = 32 * chunk_of(c) + g * ROWS + r;
-              if (in && row < t.rows)
-                *reinterpret_cast<uint4*>(out + (t.n0 + static_cast<int64_t>(row)) * p.ld_out + m +
-                                          piece * PER) = x;
-            }
-          }
-        }
-        let_go(buf);
-      } else {
-        // A lane has a row of the output: 128-byte pieces of 16 rows at a time.
-        constexpr int CH = SIZE == 4 ? 1 : 2;  // chunks of such a piece
-        const int c0 = t.n0 + half * 128, piece = lane & 7;
-        O* at = out + (static_cast<int64_t>(t.e) * p.F + m) * p.ld_out + c0 + piece * PER;
-#pragma unroll
-        for (int c = 0; c < 4; c += CH) {
-          float v[32 * CH];
+          uint32_t v[32];
           if (t.steps != 0) {
-            load(c, v);
-            if (CH == 2) load(c + CH - 1, v + 32 * (CH - 1));
-            if (c + CH == 4) let_go(buf);
+            tmem_ld_32x32b_x32(base + 32 * chunk_of(c), v);
+            tmem_ld_wait();
           } else {
 #pragma unroll
-            for (int j = 0; j < 32 * CH; ++j) v[j] = 0.f;
+            for (int j = 0; j < 32; ++j) v[j] = 0;
           }
-          if (m >= p.F || c0 + 32 * c >= p.G) continue;  // warp-uniform
-          uint32_t u[32];
+          if (m >= p.F) continue;  // warp-uniform
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            u[j] = CH == 1 ? __float_as_uint(v[j])
-                           : round_pair(v[2 * j % (32 * CH)], v[(2 * j + 1) % (32 * CH)],
-                                        static_cast<const O*>(nullptr));
-          const bool in = c0 + 32 * c + piece * PER < p.G;
+            store_rounded(__uint_as_float(v[j]), reinterpret_cast<O*>(stg) + j * 32 + lane);
+          __syncwarp();
 #pragma unroll
-          for (int g = 0; g < 2; ++g) {  // 16 rows
-            __syncwarp();
-            if (lane >> 4 == g) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j)  // 16-byte piece j of the row, swizzled
-                *reinterpret_cast<uint4*>(stg + (lane & 15) * 128 + ((j ^ piece) * 16)) =
-                    make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = 4 * i + (lane >> 3);
-              const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 128 + ((piece ^ (r & 7)) * 16));
-              if (in && m + 16 * g + r < p.F)
-                __stcs(reinterpret_cast<uint4*>(at + static_cast<int64_t>(16 * g + r) * p.ld_out + 32 * c), x);
-            }
+          for (int j = 0; j < 4; ++j) {
+            const int r = j * 8 + (lane >> 2), row = 32 * chunk_of(c) + r;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + r * 64 + piece * 16);
+            if (in && row < rows) *reinterpret_cast<uint4*>(at + row * p.ld_out + piece * 8) = x;
           }
+        }
+        if (t.steps != 0) {
+          let_go(buf);
+          ++parts;
         }
       }
     }
@@ -654,8 +602,8 @@ cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, c
 
 cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream) {
   GroupedArgs a = args_of(g);
-  a.F = g.N;
-  a.G = g.K;
+  a.F = g.K;
+  a.G = g.N;
   a.out = out;
   a.ld_out = g.K;
   a.idesc = idesc_f16(g.type, true, true);
@@ -663,8 +611,8 @@ cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cud
     return cudaMemsetAsync(out, 0, static_cast<size_t>(g.E) * g.N * g.K *
                                        (out_type == MEGAMOE_TYPE_F32 ? 4 : 2), stream);
   GroupedMaps maps;
-  if (!rows_map(&maps.m, g.grad, g.N, g.rows, g.ld_grad, 64) ||
-      !rows_map(&maps.n, g.x, g.K, g.rows, g.ld_x, 64))
+  if (!rows_map(&maps.m, g.x, g.K, g.rows, g.ld_x, 64) ||
+      !rows_map(&maps.n, g.grad, g.N, g.rows, g.ld_grad, 64))
     return cudaErrorInvalidValue;
   const int64_t tiles = static_cast<int64_t>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256);
   return launch_mode<kGradW>(maps, a, out_type, tiles, stream);
