@@ -63,22 +63,25 @@ megamoe_status check_rows(int type, int64_t rows, int64_t T, int k, int d) {
 }
 
 // Workspace of the integer linear: status, the tokens' scales (the product reads
-// them in whole vectors past the last) and their integers as fp16.
+// them in whole vectors past the last) and their integers, as fp16 or (few tokens)
+// as they are.
 struct Int8Ws {
   uint32_t* status;
   float* scales;
-  uint16_t* half;
+  void* integers;
   size_t bytes;
 };
 Int8Ws carve_int8(void* base, int64_t T, int K) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   uint8_t* p = static_cast<uint8_t*>(base);
   const size_t scales = up(4 * static_cast<size_t>(T) + 256);
+  const size_t each = int8_few_fits(T, K) ? 1 : 2;
   Int8Ws w{};
   w.status = reinterpret_cast<uint32_t*>(p);
   w.scales = reinterpret_cast<float*>(p + 256);
-  w.half = reinterpret_cast<uint16_t*>(p + 256 + scales);
-  w.bytes = 256 + scales + up(2 * static_cast<size_t>(T) * K);
+  w.integers = p + 256 + scales;
+  // (the fewest are quantised inside the product)
+  w.bytes = 256 + (int8_dots_fit(T, K) ? 0 : scales + up(each * static_cast<size_t>(T) * K));
   return w;
 }
 
@@ -245,11 +248,24 @@ megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, 
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = as_stream(stream);
   if (T == 0) return cuda_status(cudaMemsetAsync(wk.status, 0, 4, s));
-  const Int8Quant q{x, x_type, x_scales, T, ld_x, K, nullptr, wk.half, wk.scales, wk.status, true};
+  const bool few = int8_few_fits(T, K), codes = x_type == MEGAMOE_TYPE_I8;
+  Int8Quant q{x, x_type, x_scales, T, ld_x, K, nullptr, nullptr, wk.scales, wk.status, true};
+  if (few) q.codes = static_cast<int8_t*>(wk.integers);
+  else q.half = static_cast<uint16_t*>(wk.integers);
+  const Int8Product g{q.half, wk.scales, T, w_codes, w_scales, N, K, out,
+                      out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status};
+  if (int8_dots_fit(T, K) || (few && codes)) {  // in one launch
+    return cuda_status(few ? launch_int8_few(q, g, s) : launch_int8_dots(q, g, s));
+  }
   cudaError_t e = launch_int8_quantize(q, s);
   if (e != cudaSuccess) return MEGAMOE_ERR_CUDA;
-  const Int8Product g{wk.half, wk.scales, T, w_codes, w_scales, N, K, out,
-                      out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status};
+  if (few) {
+    q.x = q.codes;
+    q.type = MEGAMOE_TYPE_I8;
+    q.x_scales = wk.scales;
+    q.ld = K;
+    return cuda_status(launch_int8_few(q, g, s));
+  }
   return cuda_status(launch_int8_product(g, s));
 }
 

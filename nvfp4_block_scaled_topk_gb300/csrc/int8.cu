@@ -42,7 +42,7 @@ struct Eight {
   __device__ void load(const X* p) {
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i)
-      q[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+      q[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
   }
   __device__ void values(float (&v)[8]) const;
 };
@@ -82,17 +82,27 @@ __device__ __forceinline__ uint32_t largest(const Eight<X>& e) {
   return m;
 }
 
-__device__ __noinline__ float exact_quotient(float x, float amax) {
-  return static_cast<float>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+// rint(127 x / amax), ties to even, with no rounding before the last: for amax whose
+// products stay clear of both ends of fp32 (ordinary) |127 x| is compared with (k +
+// 1/2) amax, k = floor |t|, as sums of a rounded product and its error; both errors
+// have ten bits at most, the products are within a factor of two of each other, so
+// every difference is exact.  Otherwise in 64 bits, where 127 x is exact and a
+// quotient of two fp32 numbers that is no half is at least 2^-33 of its size away.
+constexpr float kOrdinaryLow = 0x1p-90f, kOrdinaryHigh = 0x1p118f;
+__device__ __noinline__ float exact_quotient(float x, float amax, float t, bool ordinary) {
+  if (!ordinary)
+    return static_cast<float>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+  const float k = floorf(fabsf(t)), h = k + 0.5f, a = fabsf(x);
+  const float p = __fmul_rn(127.f, a), q = __fmul_rn(h, amax);
+  const float d = __fadd_rn(__fsub_rn(p, q), __fsub_rn(__fmaf_rn(127.f, a, -p), __fmaf_rn(h, amax, -q)));
+  const bool odd = (static_cast<int>(k) & 1) != 0;
+  return copysignf(d > 0.f || (d == 0.f && odd) ? k + 1.f : k, x);
 }
 
 // rint(127 x / amax) of eight as in exact arithmetic, |x| <= amax.  The product
-// with 127 / amax is off by at most 2^-22 of the quotient; only where that could
-// change an integer (a fraction within 2^-13 of a half, or an amax whose inverse is
-// no normal number) is the quotient taken in 64 bits.  There 127 x is exact, and a
-// quotient of two fp32 numbers that is no half is at least 2^-33 of its size away
-// from one.
-__device__ __forceinline__ void quantised(const float (&x)[8], float amax, float inv, bool plain,
+// with inv = 127 / amax is off by at most 2^-23 of the quotient, below 2^-15; only a
+// fraction that near to a half needs more.
+__device__ __forceinline__ void quantised(const float (&x)[8], float amax, float inv, bool ordinary,
                                           float (&q)[8]) {
   float off = 0.f;
 #pragma unroll
@@ -101,10 +111,11 @@ __device__ __forceinline__ void quantised(const float (&x)[8], float amax, float
     q[j] = __fsub_rn(__fadd_rn(t, 12582912.f), 12582912.f);  // 1.5 * 2^23: to the nearest integer
     off = fmaxf(off, fabsf(t - q[j]));
   }
-  if (plain && off < 0.5f - 0x1p-13f) return;
+  if (ordinary && off < 0.5f - 0x1p-15f) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    if (!plain || !(fabsf(x[j] * inv - q[j]) < 0.5f - 0x1p-13f)) q[j] = exact_quotient(x[j], amax);
+    if (!ordinary || !(fabsf(x[j] * inv - q[j]) < 0.5f - 0x1p-15f))
+      q[j] = exact_quotient(x[j], amax, x[j] * inv, ordinary);
 }
 
 template <typename X>
@@ -141,7 +152,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant
     const float amax = __uint_as_float(m);
     const float inv = 127.f / amax;
     const bool zero = !finite || m == 0;
-    const bool plain = inv < INFINITY && amax < 0x1p120f;
+    const bool ordinary = amax > kOrdinaryLow && amax < kOrdinaryHigh;
     if (threadIdx.x == 0) {
       p.scales[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
       if (!finite && !p.clear) set_status(p.status, MEGAMOE_DEV_NONFINITE);
@@ -149,7 +160,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant
     auto put = [&](int i, const Eight<X>& e) {
       float v[8], q[8];
       e.values(v);
-      if (!zero) quantised(v, amax, inv, plain, q);
+      if (!zero) quantised(v, amax, inv, ordinary, q);
       const int64_t at = t * p.K + static_cast<int64_t>(i) * 8;
       if (p.half) {
         uint32_t w[4];
@@ -217,6 +228,310 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_widen(const Int8Quant p)
 }
 
 // ---------------------------------------------------------------------------
+// Few tokens: 256-row tiles would leave most SMs without work, or each with a long
+// sum.  Bound by the weights' bytes and by the launch; the first of a block's
+// weights are on their way to L2 before the kernel ahead is done (they are the
+// caller's constants).
+// ---------------------------------------------------------------------------
+constexpr int kFewThreads = 256;
+constexpr int kFewWarps = kFewThreads / 32;
+constexpr int kFewBlocks = 2;        // an SM
+constexpr int kFewSmem = 96 * 1024;  // of tokens' integers
+
+struct Int8Few {
+  const void* x;  // integers [T, K], or (dots) of `type`
+  int type;
+  const float* x_scales;
+  int T;
+  int64_t ld;
+  const int8_t* w;
+  const float* w_scales;
+  int N, K;
+  int split;  // (MMA) warps that share a row's sum, a power of two up to 8
+  void* out;
+  bool out_f32;
+  int64_t ld_out;
+  uint32_t* status;
+};
+
+__device__ __forceinline__ void few_store(const Int8Few& p, int t, int n, float sum, float scale) {
+  const float y = sum * scale * __ldg(p.w_scales + n);
+  if (p.out_f32) static_cast<float*>(p.out)[t * p.ld_out + n] = y;
+  else static_cast<__nv_bfloat16*>(p.out)[t * p.ld_out + n] = __float2bfloat16_rn(y);
+}
+__device__ __forceinline__ void few_status(const Int8Few& p, const float* scales) {
+  bool bad = false;
+  for (int t = 0; t < p.T; ++t) bad |= !(scales[t] <= 0x1.fffffep127f);
+  *p.status = bad ? MEGAMOE_DEV_NONFINITE : 0u;
+}
+
+// Up to four tokens in one launch: every block quantises them into its shared
+// memory; a warp then multiplies its rows by them, F at a time, with dp4a: sums
+// exact in 32-bit integers, no rounding but that of the sum to fp32.
+template <typename X, int T>
+__device__ __forceinline__ void few_quantise(const Int8Few& p, int8_t* s_codes,
+                                             uint32_t (*s_amax)[kFewWarps], float* s_scale) {
+  const X* x = static_cast<const X*>(p.x);
+  const int vecs = p.K / 8;
+  uint32_t m[T] = {};
+#pragma unroll 2
+  for (int i = threadIdx.x; i < vecs; i += kFewThreads) {
+    Eight<X> e[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (t < p.T) e[t].load(x + t * p.ld + i * 8);
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      if (t < p.T) m[t] = max(m[t], largest(e[t]));
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+    m[t] = __reduce_max_sync(0xffffffffu, m[t]);
+    if ((threadIdx.x & 31) == 0) s_amax[t][threadIdx.x >> 5] = m[t];
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int t = 0; t < T; ++t) {  // (a token that is not there: zeros)
+    uint32_t a = 0;
+#pragma unroll
+    for (int i = 0; i < kFewWarps; ++i) a = max(a, s_amax[t][i]);
+    const bool finite = a < 0x7f800000u, zero = !finite || a == 0;
+    const float amax = __uint_as_float(a), inv = 127.f / amax;
+    const bool ordinary = amax > kOrdinaryLow && amax < kOrdinaryHigh;
+    if (threadIdx.x == 0) s_scale[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
+#pragma unroll 2
+    for (int i = threadIdx.x; i < vecs; i += kFewThreads) {
+      uint32_t w[2] = {0, 0};
+      if (!zero) {
+        Eight<X> e;
+        e.load(x + t * p.ld + i * 8);
+        float v[8], q[8];
+        e.values(v);
+        quantised(v, amax, inv, ordinary, q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          w[j >> 2] |= static_cast<uint32_t>(__float2int_rn(q[j]) & 0xff) << (8 * (j & 3));
+      }
+      *reinterpret_cast<uint2*>(s_codes + t * p.K + i * 8) = make_uint2(w[0], w[1]);
+    }
+  }
+}
+
+template <int T, int F>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_dots(const Int8Few p) {
+  extern __shared__ __align__(16) int8_t s_codes[];  // [T][K]
+  __shared__ uint32_t s_amax[T][kFewWarps];
+  __shared__ float s_scale[T];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t warps = static_cast<int64_t>(gridDim.x) * kFewWarps;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kFewWarps + warp;
+  const int n0 = static_cast<int>(p.N * me / warps), n1 = static_cast<int>(p.N * (me + 1) / warps);
+  if (lane == 0 && n0 < n1)
+    bulk_prefetch_l2(p.w + static_cast<int64_t>(n0) * p.K,
+                     static_cast<uint32_t>(min(static_cast<int64_t>(n1 - n0) * p.K, int64_t{16384})));
+  pdl_wait();
+  pdl_trigger();
+  if (p.type == MEGAMOE_TYPE_I8) {
+#pragma unroll 1
+    for (int t = 0; t < T; ++t) {
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.x) + t * p.ld);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < p.K / 16; i += kFewThreads)
+        reinterpret_cast<uint4*>(s_codes + t * p.K)[i] = t < p.T ? __ldg(row + i) : make_uint4(0, 0, 0, 0);
+      if (threadIdx.x == 0) s_scale[t] = t < p.T ? __ldg(p.x_scales + t) : 0.f;
+    }
+  } else if (p.type == MEGAMOE_TYPE_F32) {
+    few_quantise<float, T>(p, s_codes, s_amax, s_scale);
+  } else if (p.type == MEGAMOE_TYPE_F16) {
+    few_quantise<__half, T>(p, s_codes, s_amax, s_scale);
+  } else {
+    few_quantise<__nv_bfloat16, T>(p, s_codes, s_amax, s_scale);
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) few_status(p, s_scale);
+
+  const int pieces = p.K / 16;  // of 16 bytes
+  for (int n = n0; n < n1; n += F) {
+    const uint4* row = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(n) * p.K);
+    int acc[F][T] = {};
+#pragma unroll(8 / F)
+    for (int i = lane; i < pieces; i += 32) {
+      uint4 q[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        q[f] = n + f < n1 ? __ldcs(row + static_cast<int64_t>(f) * pieces + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int t = 0; t < T; ++t) {
+        const uint4 c = *reinterpret_cast<const uint4*>(s_codes + t * p.K + i * 16);
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          acc[f][t] = __dp4a(static_cast<int>(q[f].x), static_cast<int>(c.x), acc[f][t]);
+          acc[f][t] = __dp4a(static_cast<int>(q[f].y), static_cast<int>(c.y), acc[f][t]);
+          acc[f][t] = __dp4a(static_cast<int>(q[f].z), static_cast<int>(c.z), acc[f][t]);
+          acc[f][t] = __dp4a(static_cast<int>(q[f].w), static_cast<int>(c.w), acc[f][t]);
+        }
+      }
+    }
+    int mine = 0;  // lane F t + f: token t of row n + f
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const int sum = __reduce_add_sync(0xffffffffu, acc[f][t]);
+        if (lane == F * t + f) mine = sum;
+      }
+    const int t = lane / F, c = n + lane % F;
+    if (t < p.T && c < n1) few_store(p, t, c, static_cast<float>(mine), s_scale[t < T ? t : 0]);
+  }
+}
+
+template <int T, int F>
+cudaError_t launch_dots(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
+  auto kern = k_int8_dots<T, F>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads),
+                    static_cast<size_t>(T) * a.K, stream, a);
+}
+template <int F>
+cudaError_t launch_dots_t(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
+  return a.T == 1 ? launch_dots<1, F>(a, blocks, stream)
+         : a.T == 2 ? launch_dots<2, F>(a, blocks, stream)
+                    : launch_dots<4, F>(a, blocks, stream);
+}
+
+// Up to sixteen tokens, their integers as k_int8_quantize leaves them: the warps'
+// own MMA (16 rows x 8 tokens, fp16 with fp32 sums), since the tensor cores have next
+// to nothing to do.  A row's bytes go from memory to the lanes that multiply them: a
+// lane has 16 of the 64 bytes of a step, and the order in which the MMA takes them is
+// the same for the tokens' integers.
+//
+// Rows of integers in shared memory: whole steps, and 64 bytes more so that two
+// tokens' pieces fall into different banks.
+__host__ __device__ constexpr int few_pitch(int K) { return (K + 127) / 128 * 128 + 64; }
+
+// D (16 x 8, fp32) += A (16 x 16) B (16 x 8), fp16.
+__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                            uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Sixteen integers as eight pairs.
+__device__ __forceinline__ void widen16(uint4 q, uint32_t (&v)[8]) {
+  widen4(q.x, &v[0], &v[1]);
+  widen4(q.y, &v[2], &v[3]);
+  widen4(q.z, &v[4], &v[5]);
+  widen4(q.w, &v[6], &v[7]);
+}
+
+// NT: eights of tokens.
+template <int NT>
+__global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_few(const Int8Few p) {
+  extern __shared__ __align__(16) int8_t s_codes[];  // [8 NT][pitch]
+  __shared__ float s_scale[8 * NT];
+  __shared__ float s_part[2][kFewWarps][NT * 4][32];  // sums of the warps that share a row
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r0 = static_cast<int>(static_cast<int64_t>(p.N) * blockIdx.x / gridDim.x);
+  const int r1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
+  const int pitch = few_pitch(p.K);
+  if (lane == 0) {  // a warp's eighth of the block's rows
+    const int a = r0 + (r1 - r0) * warp / kFewWarps, b = r0 + (r1 - r0) * (warp + 1) / kFewWarps;
+    if (a < b)
+      bulk_prefetch_l2(p.w + static_cast<int64_t>(a) * p.K,
+                       static_cast<uint32_t>(min(static_cast<int64_t>(b - a) * p.K, int64_t{16384})));
+  }
+  pdl_wait();
+  pdl_trigger();
+  for (int t = warp; t < 8 * NT; t += kFewWarps) {
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.x) + t * p.ld);
+    uint4* codes = reinterpret_cast<uint4*>(s_codes + t * pitch);
+#pragma unroll 8
+    for (int i = lane; i < pitch / 16; i += 32)
+      codes[i] = t < p.T && i < p.K / 16 ? __ldg(row + i) : make_uint4(0, 0, 0, 0);
+    if (lane == 0) s_scale[t] = t < p.T ? __ldg(p.x_scales + t) : 0.f;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && threadIdx.x == 0) few_status(p, s_scale);
+
+  // The block's rows in turns of up to 16 for each group of warps that share a sum,
+  // of equal size.
+  const int groups = kFewWarps / p.split, group = warp / p.split, share = warp % p.split;
+  const int turns = (r1 - r0 + 16 * groups - 1) / (16 * groups);
+  const int per = turns ? (r1 - r0 + turns * groups - 1) / (turns * groups) : 0;
+  const int pieces = p.K / 16, steps = (pieces + 3) / 4;  // of 16 and of 64 bytes
+  const int g = lane >> 2, j = lane & 3;
+  const int8_t* codes = s_codes + g * pitch + j * 16;
+  for (int turn = 0; turn < turns; ++turn) {
+    const int n0 = r0 + (turn * groups + group) * per;
+    const int live = min(per, r1 - n0);  // rows n0 + g and n0 + g + 8 are this lane's
+    const uint4* lo = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(n0 + g) * p.K) + j;
+    const uint4* hi = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(n0 + g + 8) * p.K) + j;
+    float acc[NT][4] = {};
+#pragma unroll 1
+    for (int c0 = share; c0 < steps; c0 += 4 * p.split) {
+      uint4 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * p.split;
+        const bool in = 4 * c + j < pieces;
+        a[i] = in && g < live ? __ldcs(lo + 4 * c) : make_uint4(0, 0, 0, 0);
+        b[i] = in && g + 8 < live ? __ldcs(hi + 4 * c) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = c0 + i * p.split;
+        if (c >= steps) break;
+        uint32_t u[8], v[8];
+        widen16(a[i], u);
+        widen16(b[i], v);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          uint32_t x[8];
+          widen16(*reinterpret_cast<const uint4*>(codes + n * 8 * pitch + c * 64), x);
+#pragma unroll
+          for (int h = 0; h < 8; h += 2)
+            mma_16x8x16(acc[n], u[h], v[h], u[h + 1], v[h + 1], x[h], x[h + 1]);
+        }
+      }
+    }
+    if (p.split > 1) {  // the shares in order
+      float(*part)[NT * 4][32] = s_part[turn & 1];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][n * 4 + i][lane] = acc[n][i];
+      __syncthreads();
+      if (share != 0) continue;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          for (int s = 1; s < p.split; ++s) acc[n][i] += part[warp + s][n * 4 + i][lane];
+    }
+    // rows g and g + 8 of tokens 2 j and 2 j + 1
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = 8 * n + 2 * j + (i & 1), r = g + 8 * (i >> 1);
+        if (t < p.T && r < live) few_store(p, t, n0 + r, acc[n][i], s_scale[t]);
+      }
+  }
+}
+
+template <int NT>
+cudaError_t launch_few(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
+  auto kern = k_int8_few<NT>;
+  const size_t smem = static_cast<size_t>(8 * NT) * few_pitch(a.K);
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), smem, stream, a);
+}
+
+// ---------------------------------------------------------------------------
 // The product on pairs of CTAs
 // ---------------------------------------------------------------------------
 struct Int8Maps {
@@ -235,7 +550,7 @@ struct Int8Args {
 };
 
 struct Cfg {
-  static constexpr int THREADS = 448;  // producer, MMA issuer, 8 epilogue warps, 4 that widen
+  static constexpr int THREADS = 576;  // producer, MMA issuer, 8 epilogue warps, 8 that widen
   static constexpr int STAGES = 4;     // of 128 of K
   static constexpr int W = 128 * 128;  // a CTA's bytes of weights
   static constexpr int X = 128 * 128;  // its tokens' fp16, 64 of K
@@ -324,7 +639,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&a_full[i], 8);
+      mbar_init(&a_full[i], 8);  // four warps of each CTA
       mbar_init(&a_empty[i], 1);
     }
     mbar_init(acc_full, 1);
@@ -442,47 +757,38 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     __syncwarp();
   } else if (warp >= 10) {
     // ---------------------------------------------------------- widening warps
-    // A lane has a row of 128 bytes; its 16-byte piece j is at j ^ (row % 8).
-    const int quarter = warp & 3;
-    const uint32_t to = tmem + C::A_COL0 + (static_cast<uint32_t>(quarter * 32) << 16);
-    int stage = 0, steps = 0;
+    // A lane has a row of 128 bytes; its 16-byte piece j is at j ^ (row % 8).  Four
+    // warps take the even stages and four the odd ones, each set with a buffer.
+    const int quarter = warp & 3, buf = warp >= 14 ? 1 : 0;
+    const uint32_t to = tmem + C::A_COL0 + buf * C::A_COLS + (static_cast<uint32_t>(quarter * 32) << 16);
+    const int tiles = first < total ? (total - 1 - first) / step + 1 : 0;
+    const int64_t all = static_cast<int64_t>(tiles) * KT;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int q = first; ok && q < total; q += step) {
-      for (int i = 0; i < KT; ++i, ++steps) {
-        const int buf = steps & 1;
-        if (!mbar_wait(&w_full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        const uint4* row = reinterpret_cast<const uint4*>(smem + stage * C::STAGE +
-                                                          (quarter * 32 + lane) * 128);
-        uint32_t v[64];
+    for (int64_t i = buf; i < all; i += 2, phase ^= 1u) {
+      const int stage = static_cast<int>(i % STAGES);
+      if (!mbar_wait(&w_full[stage], static_cast<uint32_t>(i / STAGES) & 1u, abort_flag, p.status,
+                     p.wait_limit_ns))
+        break;
+      const uint4* row = reinterpret_cast<const uint4*>(smem + stage * C::STAGE +
+                                                        (quarter * 32 + lane) * 128);
+      uint32_t v[64];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint4 b = row[j ^ (lane & 7)];
-          widen4(b.x, &v[8 * j], &v[8 * j + 1]);
-          widen4(b.y, &v[8 * j + 2], &v[8 * j + 3]);
-          widen4(b.z, &v[8 * j + 4], &v[8 * j + 5]);
-          widen4(b.w, &v[8 * j + 6], &v[8 * j + 7]);
-        }
-        if (!mbar_wait(&a_empty[buf], (steps >> 1 & 1) ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        tmem_st_32x32b_x32(to + buf * C::A_COLS, v);
-        tmem_st_32x32b_x32(to + buf * C::A_COLS + 32, v + 32);
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(&a_full[buf], 0);
-        __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
+      for (int j = 0; j < 8; ++j) {
+        const uint4 b = row[j ^ (lane & 7)];
+        widen4(b.x, &v[8 * j], &v[8 * j + 1]);
+        widen4(b.y, &v[8 * j + 2], &v[8 * j + 3]);
+        widen4(b.z, &v[8 * j + 4], &v[8 * j + 5]);
+        widen4(b.w, &v[8 * j + 6], &v[8 * j + 7]);
       }
+      if (!mbar_wait(&a_empty[buf], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+      tc_fence_after();
+      tmem_st_32x32b_x32(to, v);
+      tmem_st_32x32b_x32(to + 32, v + 32);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(&a_full[buf], 0);
+      __syncwarp();
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -598,6 +904,36 @@ cudaError_t launch_int8_quantize(const Int8Quant& q, cudaStream_t stream) {
                                            : k_int8_quantize<__nv_bfloat16>;
   return launch_pdl(kern, dim3(static_cast<unsigned>(std::min(q.T, most))), dim3(kQuantThreads), 0,
                     stream, q);
+}
+
+bool int8_dots_fit(int64_t T, int64_t K) { return T <= 4 && (T == 3 ? 4 : T) * K <= kFewSmem; }
+bool int8_few_fits(int64_t T, int64_t K) {
+  return !int8_dots_fit(T, K) && T <= 16 && K <= kFewSmem &&
+         (T + 7) / 8 * 8 * few_pitch(static_cast<int>(K)) <= kFewSmem;
+}
+
+static Int8Few few_of(const Int8Quant& q, const Int8Product& g) {
+  return Int8Few{q.x, q.type, q.x_scales, static_cast<int>(q.T), q.ld,      g.w,      g.w_scales, g.N,
+                 g.K, 1,      g.out,      g.out_f32,             g.ld_out,  g.status};
+}
+// Blocks of a launch: a row or more for each warp.
+static int64_t few_blocks(int64_t N) {
+  return std::min<int64_t>(static_cast<int64_t>(num_sms()) * kFewBlocks, (N + kFewWarps - 1) / kFewWarps);
+}
+
+cudaError_t launch_int8_dots(const Int8Quant& q, const Int8Product& g, cudaStream_t stream) {
+  const int64_t blocks = few_blocks(g.N);
+  const Int8Few a = few_of(q, g);
+  return g.N > 2 * blocks * kFewWarps ? launch_dots_t<4>(a, blocks, stream)
+                                      : launch_dots_t<1>(a, blocks, stream);
+}
+
+cudaError_t launch_int8_few(const Int8Quant& q, const Int8Product& g, cudaStream_t stream) {
+  // as many warps to a sum as leave each group of them 16 rows
+  const int64_t blocks = few_blocks(g.N), rows = (g.N + blocks - 1) / blocks;
+  Int8Few a = few_of(q, g);
+  a.split = rows <= 16 ? 8 : rows <= 32 ? 4 : rows <= 64 ? 2 : 1;
+  return q.T <= 8 ? launch_few<1>(a, blocks, stream) : launch_few<2>(a, blocks, stream);
 }
 
 cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {

@@ -346,6 +346,13 @@ struct Int8Product {
   uint32_t* status;
 };
 cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream);
+// The same for few tokens.  Dots: up to four, quantised in the same launch (q's
+// x, type, T, ld and x_scales; clears *status first).  Few: up to sixteen, q the
+// quantised tokens (type I8).
+bool int8_dots_fit(int64_t T, int64_t K);
+cudaError_t launch_int8_dots(const Int8Quant& q, const Int8Product& g, cudaStream_t stream);
+bool int8_few_fits(int64_t T, int64_t K);
+cudaError_t launch_int8_few(const Int8Quant& q, const Int8Product& g, cudaStream_t stream);
 
 // The gated activation and the movement of rows (rows.cu); 16-bit elements,
 // widths multiples of 8.
