@@ -69,19 +69,27 @@ struct Int8Ws {
   uint32_t* status;
   float* scales;
   void* integers;
+  float* partial;  // of tiles whose sums are shared
   size_t bytes;
 };
-Int8Ws carve_int8(void* base, int64_t T, int K) {
+Int8Ws carve_int8(void* base, int64_t T, int K, int N) {
   auto up = [](size_t n) { return (n + 255) / 256 * 256; };
   uint8_t* p = static_cast<uint8_t*>(base);
   const size_t scales = up(4 * static_cast<size_t>(T) + 256);
-  const size_t each = int8_few_fits(T, K) ? 1 : 2;
+  const bool few = int8_few_fits(T, K);
   Int8Ws w{};
   w.status = reinterpret_cast<uint32_t*>(p);
-  w.scales = reinterpret_cast<float*>(p + 256);
-  w.integers = p + 256 + scales;
-  // (the fewest are quantised inside the product)
-  w.bytes = 256 + (int8_dots_fit(T, K) ? 0 : scales + up(each * static_cast<size_t>(T) * K));
+  w.bytes = 256;
+  if (int8_dots_fit(T, K)) return w;  // quantised inside the product
+  w.scales = reinterpret_cast<float*>(p + w.bytes);
+  w.bytes += scales;
+  w.integers = p + w.bytes;
+  w.bytes += up((few ? 1 : 2) * static_cast<size_t>(T) * K);
+  if (few) return w;
+  const Int8Plan plan = int8_plan(T, N, K);
+  if (plan.split == 1) return w;
+  w.partial = reinterpret_cast<float*>(p + w.bytes);
+  w.bytes += up(4 * static_cast<size_t>(plan.split) * T * N);
   return w;
 }
 
@@ -226,7 +234,7 @@ megamoe_status megamoe_quantize_int8(const void* x, int x_type, int64_t rows, in
 
 size_t megamoe_linear_int8_workspace_size(int64_t T, int K, int N) {
   if (T < 0 || K < 1 || N < 1 || !int8_sizes_ok(T, K, N)) return 0;
-  return carve_int8(nullptr, T, K).bytes;
+  return carve_int8(nullptr, T, K, N).bytes;
 }
 
 megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, int64_t ld_x,
@@ -244,7 +252,7 @@ megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, 
       !rows_ok(out, ld_out, out_bytes) || !aligned(w_codes, 16) || !aligned(w_scales, 4) ||
       !aligned(x_scales, 4) || !aligned(ws, 256))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
-  const Int8Ws wk = carve_int8(ws, T, K);
+  const Int8Ws wk = carve_int8(ws, T, K, N);
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
   const cudaStream_t s = as_stream(stream);
   if (T == 0) return cuda_status(cudaMemsetAsync(wk.status, 0, 4, s));
@@ -253,7 +261,7 @@ megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, 
   if (few) q.codes = static_cast<int8_t*>(wk.integers);
   else q.half = static_cast<uint16_t*>(wk.integers);
   const Int8Product g{q.half, wk.scales, T, w_codes, w_scales, N, K, out,
-                      out_dtype == MEGAMOE_EPI_F32, ld_out, wk.status};
+                      out_dtype == MEGAMOE_EPI_F32, ld_out, wk.partial, wk.status};
   if (int8_dots_fit(T, K) || (few && codes)) {  // in one launch
     return cuda_status(few ? launch_int8_few(q, g, s) : launch_int8_dots(q, g, s));
   }

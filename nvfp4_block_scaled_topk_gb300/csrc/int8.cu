@@ -542,11 +542,18 @@ struct Int8Args {
   const float* x_scales;
   const float* w_scales;
   int T, N, K;
-  int per;  // tokens of a tile, a multiple of 16 up to 256
+  int per;    // tokens of a tile, a multiple of 16 up to 256
+  int split;  // shares of a tile's sum, each with a pair of CTAs
   void* out;
   int64_t ld_out;
+  float* partial;  // split > 1: [split][T][N], added up by k_int8_sum
   uint32_t* status;
   uint64_t wait_limit_ns;
+};
+
+// What a pair of CTAs does at a time: steps k0 .. k1 of a tile's sum.
+struct Item {
+  int tile, mt, nt, share, k0, k1;
 };
 
 struct Cfg {
@@ -602,6 +609,16 @@ __device__ __forceinline__ void int8_tile(int q, int MT, int NT, int* mt, int* n
   *nt = band * 8 + r - *mt * wide;
 }
 
+__device__ __forceinline__ Item int8_item(int q, int split, int MT, int NT, int KT) {
+  Item t;
+  t.tile = q / split;
+  t.share = q - t.tile * split;
+  int8_tile(t.tile, MT, NT, &t.mt, &t.nt);
+  t.k0 = t.share * KT / split;
+  t.k1 = (t.share + 1) * KT / split;
+  return t;
+}
+
 template <typename O>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     k_int8_pair(const __grid_constant__ Int8Maps maps, const Int8Args p) {
@@ -625,8 +642,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   const int rank = static_cast<int>(cluster_rank());
   const int MT = (p.N + 255) / 256, NT = (p.T + p.per - 1) / p.per;
   const int KT = (p.K + 127) / 128;
-  const int total = MT * NT;
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
+  const int total = MT * NT * p.split;
+  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // items of this pair
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&maps.w);
@@ -668,12 +685,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint32_t phase = 0;
     bool ok = true;
     for (int q = first; ok && q < total; q += step) {
-      int mt, nt;
-      int8_tile(q, MT, NT, &mt, &nt);
-      const int rows = min(p.per, p.T - nt * p.per), half = (rows + 15) / 16 * 8;
-      const int boxes = (half + 31) / 32, t0 = nt * p.per + rank * half;
-      const int m0 = mt * 256 + rank * 128;
-      for (int i = 0; i < KT; ++i) {
+      const Item it = int8_item(q, p.split, MT, NT, KT);
+      const int rows = min(p.per, p.T - it.nt * p.per), half = (rows + 15) / 16 * 8;
+      const int boxes = (half + 31) / 32, t0 = it.nt * p.per + rank * half;
+      const int m0 = it.mt * 256 + rank * 128;
+      for (int i = it.k0; i < it.k1; ++i) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
           ok = false;
           break;
@@ -712,16 +728,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step, ++tiles) {
-        int mt, nt;
-        int8_tile(q, MT, NT, &mt, &nt);
-        const int n = (min(p.per, p.T - nt * p.per) + 15) / 16 * 16;
+        const Item it = int8_item(q, p.split, MT, NT, KT);
+        const int n = (min(p.per, p.T - it.nt * p.per) + 15) / 16 * 16;
         const uint32_t idesc = idesc0 | static_cast<uint32_t>(n >> 3) << 17;
         const uint32_t acc = tmem + (tiles & 1) * C::ACC1;
-        for (int i = 0; i < KT; ++i, ++steps) {
+        for (int i = it.k0; i < it.k1; ++i, ++steps) {
           const int buf = steps & 1;
           if (!mbar_wait(&x_full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
               !mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
-              (i == 0 && !mbar_wait(acc_empty, (tiles & 1) ^ 1u, abort_flag, p.status,
+              (i == it.k0 && !mbar_wait(acc_empty, (tiles & 1) ^ 1u, abort_flag, p.status,
                                     p.wait_limit_ns))) {
             ok = false;
             break;
@@ -735,7 +750,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             for (int c = 0; c < 8; ++c)
               if (16 * c < left)
                 mma_f16_pair_ts(acc, a + 8 * c, sdesc_at(cx, (c >> 2) * C::X + 32 * (c & 3)), idesc,
-                                (i != 0 || c != 0) ? 1u : 0u);
+                                (i != it.k0 || c != 0) ? 1u : 0u);
             tc_commit_pair(&empty[stage]);
             tc_commit_pair(&a_empty[buf]);
           }
@@ -761,8 +776,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     // warps take the even stages and four the odd ones, each set with a buffer.
     const int quarter = warp & 3, buf = warp >= 14 ? 1 : 0;
     const uint32_t to = tmem + C::A_COL0 + buf * C::A_COLS + (static_cast<uint32_t>(quarter * 32) << 16);
-    const int tiles = first < total ? (total - 1 - first) / step + 1 : 0;
-    const int64_t all = static_cast<int64_t>(tiles) * KT;
+    int64_t all = 0;  // stages of this pair's items
+    for (int q = first; q < total; q += step) {
+      const Item it = int8_item(q, p.split, MT, NT, KT);
+      all += it.k1 - it.k0;
+    }
     uint32_t phase = 0;
     for (int64_t i = buf; i < all; i += 2, phase ^= 1u) {
       const int stage = static_cast<int>(i % STAGES);
@@ -807,10 +825,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     int tiles = 0;
     bool bad = false;
     for (int q = first; q < total; q += step, ++tiles) {
-      int mt, nt;
-      int8_tile(q, MT, NT, &mt, &nt);
-      const int rows = min(p.per, p.T - nt * p.per), t0 = nt * p.per;
-      const int m = mt * 256 + rank * 128 + quarter * 32;  // this warp's first feature
+      const Item it = int8_item(q, p.split, MT, NT, KT);
+      const int rows = min(p.per, p.T - it.nt * p.per), t0 = it.nt * p.per;
+      const int m = it.mt * 256 + rank * 128 + quarter * 32;  // this warp's first feature
       const float sw = m + lane < p.N ? __ldg(p.w_scales + m + lane) : 0.f;
       if (!mbar_wait(acc_full, tiles & 1, abort_flag, p.status, p.wait_limit_ns)) break;
       tc_fence_after();
@@ -834,6 +851,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         for (int h = 0; h < 2; ++h) {
           const int c = c0 + 64 * h;
           if (c >= rows) continue;
+          if (p.split > 1) {
+            float* to = p.partial + (static_cast<int64_t>(it.share) * p.T + t0 + c) * p.N + m + lane;
+            if (m + lane < p.N) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j, to += p.N)
+                if (c + j < rows) *to = __uint_as_float(v[h][j]);
+            }
+            continue;
+          }
           const float4* xs = reinterpret_cast<const float4*>(p.x_scales + t0 + c);
 #pragma unroll
           for (int g = 0; g < 32 / ROWS; ++g) {
@@ -858,12 +884,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                                           piece * PER) = x;
             }
           }
-          if (mt == 0 && c + lane < rows) {  // once for each token
-            const float s = __ldg(p.x_scales + t0 + c + lane);
-            bad |= !(s <= 0x1.fffffep127f);
-          }
         }
       }
+      if (it.mt == 0 && it.share == 0)  // once for each token
+        for (int c = threadIdx.x - 64; c < rows; c += 32 * kEpiWarps)
+          bad |= !(__ldg(p.x_scales + t0 + c) <= 0x1.fffffep127f);
     }
     if (bad) set_status(p.status, MEGAMOE_DEV_NONFINITE);
     __syncwarp();
@@ -879,14 +904,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   }
 }
 
+// The shares of a sum in their order, and the scales.  Four columns a thread.
+template <typename O>
+__global__ void __launch_bounds__(256) k_int8_sum(const Int8Args p) {
+  pdl_wait();
+  pdl_trigger();
+  const int quads = p.N / 4;
+  const int64_t total = static_cast<int64_t>(p.T) * quads;
+  for (int64_t i = blockIdx.x * int64_t{256} + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x) * 256) {
+    const int64_t t = i / quads;
+    const int c = static_cast<int>(i - t * quads) * 4;
+    const float* from = p.partial + t * p.N + c;
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < p.split; ++s) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + static_cast<int64_t>(s) * p.T * p.N));
+      sum.x += v.x;
+      sum.y += v.y;
+      sum.z += v.z;
+      sum.w += v.w;
+    }
+    const float sx = __ldg(p.x_scales + t);
+    O* to = static_cast<O*>(p.out) + t * p.ld_out + c;
+    store_rounded(sum.x * sx * __ldg(p.w_scales + c), to);
+    store_rounded(sum.y * sx * __ldg(p.w_scales + c + 1), to + 1);
+    store_rounded(sum.z * sx * __ldg(p.w_scales + c + 2), to + 2);
+    store_rounded(sum.w * sx * __ldg(p.w_scales + c + 3), to + 3);
+  }
+}
+
 template <typename O>
 cudaError_t launch_pair(const Int8Maps& maps, const Int8Args& a, int64_t tiles, cudaStream_t stream) {
   auto kern = k_int8_pair<O>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
-                    stream, maps, a);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM, stream,
+                 maps, a);
+  if (e != cudaSuccess || a.split == 1) return e;
+  const int64_t blocks = (static_cast<int64_t>(a.T) * (a.N / 4) + 255) / 256;
+  return launch_pdl(k_int8_sum<O>,
+                    dim3(static_cast<unsigned>(std::min<int64_t>(blocks, num_sms() * int64_t{16}))),
+                    dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -936,6 +996,17 @@ cudaError_t launch_int8_few(const Int8Quant& q, const Int8Product& g, cudaStream
   return q.T <= 8 ? launch_few<1>(a, blocks, stream) : launch_few<2>(a, blocks, stream);
 }
 
+Int8Plan int8_plan(int64_t T, int N, int K) {
+  Int8Plan p;
+  const int64_t nt = (T + 255) / 256;
+  p.per = static_cast<int>(((T + nt - 1) / nt + 15) / 16 * 16);
+  p.tiles = (T + p.per - 1) / p.per * ((N + 255) / 256);
+  // shares of at least two steps where pairs would idle
+  const int64_t steps = (K + 127) / 128;
+  p.split = static_cast<int>(std::max<int64_t>(1, std::min({kInt8Pairs / p.tiles, steps / 2, int64_t{16}})));
+  return p;
+}
+
 cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {
   if (g.T == 0) return cudaSuccess;
   Int8Maps maps;
@@ -944,13 +1015,12 @@ cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {
       !make_map(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.x, g.K, g.T,
                 static_cast<uint64_t>(g.K) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const int64_t nt = (g.T + 255) / 256;
-  const int per = static_cast<int>(((g.T + nt - 1) / nt + 15) / 16 * 16);
-  const Int8Args a{g.x_scales, g.w_scales, static_cast<int>(g.T), g.N, g.K, per, g.out, g.ld_out,
-                   g.status, wait_limit_ns()};
-  const int64_t tiles = nt * ((g.N + 255) / 256);
-  return g.out_f32 ? launch_pair<float>(maps, a, tiles, stream)
-                   : launch_pair<__nv_bfloat16>(maps, a, tiles, stream);
+  const Int8Plan plan = int8_plan(g.T, g.N, g.K);
+  const Int8Args a{g.x_scales, g.w_scales, static_cast<int>(g.T), g.N, g.K, plan.per, plan.split,
+                   g.out, g.ld_out, g.partial, g.status, wait_limit_ns()};
+  const int64_t items = plan.tiles * plan.split;
+  return g.out_f32 ? launch_pair<float>(maps, a, items, stream)
+                   : launch_pair<__nv_bfloat16>(maps, a, items, stream);
 }
 
 }  // namespace megamoe

@@ -343,8 +343,17 @@ struct Int8Product {
   void* out;
   bool out_f32;
   int64_t ld_out;
+  float* partial;  // plan.split > 1: [split][T][N]
   uint32_t* status;
 };
+// How the product runs on pairs of CTAs.
+struct Int8Plan {
+  int per;        // tokens of a tile
+  int64_t tiles;
+  int split;      // shares of a tile's sum
+};
+constexpr int64_t kInt8Pairs = 76;  // of SMs (counted on for workspaces, which are sized without a device)
+Int8Plan int8_plan(int64_t T, int N, int K);
 cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream);
 // The same for few tokens.  Dots: up to four, quantised in the same launch (q's
 // x, type, T, ld and x_scales; clears *status first).  Few: up to sixteen, q the
