@@ -62,7 +62,10 @@ struct GroupedArgs {
 };
 
 struct Cfg {
-  static constexpr int THREADS = 352;  // producer, MMA issuer, 8 epilogue warps, tail warp
+  static constexpr int THREADS = 384;  // producer, MMA issuer, tail warp, idle; 8 epilogue warps
+  // With fp32 results the epilogue's warps hold 128 sums each; the first four then
+  // give up registers for them.  A thread's of either (168 at launch):
+  static constexpr int FEW_REGS = 64, MANY_REGS = 216;
   static constexpr int STAGES = 6;
   static constexpr int TILE = 128 * 128;  // a CTA's part of either operand
   static constexpr int STAGE = 2 * TILE;
@@ -260,6 +263,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   const int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
 
+  if (warp < 4) {
+  if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW_REGS));
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     // (the whole warp, one lane of it issuing: elect_one)
@@ -376,8 +381,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       mbar_drain(drain, 0);
     }
     __syncwarp();
-  } else if (warp == 10) {
-    if (MODE == kGradW) {
+  } else if (MODE == kGradW && warp == 2) {
+    {
       // ---------------------------------------------------------- tail warp
       // in an expert's last stage the rows past its end become zeros, up to the
       // sixteen that are read; the other stages go from the copies to the MMAs
@@ -403,11 +408,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         __syncwarp();
       }
     }
+  }
   } else {
     // -------------------------------------------------------------- epilogue
+    if (FOLD) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MANY_REGS));
     const int quarter = warp & 3;
-    const int half = warp >= 6 ? 1 : 0;
-    uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
+    const int half = warp >= 8 ? 1 : 0;
+    uint8_t* stg = smem + C::STG_OFF + (warp - 4) * C::STG;
     // A lane has a feature, a column is a row of the output.  The two warps of a
     // quarter take chunks of 32 columns in turn.
     O* out = static_cast<O*>(p.out);
@@ -524,6 +531,14 @@ cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t 
   auto kern = k_grouped_pair<MODE, O>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
+  // what the warps hold after giving up and taking registers is what they start with
+  static const bool fits = [] {
+    cudaFuncAttributes f;
+    return sizeof(O) != 4 ||
+           (cudaFuncGetAttributes(&f, k_grouped_pair<MODE, O>) == cudaSuccess &&
+            f.numRegs * Cfg::THREADS >= 128 * Cfg::FEW_REGS + 256 * Cfg::MANY_REGS);
+  }();
+  if (!fits) return cudaErrorInvalidConfiguration;
   const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
                     stream, maps, a);
