@@ -3,6 +3,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/megamoe.h"
 #include "kernels.h"
 
@@ -35,9 +37,11 @@ megamoe_status check_grouped(int type, int64_t rows, int E, int N, int K, const 
   if (E > MEGAMOE_MAX_EXPERTS || rows >= kMaxRows || N % 8 != 0 || K % 8 != 0 || N >= kMaxWidth ||
       K >= kMaxWidth)
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
-  const int64_t most = kMaxRows - 1, mt = (N + 255) / 256, kt = (K + 255) / 256;
+  const int64_t most = int64_t{1} << 30, mt = (N + 255) / 256, kt = (K + 255) / 256;
   const int64_t per = (rows + 255) / 256 * E;
-  if (per * mt > most || per * kt > most || mt * kt > most / E) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  if (per > most / std::max(mt, kt) || mt * kt > most / E) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  // the stride between experts' weights is below 2^40 bytes
+  if (static_cast<int64_t>(N) * K >= (int64_t{1} << 39)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(offsets, 4) || !aligned(padded_offsets, 4) || !aligned(status, 4))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   return MEGAMOE_OK;

@@ -31,6 +31,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -531,14 +532,17 @@ cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t 
   auto kern = k_grouped_pair<MODE, O>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  // what the warps hold after giving up and taking registers is what they start with
-  static const bool fits = [] {
+  if (sizeof(O) == 4) {
+    // what the warps hold after giving up and taking registers is what they start with
+    static std::atomic<bool> fits{false};
     cudaFuncAttributes f;
-    return sizeof(O) != 4 ||
-           (cudaFuncGetAttributes(&f, k_grouped_pair<MODE, O>) == cudaSuccess &&
-            f.numRegs * Cfg::THREADS >= 128 * Cfg::FEW_REGS + 256 * Cfg::MANY_REGS);
-  }();
-  if (!fits) return cudaErrorInvalidConfiguration;
+    if (!fits.load(std::memory_order_relaxed)) {
+      if ((e = cudaFuncGetAttributes(&f, kern)) != cudaSuccess) return e;
+      if (f.numRegs * Cfg::THREADS < 128 * Cfg::FEW_REGS + 256 * Cfg::MANY_REGS)
+        return cudaErrorInvalidConfiguration;
+      fits.store(true, std::memory_order_relaxed);
+    }
+  }
   const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
   return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
                     stream, maps, a);

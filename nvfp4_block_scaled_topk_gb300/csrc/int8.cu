@@ -261,7 +261,7 @@ __device__ __forceinline__ void few_store(const Int8Few& p, int t, int n, float 
 }
 __device__ __forceinline__ void few_status(const Int8Few& p, const float* scales) {
   bool bad = false;
-  for (int t = 0; t < p.T; ++t) bad |= !(scales[t] <= 0x1.fffffep127f);
+  for (int t = 0; t < p.T; ++t) bad |= !(fabsf(scales[t]) <= 0x1.fffffep127f);
   *p.status = bad ? MEGAMOE_DEV_NONFINITE : 0u;
 }
 
@@ -888,7 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       }
       if (it.mt == 0 && it.share == 0)  // once for each token
         for (int c = threadIdx.x - 64; c < rows; c += 32 * kEpiWarps)
-          bad |= !(__ldg(p.x_scales + t0 + c) <= 0x1.fffffep127f);
+          bad |= !(fabsf(__ldg(p.x_scales + t0 + c)) <= 0x1.fffffep127f);
     }
     if (bad) set_status(p.status, MEGAMOE_DEV_NONFINITE);
     __syncwarp();
