@@ -71,15 +71,31 @@ __device__ __forceinline__ void Eight<float>::values(float (&v)[8]) const {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(u[i]);
 }
-// Largest magnitude of eight, as bits: NaN and Inf compare as the largest.
+// The largest magnitude so far, NaN and Inf the largest of all: as bits of fp32, or
+// of two 16-bit elements at a time.
 template <typename X>
-__device__ __forceinline__ uint32_t largest(const Eight<X>& e) {
-  float v[8];
-  e.values(v);
-  uint32_t m = 0;
+__device__ __forceinline__ void take_largest(const Eight<X>& e, uint32_t* m) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  return m;
+  for (int i = 0; i < static_cast<int>(sizeof(X) / 2); ++i) {
+    const uint32_t u[4] = {e.q[i].x, e.q[i].y, e.q[i].z, e.q[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *m = sizeof(X) == 4 ? max(*m, u[j] & 0x7fffffffu) : __vmaxu2(*m, u[j] & 0x7fff7fffu);
+  }
+}
+template <typename X>
+__device__ __forceinline__ uint32_t fp32_bits(uint32_t m);
+template <>
+__device__ __forceinline__ uint32_t fp32_bits<float>(uint32_t m) { return m; }
+template <>
+__device__ __forceinline__ uint32_t fp32_bits<__nv_bfloat16>(uint32_t m) {
+  return max(m & 0xffffu, m >> 16) << 16;
+}
+template <>
+__device__ __forceinline__ uint32_t fp32_bits<__half>(uint32_t m) {
+  const uint32_t h = max(m & 0xffffu, m >> 16);
+  return h >= 0x7c00u ? 0x7f800000u
+                      : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 
 // rint(127 x / amax), ties to even, with no rounding before the last: for amax whose
@@ -105,11 +121,16 @@ __device__ __noinline__ float exact_quotient(float x, float amax, float t, bool 
 __device__ __forceinline__ void quantised(const float (&x)[8], float amax, float inv, bool ordinary,
                                           float (&q)[8]) {
   float off = 0.f;
+  const uint64_t inv2 = pack2(inv, inv), one = pack2(-1.f, -1.f);
+  const uint64_t up = pack2(12582912.f, 12582912.f), down = pack2(-12582912.f, -12582912.f);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float t = x[j] * inv;
-    q[j] = __fsub_rn(__fadd_rn(t, 12582912.f), 12582912.f);  // 1.5 * 2^23: to the nearest integer
-    off = fmaxf(off, fabsf(t - q[j]));
+  for (int j = 0; j < 8; j += 2) {
+    const uint64_t t = mul2(pack2(x[j], x[j + 1]), inv2);
+    const uint64_t r = add2(add2(t, up), down);  // 1.5 * 2^23: to the nearest integer
+    const float2 n = unpack2(r), d = unpack2(fma2(r, one, t));
+    q[j] = n.x;
+    q[j + 1] = n.y;
+    off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
   }
   if (ordinary && off < 0.5f - 0x1p-15f) return;
 #pragma unroll
@@ -137,13 +158,13 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant
     }
 #pragma unroll
     for (int h = 0; h < kHeld; ++h)
-      if (threadIdx.x + h * kQuantThreads < vecs) m = max(m, largest(held[h]));
+      if (threadIdx.x + h * kQuantThreads < vecs) take_largest(held[h], &m);
     for (int i = threadIdx.x + kHeld * kQuantThreads; i < vecs; i += kQuantThreads) {
       Eight<X> e;
       e.load(row + static_cast<int64_t>(i) * 8);
-      m = max(m, largest(e));
+      take_largest(e, &m);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+    m = __reduce_max_sync(0xffffffffu, fp32_bits<X>(m));
     if (lane == 0) s_amax[turn][warp] = m;  // two sets in turn: one barrier a row
     __syncthreads();
 #pragma unroll
@@ -282,11 +303,11 @@ __device__ __forceinline__ void few_quantise(const Int8Few& p, int8_t* s_codes,
       if (t < p.T) e[t].load(x + t * p.ld + i * 8);
 #pragma unroll
     for (int t = 0; t < T; ++t)
-      if (t < p.T) m[t] = max(m[t], largest(e[t]));
+      if (t < p.T) take_largest(e[t], &m[t]);
   }
 #pragma unroll
   for (int t = 0; t < T; ++t) {
-    m[t] = __reduce_max_sync(0xffffffffu, m[t]);
+    m[t] = __reduce_max_sync(0xffffffffu, fp32_bits<X>(m[t]));
     if ((threadIdx.x & 31) == 0) s_amax[t][threadIdx.x >> 5] = m[t];
   }
   __syncthreads();

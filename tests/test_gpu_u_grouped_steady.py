@@ -224,7 +224,8 @@ def test_rows_far_apart(cuda_lib):
     far = megamoe.grouped_linear_backward(_wide(gr, ld), x, w, off, grad_x=_wide(x, ld))
     assert torch.equal(far[0], gx) and torch.equal(far[1], gw)
     del far
-    assert torch.equal(megamoe.silu_mul(_wide(gr, ld)), megamoe.silu_mul(gr))
+    # (half of 136 is no multiple of 8: the first 128 columns)
+    assert torch.equal(megamoe.silu_mul(_wide(gr, ld)[:, :128]), megamoe.silu_mul(gr[:, :128]))
     src = torch.arange(R - 1, -1, -1, dtype=torch.int32, device="cuda")
     rows = megamoe.gather_rows(_wide(x, ld), src, 1)
     assert torch.equal(rows, x.flip(0))
