@@ -98,16 +98,28 @@ __device__ __forceinline__ uint32_t fp32_bits<__half>(uint32_t m) {
                       : __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
 }
 
-// rint(127 x / amax), ties to even, with no rounding before the last: for amax whose
-// products stay clear of both ends of fp32 (ordinary) |127 x| is compared with (k +
-// 1/2) amax, k = floor |t|, as sums of a rounded product and its error; both errors
-// have ten bits at most, the products are within a factor of two of each other, so
-// every difference is exact.  Otherwise in 64 bits, where 127 x is exact and a
-// quotient of two fp32 numbers that is no half is at least 2^-33 of its size away.
-constexpr float kOrdinaryLow = 0x1p-90f, kOrdinaryHigh = 0x1p118f;
-__device__ __noinline__ float exact_quotient(float x, float amax, float t, bool ordinary) {
-  if (!ordinary)
-    return static_cast<float>(rint(static_cast<double>(x) * 127.0 / static_cast<double>(amax)));
+// A row's divisor.  Rows of very small or large magnitudes are scaled by a power of
+// two first (exact wherever it could change an integer), so that no step below
+// leaves fp32's normal range.
+struct RowScale {
+  float amax;  // of the scaled row
+  float inv;   // 1 / amax, fp32 elements: 127 / amax
+  float by;         // 1, 2^100 or 2^-20
+};
+template <typename X>
+__device__ __forceinline__ RowScale row_scale(float amax) {
+  RowScale r;
+  r.by = amax < 0x1p-90f ? 0x1p100f : amax > 0x1p118f ? 0x1p-20f : 1.f;
+  r.amax = amax * r.by;
+  r.inv = (sizeof(X) == 2 ? 1.f : 127.f) / r.amax;
+  return r;
+}
+
+// rint(127 x / amax) of one fp32 element by comparing |127 x| with (k + 1/2) amax, k =
+// floor |t|, each as a rounded product and its error: both errors have ten bits at
+// most and the products are within a factor of two of each other, so every
+// difference is exact.
+__device__ __noinline__ float compared(float x, float amax, float t) {
   const float k = floorf(fabsf(t)), h = k + 0.5f, a = fabsf(x);
   const float p = __fmul_rn(127.f, a), q = __fmul_rn(h, amax);
   const float d = __fadd_rn(__fsub_rn(p, q), __fsub_rn(__fmaf_rn(127.f, a, -p), __fmaf_rn(h, amax, -q)));
@@ -115,28 +127,53 @@ __device__ __noinline__ float exact_quotient(float x, float amax, float t, bool 
   return copysignf(d > 0.f || (d == 0.f && odd) ? k + 1.f : k, x);
 }
 
-// rint(127 x / amax) of eight as in exact arithmetic, |x| <= amax.  The product
-// with inv = 127 / amax is off by at most 2^-23 of the quotient, below 2^-15; only a
-// fraction that near to a half needs more.
-__device__ __forceinline__ void quantised(const float (&x)[8], float amax, float inv, bool ordinary,
-                                          float (&q)[8]) {
-  float off = 0.f;
-  const uint64_t inv2 = pack2(inv, inv), one = pack2(-1.f, -1.f);
+// rint(127 x / amax) of eight as in exact arithmetic, ties to even.
+//
+// 16-bit elements: p = 127 x is exact, t = p inv is off by 2 units, the remainder p - t
+// amax is exact, and adding its share gives the quotient Q rounded once, exactly Q
+// where fp32 holds it, so at every half.  Any other Q is further from a half than
+// that rounding: with mantissas of 11 bits, by Q 2^-20 at least.  (Halves are common:
+// where amax is 2^n, one in a few hundred.)
+//
+// fp32: t = x (127 / amax) is off by at most 2^-23 Q, below 2^-15; a fraction that
+// near to a half is compared.
+template <typename X>
+__device__ __forceinline__ void quantised(float (&x)[8], const RowScale& r, float (&q)[8]) {
+  if (r.by != 1.f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] *= r.by;
+  }
+  const uint64_t inv2 = pack2(r.inv, r.inv);
   const uint64_t up = pack2(12582912.f, 12582912.f), down = pack2(-12582912.f, -12582912.f);
+  float off = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
-    const uint64_t t = mul2(pack2(x[j], x[j + 1]), inv2);
-    const uint64_t r = add2(add2(t, up), down);  // 1.5 * 2^23: to the nearest integer
-    const float2 n = unpack2(r), d = unpack2(fma2(r, one, t));
+    const uint64_t v = pack2(x[j], x[j + 1]);
+    uint64_t t;
+    if constexpr (sizeof(X) == 2) {
+      const uint64_t p = mul2(v, pack2(127.f, 127.f));
+      t = mul2(p, inv2);
+      t = fma2(fma2(t, pack2(-r.amax, -r.amax), p), inv2, t);
+    } else {
+      t = mul2(v, inv2);
+    }
+    const uint64_t n2 = add2(add2(t, up), down);  // 1.5 * 2^23: to the nearest integer
+    const float2 n = unpack2(n2);
     q[j] = n.x;
     q[j + 1] = n.y;
-    off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+    if constexpr (sizeof(X) == 4) {
+      const float2 d = unpack2(fma2(n2, pack2(-1.f, -1.f), t));
+      off = fmaxf(off, fmaxf(fabsf(d.x), fabsf(d.y)));
+    }
   }
-  if (ordinary && off < 0.5f - 0x1p-15f) return;
+  if constexpr (sizeof(X) == 4) {
+    if (off < 0.5f - 0x1p-15f) return;
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if (!ordinary || !(fabsf(x[j] * inv - q[j]) < 0.5f - 0x1p-15f))
-      q[j] = exact_quotient(x[j], amax, x[j] * inv, ordinary);
+    for (int j = 0; j < 8; ++j) {
+      const float t = x[j] * r.inv;
+      if (!(fabsf(t - q[j]) < 0.5f - 0x1p-15f)) q[j] = compared(x[j], r.amax, t);
+    }
+  }
 }
 
 template <typename X>
@@ -171,9 +208,8 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant
     for (int i = 0; i < kQuantThreads / 32; ++i) m = max(m, s_amax[turn][i]);
     const bool finite = m < 0x7f800000u;
     const float amax = __uint_as_float(m);
-    const float inv = 127.f / amax;
     const bool zero = !finite || m == 0;
-    const bool ordinary = amax > kOrdinaryLow && amax < kOrdinaryHigh;
+    const RowScale scale = row_scale<X>(amax);
     if (threadIdx.x == 0) {
       p.scales[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
       if (!finite && !p.clear) set_status(p.status, MEGAMOE_DEV_NONFINITE);
@@ -181,7 +217,7 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_quantize(const Int8Quant
     auto put = [&](int i, const Eight<X>& e) {
       float v[8], q[8];
       e.values(v);
-      if (!zero) quantised(v, amax, inv, ordinary, q);
+      if (!zero) quantised<X>(v, scale, q);
       const int64_t at = t * p.K + static_cast<int64_t>(i) * 8;
       if (p.half) {
         uint32_t w[4];
@@ -317,8 +353,8 @@ __device__ __forceinline__ void few_quantise(const Int8Few& p, int8_t* s_codes,
 #pragma unroll
     for (int i = 0; i < kFewWarps; ++i) a = max(a, s_amax[t][i]);
     const bool finite = a < 0x7f800000u, zero = !finite || a == 0;
-    const float amax = __uint_as_float(a), inv = 127.f / amax;
-    const bool ordinary = amax > kOrdinaryLow && amax < kOrdinaryHigh;
+    const float amax = __uint_as_float(a);
+    const RowScale scale = row_scale<X>(amax);
     if (threadIdx.x == 0) s_scale[t] = finite ? amax / 127.f : __uint_as_float(0x7fffffffu);
 #pragma unroll 2
     for (int i = threadIdx.x; i < vecs; i += kFewThreads) {
@@ -328,7 +364,7 @@ __device__ __forceinline__ void few_quantise(const Int8Few& p, int8_t* s_codes,
         e.load(x + t * p.ld + i * 8);
         float v[8], q[8];
         e.values(v);
-        quantised(v, amax, inv, ordinary, q);
+        quantised<X>(v, scale, q);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           w[j >> 2] |= static_cast<uint32_t>(__float2int_rn(q[j]) & 0xff) << (8 * (j & 3));
