@@ -72,6 +72,33 @@ def test_quantise_ties_and_ends(cuda_lib, dtype):
     assert np.array_equal(scales.cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_quantise_rows_of_any_size(cuda_lib, dtype):
+    """Rows whose largest magnitude has every mantissa of few bits (which make halves
+    common) and every exponent that the type holds, elements of few bits among them."""
+    f = torch.finfo(dtype)
+    g = torch.Generator().manual_seed(8)
+    low, high = int(np.log2(f.smallest_normal * f.eps)), int(np.floor(np.log2(f.max)))
+    rows = []
+    for e in range(low, high + 1, 3 if dtype == torch.float16 else 9):
+        for mantissa in (128, 192, 160, 224, 129, 255):
+            x = torch.randint(-mantissa, mantissa + 1, (256,), generator=g).double()
+            x[:64] = (torch.rand(64, generator=g, dtype=torch.float64) * 2 - 1) * mantissa
+            x[100] = mantissa
+            rows.append(torch.ldexp(x, torch.tensor(e - 7)))
+    x = torch.stack(rows).clamp(-f.max, f.max).to(dtype)
+    codes, scales = megamoe.quantize_int8(x.cuda())
+    want = exact_codes(x)
+    assert np.array_equal(codes.cpu().numpy(), want[0])
+    assert np.array_equal(scales.cpu().numpy(), want[1])
+    w = megamoe.Int8LinearWeights.quantize(torch.eye(256, device="cuda"))
+    for T in (1, 4, 12):  # the tokens' integers in a product with 127 at their own place
+        out, _ = megamoe.linear_int8(x[5:5 + T].cuda(), w, megamoe.EPI_F32)
+        with np.errstate(all="ignore"):
+            prod = want[0][5:5 + T].astype(np.float32) * 127 * want[1][5:5 + T, None]
+            assert np.array_equal(out.cpu().numpy(), prod * w.scales.cpu().numpy())
+
+
 def test_quantise_nonfinite(cuda_lib):
     x = torch.randn(4, 64)
     x[1, 5], x[2, 63] = float("inf"), float("nan")
