@@ -1028,40 +1028,77 @@ class MxForward:
 # experts in 16 bits: products grouped by expert, activation, movement of rows
 # --------------------------------------------------------------------------
 HALF_TYPES = {torch.bfloat16: 0, torch.float16: 2}
+# (a call of a short kernel is its checks and the launch: the functions below ask for
+# each attribute once, and for the current device once a call)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _indices(t, n, name):
-    """Address of an int32 vector of n values (n None: any number)."""
-    _dev(t, torch.int32, name)
+def _first(t, types, name):
+    """(rows, columns, row stride, type code, device) of a call's first matrix: a CUDA
+    matrix of one of `types` with unit column stride, on the current device."""
+    code = types.get(t.dtype)
+    dev = t.get_device()
+    if code is None or dev < 0 or t.dim() != 2:
+        raise TypeError(f"{name} must be a CUDA matrix of {', '.join(map(str, types))}")
+    if dev != _current_device():
+        _on_current_device(t, name)
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise TypeError(f"{name} must have unit column stride")
+    return rows, cols, ld if rows > 1 else cols, code, dev
+
+
+def _next(t, dtype, name, dev):
+    """(rows, columns, row stride) of a further matrix, of this type and device."""
+    if t.dtype != dtype or t.dim() != 2 or t.get_device() < 0:
+        raise TypeError(f"{name} must be a CUDA matrix of {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on another device")
+    rows, cols = t.shape
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise TypeError(f"{name} must have unit column stride")
+    return rows, cols, ld if rows > 1 else cols
+
+
+def _values(t, dtype, n, name, dev):
+    """Address of n contiguous values (n None: any number) on the call's device; None: null."""
+    if t is None:
+        return None
+    at = t.get_device()
+    if t.dtype != dtype or at < 0 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if at != dev:
+        raise ValueError(f"{name} is on another device")
     if n is not None and t.numel() != n:
         raise ValueError(f"{name} must have {n} values")
     return t.data_ptr()
 
 
-def _status_word(t):
-    if t is None:
-        return None
-    _dev(t, torch.int32, "status")
-    if t.numel() < 1:
+def _status_word(t, dev):
+    at = _values(t, torch.int32, None, "status", dev)
+    if t is not None and t.numel() < 1:
         raise ValueError("status must hold a word")
-    return t.data_ptr()
+    return at
 
 
-def _result(out, rows, cols, dtype, device, name="out"):
+def _result(out, rows, cols, dtype, like, dev, name="out"):
     """(matrix, row stride) of a result: the caller's, or a new one."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    r, c, ld, _, _ = _matrix(out, {dtype: 0}, name)
+        return torch.empty((rows, cols), dtype=dtype, device=like.device), cols
+    r, c, ld = _next(out, dtype, name, dev)
     if r != rows or c != cols:
         raise ValueError(f"{name} must be [{rows}, {cols}]")
     return out, ld
 
 
-def _expert_weights(w, code):
+def _expert_weights(w, dtype, dev):
     """(E, N, K) of contiguous expert weights of the rows' type."""
-    if not (w.is_cuda and w.dim() == 3 and w.is_contiguous()) or HALF_TYPES.get(w.dtype) != code:
+    if w.dtype != dtype or w.dim() != 3 or w.get_device() < 0 or not w.is_contiguous():
         raise TypeError("w must be a contiguous CUDA tensor [E, N, K] of the rows' type")
-    _on_current_device(w, "w")
+    if w.get_device() != dev:
+        raise ValueError("w is on another device")
     return w.shape
 
 
@@ -1071,18 +1108,22 @@ def grouped_linear(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor, padd
     offsets [E + 1] and, where rows are padded, padded_offsets as route_permute
     gives them.  out_dtype: x's type (default) or float32.  Rows of no expert are
     left as they are (uninitialised in a new out)."""
-    rows, K, ld, code, stream = _matrix(x, HALF_TYPES, "x")
-    E, N, wK = _expert_weights(w, code)
+    rows, K, ld, code, dev = _first(x, HALF_TYPES, "x")
+    dt = x.dtype
+    E, N, wK = _expert_weights(w, dt, dev)
     if wK != K:
         raise ValueError("x and w disagree on K")
-    dt = x.dtype if out_dtype is None else out_dtype
-    if dt is not x.dtype and dt is not torch.float32:
-        raise TypeError("out_dtype must be x's type or float32")
-    out, ld_out = _result(out, rows, N, dt, x.device)
+    out_code = code
+    if out_dtype is not None and out_dtype is not dt:
+        if out_dtype is not torch.float32:
+            raise TypeError("out_dtype must be x's type or float32")
+        dt, out_code = out_dtype, 1
+    out, ld_out = _result(out, rows, N, dt, x, dev)
     _check("megamoe_grouped_linear", load().megamoe_grouped_linear(
-        x.data_ptr(), code, rows, ld, w.data_ptr(), E, N, K, _indices(offsets, E + 1, "offsets"),
-        None if padded_offsets is None else _indices(padded_offsets, E + 1, "padded_offsets"),
-        TYPES[dt], out.data_ptr(), ld_out, _status_word(status), stream))
+        x.data_ptr(), code, rows, ld, w.data_ptr(), E, N, K,
+        _values(offsets, torch.int32, E + 1, "offsets", dev),
+        _values(padded_offsets, torch.int32, E + 1, "padded_offsets", dev), out_code,
+        out.data_ptr(), ld_out, _status_word(status, dev), _raw_stream(dev)))
     return out
 
 
@@ -1093,89 +1134,84 @@ def grouped_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w: torch.Te
     """(grad_x [rows, K], grad_w [E, N, K]) of grouped_linear; need_x / need_w false:
     that gradient is None.  Rows of no expert are left as they are in grad_x; an
     expert without rows has a grad_w of zeros."""
-    rows, N, ld_g, code, stream = _matrix(grad_out, HALF_TYPES, "grad_out")
-    x_rows, K, ld_x, x_code, _ = _matrix(x, HALF_TYPES, "x")
-    E, wN, wK = _expert_weights(w, code)
-    if x_code != code:
-        raise TypeError("grad_out and x must be of one type")
+    rows, N, ld_g, code, dev = _first(grad_out, HALF_TYPES, "grad_out")
+    dt = grad_out.dtype
+    x_rows, K, ld_x = _next(x, dt, "x", dev)
+    E, wN, wK = _expert_weights(w, dt, dev)
     if x_rows != rows or wN != N or wK != K:
         raise ValueError("grad_out [rows, N], x [rows, K] and w [E, N, K] disagree")
-    if grad_w_dtype is not x.dtype and grad_w_dtype is not torch.float32:
+    if grad_w_dtype is not dt and grad_w_dtype is not torch.float32:
         raise TypeError("grad_w_dtype must be x's type or float32")
-    gx, ld_gx = _result(grad_x, rows, K, x.dtype, x.device, "grad_x") if need_x else (None, K)
+    gx, ld_gx = _result(grad_x, rows, K, dt, x, dev, "grad_x") if need_x else (None, K)
     gw = torch.empty((E, N, K), dtype=grad_w_dtype, device=x.device) if need_w else None
     _check("megamoe_grouped_linear_backward", load().megamoe_grouped_linear_backward(
         grad_out.data_ptr(), ld_g, x.data_ptr(), ld_x, w.data_ptr(), code, rows, E, N, K,
-        _indices(offsets, E + 1, "offsets"),
-        None if padded_offsets is None else _indices(padded_offsets, E + 1, "padded_offsets"),
-        _p(gx), ld_gx, TYPES[grad_w_dtype], _p(gw), _status_word(status), stream))
+        _values(offsets, torch.int32, E + 1, "offsets", dev),
+        _values(padded_offsets, torch.int32, E + 1, "padded_offsets", dev), _p(gx), ld_gx,
+        TYPES[grad_w_dtype], _p(gw), _status_word(status, dev), _raw_stream(dev)))
     return gx, gw
 
 
 def silu_mul(a: torch.Tensor, live_rows=None, out=None):
     """[rows, I] = silu(gate) * up of a [rows, 2 I] (gate columns, then up columns).
     live_rows: a device int32; rows from it on are neither read nor written."""
-    rows, width, ld, code, stream = _matrix(a, HALF_TYPES, "a")
+    rows, width, ld, code, dev = _first(a, HALF_TYPES, "a")
     if width % 2:
         raise ValueError("a must be [rows, 2 I]")
-    out, ld_out = _result(out, rows, width // 2, a.dtype, a.device)
+    out, ld_out = _result(out, rows, width // 2, a.dtype, a, dev)
     _check("megamoe_silu_mul", load().megamoe_silu_mul(
         a.data_ptr(), code, rows, width // 2, ld,
-        None if live_rows is None else _indices(live_rows, 1, "live_rows"), out.data_ptr(), ld_out,
-        stream))
+        _values(live_rows, torch.int32, 1, "live_rows", dev), out.data_ptr(), ld_out,
+        _raw_stream(dev)))
     return out
 
 
 def silu_mul_backward(grad: torch.Tensor, a: torch.Tensor, live_rows=None, grad_a=None):
     """Gradient [rows, 2 I] of silu_mul with respect to a."""
-    rows, width, ld, code, stream = _matrix(a, HALF_TYPES, "a")
-    g_rows, I, ld_g, g_code, _ = _matrix(grad, HALF_TYPES, "grad")
-    if g_code != code:
-        raise TypeError("grad and a must be of one type")
+    rows, width, ld, code, dev = _first(a, HALF_TYPES, "a")
+    g_rows, I, ld_g = _next(grad, a.dtype, "grad", dev)
     if g_rows != rows or width != 2 * I:
         raise ValueError("grad [rows, I] and a [rows, 2 I] disagree")
-    out, ld_out = _result(grad_a, rows, width, a.dtype, a.device, "grad_a")
+    out, ld_out = _result(grad_a, rows, width, a.dtype, a, dev, "grad_a")
     _check("megamoe_silu_mul_backward", load().megamoe_silu_mul_backward(
         grad.data_ptr(), ld_g, a.data_ptr(), code, rows, I, ld,
-        None if live_rows is None else _indices(live_rows, 1, "live_rows"), out.data_ptr(), ld_out,
-        stream))
+        _values(live_rows, torch.int32, 1, "live_rows", dev), out.data_ptr(), ld_out,
+        _raw_stream(dev)))
     return out
 
 
 def gather_rows(x: torch.Tensor, row_src: torch.Tensor, k: int, out=None):
     """[rows, d]: x[row_src[r] // k], zeros where row_src[r] < 0 (row_src of
     route_permute).  The gradient of x is combine_rows(grad, slot_dst)."""
-    T, d, ld, code, stream = _matrix(x, HALF_TYPES, "x")
-    src = _indices(row_src, None, "row_src")
+    T, d, ld, code, dev = _first(x, HALF_TYPES, "x")
+    src = _values(row_src, torch.int32, None, "row_src", dev)
     rows = row_src.numel()
-    out, ld_out = _result(out, rows, d, x.dtype, x.device)
+    out, ld_out = _result(out, rows, d, x.dtype, x, dev)
     _check("megamoe_gather_rows", load().megamoe_gather_rows(
-        x.data_ptr(), code, T, d, ld, src, rows, k, out.data_ptr(), ld_out, stream))
+        x.data_ptr(), code, T, d, ld, src, rows, k, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
-def _slots(slot_dst, topk_weights):
+def _slots(slot_dst, topk_weights, dev):
     """(T, k, addresses) of slot_dst [T, k] and the weights (None: all one)."""
-    _dev(slot_dst, torch.int32, "slot_dst")
+    dst = _values(slot_dst, torch.int32, None, "slot_dst", dev)
     if slot_dst.dim() != 2:
         raise ValueError("slot_dst must be [T, k]")
-    T, k = slot_dst.shape
-    if topk_weights is None:
-        return T, k, slot_dst.data_ptr(), None
-    _dev(topk_weights, torch.float32, "topk_weights")
-    if topk_weights.shape != slot_dst.shape:
+    w = _values(topk_weights, torch.float32, None, "topk_weights", dev)
+    if w is not None and topk_weights.shape != slot_dst.shape:
         raise ValueError("topk_weights must be [T, k]")
-    return T, k, slot_dst.data_ptr(), topk_weights.data_ptr()
+    T, k = slot_dst.shape
+    return T, k, dst, w
 
 
 def combine_rows(y: torch.Tensor, slot_dst: torch.Tensor, topk_weights=None, out=None):
     """[T, d] = sum_j topk_weights[t, j] * y[slot_dst[t, j]] (slots with a negative
     row skipped; no weights: all one), of y's type."""
-    rows, d, ld, code, stream = _matrix(y, HALF_TYPES, "y")
-    T, k, dst, w = _slots(slot_dst, topk_weights)
-    out, ld_out = _result(out, T, d, y.dtype, y.device)
+    rows, d, ld, code, dev = _first(y, HALF_TYPES, "y")
+    T, k, dst, w = _slots(slot_dst, topk_weights, dev)
+    out, ld_out = _result(out, T, d, y.dtype, y, dev)
     _check("megamoe_combine_rows", load().megamoe_combine_rows(
-        y.data_ptr(), code, rows, ld, dst, w, T, k, d, out.data_ptr(), ld_out, stream))
+        y.data_ptr(), code, rows, ld, dst, w, T, k, d, out.data_ptr(), ld_out, _raw_stream(dev)))
     return out
 
 
@@ -1183,18 +1219,16 @@ def combine_rows_backward(grad_out: torch.Tensor, y: torch.Tensor, slot_dst: tor
                           topk_weights=None, need_weights: bool = True, grad_y=None):
     """(grad_y [rows, d], grad_weights float32 [T, k] or None) of combine_rows, for a
     slot_dst whose rows are all different; rows of no slot are left as they are."""
-    T, d, ld_g, code, stream = _matrix(grad_out, HALF_TYPES, "grad_out")
-    rows, y_d, ld_y, y_code, _ = _matrix(y, HALF_TYPES, "y")
-    if y_code != code:
-        raise TypeError("grad_out and y must be of one type")
-    sT, k, dst, w = _slots(slot_dst, topk_weights)
+    T, d, ld_g, code, dev = _first(grad_out, HALF_TYPES, "grad_out")
+    rows, y_d, ld_y = _next(y, grad_out.dtype, "y", dev)
+    sT, k, dst, w = _slots(slot_dst, topk_weights, dev)
     if sT != T or y_d != d:
         raise ValueError("grad_out [T, d], y [rows, d] and slot_dst [T, k] disagree")
-    gy, ld_gy = _result(grad_y, rows, d, y.dtype, y.device, "grad_y")
+    gy, ld_gy = _result(grad_y, rows, d, y.dtype, y, dev, "grad_y")
     gw = torch.empty((T, k), dtype=torch.float32, device=y.device) if need_weights else None
     _check("megamoe_combine_rows_backward", load().megamoe_combine_rows_backward(
         grad_out.data_ptr(), ld_g, y.data_ptr(), code, rows, ld_y, dst, w, T, k, d, gy.data_ptr(),
-        ld_gy, _p(gw), stream))
+        ld_gy, _p(gw), _raw_stream(dev)))
     return gy, gw
 
 
@@ -1207,12 +1241,12 @@ _CODES = {torch.int8: 3}
 def quantize_int8(x: torch.Tensor, status=None):
     """x [rows, K] -> (codes int8 [rows, K], scales float32 [rows]): scale = amax / 127
     of the row, code = rint(127 x / amax)."""
-    rows, K, ld, code, stream = _matrix(x, TYPES, "x")
+    rows, K, ld, code, dev = _first(x, TYPES, "x")
     codes = torch.empty((rows, K), dtype=torch.int8, device=x.device)
     scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
     _check("megamoe_quantize_int8", load().megamoe_quantize_int8(
         x.data_ptr(), code, rows, K, ld, codes.data_ptr(), scales.data_ptr(),
-        _status_word(status), stream))
+        _status_word(status, dev), _raw_stream(dev)))
     return codes, scales
 
 
@@ -1254,19 +1288,21 @@ def linear_int8(x: torch.Tensor, w: Int8LinearWeights, out_dtype=EPI_BF16, x_sca
     x is quantised here, or is int8 codes with x_scales [T].  Returns (out, ws); ws
     holds the status word in its first four bytes and may be passed again for calls
     of the same shape."""
-    T, K, ld, code, stream = _matrix(x, _CODES if x_scales is not None else TYPES, "x")
+    T, K, ld, code, dev = _first(x, _CODES if x_scales is not None else TYPES, "x")
     N = w.N
     if K != w.K:
         raise ValueError("x and w disagree on K")
-    if w.codes.get_device() != x.get_device():
+    if w.codes.get_device() != dev:
         raise ValueError("x and w must be on one device")
-    dev = x.device
     if ws is None:
-        ws = torch.empty((max(linear_int8_workspace_size(T, K, N), 256),), dtype=torch.uint8,
-                         device=dev)
-    ws_bytes = _workspace(ws, x.get_device())
-    out, ld_out = _result(out, T, N, torch.float32 if out_dtype == EPI_F32 else torch.bfloat16, dev)
+        ws_bytes = max(linear_int8_workspace_size(T, K, N), 256)
+        ws = torch.empty((ws_bytes,), dtype=torch.uint8, device=x.device)
+    else:
+        ws_bytes = _workspace(ws, dev)
+    out, ld_out = _result(out, T, N, torch.float32 if out_dtype == EPI_F32 else torch.bfloat16, x,
+                          dev)
     _check("megamoe_linear_int8", load().megamoe_linear_int8(
-        x.data_ptr(), code, T, K, ld, _vector(x_scales, T, "x_scales"), w.codes.data_ptr(),
-        w.scales.data_ptr(), N, out_dtype, out.data_ptr(), ld_out, ws.data_ptr(), ws_bytes, stream))
+        x.data_ptr(), code, T, K, ld, _values(x_scales, torch.float32, T, "x_scales", dev),
+        w.codes.data_ptr(), w.scales.data_ptr(), N, out_dtype, out.data_ptr(), ld_out,
+        ws.data_ptr(), ws_bytes, _raw_stream(dev)))
     return out, ws
