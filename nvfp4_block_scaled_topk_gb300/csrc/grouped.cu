@@ -25,6 +25,20 @@
 //
 // Tensor memory holds two accumulators of 256 columns: a tile is read, rounded
 // and stored under the next one's products.
+//
+// What bounds it, as measured.  Few rows an expert: the weights' bytes; 48 experts of
+// 4096 x 7168 with 48 rows take 280 us for 1.88 GB (99 % of the copy rate), of 7168 x
+// 2048 with 1, 64 and 256 rows each 208, 222 and 259 us (208, 217 and 242 of bytes).
+// From there to some 500 rows what an SM takes in, 50 to 55 bytes a cycle: with 272
+// rows each expert has two tiles of 144, whose stages of 28 KB take the 560 cycles of
+// a full one, 340 us.  Many rows: the MMAs; 16384 rows of eight experts, 7168 x 2048,
+// take 260 us forward and for grad_x (1.84 PFLOP/s, 96 % of a library's dense
+// product; the tensor pipe is 93 % busy) and 255 us for grad_w in bf16.  Few tiles: 5.6
+// us for one of 512 x 512, launch and the first loads; whole turns of the 76 pairs.
+//
+// Measured and not kept: tiles of 512 rows, which load the weights once for two parts
+// (fewer stages fit: 293 against 340 us at 272 rows, 313 against 259 at 256, 468
+// against 467 at 512, and nothing left of it with uneven experts); rows on M.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -65,7 +79,8 @@ struct GroupedArgs {
 struct Cfg {
   static constexpr int THREADS = 384;  // producer, MMA issuer, tail warp, idle; 8 epilogue warps
   // With fp32 results the epilogue's warps hold 128 sums each; the first four then
-  // give up registers for them.  A thread's of either (168 at launch):
+  // give up registers for them (without that some spill: uneven experts' grad_w took
+  // 315 us, 300 with it).  A thread's of either (168 at launch):
   static constexpr int FEW_REGS = 64, MANY_REGS = 216;
   static constexpr int STAGES = 6;
   static constexpr int TILE = 128 * 128;  // a CTA's part of either operand
@@ -212,7 +227,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   // 16384 rows in one go the gradient of w was off by 2.1e-6, 4.4e-6 and 1.9e-5 of
   // its size, always towards zero.  For fp32 results the sum is taken in parts of
   // SEG stages, and the epilogue adds the parts up in registers, rounding to nearest.
-  // A 16-bit result is rounded to 2^-9 or 2^-12 of its size and takes one part.
+  // (16384 rows of eight experts, 7168 x 2048: 287 us so, 280 in one part, 255 with
+  // bf16 results, half the bytes to store.)  A 16-bit result is rounded to 2^-9 or
+  // 2^-12 of its size and takes one part.
   constexpr bool FOLD = sizeof(O) == 4;
   constexpr int SEG = FOLD ? 8 : 1 << 30;
   extern __shared__ uint8_t smem_raw[];
@@ -265,151 +282,152 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
 
   if (warp < 4) {
-  if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW_REGS));
-  if (warp == 0) {
-    // -------------------------------------------------------------- producer
-    // (the whole warp, one lane of it issuing: elect_one)
-    const bool leader = elect_one();
-    const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
-    int stage = 0, issued = 0, e_lo = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int q = first; ok && q < total; q += step) {
-      const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
-      const int m0 = t.m0 + rank * 128;
-      const int boxes = (t.n / 2 + 31) / 32;  // of 32 rows: this CTA's half of N
-      const int r0 = t.n0 + rank * (t.n / 2);
-      const uint64_t pol_m = t.again ? pol_again : pol_once;
-      for (int i = 0; i < t.steps; ++i) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sm = smem + stage * C::STAGE;
-        uint8_t* sn = sm + C::TILE;
-        if (leader) {
-          const bool ragged = MODE == kGradW && t.ragged_at(i);
-          if (rank == 0 && !ragged) {
-            mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + (MODE == kGradW ? C::TILE : boxes * 4096)));
-            mbar_arrive(&full[stage]);
-          }
-          if (MODE == kGradW) {
-            const int r = t.start + i * 64, n0 = t.n0 + rank * 128;
-            uint32_t bar = cluster_address(&full[stage], 0);
-            if (ragged) {
-              mbar_arrive_expect_tx(&tail[stage], C::STAGE);
-              bar = cluster_address(&tail[stage], rank);
-            }
-            tma_load_2d_pair(sm, &maps.m, bar, m0, r, pol_again);
-            tma_load_2d_pair(sm + 8192, &maps.m, bar, m0 + 64, r, pol_again);
-            tma_load_2d_pair(sn, &maps.n, bar, n0, r, pol_again);
-            tma_load_2d_pair(sn + 8192, &maps.n, bar, n0 + 64, r, pol_again);
-          } else {
-            const uint32_t bar = cluster_address(&full[stage], 0);
-            if (M_MN) {
-              tma_load_3d_pair(sm, &maps.m, bar, m0, i * 64, t.e, pol_m);
-              tma_load_3d_pair(sm + 8192, &maps.m, bar, m0 + 64, i * 64, t.e, pol_m);
-            } else {
-              tma_load_3d_pair(sm, &maps.m, bar, i * 64, m0, t.e, pol_m);
-            }
-            for (int b = 0; b < boxes; ++b)
-              tma_load_2d_pair(sn + b * 4096, &maps.n, bar, i * 64, r0 + b * 32, pol_again);
-          }
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    drain_pair_copies(full, STAGES, issued, rank, !ok);
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ---------------------------------------------------------- MMA issuer
+    if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW_REGS));
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      // (the whole warp, one lane of it issuing: elect_one)
       const bool leader = elect_one();
-      const uint64_t dm = M_MN ? sdesc_mn(smem_u32(smem)) : sdesc_sw128(smem_u32(smem));
-      const uint64_t dn = MODE == kGradW ? sdesc_mn(smem_u32(smem) + C::TILE)
-                                         : sdesc_sw128(smem_u32(smem) + C::TILE);
-      // 16 of the summed dimension: 32 bytes of a row, or 16 rows of 128 bytes
-      constexpr uint32_t AM = M_MN ? 2048 : 32, AN = MODE == kGradW ? 2048 : 32;
-      int stage = 0, parts = 0, e_lo = 0;
+      const uint64_t pol_once = policy_evict_first(), pol_again = policy_evict_normal();
+      int stage = 0, issued = 0, e_lo = 0;
       uint32_t phase = 0;
       bool ok = true;
       for (int q = first; ok && q < total; q += step) {
         const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
-        const uint32_t idesc = p.idesc | static_cast<uint32_t>(t.n >> 3) << 17;
-        uint32_t buf = 0;
+        const int m0 = t.m0 + rank * 128;
+        const int boxes = (t.n / 2 + 31) / 32;  // of 32 rows: this CTA's half of N
+        const int r0 = t.n0 + rank * (t.n / 2);
+        const uint64_t pol_m = t.again ? pol_again : pol_once;
         for (int i = 0; i < t.steps; ++i) {
-          if (i % SEG == 0) {
-            buf = parts & 1;
-            if (!mbar_wait(&acc_empty[buf], (parts >> 1 & 1) ^ 1u, abort_flag, p.status,
-                           p.wait_limit_ns)) {
-              ok = false;
-              break;
-            }
-            ++parts;
-          }
-          if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint64_t cm = sdesc_at(dm, stage * C::STAGE), cn = sdesc_at(dn, stage * C::STAGE);
-          // sixteens of the last stage that hold nothing are left out
-          const int left = (MODE == kGradW ? t.rows : p.sum) - i * 64;
+          uint8_t* sm = smem + stage * C::STAGE;
+          uint8_t* sn = sm + C::TILE;
           if (leader) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (16 * c < left)
-                mma_f16_pair(tmem + buf * 256, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
-                             (i % SEG != 0 || c != 0) ? 1u : 0u);
-            tc_commit_pair(&empty[stage]);
-            if (i % SEG == SEG - 1 || i == t.steps - 1) tc_commit_pair(&acc_full[buf]);
+            const bool ragged = MODE == kGradW && t.ragged_at(i);
+            if (rank == 0 && !ragged) {
+              mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + (MODE == kGradW ? C::TILE : boxes * 4096)));
+              mbar_arrive(&full[stage]);
+            }
+            if (MODE == kGradW) {
+              const int r = t.start + i * 64, n0 = t.n0 + rank * 128;
+              uint32_t bar = cluster_address(&full[stage], 0);
+              if (ragged) {
+                mbar_arrive_expect_tx(&tail[stage], C::STAGE);
+                bar = cluster_address(&tail[stage], rank);
+              }
+              tma_load_2d_pair(sm, &maps.m, bar, m0, r, pol_again);
+              tma_load_2d_pair(sm + 8192, &maps.m, bar, m0 + 64, r, pol_again);
+              tma_load_2d_pair(sn, &maps.n, bar, n0, r, pol_again);
+              tma_load_2d_pair(sn + 8192, &maps.n, bar, n0 + 64, r, pol_again);
+            } else {
+              const uint32_t bar = cluster_address(&full[stage], 0);
+              if (M_MN) {
+                tma_load_3d_pair(sm, &maps.m, bar, m0, i * 64, t.e, pol_m);
+                tma_load_3d_pair(sm + 8192, &maps.m, bar, m0 + 64, i * 64, t.e, pol_m);
+              } else {
+                tma_load_3d_pair(sm, &maps.m, bar, i * 64, m0, t.e, pol_m);
+              }
+              for (int b = 0; b < boxes; ++b)
+                tma_load_2d_pair(sn + b * 4096, &maps.n, bar, i * 64, r0 + b * 32, pol_again);
+            }
           }
           __syncwarp();
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
       }
-      // every MMA issued so far must finish before tensor memory is released
-      if (leader) tc_commit_pair(drain);
+      drain_pair_copies(full, STAGES, issued, rank, !ok);
       __syncwarp();
-      mbar_drain(drain, 0);
-    }
-    __syncwarp();
-  } else if (MODE == kGradW && warp == 2) {
-    {
-      // ---------------------------------------------------------- tail warp
-      // in an expert's last stage the rows past its end become zeros, up to the
-      // sixteen that are read; the other stages go from the copies to the MMAs
-      int at = 0, e_lo = 0;
-      uint32_t phases = 0;  // a bit for each stage's barrier
-      for (int q = first; q < total; q += step) {
-        const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
-        at = (at + t.steps) % STAGES;
-        if (!t.ragged_at(t.steps - 1)) continue;
-        const int stage = (at + STAGES - 1) % STAGES;
-        if (!mbar_wait(&tail[stage], phases >> stage & 1u, abort_flag, p.status, p.wait_limit_ns)) break;
-        phases ^= 1u << stage;
-        uint8_t* sb = smem + stage * C::STAGE;
-        const int left = t.rows - (t.steps - 1) * 64;
-        const int end = (left + 15) / 16 * 16;  // rows of 128 bytes in each of four boxes
-        for (int v = left * 8 + lane; v < end * 8; v += 32)
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ---------------------------------------------------------- MMA issuer
+        const bool leader = elect_one();
+        const uint64_t dm = M_MN ? sdesc_mn(smem_u32(smem)) : sdesc_sw128(smem_u32(smem));
+        const uint64_t dn = MODE == kGradW ? sdesc_mn(smem_u32(smem) + C::TILE)
+                                           : sdesc_sw128(smem_u32(smem) + C::TILE);
+        // 16 of the summed dimension: 32 bytes of a row, or 16 rows of 128 bytes
+        constexpr uint32_t AM = M_MN ? 2048 : 32, AN = MODE == kGradW ? 2048 : 32;
+        int stage = 0, parts = 0, e_lo = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int q = first; ok && q < total; q += step) {
+          const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+          const uint32_t idesc = p.idesc | static_cast<uint32_t>(t.n >> 3) << 17;
+          uint32_t buf = 0;
+          for (int i = 0; i < t.steps; ++i) {
+            if (i % SEG == 0) {
+              buf = parts & 1;
+              if (!mbar_wait(&acc_empty[buf], (parts >> 1 & 1) ^ 1u, abort_flag, p.status,
+                             p.wait_limit_ns)) {
+                ok = false;
+                break;
+              }
+              ++parts;
+            }
+            if (!mbar_wait(&full[stage], phase, abort_flag, p.status, p.wait_limit_ns)) {
+              ok = false;
+              break;
+            }
+            if (MODE == kGradW && t.ragged_at(i)) fence_cluster();  // the tail warps' zeros
+            tc_fence_after();
+            const uint64_t cm = sdesc_at(dm, stage * C::STAGE), cn = sdesc_at(dn, stage * C::STAGE);
+            // sixteens of the last stage that hold nothing are left out
+            const int left = (MODE == kGradW ? t.rows : p.sum) - i * 64;
+            if (leader) {
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-            *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
-        fence_async_shared();
+              for (int c = 0; c < 4; ++c)
+                if (16 * c < left)
+                  mma_f16_pair(tmem + buf * 256, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
+                               (i % SEG != 0 || c != 0) ? 1u : 0u);
+              tc_commit_pair(&empty[stage]);
+              if (i % SEG == SEG - 1 || i == t.steps - 1) tc_commit_pair(&acc_full[buf]);
+            }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+          }
+        }
+        // every MMA issued so far must finish before tensor memory is released
+        if (leader) tc_commit_pair(drain);
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(&full[stage], 0);
-        __syncwarp();
+        mbar_drain(drain, 0);
+      }
+      __syncwarp();
+    } else if (MODE == kGradW && warp == 2) {
+      {
+        // ---------------------------------------------------------- tail warp
+        // in an expert's last stage the rows past its end become zeros, up to the
+        // sixteen that are read; the other stages go from the copies to the MMAs
+        int at = 0, e_lo = 0;
+        uint32_t phases = 0;  // a bit for each stage's barrier
+        for (int q = first; q < total; q += step) {
+          const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
+          at = (at + t.steps) % STAGES;
+          if (!t.ragged_at(t.steps - 1)) continue;
+          const int stage = (at + STAGES - 1) % STAGES;
+          if (!mbar_wait(&tail[stage], phases >> stage & 1u, abort_flag, p.status, p.wait_limit_ns)) break;
+          phases ^= 1u << stage;
+          uint8_t* sb = smem + stage * C::STAGE;
+          const int left = t.rows - (t.steps - 1) * 64;
+          const int end = (left + 15) / 16 * 16;  // rows of 128 bytes in each of four boxes
+          for (int v = left * 8 + lane; v < end * 8; v += 32)
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+              *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(&full[stage], 0);
+          __syncwarp();
+        }
       }
     }
-  }
   } else {
     // -------------------------------------------------------------- epilogue
     if (FOLD) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::MANY_REGS));
