@@ -5,7 +5,9 @@
  * shared expert included) and the dense NVFP4 linear with a measured-amax
  * scale (megamoe_linear_nvfp4); and the scored router and the MXFP4 operators
  * (megamoe_router_scored_topk, megamoe_quantize_mxfp4, megamoe_linear_mxfp4,
- * megamoe_forward_mxfp4 and their companions, at the end of this file).
+ * megamoe_forward_mxfp4 and their companions), the experts' operators in 16 bits
+ * with their gradients (megamoe_grouped_linear and its companions) and the linear
+ * in 8-bit integers (megamoe_linear_int8), at the end of this file.
  *
  * What it computes (sources are the titles and sections of the pages the
  * method is taken from):

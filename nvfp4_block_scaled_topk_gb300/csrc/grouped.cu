@@ -228,8 +228,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   // its size, always towards zero.  For fp32 results the sum is taken in parts of
   // SEG stages, and the epilogue adds the parts up in registers, rounding to nearest.
   // (16384 rows of eight experts, 7168 x 2048: 287 us so, 280 in one part, 255 with
-  // bf16 results, half the bytes to store.)  A 16-bit result is rounded to 2^-9 or
-  // 2^-12 of its size and takes one part.
+  // bf16 results, half the bytes to store.)  A 16-bit result is rounded to 2^-8 or
+  // 2^-11 of its size and takes one part.
   constexpr bool FOLD = sizeof(O) == 4;
   constexpr int SEG = FOLD ? 8 : 1 << 30;
   extern __shared__ uint8_t smem_raw[];

@@ -30,7 +30,11 @@ namespace megamoe {
 namespace {
 
 // ---------------------------------------------------------------------------
-// Quantisation of tokens: a block a row
+// Quantisation of tokens: a block a row, which it holds between the search for the
+// largest magnitude and the rounding (rows past 8192 elements are read again).  8192 x
+// 7168 bf16 take 37 us, 117 MB read and 117 written as fp16 (62 % of DRAM, 56 % of the
+// issue slots, the barrier between the two in the way of the rest); 51 us with halves
+// decided by a comparison, which many rows have hundreds of.
 // ---------------------------------------------------------------------------
 constexpr int kQuantThreads = 256;
 constexpr int kHeld = 4;  // eights of elements a thread keeps between the two passes
@@ -289,6 +293,14 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_widen(const Int8Quant p)
 // sum.  Bound by the weights' bytes and by the launch; the first of a block's
 // weights are on their way to L2 before the kernel ahead is done (they are the
 // caller's constants).
+//
+// us (K -> N; dots / MMA / pairs of CTAs, the last two with the quantiser before them):
+//              1 token      4 tokens     8 tokens     16 tokens
+//   1536 24576  9.4 / 14.1  11.3 / 14.2  14.1 / 24.2  18.3 / 22.9
+//   7168  7168 11.6 / 18.6  15.9 / 18.9  18.8 / 29.9  22.5 / 22.3
+//   7168  2048  7.3 / 11.1  10.5 / 11.9  12.2 / 15.6  13.8 / 14.1
+//   4096  4096  5.3 /  8.4   7.5 /  8.3   8.4 / 15.5  11.4 / 13.4
+// 1536 -> 24576 are 37.7 MB, 5.6 us at the copy rate; 7.3 us in a stream of calls.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
 constexpr int kFewWarps = kFewThreads / 32;
@@ -589,7 +601,12 @@ cudaError_t launch_few(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
 }
 
 // ---------------------------------------------------------------------------
-// The product on pairs of CTAs
+// The product on pairs of CTAs: 256 features x up to 256 tokens a tile.  8192 x 7168
+// -> 2048 take 135 us (240 GFLOP: 1.78 PFLOP/s of fp16 MMAs, the tensor pipe 87 % busy;
+// a library's bf16 product takes 133 on operands of twice the bytes), of 256 tiles in
+// four turns of the 76 pairs.  Handing a stage of widened weights to the other CTA by a
+// releasing arrival took 310 us: the tensor-memory stores have been waited for, and
+// tcgen05's own fences order them.
 // ---------------------------------------------------------------------------
 struct Int8Maps {
   CUtensorMap w, x;
@@ -1039,6 +1056,8 @@ static int64_t few_blocks(int64_t N) {
 }
 
 cudaError_t launch_int8_dots(const Int8Quant& q, const Int8Product& g, cudaStream_t stream) {
+  // Four rows at a time where a warp has three or more (1536 -> 24576: 9.4 us, 17.5 a
+  // row at a time), else one (7168 -> 2048, four tokens: 10.5 us, 13.1 four at a time).
   const int64_t blocks = few_blocks(g.N);
   const Int8Few a = few_of(q, g);
   return g.N > 2 * blocks * kFewWarps ? launch_dots_t<4>(a, blocks, stream)
@@ -1058,7 +1077,9 @@ Int8Plan int8_plan(int64_t T, int N, int K) {
   const int64_t nt = (T + 255) / 256;
   p.per = static_cast<int>(((T + nt - 1) / nt + 15) / 16 * 16);
   p.tiles = (T + p.per - 1) / p.per * ((N + 255) / 256);
-  // shares of at least two steps where pairs would idle
+  // Shares of at least two steps where pairs would idle, added up by a kernel of their
+  // own (us, whole / shared): 7168 -> 2048 at 64 tokens 31.2 / 15.4, 256 41.1 / 20.3,
+  // 512 42.0 / 24.1; 1552 -> 2056 at 64 tokens 13.1 / 11.9, 256 17.9 / 16.0.
   const int64_t steps = (K + 127) / 128;
   p.split = static_cast<int>(std::max<int64_t>(1, std::min({kInt8Pairs / p.tiles, steps / 2, int64_t{16}})));
   return p;

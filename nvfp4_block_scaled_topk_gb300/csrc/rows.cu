@@ -1,7 +1,14 @@
 // Around the 16-bit grouped products: the gated activation between an expert's
 // two products and the movement of rows between token and expert order, each
-// with its gradient.  All are bound by their bytes (or, with few rows, by the
-// launch); sums are fp32 in ascending slot order, one rounding at the end.
+// with its gradient.  Sums are fp32 in ascending slot order, one rounding at the end.
+//
+// All are bound by their bytes, or with few rows by the launch (1.5 us for the
+// activation of 48 rows, 2.1 for the sums of eight tokens, in a stream of calls).  At
+// the copy rate / measured, us: gradient of the activation, 49152 x 2048, 148.6 / 149.7;
+// 2003 tokens of 7168 into 11777 rows 29.2 / 33.2; their sums 29.7 / 38.5; gradient of
+// the sums of 8192 tokens 221 / 230.  8192 tokens (117 MB) into 49152 rows take 181 us
+// where 121 are needed: the experts' rows come to each token six times, and it has left
+// L2 in between.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -50,7 +57,8 @@ __device__ __forceinline__ void sigmoid(float g, float* s, float* rest) {
   *rest = g >= 0.f ? er : r;
 }
 
-// 16 bytes (eight elements) a thread and step; vectors of all rows in one line.
+// 16 bytes (eight elements) a thread and step; vectors of all rows in one line, so
+// that short rows leave no lane idle.
 template <typename X, bool BACKWARD>
 __global__ void __launch_bounds__(256) k_silu(const Silu p) {
   pdl_wait();
@@ -95,7 +103,8 @@ __global__ void __launch_bounds__(256) k_silu(const Silu p) {
   }
 }
 
-// A warp copies 2 KB of a row at a time.
+// A warp copies 2 KB of a row at a time, four loads in flight; streaming stores, which
+// leave the tokens in L2 for the next expert that wants them (36.1 us without, 33.6).
 __global__ void __launch_bounds__(256) k_gather_rows(const uint16_t* __restrict__ x, int64_t T,
                                                      int vecs, int64_t ld_x,
                                                      const int32_t* __restrict__ row_src,
@@ -184,7 +193,9 @@ __global__ void __launch_bounds__(256, 4) k_combine_rows(const CombineRows p, in
 
 // A block takes a token: its gradient is read once, each slot's row of y gives a
 // share of that slot's weight's gradient and its place takes w grad.  The shares
-// are summed lane by lane, then over the warps in order.
+// are summed lane by lane, then over the warps in order.  Four blocks an SM keep
+// enough loads in flight (8192 tokens of six slots, 7168: 260 us with two, 236);
+// streaming stores took 345.
 template <typename X, int K>
 __global__ void __launch_bounds__(256, K <= 8 ? 4 : 2) k_combine_rows_grad(const CombineRows p) {
   pdl_wait();

@@ -314,10 +314,9 @@ def test_layer_and_gradients(cuda_lib):
         Y.append(torch.einsum("ti,tdi->td", H, W2[e]) * TW[:, j:j + 1])
     OUT = torch.stack(Y).sum(0)
     OUT.backward(go.double())
-    # every bf16 intermediate is off by 2^-9 of itself at most (half a step, and at
-    # most that of its size); six of them lie between an input and the furthest
-    # gradient, their errors independent of sign: six such shares of the norm bound
-    # the whole's
+    # every bf16 intermediate is off by 2^-8 of itself at most (half a step); six of
+    # them lie between an input and the furthest gradient: six such shares of the norm
+    # bound the whole's
     for got, want in ((out, OUT), (gx, X.grad), (gw13, W13.grad), (gw2, W2.grad), (glogits, L.grad)):
         want = want.detach()
         rel = (got.double() - want).norm() / want.norm()
