@@ -308,3 +308,39 @@ def test_one_row_of_any_stride(cuda_lib):
     weight = megamoe.Int8LinearWeights.quantize(w[0])
     assert torch.equal(megamoe.linear_int8(odd, weight)[0], megamoe.linear_int8(flat, weight)[0])
     assert torch.equal(megamoe.silu_mul(odd), megamoe.silu_mul(flat))
+
+
+def test_as_many_experts_as_there_may_be(cuda_lib):
+    x, gr, w, off = _case(1024, 4, 64, 72, seed=6)
+    dev = off.int().cuda()
+    y = megamoe.grouped_linear(x, w, dev, out_dtype=torch.float32)
+    gx, gw = megamoe.grouped_linear_backward(gr, x, w, dev)
+    e = torch.repeat_interleave(torch.arange(1024), off[1:] - off[:-1]).cuda()
+    p, q, g = x.double(), w.double()[e], gr.double()
+    _within(y, torch.einsum("rk,rnk->rn", p, q), 6 * U * torch.einsum("rk,rnk->rn", p.abs(), q.abs()))
+    _within(gx, torch.einsum("rn,rnk->rk", g, q), 7 * U * torch.einsum("rn,rnk->rk", g.abs(), q.abs()))
+    outer = g.unsqueeze(2) * p.unsqueeze(1)
+    want = torch.zeros((1024, 72, 64), dtype=torch.float64, device="cuda").index_add_(0, e, outer)
+    most = torch.zeros_like(want).index_add_(0, e, outer.abs())
+    _within(gw, want, 3 * U * most)
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float16])
+def test_ends_of_the_types(cuda_lib, dtype):
+    """Subnormal and the largest operands, one product a sum: exact before the rounding."""
+    f = torch.finfo(dtype)
+    tiny = f.smallest_normal * f.eps
+    a = torch.tensor([tiny, 3 * tiny, f.smallest_normal, 1.0, f.max, -tiny, 0.5, -f.max],
+                     dtype=torch.float64)
+    K = N = 64
+    x = torch.zeros((len(a), K), dtype=torch.float64)
+    x[torch.arange(len(a)), torch.arange(len(a))] = a
+    w = torch.zeros((1, N, K), dtype=torch.float64)
+    for i, v in enumerate(a):
+        w[0, i] = v  # row i of w: the same value everywhere
+    x, w = x.to(dtype).cuda(), w.to(dtype).cuda()
+    off = torch.tensor([0, len(a)], dtype=torch.int32, device="cuda")
+    want = (x.double() @ w[0].double().t()).float()  # products of two are exact in 64 bits
+    got = megamoe.grouped_linear(x, w, off, out_dtype=torch.float32)
+    # fp32's own subnormals may be lost: below 2^-126
+    assert ((got == want) | ((want.abs() < 2.0 ** -126) & (got.abs() < 2.0 ** -126))).all()
