@@ -767,8 +767,8 @@ megamoe_status megamoe_forward_mxfp4_from_logits(
  *            expert are left as they are
  *   status   device status word or null: MEGAMOE_DEV_BAD_OFFSETS where an expert's
  *            rows are not all inside the matrix (those outside are left out)
- * An expert's product does not depend on other experts' rows, on rows of no expert
- * or on the order of the launch.
+ * Values of other experts' rows and of rows of no expert have no part in an expert's
+ * product; the order of its sums is fixed by the call's sizes.
  * Requires K and N multiples of 8, 1 <= E <= 1024, rows < 2^31, pointers 16-byte
  * and rows 16-byte aligned.
  */

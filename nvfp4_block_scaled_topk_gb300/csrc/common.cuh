@@ -276,7 +276,7 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
-// Every thread of both CTAs; orders what came before it in either.
+// Every thread of the cluster's CTAs; orders what came before it in any.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                    : "memory");
@@ -371,12 +371,13 @@ __device__ __forceinline__ void tc_copy_atom_pair(uint32_t taddr, uint64_t desc)
   asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc)
                : "memory");
 }
-// tc_commit to the barrier at the same place in both CTAs.
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar) {
+// tc_commit to the barrier at the same place in both CTAs, whose ranks in the cluster
+// are `first` and the next.
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, uint32_t first = 0) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
       "[%0], %1;" ::"r"(smem_u32(bar)),
-      "h"(static_cast<uint16_t>(3))
+      "h"(static_cast<uint16_t>(3u << first))
       : "memory");
 }
 

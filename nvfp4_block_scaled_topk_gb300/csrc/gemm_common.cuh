@@ -82,6 +82,20 @@ constexpr int kEpiPartial2 = 17;
 // Token-major tiles with MXFP4 operands, SiLU * up quantised to MXFP4.
 constexpr int kEpiMxSilu = 18;
 
+// Boxes for the rows of one CTA's part of a tile, `part` of which `rows` are there: of
+// 32 rows (128 bytes each) whole, or, where the part is 16 at most, of 8 for the rows
+// that there are.  Rows past the matrix's end load slowly (an 8-bit linear of 17 tokens
+// took 25.3 us with one box of 32, 18.7 so, 19 at 32 tokens); a tile with boxes of both
+// sizes does, too (1000 rows, 7168 -> 512: 37.4 us against 35.4).
+struct RowBoxes {
+  int large, small;
+  __device__ RowBoxes(int rows, int part) {
+    large = part > 16 ? (part + 31) / 32 : 0;
+    small = part > 16 ? 0 : (max(min(rows, part), 0) + 7) / 8;
+  }
+  __device__ int bytes() const { return large * 4096 + small * 1024; }
+};
+
 struct TileInfo {
   int e, mt, nt, ntiles;  // expert, feature tile, token tile, token tiles of e
 };

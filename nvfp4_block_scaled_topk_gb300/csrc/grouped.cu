@@ -59,6 +59,7 @@ enum Mode { kForward, kGradX, kGradW };
 
 struct GroupedMaps {
   CUtensorMap m, n;  // the MMA's M and N side
+  CUtensorMap n8;    // forward, grad_x: the N side in boxes of 8 rows (n: of 32)
 };
 
 struct GroupedArgs {
@@ -72,6 +73,7 @@ struct GroupedArgs {
   void* out;
   int64_t ld_out;
   uint32_t idesc;  // instruction descriptor without N
+  int split;       // pairs that share a tile's sum (SPLIT)
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -170,6 +172,30 @@ __device__ void build_tables(const GroupedArgs& p, int MT, Range* s_range, int* 
   __syncthreads();
 }
 
+// Four floats at the same place in CTA `rank` of the cluster.
+__device__ __forceinline__ float4 load_cluster4(const float* p, uint32_t rank) {
+  float4 v;
+  asm volatile(
+      "{\n\t.reg .b32 a;\n\t"
+      "mapa.shared::cluster.u32 a, %4, %5;\n\t"
+      "ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n\t}"
+      : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+      : "r"(smem_u32(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+__device__ __forceinline__ void store4(__half* p, float4 v) {
+  const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+  *reinterpret_cast<uint2*>(p) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                            *reinterpret_cast<const uint32_t*>(&b));
+}
+
 // A tile as every role sees it.
 struct Tile {
   int e;
@@ -180,6 +206,8 @@ struct Tile {
   int n;      // the MMA's N
   int steps;  // stages of the sum
   // grad_w: a stage whose last sixteen rows are not all the expert's
+  // the first stage of a share of the sum
+  __device__ int first(int share, int of) const { return of == 1 ? share * steps : share * steps / of; }
   __device__ bool ragged_at(int i) const { return i == steps - 1 && (rows & 15) != 0; }
   bool again;  // the weights are read by other tiles, too
 };
@@ -217,8 +245,9 @@ __device__ __forceinline__ Tile decode(const GroupedArgs& p, int q, const Range*
 
 __device__ __forceinline__ void store_rounded(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_rounded(float v, __half* p) { *p = __float2half_rn(v); }
-template <Mode MODE, typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+// SPLIT: a cluster of p.split pairs shares a tile's sum, and has one tile at most.
+template <Mode MODE, typename O, bool SPLIT>
+__global__ void __launch_bounds__(Cfg::THREADS, 1)
     k_grouped_pair(const __grid_constant__ GroupedMaps maps, const GroupedArgs p) {
   using C = Cfg;
   constexpr int STAGES = C::STAGES;
@@ -248,12 +277,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   __shared__ int s_scan[C::THREADS / 32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_rank());
+  // this CTA in its pair, the pair's first CTA in the cluster, this pair's share
+  const uint32_t in_cluster = cluster_rank(), head = SPLIT ? in_cluster & ~1u : 0u;
+  const int rank = static_cast<int>(in_cluster & 1u);
+  const int split = SPLIT ? p.split : 1, share = SPLIT ? static_cast<int>(in_cluster >> 1) : 0;
   const int MT = (p.F + 255) / 256, NT = MODE == kGradW ? (p.G + 255) / 256 : 1;
 
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&maps.m);
     prefetch_tensormap(&maps.n);
+    if (MODE != kGradW) prefetch_tensormap(&maps.n8);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -278,8 +311,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   pdl_wait();
   pdl_trigger();
   build_tables(p, MT, s_range, s_toff, s_scan);
-  const int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
-  const int first = blockIdx.x >> 1, step = gridDim.x >> 1;  // tiles of this pair
+  int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
+  const int step = gridDim.x / (2 * split), first = blockIdx.x / (2 * split);  // tiles of this pair
+  if (SPLIT && total > step) {  // experts' rows overlap: there are more than any that do not have
+    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, MEGAMOE_DEV_BAD_OFFSETS);
+    total = step;
+  }
 
   if (warp < 4) {
     if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW_REGS));
@@ -294,10 +331,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       for (int q = first; ok && q < total; q += step) {
         const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
         const int m0 = t.m0 + rank * 128;
-        const int boxes = (t.n / 2 + 31) / 32;  // of 32 rows: this CTA's half of N
-        const int r0 = t.n0 + rank * (t.n / 2);
+        // forward, grad_x: a CTA has half of N
+        const int half = t.n / 2, r0 = t.n0 + rank * half;
+        const RowBoxes mine(t.rows - rank * half, half), other(t.rows - (1 - rank) * half, half);
         const uint64_t pol_m = t.again ? pol_again : pol_once;
-        for (int i = 0; i < t.steps; ++i) {
+        for (int i = t.first(share, split); i < t.first(share + 1, split); ++i) {
           if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
             break;
@@ -307,30 +345,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
           if (leader) {
             const bool ragged = MODE == kGradW && t.ragged_at(i);
             if (rank == 0 && !ragged) {
-              mbar_arrive_expect_tx(&full[stage], 2 * (C::TILE + (MODE == kGradW ? C::TILE : boxes * 4096)));
+              mbar_arrive_expect_tx(&full[stage], 2 * C::TILE + (MODE == kGradW ? 2 * C::TILE
+                                                                            : mine.bytes() + other.bytes()));
               mbar_arrive(&full[stage]);
             }
             if (MODE == kGradW) {
               const int r = t.start + i * 64, n0 = t.n0 + rank * 128;
-              uint32_t bar = cluster_address(&full[stage], 0);
+              uint32_t bar = cluster_address(&full[stage], head);
               if (ragged) {
                 mbar_arrive_expect_tx(&tail[stage], C::STAGE);
-                bar = cluster_address(&tail[stage], rank);
+                bar = cluster_address(&tail[stage], head + rank);
               }
               tma_load_2d_pair(sm, &maps.m, bar, m0, r, pol_again);
               tma_load_2d_pair(sm + 8192, &maps.m, bar, m0 + 64, r, pol_again);
               tma_load_2d_pair(sn, &maps.n, bar, n0, r, pol_again);
               tma_load_2d_pair(sn + 8192, &maps.n, bar, n0 + 64, r, pol_again);
             } else {
-              const uint32_t bar = cluster_address(&full[stage], 0);
+              const uint32_t bar = cluster_address(&full[stage], head);
               if (M_MN) {
                 tma_load_3d_pair(sm, &maps.m, bar, m0, i * 64, t.e, pol_m);
                 tma_load_3d_pair(sm + 8192, &maps.m, bar, m0 + 64, i * 64, t.e, pol_m);
               } else {
                 tma_load_3d_pair(sm, &maps.m, bar, i * 64, m0, t.e, pol_m);
               }
-              for (int b = 0; b < boxes; ++b)
+              for (int b = 0; b < mine.large; ++b)
                 tma_load_2d_pair(sn + b * 4096, &maps.n, bar, i * 64, r0 + b * 32, pol_again);
+              for (int b = 0; b < mine.small; ++b)
+                tma_load_2d_pair(sn + b * 1024, &maps.n8, bar, i * 64, r0 + b * 8, pol_again);
             }
           }
           __syncwarp();
@@ -359,8 +400,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
           const Tile t = decode<MODE>(p, q, s_range, s_toff, MT, NT, &e_lo);
           const uint32_t idesc = p.idesc | static_cast<uint32_t>(t.n >> 3) << 17;
           uint32_t buf = 0;
-          for (int i = 0; i < t.steps; ++i) {
-            if (i % SEG == 0) {
+          const int i0 = t.first(share, split), i1 = t.first(share + 1, split);
+          for (int i = i0; i < i1; ++i) {
+            const int at = (i - i0) % SEG;  // in its part
+            if (at == 0) {
               buf = parts & 1;
               if (!mbar_wait(&acc_empty[buf], (parts >> 1 & 1) ^ 1u, abort_flag, p.status,
                              p.wait_limit_ns)) {
@@ -383,9 +426,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
               for (int c = 0; c < 4; ++c)
                 if (16 * c < left)
                   mma_f16_pair(tmem + buf * 256, sdesc_at(cm, AM * c), sdesc_at(cn, AN * c), idesc,
-                               (i % SEG != 0 || c != 0) ? 1u : 0u);
-              tc_commit_pair(&empty[stage]);
-              if (i % SEG == SEG - 1 || i == t.steps - 1) tc_commit_pair(&acc_full[buf]);
+                               (at != 0 || c != 0) ? 1u : 0u);
+              tc_commit_pair(&empty[stage], head);
+              if (at == SEG - 1 || i == i1 - 1) tc_commit_pair(&acc_full[buf], head);
             }
             __syncwarp();
             if (++stage == STAGES) {
@@ -395,7 +438,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
           }
         }
         // every MMA issued so far must finish before tensor memory is released
-        if (leader) tc_commit_pair(drain);
+        if (leader) tc_commit_pair(drain, head);
         __syncwarp();
         mbar_drain(drain, 0);
       }
@@ -423,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
               *reinterpret_cast<uint4*>(sb + b * 8192 + v * 16) = make_uint4(0, 0, 0, 0);
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(&full[stage], 0);
+          if (lane == 0) mbar_arrive_cluster(&full[stage], head);
           __syncwarp();
         }
       }
@@ -451,7 +494,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       auto let_go = [&](uint32_t buf) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], 0);
+        if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], head);
       };
       float sum[FOLD ? 4 : 1][32];
       if (FOLD) {  // the parts, and the accumulator's back before anything is stored
@@ -459,7 +502,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         for (int c = 0; c < 4 * FOLD; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j) sum[c][j] = 0.f;
-        for (int i = 0; i < t.steps; i += SEG, ++parts) {
+        for (int i = t.first(share, split); i < t.first(share + 1, split); i += SEG, ++parts) {
           const uint32_t buf = parts & 1;
           if (!mbar_wait(&acc_full[buf], parts >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
@@ -483,7 +526,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         tc_fence_after();
       }
       if (!ok) break;
-      if constexpr (FOLD) {
+      if constexpr (SPLIT) {
+        // this pair's share of the sums, fp32 [rows][128 features], where the stages were
+        float* to = reinterpret_cast<float*>(smem) + quarter * 32 + lane;
+        const uint32_t buf = parts & 1;
+        const uint32_t base = tmem + buf * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (chunk_of(c) >= chunks) continue;
+          float v[32];
+          if constexpr (FOLD) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = sum[c][j];
+          } else {
+            uint32_t u[32];
+            tmem_ld_32x32b_x32(base + 32 * chunk_of(c), u);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < 32; ++j) to[(32 * chunk_of(c) + j) * 128] = v[j];
+        }
+        if (!FOLD) let_go(buf);
+      } else if constexpr (FOLD) {
         // fp32: 32 features of a row are 128 bytes as they lie
         if (m + lane < p.F) {
 #pragma unroll
@@ -534,20 +600,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     __syncwarp();
   }
   __syncthreads();
-  // rank 0's commits arrive on rank 1's barriers too: none is on its way after the last
+  if constexpr (SPLIT) {
+    // Each pair adds up its share of the tile's rows over the cluster, in the pairs'
+    // order; a CTA its 128 features, a warp a row at a time.
+    cluster_sync();  // all shares are there
+    if (first < total) {
+      int e_lo = 0;
+      const Tile t = decode<MODE>(p, first, s_range, s_toff, MT, NT, &e_lo);
+      const int m = t.m0 + rank * 128 + lane * 4;
+      const int end = (share + 1) * t.rows / split;
+      for (int r = share * t.rows / split + warp; r < end; r += C::THREADS / 32) {
+        const float* from = reinterpret_cast<const float*>(smem) + r * 128 + lane * 4;
+        float4 sum = load_cluster4(from, rank);
+        for (int s = 1; s < split; ++s) {
+          const float4 v = load_cluster4(from, 2 * s + rank);
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+        if (m < p.F) store4(static_cast<O*>(p.out) + (t.n0 + static_cast<int64_t>(r)) * p.ld_out + m, sum);
+      }
+    }
+  }
+  // the first CTA's commits arrive on the other's barriers too: none is on its way after
+  // the last
   if (warp == 1) mbar_drain(drain, 0);
   __syncwarp();
-  cluster_sync();  // neither CTA leaves while the other still reaches into it
+  cluster_sync();  // no CTA leaves while another still reaches into it
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
 }
 
-template <Mode MODE, typename O>
+template <Mode MODE, typename O, bool SPLIT>
 cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t tiles,
                          cudaStream_t stream) {
-  auto kern = k_grouped_pair<MODE, O>;
+  auto kern = k_grouped_pair<MODE, O, SPLIT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
   if (sizeof(O) == 4) {
@@ -561,17 +651,49 @@ cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t 
       fits.store(true, std::memory_order_relaxed);
     }
   }
-  const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
-  return launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
-                    stream, maps, a);
+  const int64_t pairs = SPLIT ? tiles * a.split : std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
+  return launch_pdl_cluster(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM,
+                            SPLIT ? 2 * a.split : 2, stream, maps, a);
+}
+
+// Pairs that share a tile's sum, where the others would idle.  Clusters of 4, 6 and 8
+// CTAs of which each fills an SM fit the GPU 36, 23 and 15 times; the exchange and the
+// sums over the cluster cost about eight stages, and some five more for 256 rows.
+// Whole / shared, us: 8 rows, one expert of 7168 -> 2048 (8 tiles) 29.7 / 14.6, -> 4096
+// 29.8 / 17.9, -> 7168 (28 tiles) 30.1 / 23.5; 64 rows of 4096 -> 4096 19.4 / 14.0; 1000
+// rows of 7168 -> 512 35.4 / 19.6; 64 rows of eight of 2048 -> 1024 12.2 / 11.5.
+int share_sum(const GroupedArgs& a, int64_t tiles) {
+  static constexpr int kMost[] = {0, 0, 34, 22, 14};  // tiles, by pairs
+  const double steps = (a.sum + 63) / 64, rows = std::min(256.0, static_cast<double>(a.rows) / a.E);
+  int best = 1;
+  double least = steps;
+  for (int s = 2; s <= 4; ++s) {
+    const double cost = steps / s + 8 + rows / 50;
+    if (tiles <= kMost[s] && cost < least) {
+      best = s;
+      least = cost;
+    }
+  }
+  return best;
+}
+
+template <Mode MODE, typename O>
+cudaError_t launch_shared(const GroupedMaps& maps, GroupedArgs a, int64_t tiles, cudaStream_t stream) {
+  a.split = 1;
+  if constexpr (MODE != kGradW) {
+    a.split = share_sum(a, tiles);
+    if (a.split > 1) return launch_typed<MODE, O, true>(maps, a, tiles, stream);
+  }
+  return launch_typed<MODE, O, false>(maps, a, tiles, stream);
 }
 
 template <Mode MODE>
 cudaError_t launch_mode(const GroupedMaps& maps, const GroupedArgs& a, int out_type, int64_t tiles,
                         cudaStream_t stream) {
-  if (out_type == MEGAMOE_TYPE_F32) return launch_typed<MODE, float>(maps, a, tiles, stream);
-  if (out_type == MEGAMOE_TYPE_F16) return launch_typed<MODE, __half>(maps, a, tiles, stream);
-  return launch_typed<MODE, __nv_bfloat16>(maps, a, tiles, stream);
+  if constexpr (MODE != kGradX)
+    if (out_type == MEGAMOE_TYPE_F32) return launch_shared<MODE, float>(maps, a, tiles, stream);
+  if (out_type == MEGAMOE_TYPE_F16) return launch_shared<MODE, __half>(maps, a, tiles, stream);
+  return launch_shared<MODE, __nv_bfloat16>(maps, a, tiles, stream);
 }
 
 // [E, N, K] weights, boxes of 64 x `rows`.
@@ -610,7 +732,8 @@ cudaError_t launch_grouped_forward(const Grouped& g, void* out, int out_type, in
                                    cudaStream_t stream) {
   if (g.rows == 0) return cudaSuccess;
   GroupedMaps maps;
-  if (!weight_map(&maps.m, g, 128) || !rows_map(&maps.n, g.x, g.K, g.rows, g.ld_x, 32))
+  if (!weight_map(&maps.m, g, 128) || !rows_map(&maps.n, g.x, g.K, g.rows, g.ld_x, 32) ||
+      !rows_map(&maps.n8, g.x, g.K, g.rows, g.ld_x, 8))
     return cudaErrorInvalidValue;
   GroupedArgs a = args_of(g);
   a.F = g.N;
@@ -624,7 +747,8 @@ cudaError_t launch_grouped_forward(const Grouped& g, void* out, int out_type, in
 cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, cudaStream_t stream) {
   if (g.rows == 0) return cudaSuccess;
   GroupedMaps maps;
-  if (!weight_map(&maps.m, g, 64) || !rows_map(&maps.n, g.grad, g.N, g.rows, g.ld_grad, 32))
+  if (!weight_map(&maps.m, g, 64) || !rows_map(&maps.n, g.grad, g.N, g.rows, g.ld_grad, 32) ||
+      !rows_map(&maps.n8, g.grad, g.N, g.rows, g.ld_grad, 8))
     return cudaErrorInvalidValue;
   GroupedArgs a = args_of(g);
   a.F = g.K;
@@ -633,8 +757,7 @@ cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, c
   a.ld_out = ld_out;
   a.idesc = idesc_f16(g.type, true, false);
   const int64_t tiles = grouped_tiles(g.rows, g.E, g.K);
-  return g.type == MEGAMOE_TYPE_F16 ? launch_typed<kGradX, __half>(maps, a, tiles, stream)
-                                    : launch_typed<kGradX, __nv_bfloat16>(maps, a, tiles, stream);
+  return launch_mode<kGradX>(maps, a, g.type, tiles, stream);
 }
 
 cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream) {
@@ -651,6 +774,7 @@ cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cud
   if (!rows_map(&maps.m, g.x, g.K, g.rows, g.ld_x, 64) ||
       !rows_map(&maps.n, g.grad, g.N, g.rows, g.ld_grad, 64))
     return cudaErrorInvalidValue;
+  maps.n8 = maps.n;  // not used
   const int64_t tiles = static_cast<int64_t>(g.E) * ((g.N + 255) / 256) * ((g.K + 255) / 256);
   return launch_mode<kGradW>(maps, a, out_type, tiles, stream);
 }

@@ -609,7 +609,7 @@ cudaError_t launch_few(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
 // tcgen05's own fences order them.
 // ---------------------------------------------------------------------------
 struct Int8Maps {
-  CUtensorMap w, x;
+  CUtensorMap w, x, x8;  // tokens in boxes of 32 and of 8
 };
 
 struct Int8Args {
@@ -722,6 +722,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&maps.w);
     prefetch_tensormap(&maps.x);
+    prefetch_tensormap(&maps.x8);
   }
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -761,7 +762,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     for (int q = first; ok && q < total; q += step) {
       const Item it = int8_item(q, p.split, MT, NT, KT);
       const int rows = min(p.per, p.T - it.nt * p.per), half = (rows + 15) / 16 * 8;
-      const int boxes = (half + 31) / 32, t0 = it.nt * p.per + rank * half;
+      const RowBoxes mine(rows - rank * half, half), other(rows - (1 - rank) * half, half);
+      const int t0 = it.nt * p.per + rank * half;
       const int m0 = it.mt * 256 + rank * 128;
       for (int i = it.k0; i < it.k1; ++i) {
         if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
@@ -773,12 +775,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         if (leader) {
           mbar_arrive_expect_tx(&w_full[stage], C::W);
           tma_load_2d(sw, &maps.w, &w_full[stage], i * 128, m0, pol_w);
-          if (rank == 0) mbar_arrive_expect_tx(&x_full[stage], 4 * boxes * 4096);
+          if (rank == 0) mbar_arrive_expect_tx(&x_full[stage], 2 * (mine.bytes() + other.bytes()));
           const uint32_t bar = cluster_address(&x_full[stage], 0);
-          for (int h = 0; h < 2; ++h)
-            for (int b = 0; b < boxes; ++b)
+          for (int h = 0; h < 2; ++h) {
+            for (int b = 0; b < mine.large; ++b)
               tma_load_2d_pair(sx + h * C::X + b * 4096, &maps.x, bar, i * 128 + h * 64,
                                t0 + b * 32, pol_x);
+            for (int b = 0; b < mine.small; ++b)
+              tma_load_2d_pair(sx + h * C::X + b * 1024, &maps.x8, bar, i * 128 + h * 64, t0 + b * 8,
+                               pol_x);
+          }
         }
         __syncwarp();
         ++issued;
@@ -1091,7 +1097,9 @@ cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {
   if (!make_map(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.w, g.K, g.N, g.K, 128, 128,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_map(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.x, g.K, g.T,
-                static_cast<uint64_t>(g.K) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B))
+                static_cast<uint64_t>(g.K) * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_map(&maps.x8, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.x, g.K, g.T,
+                static_cast<uint64_t>(g.K) * 2, 64, 8, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   const Int8Plan plan = int8_plan(g.T, g.N, g.K);
   const Int8Args a{g.x_scales, g.w_scales, static_cast<int>(g.T), g.N, g.K, plan.per, plan.split,

@@ -344,3 +344,55 @@ def test_ends_of_the_types(cuda_lib, dtype):
     got = megamoe.grouped_linear(x, w, off, out_dtype=torch.float32)
     # fp32's own subnormals may be lost: below 2^-126
     assert ((got == want) | ((want.abs() < 2.0 ** -126) & (got.abs() < 2.0 ** -126))).all()
+
+
+# few tiles, whose sums two, three or four pairs of CTAs share; rows that end inside a
+# part, a share of a row or none for some of them, an expert without rows
+@pytest.mark.parametrize("counts", [[1], [0, 7, 0], [200], [30, 0, 3]])
+@pytest.mark.parametrize("K,N", [(2056, 1032), (2120, 2600), (1544, 5000), (4104, 8200)])
+@pytest.mark.parametrize("out", [torch.float16, torch.float32])
+def test_shared_sums(cuda_lib, counts, K, N, out):
+    g = torch.Generator(device="cuda").manual_seed(N)
+    c = torch.tensor(counts)
+    off = torch.cat([torch.zeros(1, dtype=torch.int64), c.cumsum(0)])
+    R = int(off[-1])
+    x = torch.randn((R + 2, K), generator=g, device="cuda").half()
+    x[R:] = float("nan")
+    w = (torch.randn((len(counts), N, K), generator=g, device="cuda") / 16).half()
+    gr = torch.randn((R + 2, K), generator=g, device="cuda").half()
+    gr[R:] = float("inf")
+    wt = w.transpose(1, 2).contiguous()  # [E, K, N]: grad_x of it is a product with w
+    dev = off.int().cuda()
+    y = torch.full((R + 2, N), 7.0, dtype=out, device="cuda")
+    megamoe.grouped_linear(x, w, dev, out_dtype=out, out=y)
+    gx = torch.full((R + 2, N), 7.0, dtype=torch.float16, device="cuda")
+    xn = torch.zeros((R + 2, N), dtype=torch.float16, device="cuda")
+    megamoe.grouped_linear_backward(gr, xn, wt, dev, need_w=False, grad_x=gx)
+    for e in range(len(counts)):
+        a, b = int(off[e]), int(off[e + 1])
+        q = w[e].double()
+        for got, p in ((y, x[a:b].double()), (gx, gr[a:b].double())):
+            _within(got[a:b], p @ q.t(), (K / 16 + 6) * U * (p.abs() @ q.abs().t()))
+    assert (y[R:] == 7).all() and (gx[R:] == 7).all()
+    again = megamoe.grouped_linear(x, w, dev, out_dtype=out)
+    assert torch.equal(again[:R], y[:R])
+
+
+@pytest.mark.parametrize("out", [BF, torch.float32])
+def test_shared_waits_that_run_out(cuda_lib, out):
+    x = torch.randn((8, 7168), device="cuda").to(BF)
+    w = torch.randn((1, 2048, 7168), device="cuda").to(BF)
+    off = torch.tensor([0, 8], dtype=torch.int32, device="cuda")
+    want = megamoe.grouped_linear(x, w, off, out_dtype=out)
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    megamoe.set_wait_limit_ns(100)
+    try:
+        megamoe.grouped_linear(x, w, off, out_dtype=out, status=status)
+        torch.cuda.synchronize()
+        assert int(status) == megamoe.DEV_TIMEOUT
+    finally:
+        megamoe.set_wait_limit_ns(0)
+    status.zero_()
+    assert torch.equal(megamoe.grouped_linear(x, w, off, out_dtype=out, status=status), want)
+    assert int(status) == 0
