@@ -1078,16 +1078,36 @@ cudaError_t launch_int8_few(const Int8Quant& q, const Int8Product& g, cudaStream
   return q.T <= 8 ? launch_few<1>(a, blocks, stream) : launch_few<2>(a, blocks, stream);
 }
 
+// Tokens of a tile and shares of its sum: those with which the pairs' turns take the
+// fewest cycles.  A step of 128 of K takes four cycles a token in the tensor pipe, or
+// what an SM takes in, 16 KB of weights and 128 bytes a token at some 48 bytes a cycle;
+// a tile's start and end about 3000; adding up shares a kernel of its own and 8 bytes of
+// each share's values through L2.  us, 256 tokens and one share / as chosen: 8192 x 7168
+// -> 2048 178 / 168 (224 tokens: four turns of 296 tiles, not of 256), 3000 85 / 74, 1024
+// 42 / 35 (two shares), 256 41 / 20, 64 31 / 15.
 Int8Plan int8_plan(int64_t T, int N, int K) {
-  Int8Plan p;
-  const int64_t nt = (T + 255) / 256;
-  p.per = static_cast<int>(((T + nt - 1) / nt + 15) / 16 * 16);
-  p.tiles = (T + p.per - 1) / p.per * ((N + 255) / 256);
-  // Shares of at least two steps where pairs would idle, added up by a kernel of their
-  // own (us, whole / shared): 7168 -> 2048 at 64 tokens 31.2 / 15.4, 256 41.1 / 20.3,
-  // 512 42.0 / 24.1; 1552 -> 2056 at 64 tokens 13.1 / 11.9, 256 17.9 / 16.0.
-  const int64_t steps = (K + 127) / 128;
-  p.split = static_cast<int>(std::max<int64_t>(1, std::min({kInt8Pairs / p.tiles, steps / 2, int64_t{16}})));
+  Int8Plan p{};
+  double least = 0;
+  const int64_t mt = (N + int64_t{255}) / 256, steps = (K + 127) / 128;
+  for (int most = 256; most >= 128; most -= 16) {
+    const int64_t nt = (T + most - 1) / most;
+    const int per = static_cast<int>(((T + nt - 1) / nt + 15) / 16 * 16);
+    const int64_t tiles = (T + per - 1) / per * mt;
+    const double step = std::max(4.0 * per, 341 + 2.67 * per);
+    // shares of at least two steps where pairs would idle
+    const int64_t shares = std::max<int64_t>(1, std::min({kInt8Pairs / tiles, steps / 2, int64_t{16}}));
+    for (int64_t split = 1; split <= shares; split += std::max<int64_t>(1, shares - 1)) {
+      const double turns = static_cast<double>((tiles * split + kInt8Pairs - 1) / kInt8Pairs);
+      double cost = turns * (static_cast<double>((steps + split - 1) / split) * step + 3000);
+      if (split > 1) cost += 4700 + static_cast<double>(split) * T * N * 8 / 2600;
+      if (p.per == 0 || cost < least * 0.98) {
+        least = cost;
+        p.per = per;
+        p.tiles = tiles;
+        p.split = static_cast<int>(split);
+      }
+    }
+  }
   return p;
 }
 
