@@ -144,7 +144,7 @@ megamoe_status megamoe_grouped_linear_backward(
   cudaError_t e = cudaSuccess;
   if (grad_x) e = launch_grouped_grad_x(g, grad_x, ld_grad_x, as_stream(stream));
   if (e == cudaSuccess && grad_w)
-    e = launch_grouped_grad_w(g, grad_w, grad_w_type, as_stream(stream));
+    e = launch_grouped_grad_w(g, grad_w, grad_w_type, grad_x != nullptr, as_stream(stream));
   return cuda_status(e);
 }
 

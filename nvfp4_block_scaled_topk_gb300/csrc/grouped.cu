@@ -74,6 +74,12 @@ struct GroupedArgs {
   int64_t ld_out;
   uint32_t idesc;  // instruction descriptor without N
   int split;       // pairs that share a tile's sum (SPLIT)
+  // grad_w right behind grad_x: it needs nothing of it, and that kernel has waited for
+  // what both read before it let this one start.  So this one waits for it only at its
+  // end, for the sake of the kernel that comes next (both gradients of 8 rows of eight
+  // experts of 512 x 512 12.9 us one after the other, 8.9 so; of 4000 rows of 2048 x 2048
+  // 80.6 and 71.2).
+  bool late_wait;
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -308,7 +314,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   cluster_sync();  // both CTAs' barriers are there before either is arrived on
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
-  pdl_wait();
+  if (MODE != kGradW || !p.late_wait) pdl_wait();
   pdl_trigger();
   build_tables(p, MT, s_range, s_toff, s_scan);
   int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
@@ -632,6 +638,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
+  if (MODE == kGradW && p.late_wait) pdl_wait();
 }
 
 template <Mode MODE, typename O, bool SPLIT>
@@ -760,8 +767,10 @@ cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, c
   return launch_mode<kGradX>(maps, a, g.type, tiles, stream);
 }
 
-cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream) {
+cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, bool after_grad_x,
+                                  cudaStream_t stream) {
   GroupedArgs a = args_of(g);
+  a.late_wait = after_grad_x;
   a.F = g.K;
   a.G = g.N;
   a.out = out;

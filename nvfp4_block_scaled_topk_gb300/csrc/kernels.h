@@ -312,7 +312,9 @@ struct Grouped {
 cudaError_t launch_grouped_forward(const Grouped& g, void* out, int out_type, int64_t ld_out,
                                    cudaStream_t stream);
 cudaError_t launch_grouped_grad_x(const Grouped& g, void* out, int64_t ld_out, cudaStream_t stream);
-cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, cudaStream_t stream);
+// after_grad_x: launched right behind launch_grouped_grad_x of the same operands.
+cudaError_t launch_grouped_grad_w(const Grouped& g, void* out, int out_type, bool after_grad_x,
+                                  cudaStream_t stream);
 // Most tiles of the first two with `features` columns of output (counted in 31 bits).
 inline int64_t grouped_tiles(int64_t rows, int E, int features) {
   return (rows / 256 + (rows < E ? rows : E)) * ((features + int64_t{255}) / 256);
