@@ -602,9 +602,9 @@ cudaError_t launch_few(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------
 // The product on pairs of CTAs: 256 features x up to 256 tokens a tile.  8192 x 7168
-// -> 2048 take 135 us (240 GFLOP: 1.78 PFLOP/s of fp16 MMAs, the tensor pipe 87 % busy;
-// a library's bf16 product takes 133 on operands of twice the bytes), of 256 tiles in
-// four turns of the 76 pairs.  Handing a stage of widened weights to the other CTA by a
+// -> 2048 take 128 us (240 GFLOP: 1.88 PFLOP/s of fp16 MMAs, the tensor pipe 86 % busy;
+// a library's bf16 product takes 133 on operands of twice the bytes), 296 tiles in four
+// turns of the 76 pairs.  Handing a stage of widened weights to the other CTA by a
 // releasing arrival took 310 us: the tensor-memory stores have been waited for, and
 // tcgen05's own fences order them.
 // ---------------------------------------------------------------------------
