@@ -769,8 +769,9 @@ megamoe_status megamoe_forward_mxfp4_from_logits(
  *            rows are not all inside the matrix (those outside are left out)
  * Values of other experts' rows and of rows of no expert have no part in an expert's
  * product; the order of its sums is fixed by the call's sizes.
- * Requires K and N multiples of 8, 1 <= E <= 1024, rows < 2^31, pointers 16-byte
- * and rows 16-byte aligned.
+ * Requires K and N multiples of 8, 1 <= E <= 1024, rows, K and N below 2^30 (and tiles
+ * of 256 x 256, with all rows in every expert, as well), pointers 16-byte and rows
+ * 16-byte aligned.
  */
 megamoe_status megamoe_grouped_linear(const void* x, int type, int64_t rows, int64_t ld_x,
                                       const void* w, int E, int N, int K, const int32_t* offsets,

@@ -34,7 +34,7 @@ megamoe_status check_grouped(int type, int64_t rows, int E, int N, int K, const 
                              const int32_t* padded_offsets, const uint32_t* status) {
   if (!half_type(type) || rows < 0 || E < 1 || N < 1 || K < 1 || !offsets)
     return MEGAMOE_ERR_INVALID_ARG;
-  if (E > MEGAMOE_MAX_EXPERTS || rows >= kMaxRows || N % 8 != 0 || K % 8 != 0 || N >= kMaxWidth ||
+  if (E > MEGAMOE_MAX_EXPERTS || rows >= kMaxWidth || N % 8 != 0 || K % 8 != 0 || N >= kMaxWidth ||
       K >= kMaxWidth)
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   const int64_t most = int64_t{1} << 30, mt = (N + 255) / 256, kt = (K + 255) / 256;

@@ -211,11 +211,11 @@ struct Tile {
   int start;  // grad_w: the expert's first row
   int n;      // the MMA's N
   int steps;  // stages of the sum
-  // grad_w: a stage whose last sixteen rows are not all the expert's
+  bool again;  // the weights are read by other tiles, too
   // the first stage of a share of the sum
   __device__ int first(int share, int of) const { return of == 1 ? share * steps : share * steps / of; }
+  // grad_w: a stage whose last sixteen rows are not all the expert's
   __device__ bool ragged_at(int i) const { return i == steps - 1 && (rows & 15) != 0; }
-  bool again;  // the weights are read by other tiles, too
 };
 template <Mode MODE>
 __device__ __forceinline__ Tile decode(const GroupedArgs& p, int q, const Range* s_range,

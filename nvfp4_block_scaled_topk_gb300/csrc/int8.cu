@@ -457,10 +457,12 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_dots(const Int
 template <int T, int F>
 cudaError_t launch_dots(const Int8Few& a, int64_t blocks, cudaStream_t stream) {
   auto kern = k_int8_dots<T, F>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads),
-                    static_cast<size_t>(T) * a.K, stream, a);
+  const size_t smem = static_cast<size_t>(T) * a.K;
+  if (smem > 48 * 1024 - 256) {  // more, with the kernel's own, than a kernel has unasked
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(static_cast<unsigned>(blocks)), dim3(kFewThreads), smem, stream, a);
 }
 template <int F>
 cudaError_t launch_dots_t(const Int8Few& a, int64_t blocks, cudaStream_t stream) {

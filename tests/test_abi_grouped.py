@@ -28,7 +28,7 @@ def lib():
     (dict(type=F32), INVALID), (dict(type=I8), INVALID), (dict(out_type=F16), INVALID),
     (dict(out_type=9), INVALID), (dict(x=P), INVALID), (dict(w=P), INVALID), (dict(out=P), INVALID),
     (dict(off=P), INVALID), (dict(ld_x=56), INVALID), (dict(ld_out=64), INVALID),
-    (dict(E=1025), SHAPE), (dict(rows=BIG), SHAPE), (dict(K=60), SHAPE), (dict(N=68), SHAPE),
+    (dict(E=1025), SHAPE), (dict(rows=1 << 30, E=1), SHAPE), (dict(K=60), SHAPE), (dict(N=68), SHAPE),
     (dict(x=ODD), SHAPE), (dict(w=ODD), SHAPE), (dict(out=ODD), SHAPE), (dict(off=ODD), SHAPE),
     (dict(poff=ODD), SHAPE), (dict(status=ODD), SHAPE), (dict(ld_x=66), SHAPE),
     (dict(ld_out=74), SHAPE), (dict(ld_out=1 << 36), SHAPE),
