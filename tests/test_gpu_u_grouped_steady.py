@@ -396,3 +396,53 @@ def test_shared_waits_that_run_out(cuda_lib, out):
     status.zero_()
     assert torch.equal(megamoe.grouped_linear(x, w, off, out_dtype=out, status=status), want)
     assert int(status) == 0
+
+
+def test_an_expert_twice(cuda_lib):
+    """A token that goes to one expert twice has two rows there."""
+    ids = torch.tensor([[1, 1, 0], [2, 2, 2], [0, -1, 0]], dtype=torch.int32, device="cuda")
+    x = torch.randn((3, 64), device="cuda").to(BF)
+    tw = torch.rand((3, 3), device="cuda")
+    r = megamoe.route_permute(ids, 3)
+    dst = r["slot_dst"].view(3, 3)
+    rows = megamoe.gather_rows(x, r["row_src"], 3)
+    out = megamoe.combine_rows(rows, dst, tw)
+    share = torch.where(ids >= 0, tw, 0.0).sum(1, keepdim=True).double()
+    _within(out, x.double() * share, 4 * 2.0 ** -24 * x.double().abs() * 3)
+    gy, gtw = megamoe.combine_rows_backward(x, rows, dst, tw)
+    for t in range(3):
+        for j in range(3):
+            if ids[t, j] >= 0:
+                _within(gy[dst[t, j]], x[t].double() * tw[t, j].double(), x[t].double().abs() * 2.0 ** -24)
+    dots = (x.double() ** 2).sum(1, keepdim=True).expand(3, 3)
+    _within(gtw, torch.where(ids >= 0, dots, 0.0), 44 * 2.0 ** -24 * dots)
+    # one row in two slots: counted twice
+    twice = torch.tensor([[0, 0]], dtype=torch.int32, device="cuda")
+    assert torch.equal(megamoe.combine_rows(x, twice), 2 * x[:1])
+
+
+@pytest.mark.parametrize("T", [3, 12, 70])
+def test_graphs_that_share_a_workspace(cuda_lib, T):
+    """Replayed one after the other; the status word is each call's own."""
+    w = [megamoe.Int8LinearWeights.quantize(torch.randn((520, 2064), device="cuda")) for _ in range(2)]
+    x = [torch.randn((T, 2064), device="cuda").to(BF) for _ in range(2)]
+    want = [megamoe.linear_int8(a, b)[0] for a, b in zip(x, w)]
+    ws = torch.empty(megamoe.linear_int8_workspace_size(T, 2064, 520) + 256, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for a, b in zip(x, w):
+        megamoe.linear_int8(a, b, ws=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(megamoe.linear_int8(a, b, ws=ws)[0])
+        graphs.append(g)
+    for _ in range(3):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    x[0][0, 5] = float("nan")
+    graphs[0].replay()
+    assert int(ws[:4].view(torch.int32)) == megamoe.DEV_NONFINITE
+    graphs[1].replay()
+    assert int(ws[:4].view(torch.int32)) == 0 and torch.equal(outs[1], want[1])
