@@ -86,9 +86,9 @@ struct GroupedArgs {
 
 struct Cfg {
   static constexpr int THREADS = 384;  // producer, MMA issuer, tail warp, idle; 8 epilogue warps
-  // With fp32 results the epilogue's warps hold 128 sums each; the first four then
-  // give up registers for them (without that some spill: uneven experts' grad_w took
-  // 315 us, 300 with it).  A thread's of either (168 at launch):
+  // Where sums are added up in parts the epilogue's warps hold 128 each; the first four
+  // then give up registers for them (without that some spill: uneven experts' grad_w
+  // took 315 us, 300 with it).  A thread's of either (168 at launch):
   static constexpr int FEW_REGS = 64, MANY_REGS = 216;
   static constexpr int STAGES = 6;
   static constexpr int TILE = 128 * 128;  // a CTA's part of either operand
@@ -251,22 +251,28 @@ __device__ __forceinline__ Tile decode(const GroupedArgs& p, int q, const Range*
 
 __device__ __forceinline__ void store_rounded(float v, __nv_bfloat16* p) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void store_rounded(float v, __half* p) { *p = __float2half_rn(v); }
+
+// Sums in tensor memory drop what lies past their last bit, always towards zero: each
+// addition of 16 terms up to one unit of 2^-23 of what has been added up (2^20 terms of
+// one sign came out 0.7 % short).  So a sum is taken in parts, which the epilogue adds up
+// in registers, rounding to nearest: of 512 terms for fp32 results (off by 5e-7 at any
+// length), of 2048 for 16-bit ones, whose own half step is 2^-9 or 2^-12 and more.
+//
+// What that costs (us, one part / parts): 16384 rows of eight experts, 7168 x 2048,
+// grad_w in bf16 288 / 286, grad_x 274 / 277; 48 experts of 4096 x 7168 with a row each
+// 433 / 432; 65536 rows of 512 x 512 276 / 276.  Sums of one part are taken without (16
+// small experts' gradients 19.5 / 20.6).
+constexpr int kPart32 = 8, kPart16 = 32;  // stages
+
 // SPLIT: a cluster of p.split pairs shares a tile's sum, and has one tile at most.
-template <Mode MODE, typename O, bool SPLIT>
+// FOLD: sums are taken in parts.
+template <Mode MODE, typename O, bool SPLIT, bool FOLD>
 __global__ void __launch_bounds__(Cfg::THREADS, 1)
     k_grouped_pair(const __grid_constant__ GroupedMaps maps, const GroupedArgs p) {
   using C = Cfg;
   constexpr int STAGES = C::STAGES;
   constexpr bool M_MN = MODE != kForward;  // the M side is read MN-major
-  // Sums in tensor memory drop what lies past their last bit: at 2048, 4096 and
-  // 16384 rows in one go the gradient of w was off by 2.1e-6, 4.4e-6 and 1.9e-5 of
-  // its size, always towards zero.  For fp32 results the sum is taken in parts of
-  // SEG stages, and the epilogue adds the parts up in registers, rounding to nearest.
-  // (16384 rows of eight experts, 7168 x 2048: 287 us so, 280 in one part, 255 with
-  // bf16 results, half the bytes to store.)  A 16-bit result is rounded to 2^-8 or
-  // 2^-11 of its size and takes one part.
-  constexpr bool FOLD = sizeof(O) == 4;
-  constexpr int SEG = FOLD ? 8 : 1 << 30;
+  constexpr int SEG = !FOLD ? 1 << 30 : sizeof(O) == 4 ? kPart32 : kPart16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -555,7 +561,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
           for (int j = 0; j < 32; ++j) to[(32 * chunk_of(c) + j) * 128] = v[j];
         }
         if (!FOLD) let_go(buf);
-      } else if constexpr (FOLD) {
+      } else if constexpr (sizeof(O) == 4) {
         // fp32: 32 features of a row are 128 bytes as they lie
         if (m + lane < p.F) {
 #pragma unroll
@@ -576,19 +582,24 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           if (chunk_of(c) >= chunks) continue;
-          uint32_t v[32];
-          if (t.steps != 0) {
-            tmem_ld_32x32b_x32(base + 32 * chunk_of(c), v);
-            tmem_ld_wait();
-          } else {
+          float v[32];
+          if constexpr (FOLD) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0;
+            for (int j = 0; j < 32; ++j) v[j] = sum[c][j];
+          } else {
+            uint32_t u[32] = {};
+            if (t.steps != 0) {
+              tmem_ld_32x32b_x32(base + 32 * chunk_of(c), u);
+              tmem_ld_wait();
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(u[j]);
           }
           if (m >= p.F) continue;  // warp-uniform
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            store_rounded(__uint_as_float(v[j]), reinterpret_cast<O*>(stg) + j * 32 + lane);
+            store_rounded(v[j], reinterpret_cast<O*>(stg) + j * 32 + lane);
           __syncwarp();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -597,7 +608,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             if (in && row < rows) *reinterpret_cast<uint4*>(at + row * p.ld_out + piece * 8) = x;
           }
         }
-        if (t.steps != 0) {
+        if (!FOLD && t.steps != 0) {
           let_go(buf);
           ++parts;
         }
@@ -641,13 +652,13 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   if (MODE == kGradW && p.late_wait) pdl_wait();
 }
 
-template <Mode MODE, typename O, bool SPLIT>
+template <Mode MODE, typename O, bool SPLIT, bool FOLD>
 cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t tiles,
                          cudaStream_t stream) {
-  auto kern = k_grouped_pair<MODE, O, SPLIT>;
+  auto kern = k_grouped_pair<MODE, O, SPLIT, FOLD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
-  if (sizeof(O) == 4) {
+  if (FOLD) {
     // what the warps hold after giving up and taking registers is what they start with
     static std::atomic<bool> fits{false};
     cudaFuncAttributes f;
@@ -684,14 +695,26 @@ int share_sum(const GroupedArgs& a, int64_t tiles) {
   return best;
 }
 
+// In parts, unless a 16-bit result's sum (a pair's share of it) is one at most.
+template <Mode MODE, typename O, bool SPLIT>
+cudaError_t launch_parts(const GroupedMaps& maps, const GroupedArgs& a, int64_t tiles,
+                         cudaStream_t stream) {
+  if constexpr (sizeof(O) == 2) {
+    const int64_t stages = ((MODE == kGradW ? a.rows : a.sum) + 63) / 64;
+    if ((stages + a.split - 1) / a.split <= kPart16)
+      return launch_typed<MODE, O, SPLIT, false>(maps, a, tiles, stream);
+  }
+  return launch_typed<MODE, O, SPLIT, true>(maps, a, tiles, stream);
+}
+
 template <Mode MODE, typename O>
 cudaError_t launch_shared(const GroupedMaps& maps, GroupedArgs a, int64_t tiles, cudaStream_t stream) {
   a.split = 1;
   if constexpr (MODE != kGradW) {
     a.split = share_sum(a, tiles);
-    if (a.split > 1) return launch_typed<MODE, O, true>(maps, a, tiles, stream);
+    if (a.split > 1) return launch_parts<MODE, O, true>(maps, a, tiles, stream);
   }
-  return launch_typed<MODE, O, false>(maps, a, tiles, stream);
+  return launch_parts<MODE, O, false>(maps, a, tiles, stream);
 }
 
 template <Mode MODE>
