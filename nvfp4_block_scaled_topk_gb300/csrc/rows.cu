@@ -4,7 +4,7 @@
 //
 // All are bound by their bytes, or with few rows by the launch (1.5 us for the
 // activation of 48 rows, 2.1 for the sums of eight tokens, in a stream of calls).  At
-// the copy rate / measured, us: gradient of the activation, 49152 x 2048, 148.6 / 149.7;
+// the copy rate / measured, us: gradient of the activation, 49152 x 2048, 148.6 / 151.5;
 // 2003 tokens of 7168 into 11777 rows 29.2 / 33.2; their sums 29.7 / 38.5; gradient of
 // the sums of 8192 tokens 221 / 230.  8192 tokens (117 MB) into 49152 rows take 181 us
 // where 121 are needed: the experts' rows come to each token six times, and it has left
@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -45,22 +46,130 @@ __device__ __forceinline__ uint32_t narrow<__half>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// s = 1 / (1 + exp(-g)) and 1 - s, both to a few units of fp32: the exponential
-// is taken of -|g|, so that neither overflows nor cancels.  Its argument in
-// units of log 2 is rounded once, which is off by |g| 2^-24 in the result.
+// exp(-|g|) of a 16-bit number: its product with the leading bits of log2 e (15 of them
+// with 8 of bf16, 13 with 11 of fp16) is exact, and what those leave out of log2 e follows
+// as the factor exp(d), 1 + d and, where d is larger, d^2 / 2 (a split constant after Cody
+// and Waite; multiplied by log2 e in one, the rounding of the product alone puts the
+// result off by |g| 2^-24).
+template <typename X>
+__device__ __forceinline__ float exp_minus(float g);
+__device__ __forceinline__ float ex2(float t) {
+  float e;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  return e;
+}
+template <>
+__device__ __forceinline__ float exp_minus<__nv_bfloat16>(float g) {
+  const float a = fabsf(g), e = ex2(a * -0x1.7154p+0f);
+  return fmaf(e, a * -4.888495e-6f, e);
+}
+template <>
+__device__ __forceinline__ float exp_minus<__half>(float g) {
+  const float a = fminf(fabsf(g), 128.f), e = ex2(a * -0x1.715p+0f), d = a * -4.7194842e-5f;
+  return fmaf(e, fmaf(0.5f * d, d, d), e);
+}
+
+// The largest magnitude of eight bf16 elements.
+__device__ __forceinline__ float largest(const uint32_t (&v)[4]) {
+  auto magnitudes = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+  const __nv_bfloat162 m = __hmax2(__hmax2(magnitudes(v[0]), magnitudes(v[1])),
+                                   __hmax2(magnitudes(v[2]), magnitudes(v[3])));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+
+// SiLU(g) u = g s u with s = 1 / (1 + exp(-g)); its gradient is grad u s (1 + g (1 - s))
+// by g and grad g s by u.  The exponential is taken of -|g|, so that neither s nor 1 - s
+// overflows or cancels; it and the products are off by a few units of fp32, the
+// hardware's reciprocal of a number in [1, 2] by one.
+//
+// Near: the gates' magnitudes are below 80 (past 87 the exponential is no normal number),
+// those of the other factors, of which two are multiplied, below 2^60.  fp16 values are
+// always near enough: gates further down give less than the type's smallest number.
+// (Two forms because the far one for all takes 161 us for the gradient of 49152 x 2048,
+// 151.5 so.)
+template <typename X>
 __device__ __forceinline__ void sigmoid(float g, float* s, float* rest) {
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-fabsf(g) * 1.44269504f));
+  const float e = exp_minus<X>(g);
+  float r;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   const float er = e * r;
   *s = g >= 0.f ? r : er;
   *rest = g >= 0.f ? er : r;
 }
+template <typename X>
+__device__ __forceinline__ float silu_near(float g, float u) {
+  float s, rest;
+  sigmoid<X>(g, &s, &rest);
+  return g * s * u;
+}
+template <typename X>
+__device__ __forceinline__ void silu_grad_near(float g, float u, float grad, float* dg, float* du) {
+  float s, rest;
+  sigmoid<X>(g, &s, &rest);
+  *dg = grad * u * (s * fmaf(g, rest, 1.f));
+  *du = grad * (g * s);
+}
+
+// Far: s in the factors p p r: with h = exp(-|g| / 2), which fp32 holds down to |g| = 174,
+// and r = 1 / (1 + h h), p is 1 or (g below 0) h.  The products are ordered so that no
+// step leaves fp32's range where the result does not.
+struct FarGate {
+  float p, r, rest;
+  __device__ explicit FarGate(float g) {
+    const float h = expf(-0.5f * fabsf(g)), e = h * h;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    p = g >= 0.f ? 1.f : h;
+    rest = g >= 0.f ? e * r : r;
+  }
+};
+__device__ __forceinline__ float silu_far(float g, float u) {
+  const FarGate s(g);
+  return g * s.p * s.r * (u * s.p);
+}
+// The larger of grad and u meets the gate's factor first (halved: it can be 1.1; the
+// smaller one is doubled), all of it where the smaller one is 1 at most, else each of the
+// two takes a p.
+__device__ __forceinline__ void silu_grad_far(float g, float u, float grad, float* dg, float* du) {
+  const FarGate s(g);
+  const bool first = fabsf(grad) > fabsf(u);
+  const float big = first ? grad : u, small = first ? u : grad;
+  const bool all = fabsf(small) <= 1.f;
+  *dg = big * s.p * (s.r * fmaf(0.5f * g, s.rest, 0.5f)) * (all ? s.p : 1.f) *
+        (small * (all ? 2.f : 2.f * s.p));
+  *du = g * s.p * s.r * (grad * s.p);
+}
+
+// Eight elements of each.
+template <typename X, bool BACKWARD, bool FAR>
+__device__ __forceinline__ void silu_eight(const uint32_t (&g)[4], const uint32_t (&u)[4],
+                                           const uint32_t (&h)[4], uint32_t (&o)[4], uint32_t (&q)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 gv = widen<X>(g[j]), uv = widen<X>(u[j]);
+    if (!BACKWARD) {
+      o[j] = FAR ? narrow<X>(silu_far(gv.x, uv.x), silu_far(gv.y, uv.y))
+                 : narrow<X>(silu_near<X>(gv.x, uv.x), silu_near<X>(gv.y, uv.y));
+      continue;
+    }
+    const float2 hv = widen<X>(h[j]);
+    float2 dg, du;
+    if (FAR) {
+      silu_grad_far(gv.x, uv.x, hv.x, &dg.x, &du.x);
+      silu_grad_far(gv.y, uv.y, hv.y, &dg.y, &du.y);
+    } else {
+      silu_grad_near<X>(gv.x, uv.x, hv.x, &dg.x, &du.x);
+      silu_grad_near<X>(gv.y, uv.y, hv.y, &dg.y, &du.y);
+    }
+    o[j] = narrow<X>(dg.x, dg.y);
+    q[j] = narrow<X>(du.x, du.y);
+  }
+}
 
 // 16 bytes (eight elements) a thread and step; vectors of all rows in one line, so
-// that short rows leave no lane idle.
+// that short rows leave no lane idle.  Blocks an SM: 49152 x 2048 bf16 take 91.4 us with
+// eight and 95 with six (and more registers) forward, the gradient 155.7 and 151.5.
 template <typename X, bool BACKWARD>
-__global__ void __launch_bounds__(256) k_silu(const Silu p) {
+__global__ void __launch_bounds__(256, BACKWARD ? 6 : 8) k_silu(const Silu p) {
   pdl_wait();
   pdl_trigger();
   const uint32_t vecs = static_cast<uint32_t>(p.I) / 8;
@@ -81,22 +190,13 @@ __global__ void __launch_bounds__(256) k_silu(const Silu p) {
     const uint32_t g[4] = {g4.x, g4.y, g4.z, g4.w}, u[4] = {u4.x, u4.y, u4.z, u4.w};
     const uint32_t h[4] = {h4.x, h4.y, h4.z, h4.w};
     uint32_t o[4], q[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float2 gv = widen<X>(g[j]), uv = widen<X>(u[j]);
-      float2 s, r;
-      sigmoid(gv.x, &s.x, &r.x);
-      sigmoid(gv.y, &s.y, &r.y);
-      if (!BACKWARD) {
-        o[j] = narrow<X>(gv.x * s.x * uv.x, gv.y * s.y * uv.y);
-      } else {
-        const float2 hv = widen<X>(h[j]);
-        // d silu = s (1 + g (1 - s))
-        o[j] = narrow<X>(hv.x * uv.x * (s.x * fmaf(gv.x, r.x, 1.f)),
-                         hv.y * uv.y * (s.y * fmaf(gv.y, r.y, 1.f)));
-        q[j] = narrow<X>(hv.x * (gv.x * s.x), hv.y * (gv.y * s.y));
-      }
+    bool near = true;
+    if constexpr (!std::is_same_v<X, __half>) {
+      near = largest(g) < 80.f;
+      if (BACKWARD) near = near && largest(u) < 0x1p60f && largest(h) < 0x1p60f;
     }
+    if (near) silu_eight<X, BACKWARD, false>(g, u, h, o, q);
+    else silu_eight<X, BACKWARD, true>(g, u, h, o, q);
     X* to = static_cast<X*>(p.out) + row * p.ld_out + col;
     *reinterpret_cast<uint4*>(to) = make_uint4(o[0], o[1], o[2], o[3]);
     if (BACKWARD) *reinterpret_cast<uint4*>(to + p.I) = make_uint4(q[0], q[1], q[2], q[3]);
