@@ -755,6 +755,13 @@ megamoe_status megamoe_forward_mxfp4_from_logits(
  * MEGAMOE_TYPE_BF16 or MEGAMOE_TYPE_F16 (one of them for all operands of a
  * call); sums are fp32, each output rounded once.  Row matrices may have any row
  * stride that keeps rows on 16-byte boundaries; widths are multiples of 8.
+ *
+ * Results, here and in the linear in 8-bit integers below, have no memory in common
+ * with each other, a workspace or what the call reads: such calls are refused
+ * (MEGAMOE_ERR_INVALID_ARG; rows of one stride may lie between each other).  In place,
+ * at the same address and stride, are allowed: the activation's result in the gate or
+ * up columns of a, its gradient's two halves in those of a or in grad, combine's grad_y
+ * in y and its grad_topk_weights in topk_weights.
  * ------------------------------------------------------------------------ */
 
 /*

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <array>
 
 #include "../../include/megamoe.h"
 #include "kernels.h"
@@ -25,6 +26,36 @@ inline int64_t type_bytes(int type) {
 inline bool rows_ok(const void* p, int64_t ld, int64_t bytes) {
   return aligned(p, 16) && ld * bytes % 16 == 0 && ld < (int64_t{1} << 36);
 }
+
+// Rows of a matrix in memory, in bytes.
+struct Place {
+  uintptr_t at;
+  int64_t rows, pitch, width;
+  Place(const void* p, int64_t n, int64_t ld, int64_t cols, int64_t bytes)
+      : at(reinterpret_cast<uintptr_t>(p)), rows(p ? n : 0), pitch(ld * bytes), width(cols * bytes) {}
+  Place(const void* p, int64_t n, int64_t bytes) : Place(p, 1, n, n, bytes) { rows = p && n > 0; }
+  bool same(const Place& o) const {
+    return at == o.at && width == o.width && rows == o.rows && (rows == 1 || pitch == o.pitch);
+  }
+};
+// Whether they have a byte in common.  Rows of one pitch may lie between each other;
+// of two pitches they count as meeting where their spans do.
+bool meet(Place a, Place b) {
+  if (a.rows == 0 || b.rows == 0) return false;
+  auto span = [](const Place& m) {
+    return static_cast<unsigned __int128>(m.rows - 1) * m.pitch + m.width;
+  };
+  if (a.at + span(a) <= b.at || b.at + span(b) <= a.at) return false;
+  if (a.rows == 1 && a.width <= b.pitch) a.pitch = b.pitch;
+  if (b.rows == 1 && b.width <= a.pitch) b.pitch = a.pitch;
+  if (a.pitch != b.pitch) return true;
+  const int64_t off = b.at >= a.at ? static_cast<int64_t>((b.at - a.at) % a.pitch)
+                                   : a.pitch - 1 - static_cast<int64_t>((a.at - b.at - 1) % a.pitch);
+  return off < a.width || off + b.width > a.pitch;
+}
+// Read and written at the same place by the same thread, or nowhere in common.
+bool meet_elsewhere(const Place& a, const Place& b) { return !a.same(b) && meet(a, b); }
+
 constexpr int64_t kMaxRows = int64_t{1} << 31;
 constexpr int kMaxWidth = 1 << 30;
 
@@ -56,6 +87,12 @@ megamoe_status check_silu(const void* a, int type, int64_t rows, int I, int64_t 
       !aligned(live_rows, 4))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   return MEGAMOE_OK;
+}
+
+// The gates' columns and the others'.
+std::array<Place, 2> halves(const void* a, int64_t rows, int64_t ld, int I) {
+  return {Place(a, rows, ld, I, 2),
+          Place(a ? static_cast<const uint16_t*>(a) + I : nullptr, rows, ld, I, 2)};
 }
 
 megamoe_status check_rows(int type, int64_t rows, int64_t T, int k, int d) {
@@ -118,6 +155,9 @@ megamoe_status megamoe_grouped_linear(const void* x, int type, int64_t rows, int
   if (rows > 0 && (!x || !out)) return MEGAMOE_ERR_INVALID_ARG;
   if (!rows_ok(x, ld_x, 2) || !rows_ok(out, ld_out, type_bytes(out_type)) || !aligned(w, 16))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place to(out, rows, ld_out, N, type_bytes(out_type));
+  if (meet(to, Place(x, rows, ld_x, K, 2)) || meet(to, Place(w, static_cast<int64_t>(E) * N * K, 2)))
+    return MEGAMOE_ERR_INVALID_ARG;
   const Grouped g{x, nullptr, w, type, rows, ld_x, 0, E, N, K, offsets, padded_offsets, status};
   return cuda_status(launch_grouped_forward(g, out, out_type, ld_out, as_stream(stream)));
 }
@@ -140,6 +180,14 @@ megamoe_status megamoe_grouped_linear_backward(
       return MEGAMOE_ERR_INVALID_ARG;
     if (!rows_ok(x, ld_x, 2) || !aligned(grad_w, 16)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   }
+  // grad_w is under way before grad_x is done: neither may lie where the other reads
+  const int64_t values = static_cast<int64_t>(E) * N * K;
+  const Place from(grad_out, rows, ld_grad, N, 2), weights(grad_x ? w : nullptr, values, 2);
+  const Place tokens(grad_w ? x : nullptr, rows, ld_x, K, 2), to_x(grad_x, rows, ld_grad_x, K, 2);
+  const Place to_w(grad_w, values, type_bytes(grad_w_type));
+  if (meet(to_x, from) || meet(to_x, weights) || meet(to_x, tokens) || meet(to_x, to_w) ||
+      meet(to_w, from) || meet(to_w, weights) || meet(to_w, tokens))
+    return MEGAMOE_ERR_INVALID_ARG;
   const Grouped g{x, grad_out, w, type, rows, ld_x, ld_grad, E, N, K, offsets, padded_offsets, status};
   cudaError_t e = cudaSuccess;
   if (grad_x) e = launch_grouped_grad_x(g, grad_x, ld_grad_x, as_stream(stream));
@@ -155,6 +203,9 @@ megamoe_status megamoe_silu_mul(const void* a, int type, int64_t rows, int I, in
   if (st != MEGAMOE_OK) return st;
   if (ld_out < I || (rows > 0 && !out)) return MEGAMOE_ERR_INVALID_ARG;
   if (!rows_ok(out, ld_out, 2)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place to(out, rows, ld_out, I, 2);
+  for (const Place& from : halves(a, rows, ld_a, I))
+    if (meet_elsewhere(to, from)) return MEGAMOE_ERR_INVALID_ARG;
   return cuda_status(launch_silu(Silu{a, nullptr, type, rows, ld_a, 0, ld_out, I, live_rows, out},
                                  as_stream(stream)));
 }
@@ -169,6 +220,11 @@ megamoe_status megamoe_silu_mul_backward(const void* grad, int64_t ld_grad, cons
   if (rows > 0 && (!grad || !grad_a)) return MEGAMOE_ERR_INVALID_ARG;
   if (!rows_ok(grad, ld_grad, 2) || !rows_ok(grad_a, ld_grad_a, 2))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place from_grad(grad, rows, ld_grad, I, 2);
+  const auto from = halves(a, rows, ld_a, I), to = halves(grad_a, rows, ld_grad_a, I);
+  for (const Place& t : to)
+    if (meet_elsewhere(t, from[0]) || meet_elsewhere(t, from[1]) || meet_elsewhere(t, from_grad))
+      return MEGAMOE_ERR_INVALID_ARG;
   return cuda_status(launch_silu_backward(
       Silu{a, grad, type, rows, ld_a, ld_grad, ld_grad_a, I, live_rows, grad_a}, as_stream(stream)));
 }
@@ -182,6 +238,9 @@ megamoe_status megamoe_gather_rows(const void* x, int type, int64_t T, int d, in
     return MEGAMOE_ERR_INVALID_ARG;
   if (!rows_ok(x, ld_x, 2) || !rows_ok(out, ld_out, 2) || !aligned(row_src, 4))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place to(out, rows, ld_out, d, 2);
+  if (meet(to, Place(x, T, ld_x, d, 2)) || meet(to, Place(row_src, rows, 4)))
+    return MEGAMOE_ERR_INVALID_ARG;
   return cuda_status(launch_gather_rows(x, T, d, ld_x, row_src, rows, k, out, ld_out, as_stream(stream)));
 }
 
@@ -196,6 +255,10 @@ megamoe_status megamoe_combine_rows(const void* y, int type, int64_t rows, int64
   if (!rows_ok(y, ld_y, 2) || !rows_ok(out, ld_out, 2) || !aligned(slot_dst, 4) ||
       !aligned(topk_weights, 4))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place to(out, T, ld_out, d, 2);
+  if (meet(to, Place(y, rows, ld_y, d, 2)) || meet(to, Place(slot_dst, T * k, 4)) ||
+      meet(to, Place(topk_weights, T * k, 4)))
+    return MEGAMOE_ERR_INVALID_ARG;
   const CombineRows c{y, type, rows, ld_y, slot_dst, topk_weights, T, k, d,
                       nullptr, 0, out, ld_out, nullptr};
   return cuda_status(launch_combine_rows(c, as_stream(stream)));
@@ -218,6 +281,13 @@ megamoe_status megamoe_combine_rows_backward(const void* grad_out, int64_t ld_gr
     if (ld_y < d || (rows > 0 && !y)) return MEGAMOE_ERR_INVALID_ARG;
     if (!rows_ok(y, ld_y, 2)) return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   }
+  const Place from(grad_out, T, ld_grad, d, 2), to_y(grad_y, rows, ld_grad_y, d, 2);
+  const Place slots(slot_dst, T * k, 4), weights(topk_weights, T * k, 4);
+  const Place to_w(grad_topk_weights, T * k, 4), expert(grad_topk_weights ? y : nullptr, rows, ld_y, d, 2);
+  if (meet(to_y, from) || meet(to_y, slots) || meet(to_y, weights) || meet(to_y, to_w) ||
+      meet_elsewhere(to_y, expert) || meet(to_w, from) || meet(to_w, slots) || meet(to_w, expert) ||
+      meet_elsewhere(to_w, weights))
+    return MEGAMOE_ERR_INVALID_ARG;
   const CombineRows c{y, type, rows, ld_y, slot_dst, topk_weights, T, k, d,
                       grad_out, ld_grad, grad_y, ld_grad_y, grad_topk_weights};
   return cuda_status(launch_combine_rows_backward(c, as_stream(stream)));
@@ -232,6 +302,8 @@ megamoe_status megamoe_quantize_int8(const void* x, int x_type, int64_t rows, in
   if (K % 16 != 0 || K >= kMaxWidth || rows >= kMaxRows || !rows_ok(x, ld, type_bytes(x_type)) ||
       !aligned(codes, 16) || !aligned(scales, 4) || !aligned(status, 4))
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
+  const Place from(x, rows, ld, K, type_bytes(x_type)), to(codes, rows, K, K, 1), to_s(scales, rows, 4);
+  if (meet(to, from) || meet(to_s, from) || meet(to, to_s)) return MEGAMOE_ERR_INVALID_ARG;
   const Int8Quant q{x, x_type, nullptr, rows, ld, K, codes, nullptr, scales, status, false};
   return cuda_status(launch_int8_quantize(q, as_stream(stream)));
 }
@@ -258,6 +330,12 @@ megamoe_status megamoe_linear_int8(const void* x, int x_type, int64_t T, int K, 
     return MEGAMOE_ERR_UNSUPPORTED_SHAPE;
   const Int8Ws wk = carve_int8(ws, T, K, N);
   if (ws_bytes < wk.bytes) return MEGAMOE_ERR_WORKSPACE_TOO_SMALL;
+  const Place from[] = {Place(x, T, ld_x, K, type_bytes(x_type)), Place(w_codes, N, K, K, 1),
+                        Place(w_scales, N, 4), Place(x_scales, T, 4)};
+  const Place to(out, T, ld_out, N, out_bytes), own(ws, static_cast<int64_t>(wk.bytes), 1);
+  for (const Place& f : from)
+    if (meet(to, f) || meet(own, f)) return MEGAMOE_ERR_INVALID_ARG;
+  if (meet(to, own)) return MEGAMOE_ERR_INVALID_ARG;
   const cudaStream_t s = as_stream(stream);
   if (T == 0) return cuda_status(cudaMemsetAsync(wk.status, 0, 4, s));
   const bool few = int8_few_fits(T, K), codes = x_type == MEGAMOE_TYPE_I8;
