@@ -76,7 +76,7 @@ typedef enum megamoe_status {
 #define MEGAMOE_DEV_BAD_EXPERT_ID 0x1u /* a topk id >= E was seen (slot skipped) */
 #define MEGAMOE_DEV_NONFINITE 0x2u     /* the amax of an input was not finite    */
 #define MEGAMOE_DEV_TIMEOUT 0x4u       /* a bounded device wait gave up          */
-#define MEGAMOE_DEV_BAD_OFFSETS 0x8u   /* rows of an expert outside the matrix   */
+#define MEGAMOE_DEV_BAD_OFFSETS 0x8u   /* an expert's rows outside the matrix, or another's */
 
 /* Scale layouts. */
 #define MEGAMOE_SCALES_ROWMAJOR 0 /* [rows, K/16] bytes                         */
@@ -773,7 +773,8 @@ megamoe_status megamoe_forward_mxfp4_from_logits(
  *   out      [rows, N] of `type` or MEGAMOE_TYPE_F32, row stride ld_out; rows of no
  *            expert are left as they are
  *   status   device status word or null: MEGAMOE_DEV_BAD_OFFSETS where an expert's
- *            rows are not all inside the matrix (those outside are left out)
+ *            rows are not all inside the matrix (those outside are left out), or an
+ *            expert shares a row with one before it (which is treated as without rows)
  * Values of other experts' rows and of rows of no expert have no part in an expert's
  * product; the order of its sums is fixed by the call's sizes.
  * Requires K and N multiples of 8, 1 <= E <= 1024, rows, K and N below 2^30 (and tiles

@@ -138,35 +138,74 @@ __device__ __forceinline__ int tile_rows(int count) {
   return tiles ? ((count + tiles - 1) / tiles + 15) / 16 * 16 : 16;
 }
 
+// Experts e0 .. e1 - 1 that share a row with one before them have none.  All threads; its
+// own function because code that a call jumps over costs it 0.3 us.
+__device__ __noinline__ bool leave_out_shared(Range* s_range, int e0, int e1) {
+  uint32_t out = 0;
+  for (int e = e0; e < e1; ++e) {
+    const Range r = s_range[e];
+    for (int f = 0; f < e; ++f) {
+      const Range q = s_range[f];
+      if (min(r.start + r.count, q.start + q.count) > max(r.start, q.start)) out |= 1u << (e - e0);
+    }
+  }
+  __syncthreads();
+  for (int e = e0; e < e1; ++e)
+    if (out >> (e - e0) & 1u) s_range[e].count = 0;
+  return out != 0;
+}
+
 // Experts' rows, and s_toff[e] = first tile of expert e, s_toff[E] = all tiles
-// (forward, grad_x).  All threads.
+// (forward, grad_x).  All threads.  Tiles are at most grouped_tiles, and no two of them
+// write one row: rows outside the matrix are left out, and so is an expert that shares a
+// row with one before it.  Where experts follow each other, as they do but for broken or
+// shuffled offsets, neighbours tell that none does.
 __device__ void build_tables(const GroupedArgs& p, int MT, Range* s_range, int* s_toff,
                              int* s_scan) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.E + Cfg::THREADS - 1) / Cfg::THREADS;
   const int e0 = min(p.E, tid * per), e1 = min(p.E, e0 + per);
-  int sum = 0;
-  bool bad = false;
-  for (int e = e0; e < e1; ++e) {
+  bool bad = false, back = false;  // (back: starts before its neighbour's end)
+  int begin = 0, end = 0;          // of this thread's experts
+  auto range = [&](int e) {
     const int64_t o0 = __ldcg(p.offsets + e), o1 = __ldcg(p.offsets + e + 1);
     const int64_t s = p.padded_offsets ? __ldcg(p.padded_offsets + e) : o0;
     const int64_t start = min(max(s, int64_t{0}), p.rows);
     const int64_t count = max(min(s + o1 - o0, p.rows) - start, int64_t{0});
     bad |= start != s || count != o1 - o0;
-    s_range[e] = {static_cast<int>(start), static_cast<int>(count)};
-    const int rows = tile_rows(static_cast<int>(count));
-    s_toff[e] = (static_cast<int>(count) + rows - 1) / rows * MT;
-    sum += s_toff[e];
+    return Range{static_cast<int>(start), static_cast<int>(count)};
+  };
+  Range before{0, 0};  // the warp before's last
+  if (lane == 0 && e0 > 0 && e0 < p.E) before = range(e0 - 1);
+  for (int e = e0; e < e1; ++e) {
+    const Range r = range(e);
+    s_range[e] = r;
+    if (e == e0) begin = r.start;
+    else back |= r.start < end;
+    end = r.start + r.count;
+  }
+  const int left = __shfl_up_sync(0xffffffffu, end, 1);
+  if (e0 < e1) back |= begin < (lane ? left : before.start + before.count);
+  int sum, x;  // of this thread's tiles; with those of the warp's threads before it
+  while (true) {
+    sum = 0;
+    for (int e = e0; e < e1; ++e) {
+      const int count = s_range[e].count, rows = tile_rows(count);
+      s_toff[e] = (count + rows - 1) / rows * MT;
+      sum += s_toff[e];
+    }
+    x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) s_scan[warp] = x;
+    if (!__syncthreads_or(back)) break;
+    bad |= leave_out_shared(s_range, e0, e1);
+    back = false;
   }
   if (bad && blockIdx.x == 0) set_status(p.status, MEGAMOE_DEV_BAD_OFFSETS);
-  int x = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  if (lane == 31) s_scan[warp] = x;
-  __syncthreads();
   int base = x - sum;
   for (int w = 0; w < warp; ++w) base += s_scan[w];
   for (int e = e0; e < e1; ++e) {
@@ -323,12 +362,8 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
   if (MODE != kGradW || !p.late_wait) pdl_wait();
   pdl_trigger();
   build_tables(p, MT, s_range, s_toff, s_scan);
-  int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
+  const int total = MODE == kGradW ? p.E * MT * NT : s_toff[p.E];
   const int step = gridDim.x / (2 * split), first = blockIdx.x / (2 * split);  // tiles of this pair
-  if (SPLIT && total > step) {  // experts' rows overlap: there are more than any that do not have
-    if (blockIdx.x == 0 && threadIdx.x == 0) set_status(p.status, MEGAMOE_DEV_BAD_OFFSETS);
-    total = step;
-  }
 
   if (warp < 4) {
     if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::FEW_REGS));
