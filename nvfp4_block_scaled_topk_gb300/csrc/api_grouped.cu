@@ -127,10 +127,12 @@ Int8Ws carve_int8(void* base, int64_t T, int K, int N) {
   w.integers = p + w.bytes;
   w.bytes += up((few ? 1 : 2) * static_cast<size_t>(T) * K);
   if (few) return w;
-  const Int8Plan plan = int8_plan(T, N, K);
-  if (plan.split == 1) return w;
+  // (for either type of result)
+  const int split = std::max(int8_plan(T, N, K, false).split,
+                             int8_folds(K) ? int8_plan(T, N, K, true).split : 1);
+  if (split == 1) return w;
   w.partial = reinterpret_cast<float*>(p + w.bytes);
-  w.bytes += up(4 * static_cast<size_t>(plan.split) * T * N);
+  w.bytes += up(4 * static_cast<size_t>(split) * T * N);
   return w;
 }
 

@@ -5,8 +5,12 @@
 //
 // The tensor cores of sm_103a have no integer kind.  An 8-bit integer is exact in
 // fp16 and a product of two in fp32, so the integers are multiplied as fp16
-// (kind::f16) and the sum is exact up to 2^24, that is while sum |q_x q_w| stays
-// below it, and rounded to fp32 at each of the K / 16 additions past that.
+// (kind::f16) and a sum of up to 1024 products is exact.  Longer ones are taken in parts
+// of 1024 that are added up as 32-bit integers (K below 131072), for up to 16 tokens and
+// for fp32 results: the same bits whatever the number of tokens.  A bf16 result of more
+// tokens has its sum in one part, exact while no partial sum passes 2^24; past that each
+// of the K / 16 additions drops what lies below fp32's last bit, up to K / 16 2^-23 of
+// the sum in all, where half a step of bf16 is 2^-9 at least.
 //
 // Weights stay in memory as bytes.  A pair of CTAs has 256 features on the MMA's
 // M side: four warps of each read a stage's bytes from shared memory, widen them
@@ -20,6 +24,8 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "gemm_common.cuh"
@@ -503,7 +509,7 @@ template <int NT>
 __global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_few(const Int8Few p) {
   extern __shared__ __align__(16) int8_t s_codes[];  // [8 NT][pitch]
   __shared__ float s_scale[8 * NT];
-  __shared__ float s_part[2][kFewWarps][NT * 4][32];  // sums of the warps that share a row
+  __shared__ int s_part[2][kFewWarps][NT * 4][32];  // sums of the warps that share a row
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r0 = static_cast<int>(static_cast<int64_t>(p.N) * blockIdx.x / gridDim.x);
   const int r1 = static_cast<int>(static_cast<int64_t>(p.N) * (blockIdx.x + 1) / gridDim.x);
@@ -541,8 +547,9 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_few(const Int8
     const uint4* lo = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(n0 + g) * p.K) + j;
     const uint4* hi = reinterpret_cast<const uint4*>(p.w + static_cast<int64_t>(n0 + g + 8) * p.K) + j;
     float acc[NT][4] = {};
+    int sum[NT][4] = {};  // parts of 1024 terms: 16 steps of this warp
 #pragma unroll 1
-    for (int c0 = share; c0 < steps; c0 += 4 * p.split) {
+    for (int c0 = share, turns4 = 0; c0 < steps; c0 += 4 * p.split, ++turns4) {
       uint4 a[4], b[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -567,20 +574,28 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_few(const Int8
             mma_16x8x16(acc[n], u[h], v[h], u[h + 1], v[h + 1], x[h], x[h + 1]);
         }
       }
-    }
-    if (p.split > 1) {  // the shares in order
-      float(*part)[NT * 4][32] = s_part[turn & 1];
+      if ((turns4 & 3) != 3 && c0 + 4 * p.split < steps) continue;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) part[warp][n * 4 + i][lane] = acc[n][i];
+        for (int i = 0; i < 4; ++i) {
+          sum[n][i] += __float2int_rn(acc[n][i]);
+          acc[n][i] = 0.f;
+        }
+    }
+    if (p.split > 1) {  // the shares in order
+      int(*part)[NT * 4][32] = s_part[turn & 1];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) part[warp][n * 4 + i][lane] = sum[n][i];
       __syncthreads();
       if (share != 0) continue;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          for (int s = 1; s < p.split; ++s) acc[n][i] += part[warp + s][n * 4 + i][lane];
+          for (int s = 1; s < p.split; ++s) sum[n][i] += part[warp + s][n * 4 + i][lane];
     }
     // rows g and g + 8 of tokens 2 j and 2 j + 1
 #pragma unroll
@@ -588,7 +603,7 @@ __global__ void __launch_bounds__(kFewThreads, kFewBlocks) k_int8_few(const Int8
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int t = 8 * n + 2 * j + (i & 1), r = g + 8 * (i >> 1);
-        if (t < p.T && r < live) few_store(p, t, n0 + r, acc[n][i], s_scale[t]);
+        if (t < p.T && r < live) few_store(p, t, n0 + r, static_cast<float>(sum[n][i]), s_scale[t]);
       }
   }
 }
@@ -622,7 +637,7 @@ struct Int8Args {
   int split;  // shares of a tile's sum, each with a pair of CTAs
   void* out;
   int64_t ld_out;
-  float* partial;  // split > 1: [split][T][N], added up by k_int8_sum
+  float* partial;  // split > 1: [split][T][N], added up by k_int8_sum (FOLD: integers)
   uint32_t* status;
   uint64_t wait_limit_ns;
 };
@@ -695,11 +710,24 @@ __device__ __forceinline__ Item int8_item(int q, int split, int MT, int NT, int 
   return t;
 }
 
-template <typename O>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+// FOLD: sums in parts of PART steps (1024 terms), which the epilogue's warps add up as
+// integers in registers, 96 each: tiles have 192 tokens at most, and the accumulators no
+// columns in common.  (8192 x 7168 -> 2048: 185 us for fp32 results; 222 with 128 tokens,
+// 170 in one part.)  Those warps then take registers from the others, a warpgroup each, so
+// that the first one has two idle warps.
+struct FoldCfg {
+  static constexpr int TOKENS = 192;
+  static constexpr int THREADS = 640;
+  static constexpr int FEW_REGS = 40, WIDEN_REGS = 80, MANY_REGS = 136;  // of a thread; 96 at launch
+};
+
+template <typename O, bool FOLD>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FOLD ? FoldCfg::THREADS : Cfg::THREADS, 1)
     k_int8_pair(const __grid_constant__ Int8Maps maps, const Int8Args p) {
   using C = Cfg;
-  constexpr int STAGES = C::STAGES;
+  constexpr int STAGES = C::STAGES, PART = FOLD ? 8 : 1 << 30;
+  constexpr int EPI = FOLD ? 4 : 2, WIDEN = EPI + kEpiWarps;  // the first warps of either
+  constexpr int ACC1 = FOLD ? FoldCfg::TOKENS : C::ACC1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -709,8 +737,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   uint64_t* a_full = empty + STAGES;  // rank 0's: the widening warps of both
   uint64_t* a_empty = a_full + 2;
   uint64_t* acc_full = a_empty + 2;
-  uint64_t* acc_empty = acc_full + 1;  // rank 0's: the epilogue warps of both
-  uint64_t* drain = acc_empty + 1;
+  uint64_t* acc_empty = acc_full + 2;  // rank 0's: the epilogue warps of both
+  uint64_t* drain = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
 
@@ -735,9 +763,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&a_full[i], 8);  // four warps of each CTA
       mbar_init(&a_empty[i], 1);
+      mbar_init(&acc_full[i], 1);
+      mbar_init(&acc_empty[i], 2 * kEpiWarps);
     }
-    mbar_init(acc_full, 1);
-    mbar_init(acc_empty, 2 * kEpiWarps);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -751,112 +779,122 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   pdl_wait();
   pdl_trigger();
 
-  if (warp == 0) {
-    // -------------------------------------------------------------- producer
-    // (the whole warp, one lane of it issuing: elect_one).  Weights are waited for
-    // by this CTA's own warps, tokens by rank 0's MMAs.
-    const bool leader = elect_one();
-    const uint64_t pol_w = NT > 1 ? policy_evict_normal() : policy_evict_first();
-    const uint64_t pol_x = policy_evict_normal();
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int q = first; ok && q < total; q += step) {
-      const Item it = int8_item(q, p.split, MT, NT, KT);
-      const int rows = min(p.per, p.T - it.nt * p.per), half = (rows + 15) / 16 * 8;
-      const RowBoxes mine(rows - rank * half, half), other(rows - (1 - rank) * half, half);
-      const int t0 = it.nt * p.per + rank * half;
-      const int m0 = it.mt * 256 + rank * 128;
-      for (int i = it.k0; i < it.k1; ++i) {
-        if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
-          ok = false;
-          break;
-        }
-        uint8_t* sw = smem + stage * C::STAGE;
-        uint8_t* sx = sw + C::W;
-        if (leader) {
-          mbar_arrive_expect_tx(&w_full[stage], C::W);
-          tma_load_2d(sw, &maps.w, &w_full[stage], i * 128, m0, pol_w);
-          if (rank == 0) mbar_arrive_expect_tx(&x_full[stage], 2 * (mine.bytes() + other.bytes()));
-          const uint32_t bar = cluster_address(&x_full[stage], 0);
-          for (int h = 0; h < 2; ++h) {
-            for (int b = 0; b < mine.large; ++b)
-              tma_load_2d_pair(sx + h * C::X + b * 4096, &maps.x, bar, i * 128 + h * 64,
-                               t0 + b * 32, pol_x);
-            for (int b = 0; b < mine.small; ++b)
-              tma_load_2d_pair(sx + h * C::X + b * 1024, &maps.x8, bar, i * 128 + h * 64, t0 + b * 8,
-                               pol_x);
-          }
-        }
-        __syncwarp();
-        ++issued;
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-    }
-    drain_copies(w_full, STAGES, issued);
-    drain_pair_copies(x_full, STAGES, issued, rank, !ok);
-    __syncwarp();
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ---------------------------------------------------------- MMA issuer
+  if (warp < EPI) {
+    if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FoldCfg::FEW_REGS));
+    if (warp == 0) {
+      // -------------------------------------------------------------- producer
+      // (the whole warp, one lane of it issuing: elect_one).  Weights are waited for
+      // by this CTA's own warps, tokens by rank 0's MMAs.
       const bool leader = elect_one();
-      const uint64_t dx = sdesc_sw128(smem_u32(smem) + C::W);
-      // fp16 operands, K-major, fp32 sums, M = 256
-      constexpr uint32_t idesc0 = (1u << 4) | (256u >> 4) << 24;
-      int stage = 0, tiles = 0, steps = 0;
+      const uint64_t pol_w = NT > 1 ? policy_evict_normal() : policy_evict_first();
+      const uint64_t pol_x = policy_evict_normal();
+      int stage = 0, issued = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int q = first; ok && q < total; q += step, ++tiles) {
+      for (int q = first; ok && q < total; q += step) {
         const Item it = int8_item(q, p.split, MT, NT, KT);
-        const int n = (min(p.per, p.T - it.nt * p.per) + 15) / 16 * 16;
-        const uint32_t idesc = idesc0 | static_cast<uint32_t>(n >> 3) << 17;
-        const uint32_t acc = tmem + (tiles & 1) * C::ACC1;
-        for (int i = it.k0; i < it.k1; ++i, ++steps) {
-          const int buf = steps & 1;
-          if (!mbar_wait(&x_full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
-              !mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
-              (i == it.k0 && !mbar_wait(acc_empty, (tiles & 1) ^ 1u, abort_flag, p.status,
-                                    p.wait_limit_ns))) {
+        const int rows = min(p.per, p.T - it.nt * p.per), half = (rows + 15) / 16 * 8;
+        const RowBoxes mine(rows - rank * half, half), other(rows - (1 - rank) * half, half);
+        const int t0 = it.nt * p.per + rank * half;
+        const int m0 = it.mt * 256 + rank * 128;
+        for (int i = it.k0; i < it.k1; ++i) {
+          if (!mbar_wait(&empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_limit_ns)) {
             ok = false;
             break;
           }
-          tc_fence_after();
-          const uint64_t cx = sdesc_at(dx, stage * C::STAGE);
-          const uint32_t a = tmem + C::A_COL0 + buf * C::A_COLS;
-          const int left = p.K - i * 128;  // a multiple of 16
+          uint8_t* sw = smem + stage * C::STAGE;
+          uint8_t* sx = sw + C::W;
           if (leader) {
-#pragma unroll
-            for (int c = 0; c < 8; ++c)
-              if (16 * c < left)
-                mma_f16_pair_ts(acc, a + 8 * c, sdesc_at(cx, (c >> 2) * C::X + 32 * (c & 3)), idesc,
-                                (i != it.k0 || c != 0) ? 1u : 0u);
-            tc_commit_pair(&empty[stage]);
-            tc_commit_pair(&a_empty[buf]);
+            mbar_arrive_expect_tx(&w_full[stage], C::W);
+            tma_load_2d(sw, &maps.w, &w_full[stage], i * 128, m0, pol_w);
+            if (rank == 0) mbar_arrive_expect_tx(&x_full[stage], 2 * (mine.bytes() + other.bytes()));
+            const uint32_t bar = cluster_address(&x_full[stage], 0);
+            for (int h = 0; h < 2; ++h) {
+              for (int b = 0; b < mine.large; ++b)
+                tma_load_2d_pair(sx + h * C::X + b * 4096, &maps.x, bar, i * 128 + h * 64,
+                                 t0 + b * 32, pol_x);
+              for (int b = 0; b < mine.small; ++b)
+                tma_load_2d_pair(sx + h * C::X + b * 1024, &maps.x8, bar, i * 128 + h * 64, t0 + b * 8,
+                                 pol_x);
+            }
           }
           __syncwarp();
+          ++issued;
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1u;
           }
         }
-        if (!ok) break;
-        if (leader) tc_commit_pair(acc_full);
-        __syncwarp();
       }
-      // every MMA issued so far must finish before tensor memory is released
-      if (leader) tc_commit_pair(drain);
+      drain_copies(w_full, STAGES, issued);
+      drain_pair_copies(x_full, STAGES, issued, rank, !ok);
       __syncwarp();
-      mbar_drain(drain, 0);
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ---------------------------------------------------------- MMA issuer
+        const bool leader = elect_one();
+        const uint64_t dx = sdesc_sw128(smem_u32(smem) + C::W);
+        // fp16 operands, K-major, fp32 sums, M = 256
+        constexpr uint32_t idesc0 = (1u << 4) | (256u >> 4) << 24;
+        int stage = 0, accs = 0, steps = 0;  // accs: accumulators taken
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int q = first; ok && q < total; q += step) {
+          const Item it = int8_item(q, p.split, MT, NT, KT);
+          const int n = (min(p.per, p.T - it.nt * p.per) + 15) / 16 * 16;
+          const uint32_t idesc = idesc0 | static_cast<uint32_t>(n >> 3) << 17;
+          for (int i0 = it.k0; ok && i0 < it.k1; i0 += min(PART, it.k1 - i0), ++accs) {
+            // FOLD's accumulators have a barrier each; one that shares columns with the
+            // last waits for that one's
+            uint64_t* free = &acc_empty[FOLD ? accs & 1 : 0];
+            const uint32_t turn = FOLD ? accs >> 1 & 1 : accs & 1;
+            const uint32_t acc = tmem + (accs & 1) * ACC1;
+            const int i1 = i0 + min(PART, it.k1 - i0);
+            for (int i = i0; i < i1; ++i, ++steps) {
+              const int buf = steps & 1;
+              if (!mbar_wait(&x_full[stage], phase, abort_flag, p.status, p.wait_limit_ns) ||
+                  !mbar_wait(&a_full[buf], steps >> 1 & 1, abort_flag, p.status, p.wait_limit_ns) ||
+                  (i == i0 && !mbar_wait(free, turn ^ 1u, abort_flag, p.status, p.wait_limit_ns))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              const uint64_t cx = sdesc_at(dx, stage * C::STAGE);
+              const uint32_t a = tmem + C::A_COL0 + buf * C::A_COLS;
+              const int left = p.K - i * 128;  // a multiple of 16
+              if (leader) {
+#pragma unroll
+                for (int c = 0; c < 8; ++c)
+                  if (16 * c < left)
+                    mma_f16_pair_ts(acc, a + 8 * c, sdesc_at(cx, (c >> 2) * C::X + 32 * (c & 3)),
+                                    idesc, (i != i0 || c != 0) ? 1u : 0u);
+                tc_commit_pair(&empty[stage]);
+                tc_commit_pair(&a_empty[buf]);
+              }
+              __syncwarp();
+              if (++stage == STAGES) {
+                stage = 0;
+                phase ^= 1u;
+              }
+            }
+            if (!ok) break;
+            if (leader) tc_commit_pair(&acc_full[FOLD ? accs & 1 : 0]);
+            __syncwarp();
+          }
+        }
+        // every MMA issued so far must finish before tensor memory is released
+        if (leader) tc_commit_pair(drain);
+        __syncwarp();
+        mbar_drain(drain, 0);
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else if (warp >= 10) {
+  } else if (warp >= WIDEN) {
+    if (FOLD) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(FoldCfg::WIDEN_REGS));
     // ---------------------------------------------------------- widening warps
     // A lane has a row of 128 bytes; its 16-byte piece j is at j ^ (row % 8).  Four
     // warps take the even stages and four the odd ones, each set with a buffer.
-    const int quarter = warp & 3, buf = warp >= 14 ? 1 : 0;
+    const int quarter = warp & 3, buf = warp >= WIDEN + 4 ? 1 : 0;
     const uint32_t to = tmem + C::A_COL0 + buf * C::A_COLS + (static_cast<uint32_t>(quarter * 32) << 16);
     int64_t all = 0;  // stages of this pair's items
     for (int q = first; q < total; q += step) {
@@ -891,85 +929,123 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
       __syncwarp();
     }
   } else {
+    if (FOLD) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(FoldCfg::MANY_REGS));
     // -------------------------------------------------------------- epilogue
     // A lane has a feature, a column is a token: 64 or 128 bytes of 32 features of
     // a token at a time through shared memory.  The two warps of a quarter take
     // chunks of 32 tokens in turn, those first whose columns the next tile's
     // accumulator shares; its products may start once they have been read.
     const int quarter = warp & 3;
-    const int half = warp >= 6 ? 1 : 0;
-    uint8_t* stg = smem + C::STG_OFF + (warp - 2) * C::STG;
+    const int half = warp >= EPI + 4 ? 1 : 0;
+    uint8_t* stg = smem + C::STG_OFF + (warp - EPI) * C::STG;
     constexpr int SIZE = sizeof(O), PER = 16 / SIZE;
     constexpr int ROWS = C::STG / (32 * SIZE);  // staged at a time
     constexpr int LANES = 32 / PER;             // lanes of a token's 16-byte pieces
     const int piece = lane % LANES;
     O* out = static_cast<O*>(p.out);
-    int tiles = 0;
-    bool bad = false;
-    for (int q = first; q < total; q += step, ++tiles) {
+    int accs = 0;
+    bool bad = false, ok = true;
+    for (int q = first; q < total; q += step) {
       const Item it = int8_item(q, p.split, MT, NT, KT);
       const int rows = min(p.per, p.T - it.nt * p.per), t0 = it.nt * p.per;
       const int m = it.mt * 256 + rank * 128 + quarter * 32;  // this warp's first feature
       const float sw = m + lane < p.N ? __ldg(p.w_scales + m + lane) : 0.f;
-      if (!mbar_wait(acc_full, tiles & 1, abort_flag, p.status, p.wait_limit_ns)) break;
-      tc_fence_after();
-      const uint32_t base =
-          tmem + (tiles & 1) * C::ACC1 + (static_cast<uint32_t>(quarter * 32) << 16);
       const bool in = m + piece * PER < p.N;
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {  // 128 tokens, the shared columns first
-        const int c0 = ((tiles & 1) ^ part ^ 1) * 128 + half * 32;
-        uint32_t v[2][32];
-        if (c0 < rows) tmem_ld_32x32b_x32(base + c0, v[0]);
-        if (c0 + 64 < rows) tmem_ld_32x32b_x32(base + c0 + 64, v[1]);
-        tmem_ld_wait();
-        if (part == 0) {
+      // tokens c .. c + 31: their sums (FOLD: integers) times the scales, or as they are
+      auto put = [&](int c, const uint32_t(&v)[32]) {
+        if (c >= rows) return;
+        if (p.split > 1) {
+          float* to = p.partial + (static_cast<int64_t>(it.share) * p.T + t0 + c) * p.N + m + lane;
+          if (m + lane < p.N) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j, to += p.N)
+              if (c + j < rows) *to = __uint_as_float(v[j]);
+          }
+          return;
+        }
+        auto sum = [&](int j) {
+          return FOLD ? static_cast<float>(static_cast<int>(v[j])) : __uint_as_float(v[j]);
+        };
+        const float4* xs = reinterpret_cast<const float4*>(p.x_scales + t0 + c);
+#pragma unroll
+        for (int g = 0; g < 32 / ROWS; ++g) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < ROWS; j += 4) {
+            const float4 s = __ldg(xs + (g * ROWS + j) / 4);
+            const float sx[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store_rounded(sum(g * ROWS + j + i) * sx[i] * sw,
+                            reinterpret_cast<O*>(stg) + (j + i) * 32 + lane);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < ROWS * LANES / 32; ++j) {
+            const int r = j * (32 / LANES) + lane / LANES;
+            const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
+            const int row = c + g * ROWS + r;
+            if (in && row < rows)
+              *reinterpret_cast<uint4*>(out + (t0 + static_cast<int64_t>(row)) * p.ld_out + m +
+                                        piece * PER) = x;
+          }
+        }
+      };
+      const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+      if constexpr (FOLD) {
+        uint32_t sum[3][32];
+#pragma unroll
+        for (int j = 0; j < 96; ++j) sum[j >> 5][j & 31] = 0;
+        for (int i = it.k0; i < it.k1; i += PART, ++accs) {
+          const uint32_t buf = accs & 1;
+          if (!mbar_wait(&acc_full[buf], accs >> 1 & 1, abort_flag, p.status, p.wait_limit_ns)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 6; ++h) {  // sixteen tokens at a time
+            const int c = half * 32 + (h >> 1) * 64 + (h & 1) * 16;
+            if (c >= rows) continue;
+            uint32_t v[16];
+            tmem_ld_32x32b_x16(base + buf * ACC1 + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              sum[h >> 1][(h & 1) * 16 + j] += static_cast<uint32_t>(__float2int_rn(__uint_as_float(v[j])));
+          }
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
+          if (lane == 0) mbar_arrive_cluster_relaxed(&acc_empty[buf], 0);
         }
-        if (m >= p.N) continue;  // warp-uniform
+        if (!ok) break;
+        if (m < p.N) {  // warp-uniform
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = c0 + 64 * h;
-          if (c >= rows) continue;
-          if (p.split > 1) {
-            float* to = p.partial + (static_cast<int64_t>(it.share) * p.T + t0 + c) * p.N + m + lane;
-            if (m + lane < p.N) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j, to += p.N)
-                if (c + j < rows) *to = __uint_as_float(v[h][j]);
-            }
-            continue;
-          }
-          const float4* xs = reinterpret_cast<const float4*>(p.x_scales + t0 + c);
-#pragma unroll
-          for (int g = 0; g < 32 / ROWS; ++g) {
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < ROWS; j += 4) {
-              const float4 s = __ldg(xs + (g * ROWS + j) / 4);
-              const float sx[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                store_rounded(__uint_as_float(v[h][g * ROWS + j + i]) * sx[i] * sw,
-                              reinterpret_cast<O*>(stg) + (j + i) * 32 + lane);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int j = 0; j < ROWS * LANES / 32; ++j) {
-              const int r = j * (32 / LANES) + lane / LANES;
-              const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
-              const int row = c + g * ROWS + r;
-              if (in && row < rows)
-                *reinterpret_cast<uint4*>(out + (t0 + static_cast<int64_t>(row)) * p.ld_out + m +
-                                          piece * PER) = x;
-            }
-          }
+          for (int h = 0; h < 3; ++h) put(half * 32 + 64 * h, sum[h]);
         }
+      } else {
+        if (!mbar_wait(acc_full, accs & 1, abort_flag, p.status, p.wait_limit_ns)) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {  // 128 tokens, the shared columns first
+          const int c0 = ((accs & 1) ^ part ^ 1) * 128 + half * 32;
+          uint32_t v[2][32];
+          if (c0 < rows) tmem_ld_32x32b_x32(base + (accs & 1) * ACC1 + c0, v[0]);
+          if (c0 + 64 < rows) tmem_ld_32x32b_x32(base + (accs & 1) * ACC1 + c0 + 64, v[1]);
+          tmem_ld_wait();
+          if (part == 0) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty, 0);
+          }
+          if (m >= p.N) continue;  // warp-uniform
+          put(c0, v[0]);
+          put(c0 + 64, v[1]);
+        }
+        ++accs;
       }
       if (it.mt == 0 && it.share == 0)  // once for each token
-        for (int c = threadIdx.x - 64; c < rows; c += 32 * kEpiWarps)
+        for (int c = threadIdx.x - 32 * EPI; c < rows; c += 32 * kEpiWarps)
           bad |= !(fabsf(__ldg(p.x_scales + t0 + c)) <= 0x1.fffffep127f);
     }
     if (bad) set_status(p.status, MEGAMOE_DEV_NONFINITE);
@@ -986,8 +1062,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
   }
 }
 
-// The shares of a sum in their order, and the scales.  Four columns a thread.
-template <typename O>
+// The shares of a sum in their order (FOLD: integers), and the scales.  Four columns a
+// thread.
+template <typename O, bool FOLD>
 __global__ void __launch_bounds__(256) k_int8_sum(const Int8Args p) {
   pdl_wait();
   pdl_trigger();
@@ -998,15 +1075,17 @@ __global__ void __launch_bounds__(256) k_int8_sum(const Int8Args p) {
     const int64_t t = i / quads;
     const int c = static_cast<int>(i - t * quads) * 4;
     const float* from = p.partial + t * p.N + c;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    using V = std::conditional_t<FOLD, int4, float4>;
+    V all{};
 #pragma unroll 4
     for (int s = 0; s < p.split; ++s) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(from + static_cast<int64_t>(s) * p.T * p.N));
-      sum.x += v.x;
-      sum.y += v.y;
-      sum.z += v.z;
-      sum.w += v.w;
+      const V v = __ldcg(reinterpret_cast<const V*>(from + static_cast<int64_t>(s) * p.T * p.N));
+      all.x += v.x;
+      all.y += v.y;
+      all.z += v.z;
+      all.w += v.w;
     }
+    const float4 sum = make_float4(all.x, all.y, all.z, all.w);
     const float sx = __ldg(p.x_scales + t);
     O* to = static_cast<O*>(p.out) + t * p.ld_out + c;
     store_rounded(sum.x * sx * __ldg(p.w_scales + c), to);
@@ -1016,17 +1095,28 @@ __global__ void __launch_bounds__(256) k_int8_sum(const Int8Args p) {
   }
 }
 
-template <typename O>
+template <typename O, bool FOLD>
 cudaError_t launch_pair(const Int8Maps& maps, const Int8Args& a, int64_t tiles, cudaStream_t stream) {
-  auto kern = k_int8_pair<O>;
+  auto kern = k_int8_pair<O, FOLD>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
   if (e != cudaSuccess) return e;
+  constexpr int kThreads = FOLD ? FoldCfg::THREADS : Cfg::THREADS;
+  if (FOLD) {
+    // what the warps hold after giving up and taking registers is what they start with
+    static std::atomic<bool> fits{false};
+    cudaFuncAttributes f;
+    if (!fits.load(std::memory_order_relaxed)) {
+      if ((e = cudaFuncGetAttributes(&f, kern)) != cudaSuccess) return e;
+      if (f.numRegs * kThreads < 128 * FoldCfg::FEW_REGS + 256 * (FoldCfg::WIDEN_REGS + FoldCfg::MANY_REGS))
+        return cudaErrorInvalidConfiguration;
+      fits.store(true, std::memory_order_relaxed);
+    }
+  }
   const int64_t pairs = std::min<int64_t>(std::max(num_sms() / 2, 1), tiles);
-  e = launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(Cfg::THREADS), Cfg::SMEM, stream,
-                 maps, a);
+  e = launch_pdl(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), Cfg::SMEM, stream, maps, a);
   if (e != cudaSuccess || a.split == 1) return e;
   const int64_t blocks = (static_cast<int64_t>(a.T) * (a.N / 4) + 255) / 256;
-  return launch_pdl(k_int8_sum<O>,
+  return launch_pdl(k_int8_sum<O, FOLD>,
                     dim3(static_cast<unsigned>(std::min<int64_t>(blocks, num_sms() * int64_t{16}))),
                     dim3(256), 0, stream, a);
 }
@@ -1087,11 +1177,11 @@ cudaError_t launch_int8_few(const Int8Quant& q, const Int8Product& g, cudaStream
 // each share's values through L2.  us, 256 tokens and one share / as chosen: 8192 x 7168
 // -> 2048 178 / 168 (224 tokens: four turns of 296 tiles, not of 256), 3000 85 / 74, 1024
 // 42 / 35 (two shares), 256 41 / 20, 64 31 / 15.
-Int8Plan int8_plan(int64_t T, int N, int K) {
+Int8Plan int8_plan(int64_t T, int N, int K, bool fold) {
   Int8Plan p{};
   double least = 0;
   const int64_t mt = (N + int64_t{255}) / 256, steps = (K + 127) / 128;
-  for (int most = 256; most >= 128; most -= 16) {
+  for (int most = fold ? FoldCfg::TOKENS : 256; most >= 128; most -= 16) {
     const int64_t nt = (T + most - 1) / most;
     const int per = static_cast<int>(((T + nt - 1) / nt + 15) / 16 * 16);
     const int64_t tiles = (T + per - 1) / per * mt;
@@ -1123,12 +1213,14 @@ cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream) {
       !make_map(&maps.x8, CU_TENSOR_MAP_DATA_TYPE_UINT16, g.x, g.K, g.T,
                 static_cast<uint64_t>(g.K) * 2, 64, 8, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  const Int8Plan plan = int8_plan(g.T, g.N, g.K);
+  const bool fold = g.out_f32 && int8_folds(g.K);
+  const Int8Plan plan = int8_plan(g.T, g.N, g.K, fold);
   const Int8Args a{g.x_scales, g.w_scales, static_cast<int>(g.T), g.N, g.K, plan.per, plan.split,
                    g.out, g.ld_out, g.partial, g.status, wait_limit_ns()};
   const int64_t items = plan.tiles * plan.split;
-  return g.out_f32 ? launch_pair<float>(maps, a, items, stream)
-                   : launch_pair<__nv_bfloat16>(maps, a, items, stream);
+  return fold        ? launch_pair<float, true>(maps, a, items, stream)
+         : g.out_f32 ? launch_pair<float, false>(maps, a, items, stream)
+                     : launch_pair<__nv_bfloat16, false>(maps, a, items, stream);
 }
 
 }  // namespace megamoe

@@ -355,7 +355,9 @@ struct Int8Plan {
   int split;      // shares of a tile's sum
 };
 constexpr int64_t kInt8Pairs = 76;  // of SMs (counted on for workspaces, which are sized without a device)
-Int8Plan int8_plan(int64_t T, int N, int K);
+// Sums of fp32 results that are taken in parts: one part is exact, and 32 bits hold them.
+inline bool int8_folds(int K) { return K > 1024 && K < 131072; }
+Int8Plan int8_plan(int64_t T, int N, int K, bool fold);
 cudaError_t launch_int8_product(const Int8Product& g, cudaStream_t stream);
 // The same for few tokens.  Dots: up to four, quantised in the same launch (q's
 // x, type, T, ld and x_scales; clears *status first).  Few: up to sixteen, q the
