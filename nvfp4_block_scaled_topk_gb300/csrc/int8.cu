@@ -294,6 +294,15 @@ __global__ void __launch_bounds__(kQuantThreads) k_int8_widen(const Int8Quant p)
   }
 }
 
+// sum sx sw with the token's scale last where it is large, so that nothing overflows that
+// the other scale would have brought back.  (A small one first loses nothing: the sum is
+// whole, so their product is exact wherever it is no normal number.)
+constexpr float kLoud = 0x1p64f;
+__device__ __forceinline__ float scaled(float sum, float sx, float sw) {
+  const bool loud = fabsf(sx) > kLoud;
+  return sum * (loud ? sw : sx) * (loud ? sx : sw);
+}
+
 // ---------------------------------------------------------------------------
 // Few tokens: 256-row tiles would leave most SMs without work, or each with a long
 // sum.  Bound by the weights' bytes and by the launch; the first of a block's
@@ -330,7 +339,7 @@ struct Int8Few {
 };
 
 __device__ __forceinline__ void few_store(const Int8Few& p, int t, int n, float sum, float scale) {
-  const float y = sum * scale * __ldg(p.w_scales + n);
+  const float y = scaled(sum, scale, __ldg(p.w_scales + n));
   if (p.out_f32) static_cast<float*>(p.out)[t * p.ld_out + n] = y;
   else static_cast<__nv_bfloat16*>(p.out)[t * p.ld_out + n] = __float2bfloat16_rn(y);
 }
@@ -967,29 +976,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(FOLD ? FoldCfg::THRE
           return FOLD ? static_cast<float>(static_cast<int>(v[j])) : __uint_as_float(v[j]);
         };
         const float4* xs = reinterpret_cast<const float4*>(p.x_scales + t0 + c);
+        auto emit = [&](auto loud) {
 #pragma unroll
-        for (int g = 0; g < 32 / ROWS; ++g) {
-          __syncwarp();
+          for (int g = 0; g < 32 / ROWS; ++g) {
+            __syncwarp();
 #pragma unroll
-          for (int j = 0; j < ROWS; j += 4) {
-            const float4 s = __ldg(xs + (g * ROWS + j) / 4);
-            const float sx[4] = {s.x, s.y, s.z, s.w};
+            for (int j = 0; j < ROWS; j += 4) {
+              const float4 s = __ldg(xs + (g * ROWS + j) / 4);
+              const float sx[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              store_rounded(sum(g * ROWS + j + i) * sx[i] * sw,
-                            reinterpret_cast<O*>(stg) + (j + i) * 32 + lane);
+              for (int i = 0; i < 4; ++i)
+                store_rounded(loud ? scaled(sum(g * ROWS + j + i), sx[i], sw)
+                                   : sum(g * ROWS + j + i) * sx[i] * sw,
+                              reinterpret_cast<O*>(stg) + (j + i) * 32 + lane);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < ROWS * LANES / 32; ++j) {
+              const int r = j * (32 / LANES) + lane / LANES;
+              const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
+              const int row = c + g * ROWS + r;
+              if (in && row < rows)
+                *reinterpret_cast<uint4*>(out + (t0 + static_cast<int64_t>(row)) * p.ld_out + m +
+                                          piece * PER) = x;
+            }
           }
-          __syncwarp();
-#pragma unroll
-          for (int j = 0; j < ROWS * LANES / 32; ++j) {
-            const int r = j * (32 / LANES) + lane / LANES;
-            const uint4 x = *reinterpret_cast<const uint4*>(stg + (r * LANES + piece) * 16);
-            const int row = c + g * ROWS + r;
-            if (in && row < rows)
-              *reinterpret_cast<uint4*>(out + (t0 + static_cast<int64_t>(row)) * p.ld_out + m +
-                                        piece * PER) = x;
-          }
-        }
+        };
+        // (a choice for each value costs 0.3 us)
+        if (__any_sync(0xffffffffu, fabsf(__ldg(p.x_scales + t0 + c + lane)) > kLoud)) emit(std::true_type{});
+        else emit(std::false_type{});
       };
       const uint32_t base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
       if constexpr (FOLD) {
@@ -1088,10 +1103,10 @@ __global__ void __launch_bounds__(256) k_int8_sum(const Int8Args p) {
     const float4 sum = make_float4(all.x, all.y, all.z, all.w);
     const float sx = __ldg(p.x_scales + t);
     O* to = static_cast<O*>(p.out) + t * p.ld_out + c;
-    store_rounded(sum.x * sx * __ldg(p.w_scales + c), to);
-    store_rounded(sum.y * sx * __ldg(p.w_scales + c + 1), to + 1);
-    store_rounded(sum.z * sx * __ldg(p.w_scales + c + 2), to + 2);
-    store_rounded(sum.w * sx * __ldg(p.w_scales + c + 3), to + 3);
+    store_rounded(scaled(sum.x, sx, __ldg(p.w_scales + c)), to);
+    store_rounded(scaled(sum.y, sx, __ldg(p.w_scales + c + 1)), to + 1);
+    store_rounded(scaled(sum.z, sx, __ldg(p.w_scales + c + 2)), to + 2);
+    store_rounded(scaled(sum.w, sx, __ldg(p.w_scales + c + 3)), to + 3);
   }
 }
 
