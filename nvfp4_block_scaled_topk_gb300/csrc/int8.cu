@@ -311,10 +311,10 @@ __device__ __forceinline__ float scaled(float sum, float sx, float sw) {
 //
 // us (K -> N; dots / MMA / pairs of CTAs, the last two with the quantiser before them):
 //              1 token      4 tokens     8 tokens     16 tokens
-//   1536 24576  9.4 / 14.1  11.3 / 14.2  14.1 / 24.2  18.3 / 22.9
-//   7168  7168 11.6 / 18.6  15.9 / 18.9  18.8 / 29.9  22.5 / 22.3
-//   7168  2048  7.3 / 11.1  10.5 / 11.9  12.2 / 15.6  13.8 / 14.1
-//   4096  4096  5.3 /  8.4   7.5 /  8.3   8.4 / 15.5  11.4 / 13.4
+//   1536 24576  9.4 / 14.1  11.3 / 14.2  14.4 / 24.2  18.4 / 22.9
+//   7168  7168 11.6 / 18.6  15.9 / 18.9  19.2 / 29.9     - / 22.3
+//   7168  2048  7.3 / 11.1  10.5 / 11.9  12.3 / 15.6     - / 14.1
+//   4096  4096  5.3 /  8.4   7.5 /  8.3   8.4 / 15.5  11.2 / 13.4
 // 1536 -> 24576 are 37.7 MB, 5.6 us at the copy rate; 7.3 us in a stream of calls.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
@@ -1153,6 +1153,9 @@ cudaError_t launch_int8_quantize(const Int8Quant& q, cudaStream_t stream) {
                     stream, q);
 }
 
+// Tokens whose integers fit kFewSmem.  Dots: K up to 98304 for one token, 49152 for two,
+// 24576 for three and four; few: 12160 for up to eight, 6016 for up to sixteen (16 x 7168
+// do not fit).
 bool int8_dots_fit(int64_t T, int64_t K) { return T <= 4 && (T == 3 ? 4 : T) * K <= kFewSmem; }
 bool int8_few_fits(int64_t T, int64_t K) {
   return !int8_dots_fit(T, K) && T <= 16 && K <= kFewSmem &&
