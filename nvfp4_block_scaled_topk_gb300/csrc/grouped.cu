@@ -295,13 +295,15 @@ __device__ __forceinline__ void store_rounded(float v, __half* p) { *p = __float
 // addition of 16 terms up to one unit of 2^-23 of what has been added up (2^20 terms of
 // one sign came out 0.7 % short).  So a sum is taken in parts, which the epilogue adds up
 // in registers, rounding to nearest: of 512 terms for fp32 results (off by 5e-7 at any
-// length), of 2048 for 16-bit ones, whose own half step is 2^-9 or 2^-12 and more.
+// length), of 1024 for 16-bit ones.  Random sums of 7168 so round to another bf16 than the
+// exact ones in 0.06 % of all cases (0.40 in one part, 0.11 in parts of 2048, 0.04 with
+// fp32 products).
 //
-// What that costs (us, one part / parts): 16384 rows of eight experts, 7168 x 2048,
-// grad_w in bf16 288 / 286, grad_x 274 / 277; 48 experts of 4096 x 7168 with a row each
-// 433 / 432; 65536 rows of 512 x 512 276 / 276.  Sums of one part are taken without (16
-// small experts' gradients 19.5 / 20.6).
-constexpr int kPart32 = 8, kPart16 = 32;  // stages
+// What that costs (us, one part / parts): 48 experts of 4096 x 7168 with a row each 433 /
+// 432, of 7168 x 2048 with 245 rows on average 294 / 295; 16384 rows of eight experts,
+// 7168 x 2048, 260 / 263, their grad_w in bf16 288 / 296.  Sums of one part are taken
+// without (100 rows of each of eight experts, 1000 -> 520, 9.3 / 9.6).
+constexpr int kPart32 = 8, kPart16 = 16;  // stages
 
 // SPLIT: a cluster of p.split pairs shares a tile's sum, and has one tile at most.
 // FOLD: sums are taken in parts.
