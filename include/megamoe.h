@@ -878,9 +878,10 @@ megamoe_status megamoe_quantize_int8(const void* x, int x_type, int64_t rows, in
  *   ws        at least megamoe_linear_int8_workspace_size(T, K, N) bytes, 256-byte
  *             aligned; its first 4 bytes are the status word
  * The integers' sum of an fp32 result is exact for K below 131072, whatever T is, and
- * rounded once.  That of a bf16 result is so for up to 4 tokens (16 where their integers
- * fit on chip); else it is exact while no partial sum passes 2^24 in magnitude, and past
- * that cut towards zero at each 16 of K, by up to 2^-23 of what has been added up.
+ * rounded once.  That of a bf16 result is so for few tokens, whose integers fit on chip
+ * (up to 16, with T K up to some 96000); else it is exact while no partial sum passes
+ * 2^24 in magnitude, and past that cut towards zero at each 16 of K, by up to 2^-23 of
+ * what has been added up.
  * Requires K a multiple of 16, N of 8, T, K and N below 2^30, pointers 16-byte
  * aligned (scales 4-byte) and rows on 16-byte boundaries.
  */

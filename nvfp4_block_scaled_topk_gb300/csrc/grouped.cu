@@ -32,9 +32,9 @@
 // From there to some 500 rows what an SM takes in, 50 to 55 bytes a cycle: with 272
 // rows each expert has two tiles of 144, whose stages of 28 KB take the 560 cycles of
 // a full one, 340 us.  Many rows: the MMAs; 16384 rows of eight experts, 7168 x 2048,
-// take 260 us forward and for grad_x (1.84 PFLOP/s, 96 % of a library's dense
-// product; the tensor pipe is 93 % busy) and 255 us for grad_w in bf16.  Few tiles: 5.6
-// us for one of 512 x 512, launch and the first loads; whole turns of the 76 pairs.
+// take 266 us forward and for grad_x (1.81 PFLOP/s, 95 % of a library's dense
+// product) and 270 us for grad_w in bf16.  Few tiles: 5.8 us for one of 512 x 512,
+// launch and the first loads; whole turns of the 76 pairs.
 //
 // Measured and not kept: tiles of 512 rows, which load the weights once for two parts
 // (fewer stages fit: 293 against 340 us at 272 rows, 313 against 259 at 256, 468
@@ -77,8 +77,8 @@ struct GroupedArgs {
   // grad_w right behind grad_x: it needs nothing of it, and that kernel has waited for
   // what both read before it let this one start.  So this one waits for it only at its
   // end, for the sake of the kernel that comes next (both gradients of 8 rows of eight
-  // experts of 512 x 512 12.9 us one after the other, 8.9 so; of 4000 rows of 2048 x 2048
-  // 80.6 and 71.2).
+  // experts of 512 x 512 12.9 us one after the other, 9.2 so; of 4000 rows of 2048 x 2048
+  // 80.6 and 73.8).
   bool late_wait;
   uint32_t* status;
   uint64_t wait_limit_ns;
@@ -714,9 +714,9 @@ cudaError_t launch_typed(const GroupedMaps& maps, const GroupedArgs& a, int64_t 
 // Pairs that share a tile's sum, where the others would idle.  Clusters of 4, 6 and 8
 // CTAs of which each fills an SM fit the GPU 36, 23 and 15 times; the exchange and the
 // sums over the cluster cost about eight stages, and some five more for 256 rows.
-// Whole / shared, us: 8 rows, one expert of 7168 -> 2048 (8 tiles) 29.7 / 14.6, -> 4096
-// 29.8 / 17.9, -> 7168 (28 tiles) 30.1 / 23.5; 64 rows of 4096 -> 4096 19.4 / 14.0; 1000
-// rows of 7168 -> 512 35.4 / 19.6; 64 rows of eight of 2048 -> 1024 12.2 / 11.5.
+// Whole / shared, us: 8 rows, one expert of 7168 -> 2048 (8 tiles) 29.7 / 15.2, -> 4096
+// 29.8 / 18.6, -> 7168 (28 tiles) 30.1 / 24.3; 64 rows of 4096 -> 4096 19.4 / 14.7; 1000
+// rows of 7168 -> 512 35.4 / 20.5; 64 rows of eight of 2048 -> 1024 12.2 / 11.8.
 int share_sum(const GroupedArgs& a, int64_t tiles) {
   static constexpr int kMost[] = {0, 0, 34, 22, 14};  // tiles, by pairs
   const double steps = (a.sum + 63) / 64, rows = std::min(256.0, static_cast<double>(a.rows) / a.E);

@@ -6,8 +6,8 @@
 // The tensor cores of sm_103a have no integer kind.  An 8-bit integer is exact in
 // fp16 and a product of two in fp32, so the integers are multiplied as fp16
 // (kind::f16) and a sum of up to 1024 products is exact.  Longer ones are taken in parts
-// of 1024 that are added up as 32-bit integers (K below 131072), for up to 16 tokens and
-// for fp32 results: the same bits whatever the number of tokens.  A bf16 result of more
+// of 1024 that are added up as 32-bit integers (K below 131072), for few tokens and for
+// fp32 results: the same bits whatever the number of tokens.  A bf16 result of more
 // tokens has its sum in one part, exact while no partial sum passes 2^24; past that each
 // of the K / 16 additions drops what lies below fp32's last bit, up to K / 16 2^-23 of
 // the sum in all, where half a step of bf16 is 2^-9 at least.
@@ -311,10 +311,10 @@ __device__ __forceinline__ float scaled(float sum, float sx, float sw) {
 //
 // us (K -> N; dots / MMA / pairs of CTAs, the last two with the quantiser before them):
 //              1 token      4 tokens     8 tokens     16 tokens
-//   1536 24576  9.4 / 14.1  11.3 / 14.2  14.4 / 24.2  18.4 / 22.9
-//   7168  7168 11.6 / 18.6  15.9 / 18.9  19.2 / 29.9     - / 22.3
-//   7168  2048  7.3 / 11.1  10.5 / 11.9  12.3 / 15.6     - / 14.1
-//   4096  4096  5.3 /  8.4   7.5 /  8.3   8.4 / 15.5  11.2 / 13.4
+//   1536 24576  9.4 / 14.1  11.5 / 14.2  14.3 / 24.2  18.1 / 22.9
+//   7168  7168 11.6 / 18.6  15.8 / 18.9  19.2 / 29.9     - / 22.5
+//   7168  2048  7.3 / 11.1  10.5 / 11.9  12.5 / 15.6     - / 13.8
+//   4096  4096  5.3 /  8.4   7.6 /  8.3   8.9 / 15.5  11.4 / 13.4
 // 1536 -> 24576 are 37.7 MB, 5.6 us at the copy rate; 7.3 us in a stream of calls.
 // ---------------------------------------------------------------------------
 constexpr int kFewThreads = 256;
